@@ -4,21 +4,23 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsgemm.so")
-SOURCES = [os.path.join(CSRC, "sgemm.hip")]
+SOURCES = [os.path.join(CSRC, "sgemm.hip"), os.path.join(CSRC, "vocab.hip")]
 KERNEL_HEADERS = ("kernel_common.hpp", "kernel_mfma.hpp", "kernel_pipe.hpp", "kernel_deep.hpp", "kernel_splitk.hpp",
                   "kernel_direct.hpp", "kernel_dl.hpp", "kernel_valu.hpp")
+VOCAB_HEADERS = ("kernel_vocab.hpp", "kernel_vocab_rows.hpp")
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sgemm_kernels.hpp", "sgemm_launch.hpp", "tuned_table.inc")
-                     + KERNEL_HEADERS] + [
-    os.path.join(os.path.dirname(HERE), "include", "sgemm.h")]
+                     + KERNEL_HEADERS + VOCAB_HEADERS] + [
+    os.path.join(os.path.dirname(HERE), "include", f) for f in ("sgemm.h", "vocab.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-fvisibility=hidden",
     # no packed-fp32 instructions in any kernel (scalar fp32 VALU and MFMA only)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -62,7 +64,19 @@ def build_launch_refs(verbose: bool = False) -> str:
 
 
 def _compile(sources, out: str, verbose: bool, extra_flags) -> str:
-    cmd = [HIPCC, *FLAGS, *(extra_flags or []), *sources, "-o", out + ".tmp"]
+    """Each source to an object of its own, at the same time, then one link."""
+    objects = [f"{out}.{os.path.basename(src)}.o" for src in sources]
+    cmds = [[HIPCC, *FLAGS, *(extra_flags or []), "-c", src, "-o", obj] for src, obj in zip(sources, objects)]
+    with ThreadPoolExecutor(len(cmds)) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), cmds))
+    _run([HIPCC, f"--offload-arch={ARCH}", "-fPIC", "-shared", *objects, "-o", out + ".tmp"], verbose)
+    for obj in objects:
+        os.remove(obj)
+    os.replace(out + ".tmp", out)
+    return out
+
+
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -73,8 +87,6 @@ def _compile(sources, out: str, verbose: bool, extra_flags) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{msg}")
     if verbose and msg.strip():
         print(msg, file=sys.stderr)
-    os.replace(out + ".tmp", out)
-    return out
 
 
 def is_stale(lib: str = LIB) -> bool:

@@ -1,0 +1,409 @@
+// vocab.hip -- entry points of the vocabulary-head operators: cross entropy and distillation over
+// the logits z = alpha * X W^T, forward and gradient, without the T x V logits in memory.
+//
+// Forward: one product whose tiles end as per-token maxima and sums of exponentials (log-sum-exp),
+// and one dot product per named entry.  Gradient: the vocabulary is taken in pieces; a piece's
+// logits are recomputed into D = d(loss)/dz (bf16, or three planes of it for fp32), from which
+// dX += D W and dW = D^T X follow.  The tokens that do not count are left out at the start: the
+// others are packed together, so they cost no product, and whatever their rows hold reaches no
+// gradient.
+#include <limits.h>
+
+#include "../../include/vocab.h"
+#include "kernel_vocab_rows.hpp"
+
+namespace libsgemm {
+namespace vocab {
+namespace {
+
+constexpr int kMaxRows = INT_MAX - 1024;
+constexpr int kMaxHidden = 1 << 20;                // a tile's packed rows stay within 32-bit byte offsets
+constexpr int kMaxTokens = 1 << 21;
+constexpr long kPieceBytes = 768L << 20;           // workspace of one piece of the vocabulary
+
+struct Call {
+    bool f32, grad;
+    int T, V, H;
+    Entries e;
+    float alpha;
+    const void* X;
+    long ldx;
+    const void* W;
+    long ldw;
+    float *loss, *lse_out, *picked_out;
+    const float *lse, *picked, *dloss;
+    void* dX;
+    long lddx;
+    void* dW;
+    long lddw;
+    char* work;
+    hipStream_t stream;
+};
+
+long up(long x, long to) { return (x + to - 1) / to * to; }
+
+// The workspace: byte offsets of its arrays for a call's sizes (the pointers of the call are not
+// looked at, so that its size can be asked for beforehand).
+struct Layout {
+    int tp, hk, hp;      // padded tokens, hidden as a product's k, hidden as a product's rows
+    int piece, pieces;   // vocabulary rows of a piece (a multiple of 256), number of pieces
+    int parts, splits;
+    long count, rows, pos, z, lse_c, scale, out_scale, value, x, xt, w, wt, d, dt, part, acc, bytes;
+};
+
+constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
+
+// Tile shapes.  The large one when it fills the chip, else the small one.
+using Big1 = Tile<1, 256, 256, 128, 64, 2>;
+using Small1 = Tile<1, 128, 64, 64, 32, 3>;
+using Big3 = Tile<3, 256, 128, 64, 64, 2>;
+using Small3 = Tile<3, 128, 64, 64, 32, 2>;
+
+template <class B>
+bool fills(long rows_m, long rows_n) {
+    return up(rows_m, B::kBM) / B::kBM * (up(rows_n, B::kBN) / B::kBN) >= 192;
+}
+
+Layout layout(bool f32, bool grad, int T, int V, int H, int K, bool teacher) {
+    Layout l{};
+    const int P = f32 ? 3 : 1, bk = f32 ? 32 : 64;
+    l.tp = (int)up(T > 0 ? T : 1, 256);
+    l.hk = (int)up(H, bk);
+    l.hp = (int)up(H, 256);
+    const long vp = up(V, 256);
+    const long row = 2L * P;  // bytes of an element in planes
+    const long per = row * (l.hk + (grad ? l.hp + 2L * l.tp : 0));
+    long piece = kPieceBytes / per / 256 * 256;
+    // a launch's grid stays below 2^22 tiles, a packed row below 2^24 bytes
+    const long most = 128L * ((1L << 22) / (l.tp / 64)) / 256 * 256;
+    if (piece > most) piece = most;
+    if (piece > 1L << 21) piece = 1L << 21;
+    if (piece < 256) piece = 256;
+    if (piece > vp) piece = vp;
+    const long pieces = (vp + piece - 1) / piece;
+    l.piece = (int)up((vp + pieces - 1) / pieces, 256);
+    l.pieces = (int)((vp + l.piece - 1) / l.piece);
+    l.parts = (int)(vp / kPartRows);
+    l.splits = 1;
+    if (grad) {
+        // dX has few tiles when there are few tokens: its long axis, the vocabulary, is split then
+        const long tiles = up(T, 64) / 64 * (up(H, 128) / 128);
+        const bool big = f32 ? fills<Big3>(H, T) : fills<Big1>(H, T);
+        if (!big) {
+            long s = 512 / (tiles > 0 ? tiles : 1);
+            const long most = l.piece / bk / 8;
+            s = s > most ? most : s;
+            l.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+        }
+    }
+    long at = 0;
+    auto take = [&](long bytes) {
+        const long o = at;
+        at = up(at + bytes, 1024);
+        return o;
+    };
+    l.count = take(4);
+    l.rows = take(4L * l.tp);
+    l.pos = take(4L * l.tp);
+    if (!teacher) l.z = take(4L * l.tp);
+    l.x = take(row * l.hk * l.tp);
+    l.w = take(row * l.hk * l.piece);
+    if (grad) {
+        l.lse_c = take(4L * l.tp);
+        l.scale = take(4L * l.tp);
+        l.out_scale = take(4L * l.tp);
+        l.value = take(4L * T * K);
+        l.xt = take(row * l.hp * l.tp);
+        l.wt = take(row * l.hp * l.piece);
+        l.d = take(row * l.tp * l.piece);
+        l.dt = take(row * l.tp * l.piece);
+        l.acc = take(4L * l.splits * l.tp * l.hp);
+    } else {
+        l.part = take(8L * l.parts * l.tp);
+    }
+    l.bytes = at;
+    return l;
+}
+
+template <class Small, class Big, class F>
+void by_size(long rows_m, long rows_n, F f) {
+    if (fills<Big>(rows_m, rows_n))
+        f((Big*)nullptr);
+    else
+        f((Small*)nullptr);
+}
+
+template <typename T, int P, class Small, class Big>
+int run(const Call& c) {
+    using Pl = Planes<P>;
+    const Layout l = layout(P == 3, c.grad, c.T, c.V, c.H, c.e.k, c.e.teacher != nullptr);
+    char* ws = c.work;
+    int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
+    const T *X = (const T*)c.X, *W = (const T*)c.W;
+    const hipStream_t st = c.stream;
+    const long x_pitch = Pl::pitch(l.hk), wt_pitch = Pl::pitch(l.piece), t_pitch = Pl::pitch(l.tp);
+    const int slabs = l.hk / Pl::BK;
+    (void)hipGetLastError();
+
+    vocab_count_kernel<<<1, 1024, 0, st>>>(c.e, c.T, rows, pos, count, c.grad ? nullptr : c.loss,
+                                           c.grad ? nullptr : c.lse_out);
+    vocab_pack_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, 0, c.H, ws + l.x, x_pitch, l.hk);
+    // the logits of the named entries
+    const float* z = c.picked;
+    if (c.T > 0 && (!c.grad || !c.e.teacher)) {
+        float* zo = c.e.teacher ? c.picked_out : (float*)(ws + l.z);
+        vocab_pick_kernel<T><<<(unsigned)(up((long)c.T * c.e.k, 4) / 4), 256, 0, st>>>(
+            c.e, c.T, c.V, c.H, c.alpha, X, c.ldx, W, c.ldw, zo);
+        z = zo;
+    }
+    if (c.grad) {
+        if (c.T > 0) vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
+            c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, (float*)(ws + l.lse_c), (float*)(ws + l.scale),
+            (float*)(ws + l.out_scale), (float*)(ws + l.value));
+        if (c.dW)
+            vocab_transpose_kernel<T, P><<<dim3(l.hp / 64, l.tp / 64), 256, 0, st>>>(
+                X, c.ldx, rows, count, 0, c.H, c.e.teacher ? nullptr : (const float*)(ws + l.out_scale), ws + l.xt,
+                t_pitch);
+    }
+    const Operand xs{ws + l.x, (uint32_t)x_pitch, l.tp};
+    // W is read in place when its rows are whole aligned slabs, else packed piece by piece
+    const bool direct = P == 1 && c.H % Pl::BK == 0 && c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 &&
+                        c.ldw < (1L << 22);
+    int part = 0;
+    for (int v0 = 0; v0 < c.V; v0 += l.piece) {
+        const int vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
+        Operand w{(const char*)(W + (size_t)v0 * c.ldw), (uint32_t)(c.ldw * 2), vn};
+        if (!direct) {
+            vocab_pack_kernel<T, P><<<(unsigned)up(vn, 256), 256, 0, st>>>(W + (size_t)v0 * c.ldw, c.ldw, nullptr,
+                                                                         nullptr, vn, c.H, ws + l.w, x_pitch, l.hk);
+            w = Operand{ws + l.w, (uint32_t)x_pitch, (int)up(vn, 256)};
+        }
+        if (!c.grad) {
+            by_size<Small, Big>(vn, c.T, [&](auto* shape) {
+                using S = typename std::remove_pointer<decltype(shape)>::type;
+                const int tm = (int)up(vn, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
+                const LseArgs a{w, xs, count, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part, l.tp};
+                vocab_lse_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
+                part += tm * S::WAVES_M;
+            });
+            continue;
+        }
+        char *d = c.dX ? ws + l.d : nullptr, *dt = c.dW ? ws + l.dt : nullptr;
+        if (c.T > 0) by_size<Small, Big>(vn, c.T, [&](auto* shape) {
+            using S = typename std::remove_pointer<decltype(shape)>::type;
+            // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
+            const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
+            const GradArgs a{w, xs, count, tm, tn, slabs, vn, c.alpha, (const float*)(ws + l.lse_c),
+                             (const float*)(ws + l.scale), d, wt_pitch, dt, t_pitch};
+            vocab_grad_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
+        });
+        if (c.T > 0) vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
+            c.e, c.T, v0, vn, pos, (const float*)(ws + l.value), d, wt_pitch, dt, t_pitch);
+        if (c.T > 0 && c.dX) {
+            vocab_transpose_kernel<T, P><<<dim3(l.hp / 64, (unsigned)(up(vn, 64) / 64)), 256, 0, st>>>(
+                W + (size_t)v0 * c.ldw, c.ldw, nullptr, nullptr, vn, c.H, nullptr, ws + l.wt, wt_pitch);
+            by_size<Small, Big>(c.H, c.T, [&](auto* shape) {
+                using S = typename std::remove_pointer<decltype(shape)>::type;
+                const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
+                const DxArgs a{{ws + l.wt, (uint32_t)wt_pitch, l.hp}, {ws + l.d, (uint32_t)wt_pitch, l.tp}, count, tm,
+                               tn, (int)up(vn, Pl::BK) / Pl::BK, l.splits, (float*)(ws + l.acc), l.tp, l.hp, v0 > 0};
+                vocab_dx_kernel<S><<<dim3(tm * tn, l.splits), S::NT, 0, st>>>(a);
+            });
+        }
+        if (c.dW) {
+            by_size<Small, Big>(c.H, vn, [&](auto* shape) {
+                using S = typename std::remove_pointer<decltype(shape)>::type;
+                const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(vn, S::kBN) / S::kBN;
+                T* out = (T*)c.dW + (size_t)v0 * c.lddw;
+                const int vec = c.H % 4 == 0 && c.lddw % 4 == 0 && (uintptr_t)c.dW % (4 * sizeof(T)) == 0;
+                const DwArgs a{{ws + l.xt, (uint32_t)t_pitch, l.hp}, {ws + l.dt, (uint32_t)t_pitch, l.piece}, count,
+                               tm, tn, c.H, vn, out, c.lddw, vec};
+                vocab_dw_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
+            });
+        }
+    }
+    if (!c.grad)
+        vocab_loss_kernel<<<l.tp / 32, 256, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
+                                                     c.loss, c.lse_out);
+    else if (c.T > 0 && c.dX)
+        vocab_dx_out_kernel<T><<<c.T, 256, 0, st>>>(pos, c.H, (const float*)(ws + l.acc), l.splits, l.tp, l.hp,
+                                                    (const float*)(ws + l.out_scale), (T*)c.dX, c.lddx);
+    return (int)hipGetLastError();
+}
+
+int dispatch(const Call& c) {
+    return c.f32 ? run<float, 3, Small3, Big3>(c) : run<__bf16, 1, Small1, Big1>(c);
+}
+
+bool sizes_ok(int T, int V, int H, int K, int& bad, const int pos[4]) {
+    if (T < 0 || T > kMaxTokens) return bad = pos[0], false;
+    if (V < 1 || V > kMaxRows) return bad = pos[1], false;
+    if (H < 1 || H > kMaxHidden) return bad = pos[2], false;
+    if (K < 1 || (long)K * T > INT_MAX) return bad = pos[3], false;
+    return true;
+}
+
+// Whether two row-major matrices' spans, first to last addressed byte, meet.
+bool meet(const void* a, long rows_a, long lda, const void* b, long rows_b, long ldb, long cols, long size) {
+    if (!a || !b || rows_a == 0 || rows_b == 0) return false;
+    const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+    return p < q + ((rows_b - 1) * ldb + cols) * size && q < p + ((rows_a - 1) * lda + cols) * size;
+}
+// 1: dX overlaps an input, 2: dW overlaps an input or dX.
+int outputs_meet(const Call& c) {
+    const long s = c.f32 ? 4 : 2;
+    if (meet(c.dX, c.T, c.lddx, c.X, c.T, c.ldx, c.H, s) || meet(c.dX, c.T, c.lddx, c.W, c.V, c.ldw, c.H, s)) return 1;
+    if (meet(c.dW, c.V, c.lddw, c.X, c.T, c.ldx, c.H, s) || meet(c.dW, c.V, c.lddw, c.W, c.V, c.ldw, c.H, s) ||
+        meet(c.dW, c.V, c.lddw, c.dX, c.T, c.lddx, c.H, s))
+        return 2;
+    return 0;
+}
+
+}  // namespace
+}  // namespace vocab
+}  // namespace libsgemm
+
+using libsgemm::vocab::Call;
+
+extern "C" {
+
+long long vocab_workspace(int dtype, int grad, int T, int V, int H, int K) {
+    static const int pos[4] = {3, 4, 5, 6};
+    int bad = 0;
+    if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
+    if (!libsgemm::vocab::sizes_ok(T, V, H, K > 0 ? K : 1, bad, pos) || K < 0) return K < 0 ? -6 : -bad;
+    return libsgemm::vocab::layout(dtype == VOCAB_F32, grad != 0, T, V, H, K > 0 ? K : 1, K > 0).bytes;
+}
+
+int vocab_ce(int dtype, int T, int V, int H, float alpha, const void* X, int ldx, const void* W, int ldw,
+             const long long* target, long long ignore_index, float* loss, float* lse, void* work,
+             long long work_bytes, hipStream_t stream) {
+    static const int pos[4] = {2, 3, 4, 2};
+    int bad = 0;
+    if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
+    if (!libsgemm::vocab::sizes_ok(T, V, H, 1, bad, pos)) return -bad;
+    if (ldx < H) return -7;
+    if (ldw < H) return -9;
+    if (T == 0) return 0;
+    if (!X) return -6;
+    if (!W) return -8;
+    if (!target) return -10;
+    if (!loss) return -12;
+    if (!lse) return -13;
+    if (!work || (uintptr_t)work % 16) return -14;
+    if (work_bytes < vocab_workspace(dtype, 0, T, V, H, 0)) return -15;
+    Call c{};
+    c.f32 = dtype == VOCAB_F32;
+    c.T = T, c.V = V, c.H = H, c.alpha = alpha;
+    c.e = {target, 1, 1, ignore_index, nullptr, 0, 0.f};
+    c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
+    c.loss = loss, c.lse_out = lse;
+    c.work = (char*)work, c.stream = stream;
+    return libsgemm::vocab::dispatch(c);
+}
+
+int vocab_ce_grad(int dtype, int T, int V, int H, float alpha, const void* X, int ldx, const void* W, int ldw,
+                  const long long* target, long long ignore_index, const float* lse, const float* dloss, void* dX,
+                  int lddx, void* dW, int lddw, void* work, long long work_bytes, hipStream_t stream) {
+    static const int pos[4] = {2, 3, 4, 2};
+    int bad = 0;
+    if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
+    if (!libsgemm::vocab::sizes_ok(T, V, H, 1, bad, pos)) return -bad;
+    if (ldx < H) return -7;
+    if (ldw < H) return -9;
+    if (dX && lddx < H) return -15;
+    if (dW && lddw < H) return -17;
+    if (!dX && !dW) return 0;
+    if (T > 0) {
+        if (!X) return -6;
+        if (!target) return -10;
+        if (!lse) return -12;
+        if (!dloss) return -13;
+    }
+    if (!W) return -8;
+    if (!work || (uintptr_t)work % 16) return -18;
+    if (work_bytes < vocab_workspace(dtype, 1, T, V, H, 0)) return -19;
+    Call c{};
+    c.f32 = dtype == VOCAB_F32, c.grad = true;
+    c.T = T, c.V = V, c.H = H, c.alpha = alpha;
+    c.e = {target, 1, 1, ignore_index, nullptr, 0, 0.f};
+    c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
+    c.lse = lse, c.dloss = dloss;
+    c.dX = dX, c.lddx = lddx, c.dW = dW, c.lddw = lddw;
+    c.work = (char*)work, c.stream = stream;
+    const int bad_out = libsgemm::vocab::outputs_meet(c);
+    if (bad_out) return bad_out == 1 ? -14 : -16;
+    return libsgemm::vocab::dispatch(c);
+}
+
+int vocab_distill(int dtype, int T, int V, int H, int K, float alpha, float teacher_alpha, const void* X, int ldx,
+                  const void* W, int ldw, const long long* index, int ldi, const float* teacher, int ldt, float* loss,
+                  float* lse, float* picked, void* work, long long work_bytes, hipStream_t stream) {
+    static const int pos[4] = {2, 3, 4, 5};
+    int bad = 0;
+    if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
+    if (!libsgemm::vocab::sizes_ok(T, V, H, K, bad, pos)) return -bad;
+    if (ldx < H) return -9;
+    if (ldw < H) return -11;
+    if (ldi < K) return -13;
+    if (ldt < K) return -15;
+    if (T == 0) return 0;
+    if (!X) return -8;
+    if (!W) return -10;
+    if (!index) return -12;
+    if (!teacher) return -14;
+    if (!loss) return -16;
+    if (!lse) return -17;
+    if (!picked) return -18;
+    if (!work || (uintptr_t)work % 16) return -19;
+    if (work_bytes < vocab_workspace(dtype, 0, T, V, H, K)) return -20;
+    Call c{};
+    c.f32 = dtype == VOCAB_F32;
+    c.T = T, c.V = V, c.H = H, c.alpha = alpha;
+    c.e = {index, ldi, K, 0, teacher, ldt, teacher_alpha};
+    c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
+    c.loss = loss, c.lse_out = lse, c.picked_out = picked;
+    c.work = (char*)work, c.stream = stream;
+    return libsgemm::vocab::dispatch(c);
+}
+
+int vocab_distill_grad(int dtype, int T, int V, int H, int K, float alpha, float teacher_alpha, const void* X,
+                       int ldx, const void* W, int ldw, const long long* index, int ldi, const float* teacher,
+                       int ldt, const float* lse, const float* picked, const float* dloss, void* dX, int lddx,
+                       void* dW, int lddw, void* work, long long work_bytes, hipStream_t stream) {
+    static const int pos[4] = {2, 3, 4, 5};
+    int bad = 0;
+    if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
+    if (!libsgemm::vocab::sizes_ok(T, V, H, K, bad, pos)) return -bad;
+    if (ldx < H) return -9;
+    if (ldw < H) return -11;
+    if (ldi < K) return -13;
+    if (ldt < K) return -15;
+    if (dX && lddx < H) return -20;
+    if (dW && lddw < H) return -22;
+    if (!dX && !dW) return 0;
+    if (T > 0) {
+        if (!X) return -8;
+        if (!index) return -12;
+        if (!teacher) return -14;
+        if (!lse) return -16;
+        if (!picked) return -17;
+        if (!dloss) return -18;
+    }
+    if (!W) return -10;
+    if (!work || (uintptr_t)work % 16) return -23;
+    if (work_bytes < vocab_workspace(dtype, 1, T, V, H, K)) return -24;
+    Call c{};
+    c.f32 = dtype == VOCAB_F32, c.grad = true;
+    c.T = T, c.V = V, c.H = H, c.alpha = alpha;
+    c.e = {index, ldi, K, 0, teacher, ldt, teacher_alpha};
+    c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
+    c.lse = lse, c.picked = picked, c.dloss = dloss;
+    c.dX = dX, c.lddx = lddx, c.dW = dW, c.lddw = lddw;
+    c.work = (char*)work, c.stream = stream;
+    const int bad_out = libsgemm::vocab::outputs_meet(c);
+    if (bad_out) return bad_out == 1 ? -19 : -21;
+    return libsgemm::vocab::dispatch(c);
+}
+
+}  // extern "C"

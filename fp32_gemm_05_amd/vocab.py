@@ -1,0 +1,279 @@
+"""Tensor forms of the vocabulary-head operators (include/vocab.h): checks, allocation of results and
+workspace, and the call.  No arithmetic happens here.
+
+    loss, lse = vocab_ce(X, W, target)                                  # per token, fp32
+    dX, dW = vocab_ce_grad(X, W, target, lse, dloss)
+    loss, lse, picked = vocab_distill(X, W, index, teacher)
+    dX, dW = vocab_distill_grad(X, W, index, teacher, lse, picked, dloss)
+
+X (T x H) and W (V x H) are both float32 or both bfloat16, row-major with any row stride (a
+contiguous copy is asked for where rows overlap).  ``vocab_cross_entropy`` and
+``vocab_distillation`` are the same operators for torch's autograd.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._binding import SgemmArgumentError, SgemmError, SgemmLaunchError, _require_device, load_library
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+_HEAD = ["dtype", "T", "V", "H"]
+_MATRICES = ["X", "ldx", "W", "ldw"]
+_OUT = ["dX", "lddx", "dW", "lddw", "work", "work_bytes", "stream"]
+_NAMES = {
+    "vocab_workspace": ["dtype", "grad", "T", "V", "H", "K"],
+    "vocab_ce": _HEAD + ["alpha"] + _MATRICES + ["target", "ignore_index", "loss", "lse", "work", "work_bytes",
+                                                 "stream"],
+    "vocab_ce_grad": _HEAD + ["alpha"] + _MATRICES + ["target", "ignore_index", "lse", "dloss"] + _OUT,
+    "vocab_distill": _HEAD + ["K", "alpha", "teacher_alpha"] + _MATRICES + [
+        "index", "ldi", "teacher", "ldt", "loss", "lse", "picked", "work", "work_bytes", "stream"],
+    "vocab_distill_grad": _HEAD + ["K", "alpha", "teacher_alpha"] + _MATRICES + [
+        "index", "ldi", "teacher", "ldt", "lse", "picked", "dloss"] + _OUT,
+}
+_KINDS = {"alpha": ctypes.c_float, "teacher_alpha": ctypes.c_float, "ignore_index": ctypes.c_longlong,
+          "work_bytes": ctypes.c_longlong,
+          **dict.fromkeys(["X", "W", "target", "index", "teacher", "loss", "lse", "picked", "dloss", "dX", "dW",
+                           "work", "stream"], ctypes.c_void_p)}
+_entries = {}
+
+
+def _entry(name):
+    if name not in _entries:
+        f = getattr(load_library(), name)
+        f.argtypes = [_KINDS.get(a, ctypes.c_int) for a in _NAMES[name]]
+        f.restype = ctypes.c_longlong if name == "vocab_workspace" else ctypes.c_int
+        _entries[name] = f
+    return _entries[name]
+
+
+def _raise(code, name):
+    names = _NAMES[name]
+    if code < 0:
+        what = f"argument {-code} ({names[-code - 1] if -code <= len(names) else '?'}) is invalid"
+    else:
+        what = f"kernel launch failed with hipError_t {code}"
+    error = SgemmError.__new__(SgemmArgumentError if code < 0 else SgemmLaunchError)
+    RuntimeError.__init__(error, f"{name}: {what}")
+    error.code = code
+    raise error
+
+
+def _call(name, *args):
+    rc = _entry(name)(*args)
+    if rc != 0:
+        _raise(rc, name)
+
+
+def vocab_workspace(dtype, grad: bool, T: int, V: int, H: int, K: int = 0) -> int:
+    """Bytes of workspace of a call (K = 0: cross entropy, else the teacher's entries per token)."""
+    n = _entry("vocab_workspace")(_TYPES[dtype], int(grad), int(T), int(V), int(H), int(K))
+    if n < 0:
+        _raise(n, "vocab_workspace")
+    return n
+
+
+def _matrix(t, name, dtype=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 2 or (t.dtype not in _TYPES if dtype is None else t.dtype != dtype):
+        want = "float32 or bfloat16" if dtype is None else str(dtype).replace("torch.", "")
+        raise TypeError(f"{name} must be a 2-D {want} tensor")
+    _require_device(t, name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be row-major with unit column stride")
+    if t.shape[0] <= 1 or t.shape[1] == 0:
+        return max(1, t.shape[1])  # one row, or no element: no stride is addressed
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} has row stride {t.stride(0)} below its row length {t.shape[1]} "
+                         f"(a broadcast or overlapping view); pass a contiguous copy")
+    return t.stride(0)
+
+
+def _vector(t, name, dtype, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype or t.dim() != 1:
+        raise TypeError(f"{name} must be a 1-D {str(dtype).replace('torch.', '')} tensor")
+    _require_device(t, name)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} has {t.shape[0]} values for {n} tokens")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+
+
+class _Problem:
+    """The checked operands that every call has, and what they share."""
+
+    def __init__(self, X, W, alpha, stream, entries=0):
+        self.ldx, self.ldw = _matrix(X, "X"), _matrix(W, "W", X.dtype)
+        if X.shape[1] != W.shape[1]:
+            raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
+        if W.shape[0] < 1 or W.shape[1] < 1:
+            raise ValueError(f"W {tuple(W.shape)} has no element")
+        self.T, self.H, self.V = X.shape[0], X.shape[1], W.shape[0]
+        self.K = entries
+        self.dtype, self.device = X.dtype, X.device
+        self.head = (_TYPES[X.dtype], self.T, self.V, self.H)
+        self.matrices = (X.data_ptr(), self.ldx, W.data_ptr(), self.ldw)
+        self.alpha = float(alpha)
+        # results and workspace are allocated on the stream that uses them
+        if stream is None:
+            self.stream = torch.cuda.current_stream(self.device)
+        elif isinstance(stream, int):
+            self.stream = torch.cuda.ExternalStream(stream, device=self.device)
+        else:
+            self.stream = stream
+        self.handle = self.stream.cuda_stream
+
+    def same_device(self, *named):
+        for t, name in named:
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, X on {self.device}")
+
+    def new(self, *shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, grad):
+        n = vocab_workspace(self.dtype, grad, self.T, self.V, self.H, self.K)
+        return self.new(n, dtype=torch.uint8), n
+
+
+def _ce(X, W, target, alpha, stream):
+    p = _Problem(X, W, alpha, stream)
+    _vector(target, "target", torch.int64, p.T)
+    p.same_device((W, "W"), (target, "target"))
+    return p
+
+
+def vocab_ce(X, W, target, alpha: float = 1.0, ignore_index: int = -100, stream=None):
+    """Per-token cross entropy of alpha * X @ W.T against target (int64): (loss, lse), both fp32.
+
+    Tokens whose target is ignore_index have loss 0 and lse 0; a target outside the vocabulary
+    gives NaN."""
+    p = _ce(X, W, target, alpha, stream)
+    with torch.cuda.stream(p.stream):
+        loss, lse = p.new(p.T), p.new(p.T)
+        work, n = p.workspace(False)
+        _call("vocab_ce", *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index), loss.data_ptr(),
+              lse.data_ptr(), work.data_ptr(), n, p.handle)
+    return loss, lse
+
+
+def _outputs(p, want_dx, want_dw):
+    if not (want_dx or want_dw):
+        raise ValueError("neither dX nor dW is wanted")
+    return (p.new(p.T, p.H, dtype=p.dtype) if want_dx else None,
+            p.new(p.V, p.H, dtype=p.dtype) if want_dw else None)
+
+
+def _out_args(p, dX, dW, work, n):
+    return (None if dX is None else dX.data_ptr(), p.H, None if dW is None else dW.data_ptr(), p.H,
+            work.data_ptr(), n, p.handle)
+
+
+def vocab_ce_grad(X, W, target, lse, dloss, alpha: float = 1.0, ignore_index: int = -100, want_dx: bool = True,
+                  want_dw: bool = True, stream=None):
+    """Gradients (dX, dW) of sum(dloss * loss), from the lse of vocab_ce; one that is not wanted is None
+    and costs no product."""
+    p = _ce(X, W, target, alpha, stream)
+    _vector(lse, "lse", torch.float32, p.T)
+    _vector(dloss, "dloss", torch.float32, p.T)
+    p.same_device((lse, "lse"), (dloss, "dloss"))
+    with torch.cuda.stream(p.stream):
+        dX, dW = _outputs(p, want_dx, want_dw)
+        work, n = p.workspace(True)
+        _call("vocab_ce_grad", *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index), lse.data_ptr(),
+              dloss.data_ptr(), *_out_args(p, dX, dW, work, n))
+    return dX, dW
+
+
+def _distill(X, W, index, teacher, alpha, stream):
+    ldi, ldt = _matrix(index, "index", torch.int64), _matrix(teacher, "teacher", torch.float32)
+    if index.shape != teacher.shape:
+        raise ValueError(f"shape mismatch: index {tuple(index.shape)}, teacher {tuple(teacher.shape)}")
+    if index.shape[1] < 1:
+        raise ValueError("index has no entry")
+    p = _Problem(X, W, alpha, stream, index.shape[1])
+    if index.shape[0] != p.T:
+        raise ValueError(f"index has {index.shape[0]} rows for {p.T} tokens")
+    p.same_device((W, "W"), (index, "index"), (teacher, "teacher"))
+    return p, (index.data_ptr(), ldi, teacher.data_ptr(), ldt)
+
+
+def vocab_distill(X, W, index, teacher, alpha: float = 1.0, teacher_alpha: float = 1.0, stream=None):
+    """Per-token divergence of softmax(alpha * X @ W.T) from a teacher's top logits: (loss, lse, picked).
+
+    index (T x K, int64) names vocabulary rows, teacher (T x K, fp32) their logits; an index < 0 is
+    no entry, and a token without entries has loss 0.  picked (T x K) holds the student's logits at
+    the entries, which the gradient takes back."""
+    p, entries = _distill(X, W, index, teacher, alpha, stream)
+    with torch.cuda.stream(p.stream):
+        loss, lse, picked = p.new(p.T), p.new(p.T), p.new(p.T, p.K)
+        work, n = p.workspace(False)
+        _call("vocab_distill", *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries, loss.data_ptr(),
+              lse.data_ptr(), picked.data_ptr(), work.data_ptr(), n, p.handle)
+    return loss, lse, picked
+
+
+def vocab_distill_grad(X, W, index, teacher, lse, picked, dloss, alpha: float = 1.0, teacher_alpha: float = 1.0,
+                       want_dx: bool = True, want_dw: bool = True, stream=None):
+    """Gradients (dX, dW) of sum(dloss * loss), from the lse and picked of vocab_distill."""
+    p, entries = _distill(X, W, index, teacher, alpha, stream)
+    _vector(lse, "lse", torch.float32, p.T)
+    _vector(dloss, "dloss", torch.float32, p.T)
+    if _matrix(picked, "picked", torch.float32) != p.K or tuple(picked.shape) != (p.T, p.K):
+        raise ValueError("picked must be the contiguous T x K tensor of vocab_distill")
+    p.same_device((lse, "lse"), (dloss, "dloss"), (picked, "picked"))
+    with torch.cuda.stream(p.stream):
+        dX, dW = _outputs(p, want_dx, want_dw)
+        work, n = p.workspace(True)
+        _call("vocab_distill_grad", *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries,
+              lse.data_ptr(), picked.data_ptr(), dloss.data_ptr(), *_out_args(p, dX, dW, work, n))
+    return dX, dW
+
+
+class _CrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, target, alpha, ignore_index):
+        loss, lse = vocab_ce(X, W, target, alpha, ignore_index)
+        ctx.save_for_backward(X, W, target, lse)
+        ctx.args = alpha, ignore_index
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        X, W, target, lse = ctx.saved_tensors
+        dX, dW = vocab_ce_grad(X, W, target, lse, dloss.contiguous(), *ctx.args, want_dx=ctx.needs_input_grad[0],
+                               want_dw=ctx.needs_input_grad[1])
+        return dX, dW, None, None, None
+
+
+class _Distillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, W, index, teacher, alpha, teacher_alpha):
+        loss, lse, picked = vocab_distill(X, W, index, teacher, alpha, teacher_alpha)
+        ctx.save_for_backward(X, W, index, teacher, lse, picked)
+        ctx.args = alpha, teacher_alpha
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        X, W, index, teacher, lse, picked = ctx.saved_tensors
+        dX, dW = vocab_distill_grad(X, W, index, teacher, lse, picked, dloss.contiguous(), *ctx.args,
+                                    want_dx=ctx.needs_input_grad[0], want_dw=ctx.needs_input_grad[1])
+        return dX, dW, None, None, None, None
+
+
+def vocab_cross_entropy(X, W, target, alpha: float = 1.0, ignore_index: int = -100):
+    """vocab_ce's loss per token, differentiable with respect to X and W."""
+    return _CrossEntropy.apply(X, W, target, alpha, ignore_index)
+
+
+def vocab_distillation(X, W, index, teacher, alpha: float = 1.0, teacher_alpha: float = 1.0):
+    """vocab_distill's loss per token, differentiable with respect to X and W (not the teacher)."""
+    return _Distillation.apply(X, W, index, teacher, alpha, teacher_alpha)

@@ -663,7 +663,7 @@ struct MfmaFrag {
 // ---------------------------------------------------------------------------------
 // C := beta * C (the alpha == 0 / K == 0 case; beta == 0 writes zeros without reading C).
 // ---------------------------------------------------------------------------------
-inline __global__ void __launch_bounds__(256) sgemm_scale_kernel(int M, int N, float beta, float* C, long ldc) {
+static __global__ void __launch_bounds__(256) sgemm_scale_kernel(int M, int N, float beta, float* C, long ldc) {
     const long total = (long)M * N;
     for (long e = (long)blockIdx.x * blockDim.x + threadIdx.x; e < total; e += (long)gridDim.x * blockDim.x) {
         const long i = e / N, j = e - i * N;

@@ -1,8 +1,9 @@
 // kernel_vocab.hpp -- the matrix products of the vocabulary-head operators (gfx950, bf16 MFMA).
 //
-// One tile loop serves every product: C(m, n) = sum_k A[m][k] * B[n][k], both operands stored with
-// k contiguous, multiplied with v_mfma_f32_32x32x16_bf16 and accumulated in fp32.  What differs is
-// what the finished tile is used for:
+// One tile loop serves every product: C(m, n) = sum_k A(m, k) * B(n, k), each operand stored with k
+// along its rows or down its columns (then read from LDS with transposing loads), multiplied with
+// v_mfma_f32_32x32x16_bf16 and accumulated in fp32.  No matrix is transposed in memory.  What
+// differs is what the finished tile is used for:
 //
 //   vocab_lse_kernel    z = alpha * W X^T, reduced over the tile's vocabulary rows to the maximum
 //                       and the sum of exponentials per token: the logits are never stored;
@@ -29,6 +30,8 @@ namespace vocab {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int P>
 struct Planes {
@@ -91,109 +94,218 @@ __device__ inline void store4(char* row, long k, const float (&x)[4]) {
     for (int p = 0; p < P; ++p) *(bf16x4*)(row + Planes<P>::at(k, p)) = o[p];
 }
 
-// A product operand: rows of `pitch` bytes, rows past `rows` read as its last row.
+// A product operand, stored with k along its rows (K_ROW: A[m][k]) or down its columns (K_COL:
+// A[k][m]); rows past `rows` read as its last row, quads past row_bytes as its last quad.  Neither
+// kind of stand-in reaches a result: past-the-end m or n are never stored, past-the-end k meet
+// zeros of the other operand.
 struct Operand {
     const char* base;
-    uint32_t pitch;
+    uint32_t pitch, row_bytes;
     int rows;
 };
+enum Order { K_ROW, K_COL };
 
-// The tile loop.  The operands' slabs go straight from global memory into a ring of ST LDS stages;
-// slab s + ST - 1 is requested after the barrier that opens slab s, so each load has ST - 1 slabs
-// of matrix work to arrive in.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// One operand's side of the tile: R rows (m or n) of a slab of BK k, NT threads.
+template <int P, Order O, int R, int W, int NT>
+struct Side {
+    static constexpr int BK = Planes<P>::BK, NW = NT / 64;
+    static constexpr int BYTES = R * BK * 2 * P;                            // of a slab in LDS
+    static constexpr int QUADS = O == K_ROW ? Planes<P>::QR : R * P / 8;    // per stored row
+    static constexpr int ROW = QUADS * 16;
+    static constexpr int L = BYTES / 16 / NT;                               // loads per thread
+    static constexpr int B = W / 32;                                        // 32-row blocks of a wave
+    static constexpr int KK = BK / 16;
+    static_assert(BYTES / 16 % NT == 0, "whole loads per thread");
+
+    // K_COL: chunk c (64 bytes: 32 m of one plane) of LDS row r holds chunk c ^ flip(r).  A transposed
+    // 64-bit read is served in passes of 32 lanes, which read one chunk each of four consecutive
+    // rows: the flips put those on the four different quarters of the 64 banks.
+    static constexpr int CHUNKS = R * P / 32;
+    static_assert(O == K_ROW || CHUNKS % 2 == 0, "chunks pair up");
+    __host__ __device__ static constexpr int flip(int r) { return CHUNKS % 4 == 0 ? (r & 3) : ((r >> 1) & 1); }
+    __host__ __device__ static constexpr int source_quad(int r, int u) {
+        return O == K_ROW ? Planes<P>::swz(r, u) : (u ^ (flip(r) << 2));
+    }
+
+    const char* at;       // next slab
+    size_t step;          // bytes from slab to slab
+    uint32_t off[L];
+    int left;             // K_COL: rows from `at` to the operand's end
+    uint32_t lane_at[O == K_ROW ? KK : (B > 1 ? B : 1) * P];  // LDS offsets of this lane's fragments
+    int frag;             // wave's part of them
+
+    __device__ inline void init(const Operand& o, int row0, int k0, int wave, int lane, int wave_at) {
+        if (O == K_ROW) {
+            at = o.base + (size_t)row0 * o.pitch + (size_t)k0 * ROW;
+            step = ROW;
+            left = 0;
+        } else {
+            at = o.base + (size_t)k0 * BK * o.pitch + (size_t)row0 * 2 * P;
+            step = (size_t)BK * o.pitch;
+            left = o.rows - k0 * BK;
+        }
+        set_offsets(o, row0, wave, lane);
+        const int l = lane & 31, h = lane >> 5;
+        if (O == K_ROW) {
+            // row l of a block, quad 2 * kk + h of plane 0
+            frag = wave_at * W * ROW;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) lane_at[kk] = l * ROW + Planes<P>::swz(l, 2 * kk + h) * 16;
+        } else {
+            // lane i of a group of 16 points at k = i / 4, m = 4 * (i % 4) and gets k = 0 .. 3 of m = i
+            const int i = lane & 15, r = 8 * h + (i >> 2), f = flip(i >> 2);
+            frag = 0;
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const int c = ((wave_at * B + b) * P + p) ^ f;
+                    lane_at[b * P + p] = r * ROW + c * 64 + ((lane >> 4) & 1) * 32 + (i & 3) * 8;
+                }
+        }
+    }
+    __device__ inline void set_offsets(const Operand& o, int row0, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int i = (j * NW + wave) * 64 + lane;
+            const int r = i / QUADS, u = i - r * QUADS;
+            if (O == K_ROW) {
+                const int row = imin(row0 + r, o.rows - 1) - row0;  // the tile's first row is always valid
+                off[j] = (uint32_t)row * o.pitch + (uint32_t)(source_quad(r, u) * 16);
+            } else {
+                const uint32_t q = (uint32_t)row0 * 2 * P + (uint32_t)(source_quad(r, u) * 16);
+                const uint32_t last = o.row_bytes - 16;
+                off[j] = (uint32_t)imin(r, left - 1) * o.pitch + (q < last ? q : last) - (uint32_t)row0 * 2 * P;
+            }
+        }
+    }
+    // Requests loads [from, to) of the next slab into LDS at `lds`.
+    __device__ inline void issue(uint32_t lds, int from, int to) const {
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (j >= from && j < to) dl_load<16>(at, off[j], lds + j * NW * 1024);
+    }
+    __device__ inline void next(const Operand& o, int row0, int wave, int lane) {
+        at += step;
+        if (O == K_COL) {
+            left -= BK;
+            if (left < BK && left > 0) set_offsets(o, row0, wave, lane);
+        }
+    }
+    // The fragments of k-step kk: of a lane, 8 consecutive k of its row in each block and plane.
+    __device__ inline void read(const char* slab, int kk, bf16x8 (&v)[P][B]) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (O == K_ROW) {
+                    v[p][b] = *(const bf16x8*)(slab + frag + b * 32 * ROW + p * 64 + lane_at[kk]);
+                } else {
+                    const char* a = slab + lane_at[b * P + p] + kk * 16 * ROW;
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ROW));
+                    v[p][b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+            }
+    }
+};
+
+// The tile loop.  The operands' slabs go straight from global memory into a ring of ST LDS stages.
+// A slab's first fragments are read, and the stage of the slab before it is requested anew, behind
+// the barrier that comes before the last k-step of that slab: the matrix unit has that k-step to do
+// while the reads are on their way.
 template <int P, int BM, int BN, int WM, int WN, int ST>
 struct Tile {
     static constexpr int kP = P, kBM = BM, kBN = BN, kWM = WM, kWN = WN;
     static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
     static constexpr int MB = WM / 32, NB = WN / 32;
-    static constexpr int QR = Planes<P>::QR, ROW = Planes<P>::ROW, BK = Planes<P>::BK;
-    static constexpr int LA = BM * QR / NT, LB = BN * QR / NT;
-    static constexpr int STAGE = (BM + BN) * ROW;
+    static constexpr int BK = Planes<P>::BK, KK = BK / 16;
+    static constexpr int STAGE = (BM + BN) * BK * 2 * P;
     static constexpr int LDS_BYTES = STAGE * ST;
-    static_assert(BM * QR % NT == 0 && BN * QR % NT == 0, "whole loads per thread");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
-    static_assert((LA + LB) * (ST - 1) < 64, "vmcnt counts at most 63 loads in flight");
 
     f32x16 acc[MB][NB];
 
-    template <int ROWS, int L>
-    static __device__ inline void offsets(const Operand& o, int row0, int wave, int lane, uint32_t (&off)[L]) {
-#pragma unroll
-        for (int j = 0; j < L; ++j) {
-            const int i = (j * NW + wave) * 64 + lane;
-            const int r = i / QR, u = i - r * QR;
-            const int row = imin(row0 + r, o.rows - 1) - row0;  // the tile's first row is always valid
-            off[j] = (uint32_t)row * o.pitch + (uint32_t)(Planes<P>::swz(r, u) * 16);
-        }
-    }
-
     // Multiplies slabs [k0, k0 + slabs) of A rows m0.. and B rows n0..; lds: LDS_BYTES.
+    template <Order OA, Order OB>
     __device__ inline void run(char* lds, const Operand& a, int m0, const Operand& b, int n0, int k0, int slabs) {
+        using A = Side<P, OA, BM, WM, NT>;
+        using B = Side<P, OB, BN, WN, NT>;
+        constexpr int LA = A::L, LB = B::L, LL = LA + LB;
+        static_assert(LL * (ST - 1) < 64, "vmcnt counts at most 63 loads in flight");
         const int lane = threadIdx.x & 63;
         const int wave = (int)uniform_u32(threadIdx.x >> 6);
-        const int wm = wave / WAVES_N, wn = wave % WAVES_N;
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int j = 0; j < NB; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
-        uint32_t oa[LA], ob[LB];
-        offsets<BM, LA>(a, m0, wave, lane, oa);
-        offsets<BN, LB>(b, n0, wave, lane, ob);
-        const char* pa = a.base + (size_t)m0 * a.pitch + (size_t)k0 * ROW;
-        const char* pb = b.base + (size_t)n0 * b.pitch + (size_t)k0 * ROW;
+        if (slabs <= 0) return;
+        A sa;
+        B sb;
+        sa.init(a, m0, k0, wave, lane, wave / WAVES_N);
+        sb.init(b, n0, k0, wave, lane, wave % WAVES_N);
         const uint32_t base = lds_addr((const float*)lds) + wave * 1024;
-        auto issue = [&](int stage) {
+        // part q of KK of a slab's requests
+        auto issue = [&](int stage, int q) {
             const uint32_t at = base + stage * STAGE;
-#pragma unroll
-            for (int j = 0; j < LA; ++j) dl_load<16>(pa, oa[j], at + j * NW * 1024);
-#pragma unroll
-            for (int j = 0; j < LB; ++j) dl_load<16>(pb, ob[j], at + BM * ROW + j * NW * 1024);
-            pa += ROW;
-            pb += ROW;
+            sa.issue(at, LA * q / KK, LA * (q + 1) / KK);
+            sb.issue(at + A::BYTES, LB * q / KK, LB * (q + 1) / KK);
+            if (q == KK - 1) {
+                sa.next(a, m0, wave, lane);
+                sb.next(b, n0, wave, lane);
+            }
         };
-        // fragment addresses: row l of a block, quad (of plane p) 2 * kk + half, swizzled
-        const int l = lane & 31, h = lane >> 5;
-        constexpr int KK = BK / 16;
-        int fq[KK];
+        bf16x8 va[2][P][MB], vb[2][P][NB];
+        auto read = [&](int stage, int kk) {
+            sa.read(lds + stage * STAGE, kk, va[kk & 1]);
+            sb.read(lds + stage * STAGE + A::BYTES, kk, vb[kk & 1]);
+        };
+        auto multiply = [&](int kk) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) fq[kk] = l * ROW + Planes<P>::swz(l, 2 * kk + h) * 16;
-        const char* fa = lds + wm * WM * ROW;
-        const char* fb = lds + BM * ROW + wn * WN * ROW;
+            for (int w = P - 1; w >= 0; --w)  // planes of total weight w, the smallest terms first
 #pragma unroll
-        for (int s = 0; s < ST - 1; ++s)
-            if (s < slabs) issue(s);
+                for (int p = 0; p <= w; ++p)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[kk & 1][p][i], vb[kk & 1][w - p][j],
+                                                                               acc[i][j], 0, 0, 0);
+        };
+#pragma unroll
+        for (int s = 0; s < ST; ++s)
+            if (s < slabs)
+#pragma unroll
+                for (int q = 0; q < KK; ++q) issue(s, q);
+        wait_slabs<LL>(imin(ST, slabs) - 1);
+        dl_barrier();
+        read(0, 0);
         int stage = 0;
         for (int s = 0; s < slabs; ++s) {
-            wait_slabs<LA + LB>(imin(ST - 2, slabs - 1 - s));
-            dl_barrier();
-            if (s + ST - 1 < slabs) issue(stage == 0 ? ST - 1 : stage - 1);
-            const char* sa = fa + stage * STAGE;
-            const char* sb = fb + stage * STAGE;
+            const int next = stage + 1 == ST ? 0 : stage + 1;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                bf16x8 va[P][MB], vb[P][NB];
+                if (kk + 1 < KK) {
+                    read(stage, kk + 1);
+                } else if (s + 1 < slabs) {
+                    // this wave's reads of the slab are done; slab s + 1 has landed; later ones are in flight
+                    wait_slabs<LL>(imin(ST - 2, slabs - 2 - s));
+                    dl_barrier();
+                    read(next, 0);
+                    if (s + ST < slabs)
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-#pragma unroll
-                    for (int i = 0; i < MB; ++i) va[p][i] = *(const bf16x8*)(sa + i * 32 * ROW + p * 64 + fq[kk]);
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) vb[p][j] = *(const bf16x8*)(sb + j * 32 * ROW + p * 64 + fq[kk]);
+                        for (int q = 0; q < KK; ++q) issue(stage, q);
                 }
-#pragma unroll
-                for (int w = P - 1; w >= 0; --w)  // planes of total weight w, the smallest terms first
-#pragma unroll
-                    for (int p = 0; p <= w; ++p)
-#pragma unroll
-                        for (int i = 0; i < MB; ++i)
-#pragma unroll
-                            for (int j = 0; j < NB; ++j)
-                                acc[i][j] =
-                                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[p][i], vb[w - p][j], acc[i][j], 0, 0, 0);
+                multiply(kk);
             }
-            stage = stage + 1 == ST ? 0 : stage + 1;
+            stage = next;
         }
+        // all waves are done with the stages: a user of run may reuse lds after a barrier
     }
 
     // Element e of block (i, j) of this lane is C(m0 + row(i, e), n0 + col(j)).
@@ -224,7 +336,7 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
     const int m0 = tm * T::kBM, n0 = tn * T::kBN;
     if (n0 >= *a.count) return;
     T t;
-    t.run(lds, a.w, m0, a.x, n0, 0, a.slabs);
+    t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
     const int h = (threadIdx.x & 63) >> 5;
     const int piece = a.part0 + tm * T::WAVES_M + (threadIdx.x >> 6) / T::WAVES_N;
 #pragma unroll
@@ -260,8 +372,6 @@ struct GradArgs {
     const float* scale;  // per counted token: D = exp(z - lse) * scale
     char* d;             // [token][vocabulary piece], planes
     long d_pitch;
-    char* dt;            // [vocabulary piece][token], planes; null: not wanted
-    long dt_pitch;
 };
 
 template <class T>
@@ -270,35 +380,51 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     int tm, tn;
     tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
     const int m0 = tm * T::kBM, n0 = tn * T::kBN;
-    const int count = *a.count;
+    const int count = *a.count, h = (threadIdx.x & 63) >> 5;
     if (n0 >= count) return;
     T t;
-    t.run(lds, a.w, m0, a.x, n0, 0, a.slabs);
+    t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
         const bool live = n < count;
         const float lse = live ? a.lse[n] : 0.f, scale = live ? a.scale[n] : 0.f;
+        char* out = a.d + (size_t)n * a.d_pitch;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int m = m0 + t.row(i, 4 * g);
-                float v[4];
+            for (int g = 0; g < 4; g += 2) {
+                bf16x4 v[2][T::kP];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    // entries past the vocabulary and tokens past the count are the zeros that the
-                    // products of D run over
-                    v[q] = live && m + q < a.vocab ? __expf(t.acc[i][j][4 * g + q] * a.alpha - lse) * scale : 0.f;
-                    if (a.dt) store1<T::kP>(a.dt + (size_t)(m + q) * a.dt_pitch, n, v[q]);
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int e = 4 * (g + f) + q;
+                        // entries past the vocabulary and tokens past the count are the zeros that the
+                        // products of D run over
+                        const float x = live && m0 + t.row(i, e) < a.vocab
+                                            ? __expf(t.acc[i][j][e] * a.alpha - lse) * scale : 0.f;
+                        __bf16 x_p[T::kP];
+                        split<T::kP>(x, x_p);
+#pragma unroll
+                        for (int p = 0; p < T::kP; ++p) v[f][p][q] = x_p[p];
+                    }
+                // the lane halves hold entries 0-3, 8-11 and 4-7, 12-15 of sixteen: they trade, so that
+                // each stores eight in a row
+                const int m = m0 + t.row(i, 4 * g) + 4 * h;
+#pragma unroll
+                for (int p = 0; p < T::kP; ++p) {
+                    const u32x2 x = __builtin_bit_cast(u32x2, v[0][p]), y = __builtin_bit_cast(u32x2, v[1][p]);
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+                    *(u32x4*)(out + Planes<T::kP>::at(m, p)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
                 }
-                if (a.d) store4<T::kP>(a.d + (size_t)n * a.d_pitch, m, v);
             }
     }
 }
 
 struct DxArgs {
-    Operand wt, d;     // [hidden][vocabulary piece], [token][vocabulary piece]
+    Operand w, d;      // [vocabulary piece][hidden], [token][vocabulary piece]
     const int* count;
     int tiles_m, tiles_n, slabs, splits;
     float* acc;        // [splits][tp][hp]
@@ -318,7 +444,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dx_kernel(DxArgs a) {
     const int z = blockIdx.y;
     const int first = (int)((long)a.slabs * z / a.splits), last = (int)((long)a.slabs * (z + 1) / a.splits);
     T t;
-    t.run(lds, a.wt, m0, a.d, n0, first, last - first);
+    t.template run<K_COL, K_ROW>(lds, a.w, m0, a.d, n0, first, last - first);
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
@@ -337,7 +463,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dx_kernel(DxArgs a) {
 }
 
 struct DwArgs {
-    Operand xt, dt;    // [hidden][token], [vocabulary piece][token]
+    Operand x, d;      // [token][hidden], scaled; [token][vocabulary piece]
     const int* count;
     int tiles_m, tiles_n, hidden, vocab;
     void* out;         // [vocabulary piece][hidden] in the operands' type
@@ -354,7 +480,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
     tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
     const int m0 = tm * T::kBM, n0 = tn * T::kBN;
     T t;
-    t.run(lds, a.xt, m0, a.dt, n0, 0, (*a.count + T::BK - 1) / T::BK);
+    t.template run<K_COL, K_COL>(lds, a.x, m0, a.d, n0, 0, (*a.count + T::BK - 1) / T::BK);
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);

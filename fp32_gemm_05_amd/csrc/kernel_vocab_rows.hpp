@@ -78,45 +78,25 @@ __device__ inline float wave_max(float s) {
 }
 
 // Rows (through `map` when given) of a rows x cols matrix, packed: row i at dst + i * pitch, zero
-// past cols up to kp, whole zero rows from the number of rows to its next multiple of 256.
+// past cols up to kp, whole zero rows from the number of rows to its next multiple of 256.  scaled
+// (when given) gets the rows times scale[i].
 template <typename T, int P>
 __global__ void __launch_bounds__(256) vocab_pack_kernel(const T* src, long ld, const int* map, const int* count,
-                                                         int rows, int cols, char* dst, long pitch, int kp) {
+                                                         int rows, int cols, char* dst, long pitch, int kp,
+                                                         const float* scale, char* scaled) {
     const int i = blockIdx.x, n = count ? *count : rows;
     if (i >= (n + 255) / 256 * 256) return;
     const T* s = i < n ? src + (size_t)(map ? map[i] : i) * ld : nullptr;
-    char* d = dst + (size_t)i * pitch;
+    const float f = scaled && i < n ? scale[i] : 0.f;
     for (int k = threadIdx.x * 4; k < kp; k += 1024) {
         float v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = s && k + q < cols ? (float)s[k + q] : 0.f;
-        store4<P>(d, k, v);
-    }
-}
-
-// The transpose of the same: column c of the matrix at dst + c * pitch, the rows along it times
-// scale[row] when given, zero past the number of rows up to the end of its 64-row block.
-template <typename T, int P>
-__global__ void __launch_bounds__(256) vocab_transpose_kernel(const T* src, long ld, const int* map, const int* count,
-                                                              int rows, int cols, const float* scale, char* dst,
-                                                              long pitch) {
-    __shared__ float tile[64][65];
-    const int n = count ? *count : rows, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-    if (r0 >= (n + 63) / 64 * 64) return;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    for (int r = ty; r < 64; r += 4) {
-        float v = 0.f;
-        if (r0 + r < n && c0 + tx < cols) {
-            v = (float)src[(size_t)(map ? map[r0 + r] : r0 + r) * ld + c0 + tx];
-            if (scale) v *= scale[r0 + r];
-        }
-        tile[r][tx] = v;
-    }
-    __syncthreads();
-    const int q = threadIdx.x & 15, cy = threadIdx.x >> 4;
-    for (int c = cy; c < 64; c += 16) {
-        const float v[4] = {tile[4 * q][c], tile[4 * q + 1][c], tile[4 * q + 2][c], tile[4 * q + 3][c]};
-        store4<P>(dst + (size_t)(c0 + c) * pitch, r0 + 4 * q, v);
+        store4<P>(dst + (size_t)i * pitch, k, v);
+        if (!scaled) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] *= f;
+        store4<P>(scaled + (size_t)i * pitch, k, v);
     }
 }
 
@@ -258,19 +238,17 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, 
     }
 }
 
-// Puts the entries' values into D and its transpose where they fall into this piece.
+// Puts the entries' values into D where they fall into this piece.
 template <int P>
 __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens, int v0, int vocab, const int* pos,
-                                                          const float* value, char* d, long d_pitch, char* dt,
-                                                          long dt_pitch) {
+                                                          const float* value, char* d, long d_pitch) {
     const long j = (long)blockIdx.x * 256 + threadIdx.x;
     if (j >= (long)tokens * e.k) return;
     const long t = j / e.k, k = j - t * e.k;
     const int i = pos[t];
     const i64 v = e.index[t * e.ld + k];
     if (i < 0 || !e.counts(v) || v < v0 || v >= v0 + vocab) return;
-    if (d) store1<P>(d + (size_t)i * d_pitch, v - v0, value[j]);
-    if (dt) store1<P>(dt + (size_t)(v - v0) * dt_pitch, i, value[j]);
+    store1<P>(d + (size_t)i * d_pitch, v - v0, value[j]);
 }
 
 // dX of every token: the sum of its product's parts, or 0 where it does not count.

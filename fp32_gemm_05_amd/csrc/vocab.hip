@@ -48,7 +48,7 @@ struct Layout {
     int tp, hk, hp;      // padded tokens, hidden as a product's k, hidden as a product's rows
     int piece, pieces;   // vocabulary rows of a piece (a multiple of 256), number of pieces
     int parts, splits;
-    long count, rows, pos, z, lse_c, scale, out_scale, value, x, xt, w, wt, d, dt, part, acc, bytes;
+    long count, rows, pos, z, lse_c, scale, out_scale, value, x, xs, w, d, part, acc, bytes;
 };
 
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
@@ -72,7 +72,7 @@ Layout layout(bool f32, bool grad, int T, int V, int H, int K, bool teacher) {
     l.hp = (int)up(H, 256);
     const long vp = up(V, 256);
     const long row = 2L * P;  // bytes of an element in planes
-    const long per = row * (l.hk + (grad ? l.hp + 2L * l.tp : 0));
+    const long per = row * (l.hk + (grad ? l.tp : 0));
     long piece = kPieceBytes / per / 256 * 256;
     // a launch's grid stays below 2^22 tiles, a packed row below 2^24 bytes
     const long most = 128L * ((1L << 22) / (l.tp / 64)) / 256 * 256;
@@ -113,10 +113,8 @@ Layout layout(bool f32, bool grad, int T, int V, int H, int K, bool teacher) {
         l.scale = take(4L * l.tp);
         l.out_scale = take(4L * l.tp);
         l.value = take(4L * T * K);
-        l.xt = take(row * l.hp * l.tp);
-        l.wt = take(row * l.hp * l.piece);
+        if (!teacher) l.xs = take(row * l.hk * l.tp);
         l.d = take(row * l.tp * l.piece);
-        l.dt = take(row * l.tp * l.piece);
         l.acc = take(4L * l.splits * l.tp * l.hp);
     } else {
         l.part = take(8L * l.parts * l.tp);
@@ -141,13 +139,12 @@ int run(const Call& c) {
     int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
     const T *X = (const T*)c.X, *W = (const T*)c.W;
     const hipStream_t st = c.stream;
-    const long x_pitch = Pl::pitch(l.hk), wt_pitch = Pl::pitch(l.piece), t_pitch = Pl::pitch(l.tp);
+    const long x_pitch = Pl::pitch(l.hk), d_pitch = Pl::pitch(l.piece);
     const int slabs = l.hk / Pl::BK;
     (void)hipGetLastError();
 
     vocab_count_kernel<<<1, 1024, 0, st>>>(c.e, c.T, rows, pos, count, c.grad ? nullptr : c.loss,
                                            c.grad ? nullptr : c.lse_out);
-    vocab_pack_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, 0, c.H, ws + l.x, x_pitch, l.hk);
     // the logits of the named entries
     const float* z = c.picked;
     if (c.T > 0 && (!c.grad || !c.e.teacher)) {
@@ -160,53 +157,52 @@ int run(const Call& c) {
         if (c.T > 0) vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
             c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, (float*)(ws + l.lse_c), (float*)(ws + l.scale),
             (float*)(ws + l.out_scale), (float*)(ws + l.value));
-        if (c.dW)
-            vocab_transpose_kernel<T, P><<<dim3(l.hp / 64, l.tp / 64), 256, 0, st>>>(
-                X, c.ldx, rows, count, 0, c.H, c.e.teacher ? nullptr : (const float*)(ws + l.out_scale), ws + l.xt,
-                t_pitch);
     }
-    const Operand xs{ws + l.x, (uint32_t)x_pitch, l.tp};
+    // cross entropy multiplies dW with X scaled by token (vocab_rows_kernel), distillation with X
+    char* const xs = c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
+    vocab_pack_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, 0, c.H, ws + l.x, x_pitch, l.hk,
+                                                  (const float*)(ws + l.out_scale), xs);
+    const Operand x{ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
+    const Operand x_dw{xs ? xs : ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
+    const Operand d{ws + l.d, (uint32_t)d_pitch, (uint32_t)d_pitch, l.tp};
     // W is read in place when its rows are whole aligned slabs, else packed piece by piece
     const bool direct = P == 1 && c.H % Pl::BK == 0 && c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 &&
                         c.ldw < (1L << 22);
     int part = 0;
     for (int v0 = 0; v0 < c.V; v0 += l.piece) {
         const int vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
-        Operand w{(const char*)(W + (size_t)v0 * c.ldw), (uint32_t)(c.ldw * 2), vn};
+        Operand w{(const char*)(W + (size_t)v0 * c.ldw), (uint32_t)(c.ldw * 2), (uint32_t)(c.H * 2), vn};
         if (!direct) {
             vocab_pack_kernel<T, P><<<(unsigned)up(vn, 256), 256, 0, st>>>(W + (size_t)v0 * c.ldw, c.ldw, nullptr,
-                                                                         nullptr, vn, c.H, ws + l.w, x_pitch, l.hk);
-            w = Operand{ws + l.w, (uint32_t)x_pitch, (int)up(vn, 256)};
+                                                                         nullptr, vn, c.H, ws + l.w, x_pitch, l.hk,
+                                                                         nullptr, nullptr);
+            w = Operand{ws + l.w, (uint32_t)x_pitch, (uint32_t)x_pitch, (int)up(vn, 256)};
         }
         if (!c.grad) {
             by_size<Small, Big>(vn, c.T, [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(vn, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-                const LseArgs a{w, xs, count, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part, l.tp};
+                const LseArgs a{w, x, count, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part, l.tp};
                 vocab_lse_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
                 part += tm * S::WAVES_M;
             });
             continue;
         }
-        char *d = c.dX ? ws + l.d : nullptr, *dt = c.dW ? ws + l.dt : nullptr;
         if (c.T > 0) by_size<Small, Big>(vn, c.T, [&](auto* shape) {
             using S = typename std::remove_pointer<decltype(shape)>::type;
             // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
             const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-            const GradArgs a{w, xs, count, tm, tn, slabs, vn, c.alpha, (const float*)(ws + l.lse_c),
-                             (const float*)(ws + l.scale), d, wt_pitch, dt, t_pitch};
+            const GradArgs a{w, x, count, tm, tn, slabs, vn, c.alpha, (const float*)(ws + l.lse_c),
+                             (const float*)(ws + l.scale), ws + l.d, d_pitch};
             vocab_grad_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
         });
         if (c.T > 0) vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-            c.e, c.T, v0, vn, pos, (const float*)(ws + l.value), d, wt_pitch, dt, t_pitch);
+            c.e, c.T, v0, vn, pos, (const float*)(ws + l.value), ws + l.d, d_pitch);
         if (c.T > 0 && c.dX) {
-            vocab_transpose_kernel<T, P><<<dim3(l.hp / 64, (unsigned)(up(vn, 64) / 64)), 256, 0, st>>>(
-                W + (size_t)v0 * c.ldw, c.ldw, nullptr, nullptr, vn, c.H, nullptr, ws + l.wt, wt_pitch);
             by_size<Small, Big>(c.H, c.T, [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-                const DxArgs a{{ws + l.wt, (uint32_t)wt_pitch, l.hp}, {ws + l.d, (uint32_t)wt_pitch, l.tp}, count, tm,
-                               tn, (int)up(vn, Pl::BK) / Pl::BK, l.splits, (float*)(ws + l.acc), l.tp, l.hp, v0 > 0};
+                const DxArgs a{w, d, count, tm, tn, (int)up(vn, Pl::BK) / Pl::BK, l.splits, (float*)(ws + l.acc), l.tp, l.hp, v0 > 0};
                 vocab_dx_kernel<S><<<dim3(tm * tn, l.splits), S::NT, 0, st>>>(a);
             });
         }
@@ -216,8 +212,7 @@ int run(const Call& c) {
                 const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(vn, S::kBN) / S::kBN;
                 T* out = (T*)c.dW + (size_t)v0 * c.lddw;
                 const int vec = c.H % 4 == 0 && c.lddw % 4 == 0 && (uintptr_t)c.dW % (4 * sizeof(T)) == 0;
-                const DwArgs a{{ws + l.xt, (uint32_t)t_pitch, l.hp}, {ws + l.dt, (uint32_t)t_pitch, l.piece}, count,
-                               tm, tn, c.H, vn, out, c.lddw, vec};
+                const DwArgs a{x_dw, d, count, tm, tn, c.H, vn, out, c.lddw, vec};
                 vocab_dw_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
         }

@@ -213,19 +213,24 @@ struct Side {
     }
 };
 
-// The tile loop.  The operands' slabs go straight from global memory into a ring of ST LDS stages.
-// A slab's first fragments are read, and the stage of the slab before it is requested anew, behind
-// the barrier that comes before the last k-step of that slab: the matrix unit has that k-step to do
-// while the reads are on their way.
-template <int P, int BM, int BN, int WM, int WN, int ST>
+// The tile loop.  The operands' slabs go straight from global memory into rings of SA and SB LDS
+// stages.  A slab's first fragments are read, and the stages of the slab before it are requested
+// anew, behind the barrier that comes before the last k-step of that slab: the matrix unit has that
+// k-step to do while the reads are on their way.  The requests stand one by one between MFMAs: a
+// wave issues in order, and one that queues them all at once is held until the memory pipe has taken
+// them, its MFMAs behind them.  With SA = SB + 1 A's requests have a slab longer to arrive, and are
+// spread over the first k-steps of the next slab.
+template <int P, int BM, int BN, int WM, int WN, int SA, int SB>
 struct Tile {
     static constexpr int kP = P, kBM = BM, kBN = BN, kWM = WM, kWN = WN;
     static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
     static constexpr int MB = WM / 32, NB = WN / 32;
     static constexpr int BK = Planes<P>::BK, KK = BK / 16;
-    static constexpr int STAGE = (BM + BN) * BK * 2 * P;
-    static constexpr int LDS_BYTES = STAGE * ST;
+    static constexpr int BYTES_A = BM * BK * 2 * P, BYTES_B = BN * BK * 2 * P;
+    static constexpr int LDS_BYTES = BYTES_A * SA + BYTES_B * SB;
+    static constexpr int MFMAS = MB * NB * (P == 3 ? 6 : 1);  // per k-step
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+    static_assert(SB >= 2 && (SA == SB || SA == SB + 1), "stages");
 
     f32x16 acc[MB][NB];
 
@@ -234,8 +239,8 @@ struct Tile {
     __device__ inline void run(char* lds, const Operand& a, int m0, const Operand& b, int n0, int k0, int slabs) {
         using A = Side<P, OA, BM, WM, NT>;
         using B = Side<P, OB, BN, WN, NT>;
-        constexpr int LA = A::L, LB = B::L, LL = LA + LB;
-        static_assert(LL * (ST - 1) < 64, "vmcnt counts at most 63 loads in flight");
+        constexpr int LA = A::L, LB = B::L;
+        static_assert((LA + LB) * SB < 64, "vmcnt counts at most 63 loads in flight");
         const int lane = threadIdx.x & 63;
         const int wave = (int)uniform_u32(threadIdx.x >> 6);
 #pragma unroll
@@ -249,23 +254,12 @@ struct Tile {
         B sb;
         sa.init(a, m0, k0, wave, lane, wave / WAVES_N);
         sb.init(b, n0, k0, wave, lane, wave % WAVES_N);
-        const uint32_t base = lds_addr((const float*)lds) + wave * 1024;
-        // part q of KK of a slab's requests
-        auto issue = [&](int stage, int q) {
-            const uint32_t at = base + stage * STAGE;
-            sa.issue(at, LA * q / KK, LA * (q + 1) / KK);
-            sb.issue(at + A::BYTES, LB * q / KK, LB * (q + 1) / KK);
-            if (q == KK - 1) {
-                sa.next(a, m0, wave, lane);
-                sb.next(b, n0, wave, lane);
-            }
-        };
+        char* const lds_b = lds + SA * BYTES_A;
+        const uint32_t base_a = lds_addr((const float*)lds) + wave * 1024, base_b = base_a + SA * BYTES_A;
         bf16x8 va[2][P][MB], vb[2][P][NB];
-        auto read = [&](int stage, int kk) {
-            sa.read(lds + stage * STAGE, kk, va[kk & 1]);
-            sb.read(lds + stage * STAGE + A::BYTES, kk, vb[kk & 1]);
-        };
-        auto multiply = [&](int kk) {
+        // the MFMAs of k-step kk, `loads` calls of issue(0 ..) spread between them if there is `more`
+        auto multiply = [&](int kk, bool more, int loads, auto issue) {
+            int x = 0, q = 0;
 #pragma unroll
             for (int w = P - 1; w >= 0; --w)  // planes of total weight w, the smallest terms first
 #pragma unroll
@@ -273,39 +267,78 @@ struct Tile {
 #pragma unroll
                     for (int i = 0; i < MB; ++i)
 #pragma unroll
-                        for (int j = 0; j < NB; ++j)
+                        for (int j = 0; j < NB; ++j) {
                             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[kk & 1][p][i], vb[kk & 1][w - p][j],
                                                                                acc[i][j], 0, 0, 0);
+                            ++x;
+                            if (loads > 0) {
+                                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                                for (; q < loads && q * MFMAS < x * loads; ++q)
+                                    if (more) issue(q);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                        }
         };
+        constexpr int SMAX = SA > SB ? SA : SB;
 #pragma unroll
-        for (int s = 0; s < ST; ++s)
-            if (s < slabs)
-#pragma unroll
-                for (int q = 0; q < KK; ++q) issue(s, q);
-        wait_slabs<LL>(imin(ST, slabs) - 1);
-        dl_barrier();
-        read(0, 0);
-        int stage = 0;
-        for (int s = 0; s < slabs; ++s) {
-            const int next = stage + 1 == ST ? 0 : stage + 1;
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                if (kk + 1 < KK) {
-                    read(stage, kk + 1);
-                } else if (s + 1 < slabs) {
-                    // this wave's reads of the slab are done; slab s + 1 has landed; later ones are in flight
-                    wait_slabs<LL>(imin(ST - 2, slabs - 2 - s));
-                    dl_barrier();
-                    read(next, 0);
-                    if (s + ST < slabs)
-#pragma unroll
-                        for (int q = 0; q < KK; ++q) issue(stage, q);
-                }
-                multiply(kk);
+        for (int s = 0; s < SMAX; ++s) {
+            if (s >= slabs) continue;
+            if (s < SA) {
+                sa.issue(base_a + s * BYTES_A, 0, LA);
+                sa.next(a, m0, wave, lane);
             }
-            stage = next;
+            if (s < SB) {
+                sb.issue(base_b + s * BYTES_B, 0, LB);
+                sb.next(b, n0, wave, lane);
+            }
         }
-        // all waves are done with the stages: a user of run may reuse lds after a barrier
+        if (slabs >= SMAX)
+            wait_vm_lgkm0<LA*(SA - 1) + LB*(SB - 1)>();
+        else
+            wait_vm_lgkm0<0>();
+        dl_barrier();
+        sa.read(lds, 0, va[0]);
+        sb.read(lds_b, 0, vb[0]);
+        int ta = 0, tb = 0;  // stages of slab s
+        for (int s = 0; s < slabs; ++s) {
+            const int ta1 = ta + 1 == SA ? 0 : ta + 1, tb1 = tb + 1 == SB ? 0 : tb + 1;
+            // SA > SB: the stage of slab s - 1 takes slab s - 1 + SA
+            const bool early = SA > SB && s > 0 && s - 1 + SA < slabs;
+            const uint32_t at_early = base_a + (ta == 0 ? SA - 1 : ta - 1) * BYTES_A;
+#pragma unroll
+            for (int kk = 0; kk < KK - 1; ++kk) {
+                sa.read(lds + ta * BYTES_A, kk + 1, va[(kk + 1) & 1]);
+                sb.read(lds_b + tb * BYTES_B, kk + 1, vb[(kk + 1) & 1]);
+                const int from = LA * kk / (KK - 1), to = LA * (kk + 1) / (KK - 1);
+                multiply(kk, early, SA > SB ? to - from : 0,
+                         [&](int q) { sa.issue(at_early, from + q, from + q + 1); });
+            }
+            if (early) sa.next(a, m0, wave, lane);
+            if (s + 1 < slabs) {
+                // this wave's reads of slab s are done, its parts of slab s + 1 have landed
+                if (s + SMAX <= slabs)
+                    wait_vm_lgkm0<LA*(SA - 2) + LB*(SB - 2)>();
+                else
+                    wait_vm_lgkm0<0>();
+                dl_barrier();
+                sa.read(lds + ta1 * BYTES_A, 0, va[0]);
+                sb.read(lds_b + tb1 * BYTES_B, 0, vb[0]);
+            }
+            const uint32_t at_a = base_a + ta * BYTES_A, at_b = base_b + tb * BYTES_B;
+            multiply(KK - 1, s + SB < slabs, (SA == SB ? LA : 0) + LB, [&](int q) {
+                if (q < LB)
+                    sb.issue(at_b, q, q + 1);
+                else
+                    sa.issue(at_a, q - LB, q - LB + 1);
+            });
+            if (s + SB < slabs) {
+                sb.next(b, n0, wave, lane);
+                if (SA == SB) sa.next(a, m0, wave, lane);
+            }
+            ta = ta1;
+            tb = tb1;
+        }
     }
 
     // Element e of block (i, j) of this lane is C(m0 + row(i, e), n0 + col(j)).

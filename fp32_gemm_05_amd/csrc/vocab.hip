@@ -54,10 +54,10 @@ struct Layout {
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
 // Tile shapes.  The large one when it fills the chip, else the small one.
-using Big1 = Tile<1, 256, 256, 128, 64, 2>;
-using Small1 = Tile<1, 128, 64, 64, 32, 3>;
-using Big3 = Tile<3, 256, 128, 64, 64, 2>;
-using Small3 = Tile<3, 128, 64, 64, 32, 2>;
+using Big1 = Tile<1, 256, 256, 128, 64, 3, 2>;
+using Small1 = Tile<1, 128, 64, 64, 32, 3, 3>;
+using Big3 = Tile<3, 256, 128, 64, 64, 2, 2>;
+using Small3 = Tile<3, 128, 64, 64, 32, 2, 2>;
 
 template <class B>
 bool fills(long rows_m, long rows_n) {

@@ -1,8 +1,8 @@
-// kernel_vocab.hpp -- the matrix products of the vocabulary-head operators (gfx950, bf16 MFMA).
+// kernel_vocab.hpp -- the matrix products of the vocabulary-head operators (gfx950, 16-bit MFMA).
 //
 // One tile loop serves every product: C(m, n) = sum_k A(m, k) * B(n, k), each operand stored with k
 // along its rows or down its columns (then read from LDS with transposing loads), multiplied with
-// v_mfma_f32_32x32x16_bf16 and accumulated in fp32.  No matrix is transposed in memory.  What
+// v_mfma_f32_32x32x16 (bf16 or fp16) and accumulated in fp32.  No matrix is transposed in memory.  What
 // differs is what the finished tile is used for:
 //
 //   vocab_lse_kernel    z = alpha * W X^T, reduced over the tile's vocabulary rows to the maximum
@@ -15,11 +15,13 @@
 // vocabulary entries per 32x32 block: the reduction over the vocabulary is in registers, one
 // exchange between the lane halves at its end.
 //
-// P is the number of bf16 planes an operand is held in.  P = 1: bf16 operands, as they are.
-// P = 3: fp32 operands as the exact sum of three bf16 values (8 + 8 + 8 significand bits), a row
-// stored in blocks of 32 k as [32 high][32 middle][32 low].  The six products of weight above
-// 2^-24 are accumulated (hh, hm, mh, mm, hl, lh; the dropped ml, lm, ll are below one rounding of
-// the fp32 product): six bf16 MFMAs do the work of an fp32 product at 16/6 of the fp32 MFMA rate.
+// P is the number of 16-bit planes an operand is held in.  P = 1: bf16 operands, as they are.
+// P = 2: fp32 operands as the sum of two fp16 values, a row stored in blocks of 32 k as [32 high]
+// [32 low].  The operand is scaled by a power of two first, so that its largest value lies in
+// [2^14, 2^15); high + low then holds every value down to 2^-16 of the largest to one fp32 rounding
+// (2^-24 of itself) and smaller ones to 2^-40 of the largest.  Three products (hl, lh, hh) are
+// accumulated in fp32; the one left out, ll, is below 2^-24 of the whole.  Three fp16 MFMAs do the
+// work of an fp32 product at 16/3 of the fp32 MFMA rate, from operands of the same size.
 #pragma once
 
 #include "kernel_common.hpp"
@@ -28,71 +30,75 @@
 namespace libsgemm {
 namespace vocab {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int P>
 struct Planes {
-    static_assert(P == 1 || P == 3, "bf16 or three-plane fp32 operands");
-    static constexpr int BK = P == 1 ? 64 : 32;     // k per slab
-    static constexpr int QR = P == 1 ? 8 : 12;      // 16-byte quads per row and slab
-    static constexpr int ROW = QR * 16;             // bytes per row and slab
+    static_assert(P == 1 || P == 2, "bf16, or fp32 as two fp16 planes");
+    typedef typename std::conditional<P == 1, __bf16, _Float16>::type Half;
+    typedef Half Half8 __attribute__((ext_vector_type(8)));
+    typedef Half Half4 __attribute__((ext_vector_type(4)));
+    static constexpr int BK = 64 / P;    // k per slab
+    static constexpr int QR = 8;         // 16-byte quads per row and slab
+    static constexpr int ROW = QR * 16;  // bytes per row and slab
     // LDS quad u of row r holds the row's quad swz(r, u), an involution.  A 128-bit read is served
     // in passes of 16 lanes of one half-wave (lanes 0-3, 12-15, 20-23, 24-27 or the others) over 64
-    // banks; with 128-byte rows a pass must find 8 different quads among its even and its odd rows,
-    // with 192-byte rows 4 different ones among its rows of each residue modulo 4.
-    __host__ __device__ static constexpr int swz(int r, int u) {
-        return P == 1 ? (u ^ ((r >> 1) & 7)) : ((u & ~3) | ((u ^ (r >> 2)) & 3));
-    }
+    // banks, two rows: a pass must find 8 different quads among its even and among its odd rows.
+    __host__ __device__ static constexpr int swz(int r, int u) { return u ^ ((r >> 1) & 7); }
     // Byte offset of plane p of element k within a row.
     __host__ __device__ static constexpr long at(long k, int p) {
-        return P == 1 ? 2 * k : (k >> 5) * 192 + p * 64 + (k & 31) * 2;
+        return P == 1 ? 2 * k : (k >> 5) * 128 + p * 64 + (k & 31) * 2;
     }
     // Bytes of a row of kp elements (kp a multiple of BK).
     __host__ __device__ static constexpr long pitch(long kp) { return 2L * P * kp; }
 };
 
-// x as P bf16 values.  P = 3 is exact (each remainder fits the next value) but where the low parts
-// fall below bf16's subnormals; a value that would round to infinity is cut off instead.
+// x as P values; infinities and NaN have no low part.
 template <int P>
-__device__ inline void split(float x, __bf16 (&v)[P]) {
-    __bf16 h = (__bf16)x;
-    if (P == 3) {
-        float hf = (float)h;
-        if (__builtin_isinf(hf) && !__builtin_isinf(x)) {
-            hf = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-            h = (__bf16)hf;
-        }
-        const float r = __builtin_isfinite(x) ? x - hf : 0.f;
-        const __bf16 m = (__bf16)r;
-        v[P > 1 ? 1 : 0] = m;
-        v[P > 2 ? 2 : 0] = (__bf16)(r - (float)m);
-    }
-    v[0] = h;
+__device__ inline void split(float x, typename Planes<P>::Half (&v)[P]) {
+    typedef typename Planes<P>::Half Half;
+    v[0] = (Half)x;
+    if constexpr (P == 2) v[1] = __builtin_isfinite(x) ? (Half)(x - (float)v[0]) : (Half)0.f;
 }
 template <int P>
 __device__ inline void store1(char* row, long k, float x) {
-    __bf16 v[P];
+    typename Planes<P>::Half v[P];
     split<P>(x, v);
 #pragma unroll
-    for (int p = 0; p < P; ++p) *(__bf16*)(row + Planes<P>::at(k, p)) = v[p];
+    for (int p = 0; p < P; ++p) *(typename Planes<P>::Half*)(row + Planes<P>::at(k, p)) = v[p];
 }
 // Four consecutive k, the first a multiple of 4.
 template <int P>
 __device__ inline void store4(char* row, long k, const float (&x)[4]) {
-    bf16x4 o[P];
+    typename Planes<P>::Half4 o[P];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        __bf16 v[P];
+        typename Planes<P>::Half v[P];
         split<P>(x[j], v);
 #pragma unroll
         for (int p = 0; p < P; ++p) o[p][j] = v[p];
     }
 #pragma unroll
-    for (int p = 0; p < P; ++p) *(bf16x4*)(row + Planes<P>::at(k, p)) = o[p];
+    for (int p = 0; p < P; ++p) *(typename Planes<P>::Half4*)(row + Planes<P>::at(k, p)) = o[p];
 }
+template <int P>
+__device__ inline f32x16 mfma(typename Planes<P>::Half8 a, typename Planes<P>::Half8 b, f32x16 c) {
+    if constexpr (P == 1)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// The scale of P = 2 operands: the power of two that brings a largest value m into [2^14, 2^15).
+// m of 0 (or nothing finite) gives 1; an m so small or large that the power would leave fp32's
+// range gives the nearest that does not.
+__device__ inline int scale_exponent(float m) {
+    if (!(m > 0.f)) return 0;
+    const int e = 14 - ilogbf(m);
+    return e > 126 ? 126 : e < -126 ? -126 : e;
+}
+constexpr float kDScale = 0x1p15f;  // of D, whose entries are at most 1 in magnitude
 
 // A product operand, stored with k along its rows (K_ROW: A[m][k]) or down its columns (K_COL:
 // A[k][m]); rows past `rows` read as its last row, quads past row_bytes as its last quad.  Neither
@@ -134,7 +140,7 @@ struct Side {
     size_t step;          // bytes from slab to slab
     uint32_t off[L];
     int left;             // K_COL: rows from `at` to the operand's end
-    uint32_t lane_at[O == K_ROW ? KK : (B > 1 ? B : 1) * P];  // LDS offsets of this lane's fragments
+    uint32_t lane_at[O == K_ROW ? KK * P : B * P];  // LDS offsets of this lane's fragments
     int frag;             // wave's part of them
 
     __device__ inline void init(const Operand& o, int row0, int k0, int wave, int lane, int wave_at) {
@@ -150,10 +156,10 @@ struct Side {
         set_offsets(o, row0, wave, lane);
         const int l = lane & 31, h = lane >> 5;
         if (O == K_ROW) {
-            // row l of a block, quad 2 * kk + h of plane 0
+            // row l of a block, quad 2 * kk + h of plane p
             frag = wave_at * W * ROW;
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) lane_at[kk] = l * ROW + Planes<P>::swz(l, 2 * kk + h) * 16;
+            for (int q = 0; q < KK * P; ++q) lane_at[q] = l * ROW + Planes<P>::swz(l, 2 * q + h) * 16;
         } else {
             // lane i of a group of 16 points at k = i / 4, m = 4 * (i % 4) and gets k = 0 .. 3 of m = i
             const int i = lane & 15, r = 8 * h + (i >> 2), f = flip(i >> 2);
@@ -196,18 +202,19 @@ struct Side {
         }
     }
     // The fragments of k-step kk: of a lane, 8 consecutive k of its row in each block and plane.
-    __device__ inline void read(const char* slab, int kk, bf16x8 (&v)[P][B]) const {
+    __device__ inline void read(const char* slab, int kk, typename Planes<P>::Half8 (&v)[P][B]) const {
+        typedef typename Planes<P>::Half8 Half8;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 if (O == K_ROW) {
-                    v[p][b] = *(const bf16x8*)(slab + frag + b * 32 * ROW + p * 64 + lane_at[kk]);
+                    v[p][b] = *(const Half8*)(slab + frag + b * 32 * ROW + lane_at[p * KK + kk]);
                 } else {
                     const char* a = slab + lane_at[b * P + p] + kk * 16 * ROW;
                     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
                     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ROW));
-                    v[p][b] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                    v[p][b] = __builtin_bit_cast(Half8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
                 }
             }
     }
@@ -228,7 +235,7 @@ struct Tile {
     static constexpr int BK = Planes<P>::BK, KK = BK / 16;
     static constexpr int BYTES_A = BM * BK * 2 * P, BYTES_B = BN * BK * 2 * P;
     static constexpr int LDS_BYTES = BYTES_A * SA + BYTES_B * SB;
-    static constexpr int MFMAS = MB * NB * (P == 3 ? 6 : 1);  // per k-step
+    static constexpr int MFMAS = MB * NB * (P == 2 ? 3 : 1);  // per k-step
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
     static_assert(SB >= 2 && (SA == SB || SA == SB + 1), "stages");
 
@@ -256,7 +263,7 @@ struct Tile {
         sb.init(b, n0, k0, wave, lane, wave % WAVES_N);
         char* const lds_b = lds + SA * BYTES_A;
         const uint32_t base_a = lds_addr((const float*)lds) + wave * 1024, base_b = base_a + SA * BYTES_A;
-        bf16x8 va[2][P][MB], vb[2][P][NB];
+        typename Planes<P>::Half8 va[2][P][MB], vb[2][P][NB];
         // the MFMAs of k-step kk, `loads` calls of issue(0 ..) spread between them if there is `more`
         auto multiply = [&](int kk, bool more, int loads, auto issue) {
             int x = 0, q = 0;
@@ -268,8 +275,7 @@ struct Tile {
                     for (int i = 0; i < MB; ++i)
 #pragma unroll
                         for (int j = 0; j < NB; ++j) {
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[kk & 1][p][i], vb[kk & 1][w - p][j],
-                                                                               acc[i][j], 0, 0, 0);
+                            acc[i][j] = mfma<P>(va[kk & 1][p][i], vb[kk & 1][w - p][j], acc[i][j]);
                             ++x;
                             if (loads > 0) {
                                 __builtin_amdgcn_sched_barrier(0);
@@ -353,11 +359,13 @@ struct Tile {
 };
 
 struct LseArgs {
-    Operand w, x;     // vocabulary rows of this piece, counted tokens
-    const int* count; // number of counted tokens
+    Operand w, x;          // vocabulary rows of this piece, counted tokens
+    const int* count;      // number of counted tokens
+    const float* w_unit;   // P = 2: what a packed unit of W, and of each token's row of X, stands for
+    const float* x_unit;
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;
-    float2* part;     // [vocabulary pieces of WM rows][tp]: maximum and sum of exp(z - maximum)
+    float2* part;          // [vocabulary pieces of WM rows][tp]: maximum and sum of exp(z - maximum)
     int part0, tp;
 };
 
@@ -367,19 +375,23 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
     int tm, tn;
     tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
     const int m0 = tm * T::kBM, n0 = tn * T::kBN;
-    if (n0 >= *a.count) return;
+    const int count = *a.count;
+    if (n0 >= count) return;
     T t;
     t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
     const int h = (threadIdx.x & 63) >> 5;
     const int piece = a.part0 + tm * T::WAVES_M + (threadIdx.x >> 6) / T::WAVES_N;
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
+        const int n = n0 + t.col(j);
+        float alpha = a.alpha;
+        if (T::kP == 2) alpha *= *a.w_unit * (n < count ? a.x_unit[n] : 0.f);
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                const float z = m0 + t.row(i, e) < a.vocab ? t.acc[i][j][e] * a.alpha : -INFINITY;
+                const float z = m0 + t.row(i, e) < a.vocab ? t.acc[i][j][e] * alpha : -INFINITY;
                 t.acc[i][j][e] = z;
                 top = z > top || z != z ? z : top;  // a NaN stays
             }
@@ -392,23 +404,34 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) sum += __expf(t.acc[i][j][e] - ref);
         sum += __shfl_xor(sum, 32);
-        if (h == 0) a.part[(size_t)piece * a.tp + n0 + t.col(j)] = make_float2(top, sum);
+        if (h == 0) a.part[(size_t)piece * a.tp + n] = make_float2(top, sum);
     }
 }
 
 struct GradArgs {
     Operand w, x;
     const int* count;
+    const float *w_unit, *x_unit;  // P = 2, as in LseArgs
+    const float* x_most;           // P = 2: the largest |weight * x_unit| of a counted token
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;
-    const float* lse;    // per counted token
-    const float* scale;  // per counted token: D = exp(z - lse) * scale
-    char* d;             // [token][vocabulary piece], planes
+    const float* lse;      // per counted token
+    const float* scale;    // per counted token: D = exp(z - lse) * scale
+    const float* weight;   // P = 2, per counted token: D's rows in dX and dW
+    char* d;               // [token][vocabulary piece], planes
     long d_pitch;
 };
 
+// P = 2: what D's row of a token is stored in: its weight relative to the largest one, which makes
+// dW's sum over tokens uniform, times kDScale.
+__device__ inline float d_factor(float weight, float x_unit, float x_most) {
+    return x_most > 0.f ? weight * x_unit / x_most * kDScale : 0.f;
+}
+
 template <class T>
 __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
+    typedef typename Planes<T::kP>::Half Half;
+    typedef typename Planes<T::kP>::Half4 Half4;
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     int tm, tn;
     tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
@@ -421,13 +444,19 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
         const bool live = n < count;
-        const float lse = live ? a.lse[n] : 0.f, scale = live ? a.scale[n] : 0.f;
+        const float lse = live ? a.lse[n] : 0.f;
+        float scale = live ? a.scale[n] : 0.f, alpha = a.alpha;
+        if (T::kP == 2 && live) {
+            const float unit = a.x_unit[n];
+            alpha *= *a.w_unit * unit;
+            scale *= d_factor(a.weight[n], unit, *a.x_most);
+        }
         char* out = a.d + (size_t)n * a.d_pitch;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
             for (int g = 0; g < 4; g += 2) {
-                bf16x4 v[2][T::kP];
+                Half4 v[2][T::kP];
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -436,8 +465,8 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
                         // entries past the vocabulary and tokens past the count are the zeros that the
                         // products of D run over
                         const float x = live && m0 + t.row(i, e) < a.vocab
-                                            ? __expf(t.acc[i][j][e] * a.alpha - lse) * scale : 0.f;
-                        __bf16 x_p[T::kP];
+                                            ? __expf(t.acc[i][j][e] * alpha - lse) * scale : 0.f;
+                        Half x_p[T::kP];
                         split<T::kP>(x, x_p);
 #pragma unroll
                         for (int p = 0; p < T::kP; ++p) v[f][p][q] = x_p[p];
@@ -456,12 +485,25 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     }
 }
 
+// How dX's product is cut: its tiles are few when tokens or hidden are, so the vocabulary is split
+// until `groups` workgroups have work.  The same for every piece of a call and for vocab_dx_out.
+struct DxCut {
+    int tiles_m, bn, groups, most;
+    __device__ int splits(int count) const {
+        const int tiles = tiles_m * ((count + bn - 1) / bn);
+        const int s = tiles > 0 ? groups / tiles : 1;
+        return s < 1 ? 1 : s > most ? most : s;
+    }
+    __device__ size_t rows(int count) const { return (size_t)((count + bn - 1) / bn) * bn; }
+};
+
 struct DxArgs {
     Operand w, d;      // [vocabulary piece][hidden], [token][vocabulary piece]
     const int* count;
-    int tiles_m, tiles_n, slabs, splits;
-    float* acc;        // [splits][tp][hp]
-    long tp;
+    const float* w_unit;
+    DxCut cut;
+    int slabs;
+    float* acc;        // [splits][rows][hp]
     int hp;
     int add;           // not the first piece
 };
@@ -469,26 +511,31 @@ struct DxArgs {
 template <class T>
 __global__ void __launch_bounds__(T::NT) vocab_dx_kernel(DxArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
-    int tm, tn;
-    tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
-    const int m0 = tm * T::kBM, n0 = tn * T::kBN;
     const int count = *a.count;
-    if (n0 >= count) return;
-    const int z = blockIdx.y;
-    const int first = (int)((long)a.slabs * z / a.splits), last = (int)((long)a.slabs * (z + 1) / a.splits);
+    const int splits = a.cut.splits(count), tiles_n = (count + T::kBN - 1) / T::kBN;
+    const int tiles = a.cut.tiles_m * tiles_n;
+    if ((int)blockIdx.x >= tiles * splits) return;
+    const int z = blockIdx.x / tiles;
+    int tm, tn;
+    tile_of(blockIdx.x - z * tiles, tiles, a.cut.tiles_m, tiles_n, 4, tm, tn);
+    const int m0 = tm * T::kBM, n0 = tn * T::kBN;
+    const int first = (int)((long)a.slabs * z / splits), last = (int)((long)a.slabs * (z + 1) / splits);
     T t;
     t.template run<K_COL, K_ROW>(lds, a.w, m0, a.d, n0, first, last - first);
+    const float unit = T::kP == 2 ? *a.w_unit : 1.f;
+    const size_t rows = a.cut.rows(count);
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
         if (n >= count) continue;
-        float* out = a.acc + ((size_t)z * a.tp + n) * a.hp + m0;
+        float* out = a.acc + (z * rows + n) * a.hp + m0;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 f32x4* p = (f32x4*)(out + t.row(i, 4 * g));
                 f32x4 v = {t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1], t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
+                if (T::kP == 2) v *= unit;
                 if (a.add) v += *p;
                 *p = v;
             }
@@ -496,8 +543,9 @@ __global__ void __launch_bounds__(T::NT) vocab_dx_kernel(DxArgs a) {
 }
 
 struct DwArgs {
-    Operand x, d;      // [token][hidden], scaled; [token][vocabulary piece]
+    Operand x, d;      // [token][hidden]; [token][vocabulary piece]
     const int* count;
+    const float* x_most;
     int tiles_m, tiles_n, hidden, vocab;
     void* out;         // [vocabulary piece][hidden] in the operands' type
     long ld;
@@ -514,6 +562,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
     const int m0 = tm * T::kBM, n0 = tn * T::kBN;
     T t;
     t.template run<K_COL, K_COL>(lds, a.x, m0, a.d, n0, 0, (*a.count + T::BK - 1) / T::BK);
+    const float unit = T::kP == 2 ? *a.x_most / kDScale : 1.f;
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
@@ -524,15 +573,15 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int m = m0 + t.row(i, 4 * g);
-                if (a.vec) {
-                    O4 v;
+                O4 v;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = (O)t.acc[i][j][4 * g + q];
+                for (int q = 0; q < 4; ++q) v[q] = (O)(t.acc[i][j][4 * g + q] * unit);
+                if (a.vec) {
                     if (m < a.hidden) *(O4*)(out + m) = v;
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (m + q < a.hidden) out[m + q] = (O)t.acc[i][j][4 * g + q];
+                        if (m + q < a.hidden) out[m + q] = v[q];
                 }
             }
     }

@@ -25,46 +25,81 @@ struct Entries {
 };
 
 // rows[0 .. *count): the tokens that count, in order; pos: a token's place in rows, or -1.  One
-// workgroup walks the tokens.  loss and lse (when given) of the others are 0.
+// workgroup walks the tokens, 8192 at a time so that their entries are read together.  loss and lse
+// (when given) of the others are 0.  Clears `zero` as well, the maxima that later kernels raise.
 __global__ void __launch_bounds__(1024) vocab_count_kernel(Entries e, int tokens, int* rows, int* pos, int* count,
-                                                           float* loss, float* lse) {
-    __shared__ int waves[16];
+                                                           float* loss, float* lse, uint32_t* zero, int zeros) {
+    constexpr int R = 8;
+    __shared__ int waves[R][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int i = threadIdx.x; i < zeros; i += 1024) zero[i] = 0;
     int done = 0;
-    for (int t0 = 0; t0 < tokens; t0 += 1024) {
-        const int t = t0 + threadIdx.x;
-        bool live = false;
-        if (t < tokens)
-            for (int k = 0; k < e.k && !live; ++k) live = e.counts(e.index[(size_t)t * e.ld + k]);
-        const unsigned long long m = __ballot(live);
-        if (lane == 0) waves[wave] = __popcll(m);
+    for (int t0 = 0; t0 < tokens; t0 += 1024 * R) {
+        bool live[R];
+        unsigned long long m[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = t0 + r * 1024 + threadIdx.x;
+            live[r] = t < tokens && e.counts(e.index[(size_t)t * e.ld]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = t0 + r * 1024 + threadIdx.x;
+            if (t < tokens)
+                for (int k = 1; k < e.k && !live[r]; ++k) live[r] = e.counts(e.index[(size_t)t * e.ld + k]);
+            m[r] = __ballot(live[r]);
+            if (lane == 0) waves[r][wave] = __popcll(m[r]);
+        }
         __syncthreads();
-        int before = done, all = 0;
-        for (int w = 0; w < 16; ++w) {
-            before += w < wave ? waves[w] : 0;
-            all += waves[w];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            int before = done;
+            for (int w = 0; w < 16; ++w) {
+                before += w < wave ? waves[r][w] : 0;
+                done += waves[r][w];
+            }
+            const int t = t0 + r * 1024 + threadIdx.x;
+            if (t >= tokens) continue;
+            const int at = before + __popcll(m[r] & ((1ull << lane) - 1));
+            pos[t] = live[r] ? at : -1;
+            if (live[r]) rows[at] = t;
+            if (!live[r] && loss) loss[t] = 0.f;
+            if (!live[r] && lse) lse[t] = 0.f;
         }
-        if (t < tokens) {
-            const int at = before + __popcll(m & ((1ull << lane) - 1));
-            pos[t] = live ? at : -1;
-            if (live) rows[at] = t;
-            if (!live && loss) loss[t] = 0.f;
-            if (!live && lse) lse[t] = 0.f;
-        }
-        done += all;
         __syncthreads();
     }
     if (threadIdx.x == 0) *count = done;
 }
 
+// N consecutive values, at any alignment of their type (gfx950 loads unaligned vectors).
+template <int N, typename T>
+__device__ inline void load(const T* p, float (&v)[N]) {
+    T t[N];
+    __builtin_memcpy(t, p, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = (float)t[i];
+}
 template <typename T>
 __device__ inline float wave_dot(const T* x, const T* w, int n) {
+    constexpr int N = 16 / sizeof(T);
     const int lane = threadIdx.x & 63;
-    float s = 0.f;
-    for (int i = lane; i < n; i += 64) s = __builtin_fmaf((float)x[i], (float)w[i], s);
+    float s[N] = {};
+    int i = lane * N;
+#pragma unroll 4
+    for (; i + N <= n; i += 64 * N) {
+        float a[N], b[N];
+        load(x + i, a);
+        load(w + i, b);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    return s;
+        for (int q = 0; q < N; ++q) s[q] = __builtin_fmaf(a[q], b[q], s[q]);
+    }
+    for (; i < n; ++i) s[0] = __builtin_fmaf((float)x[i], (float)w[i], s[0]);  // the lane with the row's end
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < N; ++q) t += s[q];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) t += __shfl_xor(t, o);
+    return t;
 }
 __device__ inline float wave_sum(float s) {
 #pragma unroll
@@ -77,26 +112,117 @@ __device__ inline float wave_max(float s) {
     return s;
 }
 
-// Rows (through `map` when given) of a rows x cols matrix, packed: row i at dst + i * pitch, zero
-// past cols up to kp, whole zero rows from the number of rows to its next multiple of 256.  scaled
-// (when given) gets the rows times scale[i].
-template <typename T, int P>
-__global__ void __launch_bounds__(256) vocab_pack_kernel(const T* src, long ld, const int* map, const int* count,
-                                                         int rows, int cols, char* dst, long pitch, int kp,
-                                                         const float* scale, char* scaled) {
-    const int i = blockIdx.x, n = count ? *count : rows;
-    if (i >= (n + 255) / 256 * 256) return;
-    const T* s = i < n ? src + (size_t)(map ? map[i] : i) * ld : nullptr;
-    const float f = scaled && i < n ? scale[i] : 0.f;
-    for (int k = threadIdx.x * 4; k < kp; k += 1024) {
-        float v[4];
+// The largest finite |x|.
+__device__ inline float finite_max(float m, float x) { return __builtin_isfinite(x) ? fmaxf(m, fabsf(x)) : m; }
+template <int N>
+__device__ inline float block_max(float m) {
+    __shared__ float part[N / 64];
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = s && k + q < cols ? (float)s[k + q] : 0.f;
-        store4<P>(dst + (size_t)i * pitch, k, v);
-        if (!scaled) continue;
+    for (int w = 0; w < N / 64; ++w) m = fmaxf(m, part[w]);
+    return m;
+}
+
+// The counted tokens' rows of X, packed: row i at dst + i * pitch, zero past the hidden size up to
+// kp, whole zero rows from the number of tokens to its next multiple of 256.
+//
+// P = 1: `scaled` (when given) gets the rows times weight[i].  P = 2: each row in its own power of
+// two, unit[i] what it is to be multiplied with; most (when given) the largest |weight| * unit.
+template <typename T, int P>
+__global__ void __launch_bounds__(256) vocab_pack_x_kernel(const T* src, long ld, const int* map, const int* count,
+                                                           int cols, char* dst, long pitch, int kp,
+                                                           const float* weight, char* scaled, float* unit,
+                                                           uint32_t* most) {
+    const int i = blockIdx.x, n = *count;
+    if (i >= (n + 255) / 256 * 256) return;
+    const T* s = i < n ? src + (size_t)map[i] * ld : nullptr;
+    float f = 1.f;
+    if constexpr (P == 2) {
+        if (s) {
+            float m = 0.f;
+            for (int k = threadIdx.x * 4; k < cols; k += 1024)
+                if (k + 4 <= cols) {
+                    float v[4];
+                    load(s + k, v);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
+                } else {
+                    for (int q = k; q < cols; ++q) m = finite_max(m, (float)s[q]);
+                }
+            const int e = scale_exponent(block_max<256>(m));
+            f = ldexpf(1.f, e);
+            if (threadIdx.x == 0) {
+                const float u = ldexpf(1.f, -e);
+                unit[i] = u;
+                const float w = most ? fabsf(weight[i] * u) : 0.f;
+                if (w > 0.f) atomicMax(most, __float_as_uint(w));
+            }
+        }
+    } else if (scaled && s) {
+        f = weight[i];
+    }
+    for (int k = threadIdx.x * 4; k < kp; k += 1024) {
+        float v[4] = {};
+        if (s && k + 4 <= cols)
+            load(s + k, v);
+        else if (s)
+            for (int q = 0; q < 4; ++q) v[q] = k + q < cols ? (float)s[k + q] : 0.f;
+        if constexpr (P == 1) {
+            store4<P>(dst + (size_t)i * pitch, k, v);
+            if (!scaled) continue;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] *= f;
-        store4<P>(scaled + (size_t)i * pitch, k, v);
+        store4<P>((P == 1 ? scaled : dst) + (size_t)i * pitch, k, v);
+    }
+}
+
+// The largest finite magnitude of a piece of W, as the bits of a float.
+template <typename T>
+__global__ void __launch_bounds__(256) vocab_max_kernel(const T* src, long ld, int rows, int cols, uint32_t* most) {
+    float m = 0.f;
+    const int lane = threadIdx.x & 63;
+    for (int r = blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4) {
+        const T* s = src + (size_t)r * ld;
+        int k = lane * 4;
+#pragma unroll 4
+        for (; k + 4 <= cols; k += 256) {
+            float v[4];
+            load(s + k, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
+        }
+        for (; k < cols; ++k) m = finite_max(m, (float)s[k]);
+    }
+    m = block_max<256>(m);
+    if (threadIdx.x == 0 && m > 0.f) atomicMax(most, __float_as_uint(m));
+}
+
+// A piece of W packed, zero past the hidden size up to kp and from its rows to their next multiple
+// of 256; P = 2: in the power of two of its largest value, *unit what a packed unit stands for.
+template <typename T, int P>
+__global__ void __launch_bounds__(256) vocab_pack_w_kernel(const T* src, long ld, int rows, int cols, char* dst,
+                                                           long pitch, int kp, const uint32_t* most, float* unit) {
+    const int i = blockIdx.x;
+    const T* s = i < rows ? src + (size_t)i * ld : nullptr;
+    float f = 1.f;
+    if constexpr (P == 2) {
+        const int e = scale_exponent(__uint_as_float(*most));
+        f = ldexpf(1.f, e);
+        if (i == 0 && threadIdx.x == 0) *unit = ldexpf(1.f, -e);
+    }
+    for (int k = threadIdx.x * 4; k < kp; k += 1024) {
+        float v[4] = {};
+        if (s && k + 4 <= cols)
+            load(s + k, v);
+        else if (s)
+            for (int q = 0; q < 4; ++q) v[q] = k + q < cols ? (float)s[k + q] : 0.f;
+        if constexpr (P == 2)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] *= f;
+        store4<P>(dst + (size_t)i * pitch, k, v);
     }
 }
 
@@ -130,31 +256,36 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
 }
 
 // lse of each counted token from its partial maxima and sums, then its loss.  A workgroup takes 32
-// tokens, 8 threads each.
-__global__ void __launch_bounds__(256) vocab_loss_kernel(Entries e, const int* rows, const int* count,
-                                                         const float2* part, int parts, int tp, const float* z,
-                                                         float* loss, float* lse) {
-    __shared__ float tops[8][32], sums[8][32], lses[32];
+// tokens, 32 threads each: once through the maxima, once through the sums, so that no load waits
+// for an exponential.
+__global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* rows, const int* count,
+                                                          const float2* part, int parts, int tp, const float* z,
+                                                          float* loss, float* lse) {
+    __shared__ float slot[32][33], lses[32];
     const int n = *count, tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i0 = blockIdx.x * 32, i = i0 + tx;
     if (i0 >= n) return;
-    float top = -INFINITY, sum = 0.f;
+    const auto larger = [](float a, float b) { return b > a || b != b ? b : a; };  // a NaN stays
+    float top = -INFINITY;
     if (i < n)
-        for (int p = ty; p < parts; p += 8) {
+#pragma unroll 4
+        for (int p = ty; p < parts; p += 32) top = larger(top, part[(size_t)p * tp + i].x);
+    slot[ty][tx] = top;
+    __syncthreads();
+    for (int y = 0; y < 32; ++y) top = larger(top, slot[y][tx]);
+    __syncthreads();
+    float sum = 0.f;
+    if (i < n && top != -INFINITY)
+#pragma unroll 4
+        for (int p = ty; p < parts; p += 32) {
             const float2 v = part[(size_t)p * tp + i];
-            const float m = v.x > top || v.x != v.x ? v.x : top;
-            if (m == -INFINITY) continue;
-            sum = sum * expf(top - m) + v.y * expf(v.x - m);
-            top = m;
+            sum += v.y * expf(v.x - top);
         }
-    tops[ty][tx] = top;
-    sums[ty][tx] = sum;
+    slot[ty][tx] = sum;
     __syncthreads();
     if (ty == 0 && i < n) {
-        float m = top;
-        for (int y = 1; y < 8; ++y) m = tops[y][tx] > m || tops[y][tx] != tops[y][tx] ? tops[y][tx] : m;
-        float s = 0.f;
-        for (int y = 0; y < 8; ++y) s += m == -INFINITY ? 0.f : sums[y][tx] * expf(tops[y][tx] - m);
-        const float l = m + logf(s);
+        sum = 0.f;
+        for (int y = 0; y < 32; ++y) sum += slot[y][tx];
+        const float l = top + logf(sum);
         const int t = rows[i];
         lses[tx] = l;
         lse[t] = l;
@@ -163,7 +294,7 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(Entries e, const int* r
     if (!e.teacher) return;
     __syncthreads();
     const int lane = threadIdx.x & 63;
-    for (int y = threadIdx.x >> 6; y < 32; y += 4) {
+    for (int y = threadIdx.x >> 6; y < 32; y += 16) {
         if (i0 + y >= n) break;
         const int t = rows[i0 + y];
         const float l = lses[y];
@@ -190,12 +321,13 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(Entries e, const int* r
 // would be rounded.  c comes from expm1, so a p close to 1 costs no digits; a c below 2^-25, where
 // fp32 cannot tell p from 1, is raised to it.
 //
-// Distillation: row i of D is s * p, and s * (p - sum of q over the entries that name the same
-// vocabulary row) at the entries; X and the product enter as they are.
+// Distillation: row i of D is p, and p - (sum of q over the entries that name the same vocabulary
+// row) at the entries.  bf16: times s, with X and the product as they are, so that dW's factors are
+// rounded once (D) and not twice; fp32 (`apart`): s enters with X and the product.
 __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, int vocab, float alpha,
                                                          const int* pos, const float* lse, const float* dloss,
                                                          const float* z, float* lse_c, float* scale, float* out_scale,
-                                                         float* value) {
+                                                         float* value, bool apart) {
     const long t = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (t >= tokens) return;
@@ -224,12 +356,12 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, 
                 float q = 0.f;
                 for (int o = 0; o < e.k; ++o)
                     if (index[o] == v) q += expf(teacher[o] * e.teacher_alpha - top - log_total);
-                d = s * (expf(z[t * e.k + k] - l) - q);
+                d = (apart ? 1.f : s) * (expf(z[t * e.k + k] - l) - q);
             }
             value[t * e.k + k] = d;
         }
-        sc = __all(good) ? s : NAN;
-        os = 1.f;
+        sc = __all(good) ? (apart ? 1.f : s) : NAN;
+        os = apart ? s : 1.f;
     }
     if (lane == 0) {
         lse_c[i] = l;
@@ -241,29 +373,35 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, 
 // Puts the entries' values into D where they fall into this piece.
 template <int P>
 __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens, int v0, int vocab, const int* pos,
-                                                          const float* value, char* d, long d_pitch) {
+                                                          const float* value, const float* weight,
+                                                          const float* x_unit, const float* x_most, char* d,
+                                                          long d_pitch) {
     const long j = (long)blockIdx.x * 256 + threadIdx.x;
     if (j >= (long)tokens * e.k) return;
     const long t = j / e.k, k = j - t * e.k;
     const int i = pos[t];
     const i64 v = e.index[t * e.ld + k];
     if (i < 0 || !e.counts(v) || v < v0 || v >= v0 + vocab) return;
-    store1<P>(d + (size_t)i * d_pitch, v - v0, value[j]);
+    const float f = P == 2 ? d_factor(weight[i], x_unit[i], *x_most) : 1.f;
+    store1<P>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
 }
 
 // dX of every token: the sum of its product's parts, or 0 where it does not count.
-template <typename T>
-__global__ void __launch_bounds__(256) vocab_dx_out_kernel(const int* pos, int hidden, const float* acc, int splits,
-                                                           long tp, int hp, const float* scale, T* dx, long ld) {
-    const int t = blockIdx.x, i = pos[t];
-    const float s = i < 0 ? 0.f : scale[i];
-    for (int h = threadIdx.x; h < hidden; h += 256) {
-        float v = 0.f;
-        if (i >= 0) {
-            for (int z = 0; z < splits; ++z) v += acc[((size_t)z * tp + i) * hp + h];
-            v *= s;
-        }
-        dx[(size_t)t * ld + h] = (T)v;
+template <typename T, int P>
+__global__ void __launch_bounds__(256) vocab_dx_out_kernel(const int* pos, const int* count, int hidden,
+                                                           const float* acc, DxCut cut, int hp, const float* weight,
+                                                           const float* x_unit, const float* x_most, T* dx, long ld) {
+    const int t = blockIdx.x, i = pos[t], splits = cut.splits(*count);
+    const size_t rows = cut.rows(*count);
+    float s = 0.f;
+    if (i >= 0) s = P == 1 ? weight[i] : *x_most / (x_unit[i] * kDScale);
+    for (int h = threadIdx.x * 4; h < hidden; h += 1024) {
+        f32x4 v = {};
+        if (i >= 0)
+            for (int z = 0; z < splits; ++z) v += *(const f32x4*)(acc + (z * rows + i) * hp + h);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (h + q < hidden) dx[(size_t)t * ld + h + q] = (T)(v[q] * s);
     }
 }
 

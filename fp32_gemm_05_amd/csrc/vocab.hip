@@ -3,7 +3,7 @@
 //
 // Forward: one product whose tiles end as per-token maxima and sums of exponentials (log-sum-exp),
 // and one dot product per named entry.  Gradient: the vocabulary is taken in pieces; a piece's
-// logits are recomputed into D = d(loss)/dz (bf16, or three planes of it for fp32), from which
+// logits are recomputed into D = d(loss)/dz (bf16, or two fp16 planes for fp32), from which
 // dX += D W and dW = D^T X follow.  The tokens that do not count are left out at the start: the
 // others are packed together, so they cost no product, and whatever their rows hold reaches no
 // gradient.
@@ -45,34 +45,35 @@ long up(long x, long to) { return (x + to - 1) / to * to; }
 // The workspace: byte offsets of its arrays for a call's sizes (the pointers of the call are not
 // looked at, so that its size can be asked for beforehand).
 struct Layout {
-    int tp, hk, hp;      // padded tokens, hidden as a product's k, hidden as a product's rows
-    int piece, pieces;   // vocabulary rows of a piece (a multiple of 256), number of pieces
-    int parts, splits;
-    long count, rows, pos, z, lse_c, scale, out_scale, value, x, xs, w, d, part, acc, bytes;
+    int tp, hk, hp;     // padded tokens, hidden as a product's k, hidden as a product's rows
+    int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces
+    DxCut cut;
+    bool dx_big;
+    long count, rows, pos, z, lse_c, scale, weight, x_unit, maxima, w_unit, value, x, xs, w, d, part, acc, bytes;
 };
 
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
-// Tile shapes.  The large one when it fills the chip, else the small one.
-using Big1 = Tile<1, 256, 256, 128, 64, 3, 2>;
-using Small1 = Tile<1, 128, 64, 64, 32, 3, 3>;
-using Big3 = Tile<3, 256, 128, 64, 64, 2, 2>;
-using Small3 = Tile<3, 128, 64, 64, 32, 2, 2>;
+// Tile shapes: the large one when it fills the chip, else the small one.
+template <int P>
+using Big = Tile<P, 256, 256, 128, 64, 3, 2>;
+template <int P>
+using Small = Tile<P, 128, 64, 64, 32, 3, 3>;
 
 template <class B>
 bool fills(long rows_m, long rows_n) {
     return up(rows_m, B::kBM) / B::kBM * (up(rows_n, B::kBN) / B::kBN) >= 192;
 }
 
-Layout layout(bool f32, bool grad, int T, int V, int H, int K, bool teacher) {
+Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     Layout l{};
-    const int P = f32 ? 3 : 1, bk = f32 ? 32 : 64;
+    const int bk = 64 / P;
     l.tp = (int)up(T > 0 ? T : 1, 256);
     l.hk = (int)up(H, bk);
     l.hp = (int)up(H, 256);
     const long vp = up(V, 256);
-    const long row = 2L * P;  // bytes of an element in planes
-    const long per = row * (l.hk + (grad ? l.tp : 0));
+    const long element = 2L * P;  // bytes in planes
+    const long per = element * (l.hk + (grad ? l.tp : 0));
     long piece = kPieceBytes / per / 256 * 256;
     // a launch's grid stays below 2^22 tiles, a packed row below 2^24 bytes
     const long most = 128L * ((1L << 22) / (l.tp / 64)) / 256 * 256;
@@ -83,19 +84,13 @@ Layout layout(bool f32, bool grad, int T, int V, int H, int K, bool teacher) {
     const long pieces = (vp + piece - 1) / piece;
     l.piece = (int)up((vp + pieces - 1) / pieces, 256);
     l.pieces = (int)((vp + l.piece - 1) / l.piece);
-    l.parts = (int)(vp / kPartRows);
-    l.splits = 1;
-    if (grad) {
-        // dX has few tiles when there are few tokens: its long axis, the vocabulary, is split then
-        const long tiles = up(T, 64) / 64 * (up(H, 128) / 128);
-        const bool big = f32 ? fills<Big3>(H, T) : fills<Big1>(H, T);
-        if (!big) {
-            long s = 512 / (tiles > 0 ? tiles : 1);
-            const long most = l.piece / bk / 8;
-            s = s > most ? most : s;
-            l.splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
-        }
-    }
+    // dX's workgroups: its tiles, or about as many as the chip has places for (one large tile a
+    // compute unit, two small ones)
+    l.dx_big = T > 128 && H > 128;
+    const int bm = l.dx_big ? Big<1>::kBM : Small<1>::kBM, bn = l.dx_big ? Big<1>::kBN : Small<1>::kBN;
+    const int tiles_m = (int)(up(H, bm) / bm), tiles = tiles_m * (int)(up(l.tp, bn) / bn);
+    const int places = l.dx_big ? 256 : 512, slabs = l.piece / bk;
+    l.cut = {tiles_m, bn, tiles > places ? tiles : places / tiles * tiles, slabs / 8 > 1 ? slabs / 8 : 1};
     long at = 0;
     auto take = [&](long bytes) {
         const long o = at;
@@ -106,37 +101,43 @@ Layout layout(bool f32, bool grad, int T, int V, int H, int K, bool teacher) {
     l.rows = take(4L * l.tp);
     l.pos = take(4L * l.tp);
     if (!teacher) l.z = take(4L * l.tp);
-    l.x = take(row * l.hk * l.tp);
-    l.w = take(row * l.hk * l.piece);
+    l.x_unit = take(4L * l.tp);
+    l.maxima = take(4L * (l.pieces + 1));
+    l.w_unit = take(4L * l.pieces);
+    l.x = take(element * l.hk * l.tp);
+    l.w = take(element * l.hk * l.piece);
     if (grad) {
         l.lse_c = take(4L * l.tp);
         l.scale = take(4L * l.tp);
-        l.out_scale = take(4L * l.tp);
+        l.weight = take(4L * l.tp);
         l.value = take(4L * T * K);
-        if (!teacher) l.xs = take(row * l.hk * l.tp);
-        l.d = take(row * l.tp * l.piece);
-        l.acc = take(4L * l.splits * l.tp * l.hp);
+        if (P == 1 && !teacher) l.xs = take(element * l.hk * l.tp);
+        l.d = take(element * l.tp * l.piece);
+        l.acc = take(4L * l.hp * ((long)l.cut.groups / tiles_m * bn));
     } else {
-        l.part = take(8L * l.parts * l.tp);
+        l.part = take(8L * (vp / kPartRows) * l.tp);
     }
     l.bytes = at;
     return l;
 }
 
-template <class Small, class Big, class F>
-void by_size(long rows_m, long rows_n, F f) {
-    if (fills<Big>(rows_m, rows_n))
-        f((Big*)nullptr);
+template <int P, class F>
+void by_size(bool big, F f) {
+    if (big)
+        f((Big<P>*)nullptr);
     else
-        f((Small*)nullptr);
+        f((Small<P>*)nullptr);
 }
 
-template <typename T, int P, class Small, class Big>
+template <typename T, int P>
 int run(const Call& c) {
     using Pl = Planes<P>;
-    const Layout l = layout(P == 3, c.grad, c.T, c.V, c.H, c.e.k, c.e.teacher != nullptr);
+    const Layout l = layout(P, c.grad, c.T, c.V, c.H, c.e.k, c.e.teacher != nullptr);
     char* ws = c.work;
+    auto floats = [&](long at) { return (float*)(ws + at); };
     int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
+    float* const x_most = P == 2 ? floats(l.maxima) : nullptr;
+    float* const x_unit = floats(l.x_unit);
     const T *X = (const T*)c.X, *W = (const T*)c.W;
     const hipStream_t st = c.stream;
     const long x_pitch = Pl::pitch(l.hk), d_pitch = Pl::pitch(l.piece);
@@ -144,24 +145,25 @@ int run(const Call& c) {
     (void)hipGetLastError();
 
     vocab_count_kernel<<<1, 1024, 0, st>>>(c.e, c.T, rows, pos, count, c.grad ? nullptr : c.loss,
-                                           c.grad ? nullptr : c.lse_out);
+                                           c.grad ? nullptr : c.lse_out, (uint32_t*)(ws + l.maxima),
+                                           P == 2 ? l.pieces + 1 : 0);
     // the logits of the named entries
     const float* z = c.picked;
     if (c.T > 0 && (!c.grad || !c.e.teacher)) {
-        float* zo = c.e.teacher ? c.picked_out : (float*)(ws + l.z);
+        float* zo = c.e.teacher ? c.picked_out : floats(l.z);
         vocab_pick_kernel<T><<<(unsigned)(up((long)c.T * c.e.k, 4) / 4), 256, 0, st>>>(
             c.e, c.T, c.V, c.H, c.alpha, X, c.ldx, W, c.ldw, zo);
         z = zo;
     }
-    if (c.grad) {
-        if (c.T > 0) vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
-            c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, (float*)(ws + l.lse_c), (float*)(ws + l.scale),
-            (float*)(ws + l.out_scale), (float*)(ws + l.value));
-    }
-    // cross entropy multiplies dW with X scaled by token (vocab_rows_kernel), distillation with X
-    char* const xs = c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
-    vocab_pack_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, 0, c.H, ws + l.x, x_pitch, l.hk,
-                                                  (const float*)(ws + l.out_scale), xs);
+    if (c.grad && c.T > 0)
+        vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
+            c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, floats(l.lse_c), floats(l.scale), floats(l.weight),
+            floats(l.value), P == 2);
+    // bf16 cross entropy multiplies dW with X times each token's weight (vocab_rows_kernel)
+    char* const xs = P == 1 && c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
+    vocab_pack_x_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, c.H, ws + l.x, x_pitch, l.hk,
+                                                    floats(l.weight), xs, x_unit,
+                                                    c.grad ? (uint32_t*)x_most : nullptr);
     const Operand x{ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
     const Operand x_dw{xs ? xs : ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
     const Operand d{ws + l.d, (uint32_t)d_pitch, (uint32_t)d_pitch, l.tp};
@@ -169,65 +171,71 @@ int run(const Call& c) {
     const bool direct = P == 1 && c.H % Pl::BK == 0 && c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 &&
                         c.ldw < (1L << 22);
     int part = 0;
-    for (int v0 = 0; v0 < c.V; v0 += l.piece) {
-        const int vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
-        Operand w{(const char*)(W + (size_t)v0 * c.ldw), (uint32_t)(c.ldw * 2), (uint32_t)(c.H * 2), vn};
+    for (int p = 0; p < l.pieces; ++p) {
+        const int v0 = p * l.piece, vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
+        const T* Wp = W + (size_t)v0 * c.ldw;
+        float* const w_unit = floats(l.w_unit) + p;
+        Operand w{(const char*)Wp, (uint32_t)(c.ldw * 2), (uint32_t)(c.H * 2), vn};
         if (!direct) {
-            vocab_pack_kernel<T, P><<<(unsigned)up(vn, 256), 256, 0, st>>>(W + (size_t)v0 * c.ldw, c.ldw, nullptr,
-                                                                         nullptr, vn, c.H, ws + l.w, x_pitch, l.hk,
-                                                                         nullptr, nullptr);
+            uint32_t* const most = (uint32_t*)(ws + l.maxima) + 1 + p;
+            if (P == 2)
+                vocab_max_kernel<T><<<(unsigned)(vn < 8192 ? up(vn, 4) / 4 : 2048), 256, 0, st>>>(Wp, c.ldw, vn, c.H,
+                                                                                                 most);
+            vocab_pack_w_kernel<T, P><<<(unsigned)up(vn, 256), 256, 0, st>>>(Wp, c.ldw, vn, c.H, ws + l.w, x_pitch,
+                                                                           l.hk, most, w_unit);
             w = Operand{ws + l.w, (uint32_t)x_pitch, (uint32_t)x_pitch, (int)up(vn, 256)};
         }
-        if (!c.grad) {
-            by_size<Small, Big>(vn, c.T, [&](auto* shape) {
+        if (c.T == 0) {
+            // only dW, which is 0, is left to do
+        } else if (!c.grad) {
+            by_size<P>(fills<Big<P>>(vn, c.T), [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(vn, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-                const LseArgs a{w, x, count, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part, l.tp};
+                const LseArgs a{w, x, count, w_unit, x_unit, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part,
+                                l.tp};
                 vocab_lse_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
                 part += tm * S::WAVES_M;
             });
             continue;
-        }
-        if (c.T > 0) by_size<Small, Big>(vn, c.T, [&](auto* shape) {
-            using S = typename std::remove_pointer<decltype(shape)>::type;
-            // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
-            const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-            const GradArgs a{w, x, count, tm, tn, slabs, vn, c.alpha, (const float*)(ws + l.lse_c),
-                             (const float*)(ws + l.scale), ws + l.d, d_pitch};
-            vocab_grad_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
-        });
-        if (c.T > 0) vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-            c.e, c.T, v0, vn, pos, (const float*)(ws + l.value), ws + l.d, d_pitch);
-        if (c.T > 0 && c.dX) {
-            by_size<Small, Big>(c.H, c.T, [&](auto* shape) {
+        } else {
+            by_size<P>(fills<Big<P>>(vn, c.T), [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
-                const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-                const DxArgs a{w, d, count, tm, tn, (int)up(vn, Pl::BK) / Pl::BK, l.splits, (float*)(ws + l.acc), l.tp, l.hp, v0 > 0};
-                vocab_dx_kernel<S><<<dim3(tm * tn, l.splits), S::NT, 0, st>>>(a);
+                // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
+                const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
+                const GradArgs a{w, x, count, w_unit, x_unit, x_most, tm, tn, slabs, vn, c.alpha, floats(l.lse_c),
+                                 floats(l.scale), floats(l.weight), ws + l.d, d_pitch};
+                vocab_grad_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
+            vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
+                c.e, c.T, v0, vn, pos, floats(l.value), floats(l.weight), x_unit, x_most, ws + l.d, d_pitch);
+            if (c.dX)
+                by_size<P>(l.dx_big, [&](auto* shape) {
+                    using S = typename std::remove_pointer<decltype(shape)>::type;
+                    const DxArgs a{w, d, count, w_unit, l.cut, (int)up(vn, Pl::BK) / Pl::BK, floats(l.acc), l.hp, p > 0};
+                    vocab_dx_kernel<S><<<l.cut.groups, S::NT, 0, st>>>(a);
+                });
         }
-        if (c.dW) {
-            by_size<Small, Big>(c.H, vn, [&](auto* shape) {
+        if (c.dW)
+            by_size<P>(fills<Big<P>>(c.H, vn), [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(vn, S::kBN) / S::kBN;
                 T* out = (T*)c.dW + (size_t)v0 * c.lddw;
                 const int vec = c.H % 4 == 0 && c.lddw % 4 == 0 && (uintptr_t)c.dW % (4 * sizeof(T)) == 0;
-                const DwArgs a{x_dw, d, count, tm, tn, c.H, vn, out, c.lddw, vec};
+                const DwArgs a{x_dw, d, count, x_most, tm, tn, c.H, vn, out, c.lddw, vec};
                 vocab_dw_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
-        }
     }
     if (!c.grad)
-        vocab_loss_kernel<<<l.tp / 32, 256, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
-                                                     c.loss, c.lse_out);
+        vocab_loss_kernel<<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
+                                                      c.loss, c.lse_out);
     else if (c.T > 0 && c.dX)
-        vocab_dx_out_kernel<T><<<c.T, 256, 0, st>>>(pos, c.H, (const float*)(ws + l.acc), l.splits, l.tp, l.hp,
-                                                    (const float*)(ws + l.out_scale), (T*)c.dX, c.lddx);
+        vocab_dx_out_kernel<T, P><<<c.T, 256, 0, st>>>(pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight),
+                                                       x_unit, x_most, (T*)c.dX, c.lddx);
     return (int)hipGetLastError();
 }
 
 int dispatch(const Call& c) {
-    return c.f32 ? run<float, 3, Small3, Big3>(c) : run<__bf16, 1, Small1, Big1>(c);
+    return c.f32 ? run<float, 2>(c) : run<__bf16, 1>(c);
 }
 
 bool sizes_ok(int T, int V, int H, int K, int& bad, const int pos[4]) {
@@ -267,7 +275,7 @@ long long vocab_workspace(int dtype, int grad, int T, int V, int H, int K) {
     int bad = 0;
     if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
     if (!libsgemm::vocab::sizes_ok(T, V, H, K > 0 ? K : 1, bad, pos) || K < 0) return K < 0 ? -6 : -bad;
-    return libsgemm::vocab::layout(dtype == VOCAB_F32, grad != 0, T, V, H, K > 0 ? K : 1, K > 0).bytes;
+    return libsgemm::vocab::layout(dtype == VOCAB_F32 ? 2 : 1, grad != 0, T, V, H, K > 0 ? K : 1, K > 0).bytes;
 }
 
 int vocab_ce(int dtype, int T, int V, int H, float alpha, const void* X, int ldx, const void* W, int ldw,

@@ -32,11 +32,12 @@
  * gives the same bits.
  *
  * Precision: loss, lse, picked, dloss and teacher are fp32, as are all sums and softmax
- * statistics.  fp32 X and W are multiplied as three bf16 parts each (exact), with products below
- * 2^-24 of the whole left out: the result is as near as an fp32 product's, but an infinity in W
- * makes NaN of every logit of its row.  With bf16 X and W, D is rounded to bf16 for the two
- * gradient products (cross entropy scales a token's row so that its target's entry is exact), and
- * dX and dW are rounded to bf16 at the end.
+ * statistics.  fp32 X and W are multiplied as two fp16 parts each, scaled by a power of two (a
+ * token's own for X, one for up to 2^21 rows of W): values down to 2^-16 of the largest keep their
+ * 24 bits, smaller ones are held to 2^-40 of the largest, D to 2^-40 of its largest possible entry.
+ * An infinity in W makes NaN of every logit of its row.  With bf16 X and W, D is rounded to bf16
+ * for the two gradient products (cross entropy scales a token's row so that its target's entry is
+ * exact), and dX and dW are rounded to bf16 at the end.
  *
  * Return codes as in sgemm.h: 0, -i for argument i, +hipError_t from a launch.  T = 0 is a quick
  * return (dW, when wanted, is set to 0).

@@ -145,7 +145,7 @@ struct Side {
 
     __device__ inline void init(const Operand& o, int row0, int k0, int wave, int lane, int wave_at) {
         if (O == K_ROW) {
-            at = o.base + (size_t)row0 * o.pitch + (size_t)k0 * ROW;
+            at = o.base + (size_t)first_row(o, row0) * o.pitch + (size_t)k0 * ROW;
             step = ROW;
             left = 0;
         } else {
@@ -173,13 +173,15 @@ struct Side {
                 }
         }
     }
+    // A tile may lie past the operand's rows as a whole (the zero padding of D): it reads the last row.
+    static __device__ inline int first_row(const Operand& o, int row0) { return imin(row0, o.rows - 1); }
     __device__ inline void set_offsets(const Operand& o, int row0, int wave, int lane) {
 #pragma unroll
         for (int j = 0; j < L; ++j) {
             const int i = (j * NW + wave) * 64 + lane;
             const int r = i / QUADS, u = i - r * QUADS;
             if (O == K_ROW) {
-                const int row = imin(row0 + r, o.rows - 1) - row0;  // the tile's first row is always valid
+                const int row = imin(row0 + r, o.rows - 1) - first_row(o, row0);
                 off[j] = (uint32_t)row * o.pitch + (uint32_t)(source_quad(r, u) * 16);
             } else {
                 const uint32_t q = (uint32_t)row0 * 2 * P + (uint32_t)(source_quad(r, u) * 16);

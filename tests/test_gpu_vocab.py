@@ -118,7 +118,9 @@ def run_distill(X, W, index, teacher, dloss, alpha, teacher_alpha, dtype):
 
 
 SIZES = [(1, 1, 1), (1, 500, 64), (3, 257, 33), (16, 1000, 128), (64, 512, 64), (65, 4097, 200), (130, 777, 65),
-         (256, 2048, 256), (300, 5003, 129), (1000, 3001, 320), (129, 50000, 257), (2050, 6400, 512)]
+         (256, 2048, 256), (300, 5003, 129), (1000, 3001, 320), (129, 50000, 257), (2050, 6400, 512),
+         # rows of whole slabs, read in place, and a vocabulary whose last 256 rows hold a whole empty tile
+         (22, 1152, 192), (300, 1025, 64), (700, 33000, 128)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

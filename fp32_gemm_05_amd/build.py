@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libsgemm.so")
 SOURCES = [os.path.join(CSRC, "sgemm.hip"), os.path.join(CSRC, "vocab.hip")]
 KERNEL_HEADERS = ("kernel_common.hpp", "kernel_mfma.hpp", "kernel_pipe.hpp", "kernel_deep.hpp", "kernel_splitk.hpp",
                   "kernel_direct.hpp", "kernel_dl.hpp", "kernel_valu.hpp")
-VOCAB_HEADERS = ("kernel_vocab.hpp", "kernel_vocab_rows.hpp")
+VOCAB_HEADERS = ("kernel_vocab.hpp", "kernel_vocab_rows.hpp", "kernel_vocab_few.hpp")
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sgemm_kernels.hpp", "sgemm_launch.hpp", "tuned_table.inc")
                      + KERNEL_HEADERS + VOCAB_HEADERS] + [
     os.path.join(os.path.dirname(HERE), "include", f) for f in ("sgemm.h", "vocab.h")]

@@ -255,36 +255,45 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
     log_total = logf(wave_sum(s));
 }
 
-// lse of each counted token from its partial maxima and sums, then its loss.  A workgroup takes 32
-// tokens, 32 threads each: once through the maxima, once through the sums, so that no load waits
+// lse of each counted token from its partial maxima and sums, then its loss.  A workgroup takes TX
+// tokens, TY threads each: once through the maxima, once through the sums, so that no load waits
 // for an exponential.
+template <int TX>
 __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* rows, const int* count,
                                                           const float2* part, int parts, int tp, const float* z,
                                                           float* loss, float* lse) {
-    __shared__ float slot[32][33], lses[32];
-    const int n = *count, tx = threadIdx.x & 31, ty = threadIdx.x >> 5, i0 = blockIdx.x * 32, i = i0 + tx;
+    constexpr int TY = 1024 / TX;
+    __shared__ float slot[16][TX], lses[TX];
+    const int n = *count, tx = threadIdx.x % TX, ty = threadIdx.x / TX, i0 = blockIdx.x * TX, i = i0 + tx;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (i0 >= n) return;
     const auto larger = [](float a, float b) { return b > a || b != b ? b : a; };  // a NaN stays
     float top = -INFINITY;
     if (i < n)
-#pragma unroll 4
-        for (int p = ty; p < parts; p += 32) top = larger(top, part[(size_t)p * tp + i].x);
-    slot[ty][tx] = top;
+#pragma unroll 8
+        for (int p = ty; p < parts; p += TY) top = larger(top, part[(size_t)p * tp + i].x);
+#pragma unroll
+    for (int o = TX; o < 64; o *= 2) top = larger(top, __shfl_xor(top, o));
+    if (lane < TX) slot[wave][tx] = top;
     __syncthreads();
-    for (int y = 0; y < 32; ++y) top = larger(top, slot[y][tx]);
+#pragma unroll
+    for (int y = 0; y < 16; ++y) top = larger(top, slot[y][tx]);
     __syncthreads();
     float sum = 0.f;
     if (i < n && top != -INFINITY)
-#pragma unroll 4
-        for (int p = ty; p < parts; p += 32) {
+#pragma unroll 8
+        for (int p = ty; p < parts; p += TY) {
             const float2 v = part[(size_t)p * tp + i];
             sum += v.y * expf(v.x - top);
         }
-    slot[ty][tx] = sum;
+#pragma unroll
+    for (int o = TX; o < 64; o *= 2) sum += __shfl_xor(sum, o);
+    if (lane < TX) slot[wave][tx] = sum;
     __syncthreads();
     if (ty == 0 && i < n) {
         sum = 0.f;
-        for (int y = 0; y < 32; ++y) sum += slot[y][tx];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) sum += slot[y][tx];
         const float l = top + logf(sum);
         const int t = rows[i];
         lses[tx] = l;
@@ -293,8 +302,7 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
     }
     if (!e.teacher) return;
     __syncthreads();
-    const int lane = threadIdx.x & 63;
-    for (int y = threadIdx.x >> 6; y < 32; y += 16) {
+    for (int y = wave; y < TX; y += 16) {
         if (i0 + y >= n) break;
         const int t = rows[i0 + y];
         const float l = lses[y];
@@ -313,6 +321,8 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
     }
 }
 
+enum DForm { D_PACKED, D_APART, D_WHOLE };
+
 // Per counted token what its row of D needs; one wave per token.
 //
 // Cross entropy: with s = alpha * dloss, p the softmax and c = 1 - p[target], row i of D is p / c
@@ -323,11 +333,14 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
 //
 // Distillation: row i of D is p, and p - (sum of q over the entries that name the same vocabulary
 // row) at the entries.  bf16: times s, with X and the product as they are, so that dW's factors are
-// rounded once (D) and not twice; fp32 (`apart`): s enters with X and the product.
+// rounded once (D) and not twice; fp32 (D_APART): s enters with X and the product.
+//
+// D_WHOLE, for few tokens, whose D is kept wide: both operators' rows are s * (p - y), and X and the
+// product enter as they are.
 __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, int vocab, float alpha,
                                                          const int* pos, const float* lse, const float* dloss,
                                                          const float* z, float* lse_c, float* scale, float* out_scale,
-                                                         float* value, bool apart) {
+                                                         float* value, DForm form) {
     const long t = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (t >= tokens) return;
@@ -339,9 +352,9 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, 
         const i64 v = e.index[t * e.ld];
         const float c = fmaxf(-expm1f(z[t] - l), 0x1p-25f);
         const bool good = v >= 0 && v < vocab;
-        sc = good ? 1.f / c : NAN;
-        os = good ? s * c : NAN;
-        if (lane == 0) value[t] = -1.f;
+        sc = !good ? NAN : form == D_WHOLE ? s : 1.f / c;
+        os = !good ? NAN : form == D_WHOLE ? 1.f : s * c;
+        if (lane == 0) value[t] = form == D_WHOLE ? -s * c : -1.f;
     } else {
         bool good = true;
         float top, log_total;
@@ -356,12 +369,12 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, 
                 float q = 0.f;
                 for (int o = 0; o < e.k; ++o)
                     if (index[o] == v) q += expf(teacher[o] * e.teacher_alpha - top - log_total);
-                d = (apart ? 1.f : s) * (expf(z[t * e.k + k] - l) - q);
+                d = (form == D_APART ? 1.f : s) * (expf(z[t * e.k + k] - l) - q);
             }
             value[t * e.k + k] = d;
         }
-        sc = __all(good) ? (apart ? 1.f : s) : NAN;
-        os = apart ? s : 1.f;
+        sc = __all(good) ? (form == D_APART ? 1.f : s) : NAN;
+        os = form == D_APART ? s : 1.f;
     }
     if (lane == 0) {
         lse_c[i] = l;
@@ -370,7 +383,7 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, 
     }
 }
 
-// Puts the entries' values into D where they fall into this piece.
+// Puts the entries' values into D where they fall into this piece (P = 0: a D in fp32).
 template <int P>
 __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens, int v0, int vocab, const int* pos,
                                                           const float* value, const float* weight,
@@ -382,8 +395,12 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
     const int i = pos[t];
     const i64 v = e.index[t * e.ld + k];
     if (i < 0 || !e.counts(v) || v < v0 || v >= v0 + vocab) return;
+    if constexpr (P == 0) {
+        ((float*)(d + (size_t)i * d_pitch))[v - v0] = value[j];
+        return;
+    }
     const float f = P == 2 ? d_factor(weight[i], x_unit[i], *x_most) : 1.f;
-    store1<P>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
+    store1<P == 2 ? 2 : 1>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
 }
 
 // dX of every token: the sum of its product's parts, or 0 where it does not count.

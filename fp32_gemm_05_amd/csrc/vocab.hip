@@ -10,7 +10,7 @@
 #include <limits.h>
 
 #include "../../include/vocab.h"
-#include "kernel_vocab_rows.hpp"
+#include "kernel_vocab_few.hpp"
 
 namespace libsgemm {
 namespace vocab {
@@ -121,6 +121,133 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     return l;
 }
 
+// At most kFewTokens tokens (kernel_vocab_few.hpp).  nb: blocks of 16 tokens.
+struct FewLayout {
+    int nb, kt, piece, pieces, splits;
+    long steps, hb, hp, vp, count, rows, pos, z, lse_c, scale, weight, value, xf, xtf, d, part, acc, bytes;
+};
+
+int few_rows(int nb) { return nb == 4 ? 64 : 32; }  // vocabulary rows of a workgroup
+
+FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
+    FewLayout l{};
+    const int e = f32 ? 4 : 8;
+    l.nb = T > 32 ? 4 : T > 16 ? 2 : 1;
+    l.kt = (int)up(16 * l.nb, 4 * e) / (4 * e);
+    l.steps = up(H, 4 * e) / (4 * e);
+    l.hb = up(H, 16) / 16;
+    l.hp = up(H, 16 * e);
+    const long vp = up(V, 64);
+    l.piece = (int)(vp < 1L << 21 ? vp : 1L << 21);
+    l.pieces = (int)((vp + l.piece - 1) / l.piece);
+    l.vp = l.piece;
+    // dX's pass over W in enough parts to fill the chip four times, each of 16 steps or more
+    const long strips = l.hp / (16 * e), most = l.vp / (4 * e) / 16;
+    const long s = 1024 / strips < most ? 1024 / strips : most;
+    l.splits = (int)(s < 1 ? 1 : s);
+    long at = 0;
+    auto take = [&](long bytes) {
+        const long o = at;
+        at = up(at + bytes, 1024);
+        return o;
+    };
+    l.count = take(4);
+    l.rows = take(4 * kFewTokens);
+    l.pos = take(4 * kFewTokens);
+    l.z = take(4 * kFewTokens);
+    l.xf = take(1024 * l.steps * l.nb);
+    if (grad) {
+        l.lse_c = take(4 * kFewTokens);
+        l.scale = take(4 * kFewTokens);
+        l.weight = take(4 * kFewTokens);
+        l.value = take(4L * T * K);
+        l.xtf = take(1024 * l.hb * l.kt);
+        l.d = take(4L * 16 * l.nb * l.vp);
+        l.acc = take(4L * l.splits * 16 * l.nb * l.hp);
+    } else {
+        l.part = take(8L * kFewTokens * (vp / 32));
+    }
+    l.bytes = at;
+    return l;
+}
+
+bool few(int T) { return T > 0 && T <= kFewTokens; }
+
+template <typename T, int NB>
+int run_few(const Call& c, const FewLayout& l) {
+    typedef Chunk<T> Ch;
+    char* ws = c.work;
+    auto floats = [&](long at) { return (float*)(ws + at); };
+    int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
+    const T *X = (const T*)c.X, *W = (const T*)c.W;
+    const hipStream_t st = c.stream;
+    (void)hipGetLastError();
+
+    const int xf_chunks = (int)(64 * l.steps * l.nb), xtf_chunks = c.grad && c.dW ? (int)(64 * l.hb * l.kt) : 0;
+    const FewPrepArgs prep{c.e, c.T, l.nb, l.kt, c.H, rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out,
+                           ws + l.xf, ws + l.xtf, xf_chunks, xtf_chunks};
+    vocab_few_prep_kernel<T><<<(xf_chunks + xtf_chunks + 255) / 256, 256, 0, st>>>(prep, X, c.ldx);
+    const float* z = c.picked;
+    if (!c.grad || !c.e.teacher) {
+        float* zo = c.e.teacher ? c.picked_out : floats(l.z);
+        vocab_pick_kernel<T><<<(unsigned)(up((long)c.T * c.e.k, 4) / 4), 256, 0, st>>>(
+            c.e, c.T, c.V, c.H, c.alpha, X, c.ldx, W, c.ldw, zo);
+        z = zo;
+    }
+    if (c.grad)
+        vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
+            c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, floats(l.lse_c), floats(l.scale), floats(l.weight),
+            floats(l.value), D_WHOLE);
+    const int per = few_rows(NB);
+    int part = 0;
+    for (int p = 0; p < l.pieces; ++p) {
+        const int v0 = p * l.piece, vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
+        const T* Wp = W + (size_t)v0 * c.ldw;
+        const int groups = (int)up(vn, per) / per;
+        const FewArgs a{Wp, c.ldw, vn, c.H, ws + l.xf, count, c.alpha,
+                        (float2*)(ws + l.part) + (size_t)part * kFewTokens, floats(l.lse_c), floats(l.scale),
+                        floats(l.d), l.vp};
+        if (!c.grad) {
+            vocab_few_logits_kernel<T, NB, false><<<groups, 256, 0, st>>>(a);
+            part += groups;
+            continue;
+        }
+        vocab_few_logits_kernel<T, NB, true><<<groups, 256, 0, st>>>(a);
+        vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
+            c.e, c.T, v0, vn, pos, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
+        if (c.dX) {
+            const FewDxArgs x{Wp, c.ldw, vn, c.H, l.splits, count, floats(l.d), l.vp, floats(l.acc), (int)l.hp, p > 0};
+            vocab_few_dx_kernel<T, NB><<<dim3((unsigned)(l.hp / (16 * Ch::E)), l.splits), 256, 0, st>>>(x);
+        }
+        if (c.dW) {
+            // 256 vocabulary rows and as many hidden blocks as leave two workgroups a compute unit
+            const long row_groups = up(vn, 256) / 256;
+            const long cols = 512 / row_groups < 1 ? 1 : 512 / row_groups;
+            const int blocks = (int)((l.hb + cols - 1) / cols);
+            const int vec = c.H % 4 == 0 && c.lddw % 4 == 0 && (uintptr_t)c.dW % (4 * sizeof(T)) == 0;
+            const FewDwArgs w{ws + l.xtf, count, floats(l.d), l.vp, vn, c.H, blocks,
+                              (T*)c.dW + (size_t)v0 * c.lddw, c.lddw, vec};
+            vocab_few_dw_kernel<T, NB><<<dim3((unsigned)row_groups, (unsigned)((l.hb + blocks - 1) / blocks)), 256, 0,
+                                        st>>>(w);
+        }
+    }
+    if (!c.grad) {
+        vocab_loss_kernel<4><<<(unsigned)(up(c.T, 4) / 4), 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part,
+                                                              kFewTokens, z, c.loss, c.lse_out);
+    } else if (c.dX) {
+        const DxCut cut{1, 16 * NB, l.splits, l.splits};
+        vocab_dx_out_kernel<T, 1><<<c.T, 256, 0, st>>>(pos, count, c.H, floats(l.acc), cut, (int)l.hp,
+                                                       floats(l.weight), nullptr, nullptr, (T*)c.dX, c.lddx);
+    }
+    return (int)hipGetLastError();
+}
+
+template <typename T>
+int run_few(const Call& c) {
+    const FewLayout l = few_layout(sizeof(T) == 4, c.grad, c.T, c.V, c.H, c.e.k);
+    return l.nb == 1 ? run_few<T, 1>(c, l) : l.nb == 2 ? run_few<T, 2>(c, l) : run_few<T, 4>(c, l);
+}
+
 template <int P, class F>
 void by_size(bool big, F f) {
     if (big)
@@ -158,7 +285,7 @@ int run(const Call& c) {
     if (c.grad && c.T > 0)
         vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
             c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, floats(l.lse_c), floats(l.scale), floats(l.weight),
-            floats(l.value), P == 2);
+            floats(l.value), P == 2 ? D_APART : D_PACKED);
     // bf16 cross entropy multiplies dW with X times each token's weight (vocab_rows_kernel)
     char* const xs = P == 1 && c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
     vocab_pack_x_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, c.H, ws + l.x, x_pitch, l.hk,
@@ -226,7 +353,7 @@ int run(const Call& c) {
             });
     }
     if (!c.grad)
-        vocab_loss_kernel<<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
+        vocab_loss_kernel<32><<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
                                                       c.loss, c.lse_out);
     else if (c.T > 0 && c.dX)
         vocab_dx_out_kernel<T, P><<<c.T, 256, 0, st>>>(pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight),
@@ -235,6 +362,7 @@ int run(const Call& c) {
 }
 
 int dispatch(const Call& c) {
+    if (few(c.T)) return c.f32 ? run_few<float>(c) : run_few<__bf16>(c);
     return c.f32 ? run<float, 2>(c) : run<__bf16, 1>(c);
 }
 
@@ -275,6 +403,8 @@ long long vocab_workspace(int dtype, int grad, int T, int V, int H, int K) {
     int bad = 0;
     if (dtype != VOCAB_F32 && dtype != VOCAB_BF16) return -1;
     if (!libsgemm::vocab::sizes_ok(T, V, H, K > 0 ? K : 1, bad, pos) || K < 0) return K < 0 ? -6 : -bad;
+    if (libsgemm::vocab::few(T))
+        return libsgemm::vocab::few_layout(dtype == VOCAB_F32, grad != 0, T, V, H, K > 0 ? K : 1).bytes;
     return libsgemm::vocab::layout(dtype == VOCAB_F32 ? 2 : 1, grad != 0, T, V, H, K > 0 ? K : 1, K > 0).bytes;
 }
 

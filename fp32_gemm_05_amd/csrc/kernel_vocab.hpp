@@ -412,15 +412,16 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
 
 struct GradArgs {
     Operand w, x;
-    const int* count;
+    const int *count, *rows;       // the counted tokens
     const float *w_unit, *x_unit;  // P = 2, as in LseArgs
     const float* x_most;           // P = 2: the largest |weight * x_unit| of a counted token
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;
-    const float* lse;      // per counted token
-    const float* scale;    // per counted token: D = exp(z - lse) * scale
-    const float* weight;   // P = 2, per counted token: D's rows in dX and dW
-    char* d;               // [token][vocabulary piece], planes
+    const float *lse, *scale, *weight;  // per token: D = exp(z - lse) * scale; its weight in dX and dW
+    const long long* target;       // cross entropy: the entries that take `value`, per token
+    const float* value;
+    long long v0;                  // first vocabulary row of this piece
+    char* d;                       // [counted token][vocabulary piece], planes
     long d_pitch;
 };
 
@@ -446,12 +447,20 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
         const bool live = n < count;
-        const float lse = live ? a.lse[n] : 0.f;
-        float scale = live ? a.scale[n] : 0.f, alpha = a.alpha;
+        const int token = live ? a.rows[n] : 0;
+        const float lse = live ? a.lse[token] : 0.f;
+        float scale = live ? a.scale[token] : 0.f, alpha = a.alpha, value = 0.f;
+        int entry = -1;  // the target's place in this piece
+        if (a.target && live) {
+            const long long v = a.target[token] - a.v0;
+            entry = v >= 0 && v < a.vocab ? (int)v : -1;
+            value = a.value[token];
+        }
         if (T::kP == 2 && live) {
-            const float unit = a.x_unit[n];
+            const float unit = a.x_unit[n], f = d_factor(a.weight[token], unit, *a.x_most);
             alpha *= *a.w_unit * unit;
-            scale *= d_factor(a.weight[n], unit, *a.x_most);
+            scale *= f;
+            value *= f;
         }
         char* out = a.d + (size_t)n * a.d_pitch;
 #pragma unroll
@@ -466,8 +475,9 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
                         const int e = 4 * (g + f) + q;
                         // entries past the vocabulary and tokens past the count are the zeros that the
                         // products of D run over
-                        const float x = live && m0 + t.row(i, e) < a.vocab
-                                            ? __expf(t.acc[i][j][e] * alpha - lse) * scale : 0.f;
+                        const int m = m0 + t.row(i, e);
+                        float x = live && m < a.vocab ? __expf(t.acc[i][j][e] * alpha - lse) * scale : 0.f;
+                        x = m == entry ? value : x;
                         Half x_p[T::kP];
                         split<T::kP>(x, x_p);
 #pragma unroll
@@ -551,13 +561,11 @@ struct DwArgs {
     int tiles_m, tiles_n, hidden, vocab;
     void* out;         // [vocabulary piece][hidden] in the operands' type
     long ld;
-    int vec;           // rows hold whole aligned groups of four
 };
 
 template <class T>
 __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
     using O = typename std::conditional<T::kP == 1, __bf16, float>::type;
-    typedef O O4 __attribute__((ext_vector_type(4)));
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     int tm, tn;
     tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
@@ -575,16 +583,15 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const int m = m0 + t.row(i, 4 * g);
-                O4 v;
+                O v[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = (O)(t.acc[i][j][4 * g + q] * unit);
-                if (a.vec) {
-                    if (m < a.hidden) *(O4*)(out + m) = v;
-                } else {
+                if (m + 4 <= a.hidden)
+                    __builtin_memcpy(out + m, v, sizeof(v));  // at any alignment of O
+                else
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (m + q < a.hidden) out[m + q] = v[q];
-                }
             }
     }
 }

@@ -41,76 +41,87 @@ struct Chunk {
             if (i < n) v[i] = p[i];
         return v;
     }
-    static __device__ inline f32x4 mma(V a, V b, f32x4 c) {
-        if constexpr (sizeof(T) == 2) {
-            return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-        } else {
+    // A store of N consecutive values, at any alignment of T.
+    template <int N>
+    static __device__ inline void store(T* p, const T (&v)[N]) { __builtin_memcpy(p, v, N * sizeof(T)); }
+    // c[m][b] += a[m] b[b] over a step; the products of one c stand apart, none waits for the one before.
+    template <int M, int B>
+    static __device__ inline void mma(const V (&a)[M], const V (&b)[B], f32x4 (&c)[M][B]) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
-            return c;
-        }
+        for (int s = 0; s < (sizeof(T) == 2 ? 1 : 4); ++s)
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if constexpr (sizeof(T) == 2)
+                        c[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], c[i][j], 0, 0, 0);
+                    else
+                        c[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i][s], b[j][s], c[i][j], 0, 0, 0);
     }
 };
 
-// D's values as operands: fp32 as they are, or as bf16 high and low.
+// D's values as operands: fp32 as they are (PARTS 1), or as bf16 low and high.
 template <typename T>
 struct Wide {
-    typename Chunk<T>::V v[sizeof(T) == 2 ? 2 : 1];
-    __device__ inline void set(int i, float x) {
-        v[0][i] = (T)x;
-        if constexpr (sizeof(T) == 2) v[1][i] = __builtin_isfinite(x) ? (T)(x - (float)v[0][i]) : (T)0.f;
-    }
-    static __device__ inline f32x4 mma(typename Chunk<T>::V a, const Wide& b, f32x4 c) {
-        if constexpr (sizeof(T) == 2) c = Chunk<T>::mma(a, b.v[1], c);
-        return Chunk<T>::mma(a, b.v[0], c);
+    static constexpr int PARTS = sizeof(T) == 2 ? 2 : 1;
+    // Element i of the parts.
+    static __device__ inline void set(typename Chunk<T>::V (&v)[PARTS], int i, float x) {
+        const T high = (T)x;
+        v[PARTS - 1][i] = high;
+        if constexpr (PARTS == 2) v[0][i] = __builtin_isfinite(x) ? (T)(x - (float)high) : (T)0.f;
     }
 };
 
-struct FewPrepArgs {
-    Entries e;
-    int tokens, nb, kt, hidden;
-    int *rows, *pos, *count;
-    float *loss, *lse;  // forward: 0 for the tokens that do not count
-    char* xf;           // chunk (step * nb + b) * 64 + lane: token 16 b + lane % 16, hidden from step * STEP + lane / 16 * E
-    char* xtf;          // chunk (hb * kt + j) * 64 + lane: hidden 16 hb + lane % 16, tokens from j * STEP + lane / 16 * E
-    int xf_chunks, xtf_chunks;
+struct FewScanArgs {
+    TokenArgs t;
+    Counted c;
+    int nb, kt;
+    char* xf;   // chunk (step * nb + b) * 64 + lane: token 16 b + lane % 16, hidden from step * STEP + lane / 16 * E
+    char* xtf;  // chunk (hb * kt + j) * 64 + lane: hidden 16 hb + lane % 16, tokens from j * STEP + lane / 16 * E
+    int xf_chunks, xtf_chunks, chunk_blocks;
 };
 
-// Which of at most 64 tokens count, and their rows of X in the two orders of chunks above.
-template <typename T>
-__global__ void __launch_bounds__(256) vocab_few_prep_kernel(FewPrepArgs a, const T* x, long ldx) {
+// All that reads the inputs alone, in one launch: chunk_blocks workgroups put the counted tokens' rows
+// of X into the two orders of chunks above (each finds out by itself which count), the rest look at
+// four entries or tokens each.
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(256) vocab_few_scan_kernel(FewScanArgs a) {
     typedef Chunk<T> C;
+    if ((int)blockIdx.x >= a.chunk_blocks)
+        return token_wave<T, GRAD>(a.t, (long)(blockIdx.x - a.chunk_blocks) * 4 + (threadIdx.x >> 6));
     __shared__ int rows[kFewTokens], counted;
+    const Entries& e = a.t.e;
     if (threadIdx.x < 64) {
         const int t = threadIdx.x;
         bool live = false;
-        for (int k = 0; k < a.e.k && t < a.tokens && !live; ++k) live = a.e.counts(a.e.index[(size_t)t * a.e.ld + k]);
+        for (int k = 0; k < e.k && t < a.t.tokens && !live; ++k) live = e.counts(e.index[(size_t)t * e.ld + k]);
         const unsigned long long m = __ballot(live);
         const int at = __popcll(m & ((1ull << t) - 1));
         if (live) rows[at] = t;
         if (t == 0) counted = __popcll(m);
         if (blockIdx.x == 0) {
-            if (t < a.tokens) a.pos[t] = live ? at : -1;
-            if (live) a.rows[at] = t;
-            if (t == 0) *a.count = __popcll(m);
-            if (a.loss && t < a.tokens && !live) a.loss[t] = a.lse[t] = 0.f;
+            if (t < a.t.tokens) a.c.pos[t] = live ? at : -1;
+            if (live) a.c.rows[at] = t;
+            if (t == 0) *a.c.count = __popcll(m);
+            if (a.c.loss && t < a.t.tokens && !live) a.c.loss[t] = a.c.lse[t] = 0.f;
         }
     }
     __syncthreads();
     const int n = counted;
+    const T* x = (const T*)a.t.x;
     int i = blockIdx.x * 256 + threadIdx.x;
     typename C::V v = {};
     if (i < a.xf_chunks) {
         const int lane = i & 63, b = (i >> 6) % a.nb, step = (i >> 6) / a.nb;
         const int t = 16 * b + (lane & 15), k = step * C::STEP + (lane >> 4) * C::E;
-        if (t < n && k < a.hidden) v = C::load(x + rows[t] * ldx + k, a.hidden - k);
+        if (t < n && k < a.t.hidden) v = C::load(x + rows[t] * a.t.ldx + k, a.t.hidden - k);
         *(typename C::V*)(a.xf + 16L * i) = v;
     } else if ((i -= a.xf_chunks) < a.xtf_chunks) {
         const int lane = i & 63, j = (i >> 6) % a.kt, hb = (i >> 6) / a.kt;
         const int h = 16 * hb + (lane & 15), t = j * C::STEP + (lane >> 4) * C::E;
 #pragma unroll
         for (int q = 0; q < C::E; ++q)
-            if (t + q < n && h < a.hidden) v[q] = x[rows[t + q] * ldx + h];
+            if (t + q < n && h < a.t.hidden) v[q] = x[rows[t + q] * a.t.ldx + h];
         *(typename C::V*)(a.xtf + 16L * i) = v;
     }
 }
@@ -120,12 +131,15 @@ struct FewArgs {
     long ldw;
     int vocab, hidden;
     const char* xf;
-    const int* count;
+    const int *count, *rows;
     float alpha;
     float2* part;        // forward: [workgroup][kFewTokens]
-    const float* lse;    // gradient: per counted token
-    const float* scale;
-    float* d;            // gradient: [token][vp]
+    // gradient, as in GradArgs
+    const float *lse, *scale;
+    const i64* target;
+    const float* value;
+    i64 v0;
+    float* d;            // [counted token][vp]
     long vp;
 };
 
@@ -137,7 +151,10 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
     typedef Chunk<T> C;
     typedef typename C::V V;
     constexpr int MR = NB == 4 ? 4 : 2, U = NB == 4 ? 2 : 4;
-    __shared__ f32x4 sums[4][MR * NB][64];
+    // all loads before the first MFMA, where the compiler would keep too few in flight; the long fp32 runs
+    // of NB > 1 do better with loads between them
+    constexpr bool HOLD = sizeof(T) == 2 || NB == 1;
+    __shared__ f32x4 sums[4][NB][64];
     const int count = *a.count;
     if (count == 0) return;
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
@@ -153,71 +170,68 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[m][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int full = a.hidden / C::STEP;  // steps without an end of the rows
-    for (int s0 = wave * U; s0 < full; s0 += 4 * U) {
-        if (s0 + U <= full) {
-            V vw[U][MR], vx[U][NB];
+    const int groups = full / U;  // of U steps; this wave's are wave, wave + 4, ..
+    for (int q = wave; q < groups; q += 4) {
+        V vw[U][MR], vx[U][NB];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int m = 0; m < MR; ++m) {
+            const T* p = w[m] + (size_t)q * U * C::STEP;
 #pragma unroll
-                for (int m = 0; m < MR; ++m) vw[u][m] = C::load(w[m] + (size_t)(s0 + u) * C::STEP);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int b = 0; b < NB; ++b) vx[u][b] = xf[((s0 + u) * NB + b) * 64];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int m = 0; m < MR; ++m)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) acc[m][b] = C::mma(vw[u][m], vx[u][b], acc[m][b]);
-        } else {
-            for (int s = s0; s < full; ++s) {
-                V vw[MR];
-#pragma unroll
-                for (int m = 0; m < MR; ++m) vw[m] = C::load(w[m] + (size_t)s * C::STEP);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const V vx = xf[(s * NB + b) * 64];
-#pragma unroll
-                    for (int m = 0; m < MR; ++m) acc[m][b] = C::mma(vw[m], vx, acc[m][b]);
-                }
-            }
+            for (int u = 0; u < U; ++u) vw[u][m] = C::load(p + u * C::STEP);
         }
+        const V* x = xf + (size_t)q * U * NB * 64;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) vx[u][b] = x[(u * NB + b) * 64];
+        if (HOLD) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) C::mma(vw[u], vx[u], acc);
+    }
+    for (int s = groups * U + wave; s < full; s += 4) {
+        V vw[MR], vx[NB];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) vw[m] = C::load(w[m] + (size_t)s * C::STEP);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vx[b] = xf[(s * NB + b) * 64];
+        C::mma(vw, vx, acc);
     }
     if (full * C::STEP < a.hidden && wave == 3) {
         const int n = a.hidden - full * C::STEP - g * C::E;  // elements of this lane's chunk, maybe none
+        V vw[MR], vx[NB];
 #pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            const V vw = C::load(w[m] + (size_t)full * C::STEP, n);
+        for (int m = 0; m < MR; ++m) vw[m] = C::load(w[m] + (size_t)full * C::STEP, n);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[m][b] = C::mma(vw, xf[(full * NB + b) * 64], acc[m][b]);
-        }
+        for (int b = 0; b < NB; ++b) vx[b] = xf[(full * NB + b) * 64];
+        C::mma(vw, vx, acc);
     }
-#pragma unroll
-    for (int m = 0; m < MR; ++m)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) sums[wave][m * NB + b][lane] = acc[m][b];
-    __syncthreads();
-    if (wave >= NB) return;
-    // wave b: tokens 16 b + l, vocabulary rows r0 + 16 m + 4 g + i
-    const int n = 16 * wave + l;
+    // wave b gets the sums of tokens 16 b + l, vocabulary rows r0 + 16 m + 4 g + i
     f32x4 z[MR];
 #pragma unroll
     for (int m = 0; m < MR; ++m) {
-        z[m] = sums[0][m * NB + wave][lane];
+        if (m > 0) __syncthreads();
 #pragma unroll
-        for (int y = 1; y < 4; ++y) z[m] += sums[y][m * NB + wave][lane];
+        for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[m][b];
+        __syncthreads();
+        if (wave < NB) z[m] = sums[0][wave][lane] + sums[1][wave][lane] + sums[2][wave][lane] + sums[3][wave][lane];
     }
+    if (wave >= NB) return;
+    const int n = 16 * wave + l;
     if constexpr (GRAD) {
         const bool live = n < count;
-        const float lse = live ? a.lse[n] : 0.f, scale = live ? a.scale[n] : 0.f;
+        const int token = live ? a.rows[n] : 0;
+        const float lse = live ? a.lse[token] : 0.f, scale = live ? a.scale[token] : 0.f;
+        const i64 entry = a.target && live ? a.target[token] - a.v0 : -1;
+        const float value = a.target && live ? a.value[token] : 0.f;
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
             const int v = r0 + 16 * m + 4 * g;
             f32x4 d;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
                 d[i] = live && v + i < a.vocab ? __expf(z[m][i] * a.alpha - lse) * scale : 0.f;
+                if (v + i == entry && v + i < a.vocab) d[i] = value;
+            }
             *(f32x4*)(a.d + n * a.vp + v) = d;
         }
     } else {
@@ -254,7 +268,6 @@ struct FewDwArgs {
     int vocab, hidden, blocks;  // blocks of 16 hidden per workgroup
     void* out;
     long ld;
-    int vec;
 };
 
 // dW of 256 vocabulary rows, 64 a wave, and `blocks` blocks of 16 hidden: a wave holds D of its rows
@@ -263,13 +276,13 @@ template <typename T, int NB>
 __global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
     typedef Chunk<T> C;
     typedef typename C::V V;
-    typedef T T4 __attribute__((ext_vector_type(4)));
     constexpr int KT = (16 * NB + C::STEP - 1) / C::STEP;
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
     const int v0 = blockIdx.x * 256 + (threadIdx.x >> 6) * 64;
     if (v0 >= a.vocab) return;
     const int count = *a.count;
-    Wide<T> d[4][KT];
+    constexpr int PARTS = Wide<T>::PARTS;
+    V d[KT][4][PARTS];
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -277,27 +290,32 @@ __global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
 #pragma unroll
             for (int q = 0; q < C::E; ++q) {
                 const int t = j * C::STEP + g * C::E + q, v = v0 + 16 * b + l;
-                d[b][j].set(q, t < count && v < a.vocab ? a.d[t * a.vp + v] : 0.f);
+                Wide<T>::set(d[j][b], q, t < count && v < a.vocab ? a.d[t * a.vp + v] : 0.f);
             }
     const int h_end = imin((int)(blockIdx.y + 1) * a.blocks, (a.hidden + 15) / 16);
     for (int hb = blockIdx.y * a.blocks; hb < h_end; ++hb) {
-        V x[KT];
+        f32x4 c[1][4] = {};
 #pragma unroll
-        for (int j = 0; j < KT; ++j) x[j] = ((const V*)a.xtf)[(hb * KT + j) * 64 + lane];
+        for (int j = 0; j < KT; ++j) {
+            const V x[1] = {((const V*)a.xtf)[(hb * KT + j) * 64 + lane]};
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                const V y[4] = {d[j][0][p], d[j][1][p], d[j][2][p], d[j][3][p]};
+                C::mma(x, y, c);
+            }
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < KT; ++j) c = Wide<T>::mma(x[j], d[b][j], c);
             const int v = v0 + 16 * b + l, h = 16 * hb + 4 * g;
             if (v >= a.vocab) continue;
             T* out = (T*)a.out + (size_t)v * a.ld + h;
-            if (a.vec) {
-                if (h < a.hidden) *(T4*)out = T4{(T)c[0], (T)c[1], (T)c[2], (T)c[3]};
+            const T o[4] = {(T)c[0][b][0], (T)c[0][b][1], (T)c[0][b][2], (T)c[0][b][3]};
+            if (h + 4 <= a.hidden) {
+                C::store(out, o);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (h + i < a.hidden) out[i] = (T)c[i];
+                    if (h + i < a.hidden) out[i] = o[i];
             }
         }
     }
@@ -329,46 +347,62 @@ __global__ void __launch_bounds__(256) vocab_few_dx_kernel(FewDxArgs a) {
     const int h0 = blockIdx.x * 16 * E, h = h0 + l * E, n = a.hidden - h;
     const int steps = (a.vocab + C::STEP - 1) / C::STEP, z = blockIdx.y;
     const int first = (int)((long)steps * z / a.splits), last = (int)((long)steps * (z + 1) / a.splits);
-    f32x4 acc[NB][E];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[b][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int PARTS = Wide<T>::PARTS, U = 8 / E;
+    f32x4 acc[E][NB] = {};
     const T* w = (const T*)a.w + h;
-    for (int s = first + wave; s < last; s += 4) {
-        const int v = s * C::STEP + g * E;
-        V rows[E];
+    auto load = [&](int s0, V (&rows)[U][E], f32x4 (&x)[U][NB][E / 4]) {
+        // D is 0 past the vocabulary, where the last row stands in, but not past this part
 #pragma unroll
-        for (int q = 0; q < E; ++q) {
-            // D is 0 past the vocabulary, where the last row stands in
-            const T* p = w + (size_t)imin(v + q, a.vocab - 1) * a.ldw;
-            rows[q] = n >= E ? C::load(p) : C::load(p, n);
-        }
-        Wide<T> d[NB];
+        for (int u = 0; u < U; ++u) {
+            const int v = (s0 + u) * C::STEP + g * E;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const float* p = a.d + (16 * b + l) * a.vp + v;
-#pragma unroll
-            for (int q = 0; q < E; q += 4) {
-                const f32x4 x = *(const f32x4*)(p + q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[b].set(q + i, x[i]);
+            for (int q = 0; q < E; ++q) {
+                const T* p = w + (size_t)imin(v + q, a.vocab - 1) * a.ldw;
+                rows[u][q] = n >= E ? C::load(p) : C::load(p, n);
             }
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            V x;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int q = 0; q < E; ++q) x[q] = rows[q][e];
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) acc[b][e] = Wide<T>::mma(x, d[b], acc[b][e]);
+                for (int q = 0; q < E / 4; ++q)
+                    x[u][b][q] = s0 + u < last ? ((const f32x4*)(a.d + (16 * b + l) * a.vp + (s0 + u) * C::STEP + g * E))[q]
+                                               : f32x4{0.f, 0.f, 0.f, 0.f};
+        if (sizeof(T) == 2 || NB == 1) __builtin_amdgcn_sched_barrier(0);  // as above
+    };
+    auto multiply = [&](const V (&rows)[U][E], const f32x4 (&x)[U][NB][E / 4]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            V d[NB][PARTS], t[E];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int q = 0; q < E; ++q) Wide<T>::set(d[b], q, x[u][b][q / 4][q % 4]);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int q = 0; q < E; ++q) t[e][q] = rows[u][q][e];
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+                V y[NB];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) y[b] = d[b][p];
+                C::mma(t, y, acc);
+            }
         }
+    };
+    for (int s = first + wave * U; s < last; s += 4 * U) {
+        V rows[U][E];
+        f32x4 x[U][NB][E / 4];
+        load(s, rows, x);
+        multiply(rows, x);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         if (b > 0) __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; ++e) sums[wave][e][lane] = acc[b][e];
+        for (int e = 0; e < E; ++e) sums[wave][e][lane] = acc[e][b];
         __syncthreads();
         // element i of block e: token 16 b + l, hidden h0 + E * (4 g + i) + e
         float* out = a.acc + ((size_t)z * 16 * NB + 16 * b + l) * a.hp + h0 + E * 4 * g;

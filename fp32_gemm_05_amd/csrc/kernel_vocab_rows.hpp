@@ -24,27 +24,29 @@ struct Entries {
     __device__ bool counts(i64 v) const { return teacher ? v >= 0 : v != ignore; }
 };
 
-// rows[0 .. *count): the tokens that count, in order; pos: a token's place in rows, or -1.  One
-// workgroup walks the tokens, 8192 at a time so that their entries are read together.  loss and lse
-// (when given) of the others are 0.  Clears `zero` as well, the maxima that later kernels raise.
-__global__ void __launch_bounds__(1024) vocab_count_kernel(Entries e, int tokens, int* rows, int* pos, int* count,
-                                                           float* loss, float* lse, uint32_t* zero, int zeros) {
-    constexpr int R = 8;
-    __shared__ int waves[R][16];
+// rows[0 .. *count): the tokens that count, in order; pos: a token's place in rows, or -1; loss and
+// lse (when given) of the others 0.  By one workgroup of 256, 4096 tokens at a time so that their
+// entries are read together.
+struct Counted {
+    int *rows, *pos, *count;
+    float *loss, *lse;
+};
+__device__ inline void count_tokens(const Entries& e, int tokens, const Counted& c) {
+    constexpr int R = 16;
+    __shared__ int waves[R][4];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < zeros; i += 1024) zero[i] = 0;
     int done = 0;
-    for (int t0 = 0; t0 < tokens; t0 += 1024 * R) {
+    for (int t0 = 0; t0 < tokens; t0 += 256 * R) {
         bool live[R];
         unsigned long long m[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int t = t0 + r * 1024 + threadIdx.x;
+            const int t = t0 + r * 256 + threadIdx.x;
             live[r] = t < tokens && e.counts(e.index[(size_t)t * e.ld]);
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int t = t0 + r * 1024 + threadIdx.x;
+            const int t = t0 + r * 256 + threadIdx.x;
             if (t < tokens)
                 for (int k = 1; k < e.k && !live[r]; ++k) live[r] = e.counts(e.index[(size_t)t * e.ld + k]);
             m[r] = __ballot(live[r]);
@@ -54,21 +56,21 @@ __global__ void __launch_bounds__(1024) vocab_count_kernel(Entries e, int tokens
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             int before = done;
-            for (int w = 0; w < 16; ++w) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
                 before += w < wave ? waves[r][w] : 0;
                 done += waves[r][w];
             }
-            const int t = t0 + r * 1024 + threadIdx.x;
+            const int t = t0 + r * 256 + threadIdx.x;
             if (t >= tokens) continue;
             const int at = before + __popcll(m[r] & ((1ull << lane) - 1));
-            pos[t] = live[r] ? at : -1;
-            if (live[r]) rows[at] = t;
-            if (!live[r] && loss) loss[t] = 0.f;
-            if (!live[r] && lse) lse[t] = 0.f;
+            c.pos[t] = live[r] ? at : -1;
+            if (live[r]) c.rows[at] = t;
+            if (!live[r] && c.loss) c.loss[t] = c.lse[t] = 0.f;
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) *count = done;
+    if (threadIdx.x == 0) *c.count = done;
 }
 
 // N consecutive values, at any alignment of their type (gfx950 loads unaligned vectors).
@@ -112,134 +114,6 @@ __device__ inline float wave_max(float s) {
     return s;
 }
 
-// The largest finite |x|.
-__device__ inline float finite_max(float m, float x) { return __builtin_isfinite(x) ? fmaxf(m, fabsf(x)) : m; }
-template <int N>
-__device__ inline float block_max(float m) {
-    __shared__ float part[N / 64];
-    m = wave_max(m);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < N / 64; ++w) m = fmaxf(m, part[w]);
-    return m;
-}
-
-// The counted tokens' rows of X, packed: row i at dst + i * pitch, zero past the hidden size up to
-// kp, whole zero rows from the number of tokens to its next multiple of 256.
-//
-// P = 1: `scaled` (when given) gets the rows times weight[i].  P = 2: each row in its own power of
-// two, unit[i] what it is to be multiplied with; most (when given) the largest |weight| * unit.
-template <typename T, int P>
-__global__ void __launch_bounds__(256) vocab_pack_x_kernel(const T* src, long ld, const int* map, const int* count,
-                                                           int cols, char* dst, long pitch, int kp,
-                                                           const float* weight, char* scaled, float* unit,
-                                                           uint32_t* most) {
-    const int i = blockIdx.x, n = *count;
-    if (i >= (n + 255) / 256 * 256) return;
-    const T* s = i < n ? src + (size_t)map[i] * ld : nullptr;
-    float f = 1.f;
-    if constexpr (P == 2) {
-        if (s) {
-            float m = 0.f;
-            for (int k = threadIdx.x * 4; k < cols; k += 1024)
-                if (k + 4 <= cols) {
-                    float v[4];
-                    load(s + k, v);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
-                } else {
-                    for (int q = k; q < cols; ++q) m = finite_max(m, (float)s[q]);
-                }
-            const int e = scale_exponent(block_max<256>(m));
-            f = ldexpf(1.f, e);
-            if (threadIdx.x == 0) {
-                const float u = ldexpf(1.f, -e);
-                unit[i] = u;
-                const float w = most ? fabsf(weight[i] * u) : 0.f;
-                if (w > 0.f) atomicMax(most, __float_as_uint(w));
-            }
-        }
-    } else if (scaled && s) {
-        f = weight[i];
-    }
-    for (int k = threadIdx.x * 4; k < kp; k += 1024) {
-        float v[4] = {};
-        if (s && k + 4 <= cols)
-            load(s + k, v);
-        else if (s)
-            for (int q = 0; q < 4; ++q) v[q] = k + q < cols ? (float)s[k + q] : 0.f;
-        if constexpr (P == 1) {
-            store4<P>(dst + (size_t)i * pitch, k, v);
-            if (!scaled) continue;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] *= f;
-        store4<P>((P == 1 ? scaled : dst) + (size_t)i * pitch, k, v);
-    }
-}
-
-// The largest finite magnitude of a piece of W, as the bits of a float.
-template <typename T>
-__global__ void __launch_bounds__(256) vocab_max_kernel(const T* src, long ld, int rows, int cols, uint32_t* most) {
-    float m = 0.f;
-    const int lane = threadIdx.x & 63;
-    for (int r = blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4) {
-        const T* s = src + (size_t)r * ld;
-        int k = lane * 4;
-#pragma unroll 4
-        for (; k + 4 <= cols; k += 256) {
-            float v[4];
-            load(s + k, v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
-        }
-        for (; k < cols; ++k) m = finite_max(m, (float)s[k]);
-    }
-    m = block_max<256>(m);
-    if (threadIdx.x == 0 && m > 0.f) atomicMax(most, __float_as_uint(m));
-}
-
-// A piece of W packed, zero past the hidden size up to kp and from its rows to their next multiple
-// of 256; P = 2: in the power of two of its largest value, *unit what a packed unit stands for.
-template <typename T, int P>
-__global__ void __launch_bounds__(256) vocab_pack_w_kernel(const T* src, long ld, int rows, int cols, char* dst,
-                                                           long pitch, int kp, const uint32_t* most, float* unit) {
-    const int i = blockIdx.x;
-    const T* s = i < rows ? src + (size_t)i * ld : nullptr;
-    float f = 1.f;
-    if constexpr (P == 2) {
-        const int e = scale_exponent(__uint_as_float(*most));
-        f = ldexpf(1.f, e);
-        if (i == 0 && threadIdx.x == 0) *unit = ldexpf(1.f, -e);
-    }
-    for (int k = threadIdx.x * 4; k < kp; k += 1024) {
-        float v[4] = {};
-        if (s && k + 4 <= cols)
-            load(s + k, v);
-        else if (s)
-            for (int q = 0; q < 4; ++q) v[q] = k + q < cols ? (float)s[k + q] : 0.f;
-        if constexpr (P == 2)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] *= f;
-        store4<P>(dst + (size_t)i * pitch, k, v);
-    }
-}
-
-// z[t][k] = alpha * X[t] . W[index[t][k]], one wave each; 0 where there is no entry, NaN where an
-// entry lies past the vocabulary.
-template <typename T>
-__global__ void __launch_bounds__(256) vocab_pick_kernel(Entries e, int tokens, int vocab, int hidden, float alpha,
-                                                         const T* x, long ldx, const T* w, long ldw, float* z) {
-    const long i = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= (long)tokens * e.k) return;
-    const long t = i / e.k, k = i - t * e.k;
-    const i64 v = e.index[t * e.ld + k];
-    float s = 0.f;
-    if (e.counts(v)) s = v >= 0 && v < vocab ? alpha * wave_dot(x + t * ldx, w + (size_t)v * ldw, hidden) : NAN;
-    if ((threadIdx.x & 63) == 0) z[i] = s;
-}
-
 // The teacher's softmax over a token's entries, by one wave: maximum and log of the sum.
 __device__ inline void teacher_stats(const Entries& e, long t, float& top, float& log_total) {
     const int lane = threadIdx.x & 63;
@@ -253,6 +127,244 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
     for (int k = lane; k < e.k; k += 64)
         if (index[k] >= 0) s += expf(teacher[k] * e.teacher_alpha - top);
     log_total = logf(wave_sum(s));
+}
+
+// What a token's row of D is held in.
+//
+// Cross entropy: with s = alpha * dloss, p the softmax and c = 1 - p[target].  D_PACKED, D_APART: p / c
+// with -1 at the target, and s * c is X's weight in dW and the product's in dX.  The target's entry
+// carries most of the gradient: as -1 it is exact in bf16, where s * (p - 1) would be rounded.  c
+// comes from expm1, so a p close to 1 costs no digits; a c below 2^-25, where fp32 cannot tell p from
+// 1, is raised to it.
+//
+// Distillation: p, and p - (sum of q over the entries that name the same vocabulary row) at the
+// entries.  D_PACKED (bf16): times s, with X and the product as they are, so that dW's factors are
+// rounded once (D) and not twice; D_APART (fp32): s is the weight of X and the product.
+//
+// D_WHOLE, for few tokens, whose D is kept wide: both operators' rows are s * (p - y), weight 1.
+enum DForm { D_PACKED, D_APART, D_WHOLE };
+
+struct TokenArgs {
+    Entries e;
+    int tokens, vocab, hidden;
+    float alpha;
+    const void *x, *w;
+    long ldx, ldw;
+    float* z;                    // forward: [token][entry]
+    const float *lse, *dloss, *picked;
+    float *scale, *weight, *value;  // gradient, per token (value: per entry): D = exp(z - lse) * scale
+    DForm form;
+};
+
+// z[t][k] = alpha * X[t] . W[index[t][k]] by one wave; 0 where there is no entry, NaN where an entry
+// lies past the vocabulary.
+template <typename T>
+__device__ inline float entry_logit(const TokenArgs& a, long t, long k) {
+    const i64 v = a.e.index[t * a.e.ld + k];
+    if (!a.e.counts(v)) return 0.f;
+    if (v < 0 || v >= a.vocab) return NAN;
+    return a.alpha * wave_dot((const T*)a.x + t * a.ldx, (const T*)a.w + (size_t)v * a.ldw, a.hidden);
+}
+
+// The work of wave i: forward, the logit of one entry; gradient, one token's scale, weight, values.
+template <typename T, bool GRAD>
+__device__ inline void token_wave(const TokenArgs& a, long i) {
+    const int lane = threadIdx.x & 63;
+    const Entries& e = a.e;
+    if constexpr (!GRAD) {
+        if (i >= (long)a.tokens * e.k) return;
+        const float z = entry_logit<T>(a, i / e.k, i % e.k);
+        if (lane == 0) a.z[i] = z;
+    } else {
+        const long t = i;
+        if (t >= a.tokens) return;
+        const float s = a.alpha * a.dloss[t], l = a.lse[t];
+        float scale, weight;
+        if (!e.teacher) {
+            const i64 v = e.index[t * e.ld];
+            if (!e.counts(v)) return;
+            const float c = fmaxf(-expm1f(entry_logit<T>(a, t, 0) - l), 0x1p-25f);
+            const bool good = v >= 0 && v < a.vocab;
+            scale = !good ? NAN : a.form == D_WHOLE ? s : 1.f / c;
+            weight = !good ? NAN : a.form == D_WHOLE ? 1.f : s * c;
+            if (lane == 0) a.value[t] = a.form == D_WHOLE ? -s * c : -1.f;
+        } else {
+            bool good = true;
+            float top, log_total;
+            teacher_stats(e, t, top, log_total);
+            const i64* index = e.index + t * e.ld;
+            const float* teacher = e.teacher + t * e.ld_teacher;
+            for (int k = lane; k < e.k; k += 64) {
+                const i64 v = index[k];
+                float d = 0.f;
+                if (v >= 0) {
+                    good = good && v < a.vocab;
+                    float q = 0.f;
+                    for (int o = 0; o < e.k; ++o)
+                        if (index[o] == v) q += expf(teacher[o] * e.teacher_alpha - top - log_total);
+                    d = (a.form == D_APART ? 1.f : s) * (expf(a.picked[t * e.k + k] - l) - q);
+                }
+                a.value[t * e.k + k] = d;
+            }
+            scale = __all(good) ? (a.form == D_APART ? 1.f : s) : NAN;
+            weight = a.form == D_APART ? s : 1.f;
+        }
+        if (lane == 0) {
+            a.scale[t] = scale;
+            a.weight[t] = weight;
+        }
+    }
+}
+
+// The largest finite |x|.
+__device__ inline float finite_max(float m, float x) { return __builtin_isfinite(x) ? fmaxf(m, fabsf(x)) : m; }
+__device__ inline float block_max(float m) {  // of 256 threads
+    __shared__ float part[4];
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    return fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+}
+
+struct ScanArgs {
+    TokenArgs t;
+    Counted c;
+    int token_blocks;
+    float* w_part;    // max_blocks maxima of |W|'s finite values
+    int max_blocks;
+    uint32_t* x_most; // cleared for vocab_pack_kernel
+};
+
+// All that reads the inputs alone, in one launch: workgroup 0 counts, the next token_blocks look at
+// four entries or tokens each, the rest (fp32) at W's magnitude.
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
+    int b = blockIdx.x;
+    if (b == 0) {
+        if (threadIdx.x == 0) *a.x_most = 0;
+        count_tokens(a.t.e, a.t.tokens, a.c);
+        return;
+    }
+    b -= 1;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (b < a.token_blocks) return token_wave<T, GRAD>(a.t, (long)b * 4 + wave);
+    b -= a.token_blocks;
+    float m = 0.f;
+    for (int r = b * 4 + wave; r < a.t.vocab; r += a.max_blocks * 4) {
+        const T* s = (const T*)a.t.w + (size_t)r * a.t.ldw;
+        int k = lane * 4;
+#pragma unroll 4
+        for (; k + 4 <= a.t.hidden; k += 256) {
+            float v[4];
+            load(s + k, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
+        }
+        for (; k < a.t.hidden; ++k) m = finite_max(m, (float)s[k]);
+    }
+    m = block_max(m);
+    if (threadIdx.x == 0) a.w_part[b] = m;
+}
+
+// Four values of a row that has `cols`, zero past them (and where there is no row).
+template <typename T>
+__device__ inline void load_row(const T* s, int k, int cols, float (&v)[4]) {
+    if (s && k + 4 <= cols) return load(s + k, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = s && k + q < cols ? (float)s[k + q] : 0.f;
+}
+
+struct PackArgs {
+    int cols, kp;         // hidden size, and what it is padded to with zeros
+    long pitch;
+    // X: the counted tokens' rows, and zero rows to the next multiple of 256
+    const void* x;
+    long ldx;
+    const int *rows, *count;
+    int x_blocks;
+    char* x_out;
+    const float* weight;  // per token
+    char* scaled;         // P = 1, when wanted: the rows times their weight
+    float* x_unit;        // P = 2: each row in its own power of two, x_unit what a packed unit stands for
+    uint32_t* x_most;     // P = 2: the largest |weight| * x_unit, in a gradient's call (weight given)
+    // W: `vocab` rows, and zero rows to the next multiple of 256
+    const void* w;
+    long ldw;
+    int vocab;
+    char* w_out;
+    const float* w_part;  // P = 2: the power of two of its largest value
+    int w_parts;
+    float* w_unit;
+};
+constexpr int kPackRows = 8;  // of W by one workgroup
+
+template <typename T, int P>
+__device__ inline void pack_x(const PackArgs& a, int i) {
+    const int n = *a.count;
+    if (i >= (n + 255) / 256 * 256) return;
+    const int t = i < n ? a.rows[i] : 0;
+    const T* s = i < n ? (const T*)a.x + (size_t)t * a.ldx : nullptr;
+    float f = 1.f;
+    if constexpr (P == 2) {
+        if (s) {
+            float m = 0.f;
+            for (int k = threadIdx.x * 4; k < a.cols; k += 1024) {
+                float v[4];
+                load_row(s, k, a.cols, v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
+            }
+            const int e = scale_exponent(block_max(m));
+            f = ldexpf(1.f, e);
+            if (threadIdx.x == 0) {
+                const float u = ldexpf(1.f, -e);
+                a.x_unit[i] = u;
+                const float w = a.weight ? fabsf(a.weight[t] * u) : 0.f;
+                if (w > 0.f) atomicMax(a.x_most, __float_as_uint(w));  // a maximum: the order does not matter
+            }
+        }
+    } else if (a.scaled && s) {
+        f = a.weight[t];
+    }
+    for (int k = threadIdx.x * 4; k < a.kp; k += 1024) {
+        float v[4];
+        load_row(s, k, a.cols, v);
+        if constexpr (P == 1) {
+            store4<P>(a.x_out + (size_t)i * a.pitch, k, v);
+            if (!a.scaled) continue;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] *= f;
+        store4<P>((P == 1 ? a.scaled : a.x_out) + (size_t)i * a.pitch, k, v);
+    }
+}
+
+// The packed operands, in one launch: x_blocks workgroups take a row of X each, the rest kPackRows
+// rows of W.
+template <typename T, int P>
+__global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
+    if ((int)blockIdx.x < a.x_blocks) return pack_x<T, P>(a, blockIdx.x);
+    const int b = blockIdx.x - a.x_blocks;
+    float f = 1.f;
+    if constexpr (P == 2) {
+        float m = 0.f;
+        for (int i = threadIdx.x; i < a.w_parts; i += 256) m = fmaxf(m, a.w_part[i]);
+        const int e = scale_exponent(block_max(m));
+        f = ldexpf(1.f, e);
+        if (b == 0 && threadIdx.x == 0) *a.w_unit = ldexpf(1.f, -e);
+    }
+    for (int k = threadIdx.x * 4; k < a.kp; k += 1024) {
+#pragma unroll
+        for (int r = 0; r < kPackRows; ++r) {
+            const int i = b * kPackRows + r;
+            float v[4];
+            load_row(i < a.vocab ? (const T*)a.w + (size_t)i * a.ldw : nullptr, k, a.cols, v);
+            if constexpr (P == 2)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] *= f;
+            store4<P>(a.w_out + (size_t)i * a.pitch, k, v);
+        }
+    }
 }
 
 // lse of each counted token from its partial maxima and sums, then its loss.  A workgroup takes TX
@@ -321,69 +433,7 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
     }
 }
 
-enum DForm { D_PACKED, D_APART, D_WHOLE };
-
-// Per counted token what its row of D needs; one wave per token.
-//
-// Cross entropy: with s = alpha * dloss, p the softmax and c = 1 - p[target], row i of D is p / c
-// with -1 at the target, and X enters dW, and the product enters dX, times s * c.  The target's
-// entry carries most of the gradient: as -1 it is exact in bf16, where alpha * dloss * (p - 1)
-// would be rounded.  c comes from expm1, so a p close to 1 costs no digits; a c below 2^-25, where
-// fp32 cannot tell p from 1, is raised to it.
-//
-// Distillation: row i of D is p, and p - (sum of q over the entries that name the same vocabulary
-// row) at the entries.  bf16: times s, with X and the product as they are, so that dW's factors are
-// rounded once (D) and not twice; fp32 (D_APART): s enters with X and the product.
-//
-// D_WHOLE, for few tokens, whose D is kept wide: both operators' rows are s * (p - y), and X and the
-// product enter as they are.
-__global__ void __launch_bounds__(256) vocab_rows_kernel(Entries e, int tokens, int vocab, float alpha,
-                                                         const int* pos, const float* lse, const float* dloss,
-                                                         const float* z, float* lse_c, float* scale, float* out_scale,
-                                                         float* value, DForm form) {
-    const long t = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (t >= tokens) return;
-    const int i = pos[t];
-    if (i < 0) return;
-    const float s = alpha * dloss[t], l = lse[t];
-    float sc, os;
-    if (!e.teacher) {
-        const i64 v = e.index[t * e.ld];
-        const float c = fmaxf(-expm1f(z[t] - l), 0x1p-25f);
-        const bool good = v >= 0 && v < vocab;
-        sc = !good ? NAN : form == D_WHOLE ? s : 1.f / c;
-        os = !good ? NAN : form == D_WHOLE ? 1.f : s * c;
-        if (lane == 0) value[t] = form == D_WHOLE ? -s * c : -1.f;
-    } else {
-        bool good = true;
-        float top, log_total;
-        teacher_stats(e, t, top, log_total);
-        const i64* index = e.index + t * e.ld;
-        const float* teacher = e.teacher + t * e.ld_teacher;
-        for (int k = lane; k < e.k; k += 64) {
-            const i64 v = index[k];
-            float d = 0.f;
-            if (v >= 0) {
-                good = good && v < vocab;
-                float q = 0.f;
-                for (int o = 0; o < e.k; ++o)
-                    if (index[o] == v) q += expf(teacher[o] * e.teacher_alpha - top - log_total);
-                d = (form == D_APART ? 1.f : s) * (expf(z[t * e.k + k] - l) - q);
-            }
-            value[t * e.k + k] = d;
-        }
-        sc = __all(good) ? (form == D_APART ? 1.f : s) : NAN;
-        os = form == D_APART ? s : 1.f;
-    }
-    if (lane == 0) {
-        lse_c[i] = l;
-        scale[i] = sc;
-        out_scale[i] = os;
-    }
-}
-
-// Puts the entries' values into D where they fall into this piece (P = 0: a D in fp32).
+// Puts the values of a teacher's entries into D where they fall into this piece (P = 0: a D in fp32).
 template <int P>
 __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens, int v0, int vocab, const int* pos,
                                                           const float* value, const float* weight,
@@ -399,27 +449,41 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
         ((float*)(d + (size_t)i * d_pitch))[v - v0] = value[j];
         return;
     }
-    const float f = P == 2 ? d_factor(weight[i], x_unit[i], *x_most) : 1.f;
+    const float f = P == 2 ? d_factor(weight[t], x_unit[i], *x_most) : 1.f;
     store1<P == 2 ? 2 : 1>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
 }
 
-// dX of every token: the sum of its product's parts, or 0 where it does not count.
+// dX of every token: the sum of its product's parts, or 0 where it does not count.  A workgroup
+// takes 64 hidden of one token, its sixteen groups of threads every sixteenth part each.
 template <typename T, int P>
 __global__ void __launch_bounds__(256) vocab_dx_out_kernel(const int* pos, const int* count, int hidden,
                                                            const float* acc, DxCut cut, int hp, const float* weight,
                                                            const float* x_unit, const float* x_most, T* dx, long ld) {
+    __shared__ f32x4 part[16][16];
     const int t = blockIdx.x, i = pos[t], splits = cut.splits(*count);
     const size_t rows = cut.rows(*count);
-    float s = 0.f;
-    if (i >= 0) s = P == 1 ? weight[i] : *x_most / (x_unit[i] * kDScale);
-    for (int h = threadIdx.x * 4; h < hidden; h += 1024) {
-        f32x4 v = {};
-        if (i >= 0)
-            for (int z = 0; z < splits; ++z) v += *(const f32x4*)(acc + (z * rows + i) * hp + h);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (h + q < hidden) dx[(size_t)t * ld + h + q] = (T)(v[q] * s);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, h = blockIdx.y * 64 + tx * 4;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (i >= 0 && h < hidden)
+#pragma unroll 4
+        for (int z = ty; z < splits; z += 16) v += *(const f32x4*)(acc + (z * rows + i) * hp + h);
+    if (splits > 1) {
+        part[ty][tx] = v;
+        __syncthreads();
+        if (ty > 0) return;
+        for (int y = 1; y < 16; ++y) v += part[y][tx];
     }
+    if (ty > 0 || h >= hidden) return;
+    float s = 0.f;
+    if (i >= 0) s = P == 1 ? weight[t] : *x_most / (x_unit[i] * kDScale);
+    T o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = (T)(i < 0 ? 0.f : v[q] * s);
+    T* out = dx + (size_t)t * ld + h;
+    if (h + 4 <= hidden)
+        __builtin_memcpy(out, o, sizeof(o));
+    else
+        for (int q = 0; h + q < hidden; ++q) out[q] = o[q];
 }
 
 }  // namespace vocab

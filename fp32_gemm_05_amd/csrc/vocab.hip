@@ -49,9 +49,10 @@ struct Layout {
     int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces
     DxCut cut;
     bool dx_big;
-    long count, rows, pos, z, lse_c, scale, weight, x_unit, maxima, w_unit, value, x, xs, w, d, part, acc, bytes;
+    long count, rows, pos, z, scale, weight, x_unit, x_most, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
 };
 
+constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
 // Tile shapes: the large one when it fills the chip, else the small one.
@@ -102,12 +103,12 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     l.pos = take(4L * l.tp);
     if (!teacher) l.z = take(4L * l.tp);
     l.x_unit = take(4L * l.tp);
-    l.maxima = take(4L * (l.pieces + 1));
-    l.w_unit = take(4L * l.pieces);
+    l.x_most = take(4);
+    l.w_unit = take(4);
+    l.w_part = take(4L * kMaxBlocks);
     l.x = take(element * l.hk * l.tp);
     l.w = take(element * l.hk * l.piece);
     if (grad) {
-        l.lse_c = take(4L * l.tp);
         l.scale = take(4L * l.tp);
         l.weight = take(4L * l.tp);
         l.value = take(4L * T * K);
@@ -124,7 +125,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
 // At most kFewTokens tokens (kernel_vocab_few.hpp).  nb: blocks of 16 tokens.
 struct FewLayout {
     int nb, kt, piece, pieces, splits;
-    long steps, hb, hp, vp, count, rows, pos, z, lse_c, scale, weight, value, xf, xtf, d, part, acc, bytes;
+    long steps, hb, hp, vp, count, rows, pos, z, scale, weight, value, xf, xtf, d, part, acc, bytes;
 };
 
 int few_rows(int nb) { return nb == 4 ? 64 : 32; }  // vocabulary rows of a workgroup
@@ -141,8 +142,8 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     l.piece = (int)(vp < 1L << 21 ? vp : 1L << 21);
     l.pieces = (int)((vp + l.piece - 1) / l.piece);
     l.vp = l.piece;
-    // dX's pass over W in enough parts to fill the chip four times, each of 16 steps or more
-    const long strips = l.hp / (16 * e), most = l.vp / (4 * e) / 16;
+    // dX's pass over W in enough parts to fill the chip four times, each of 4 or 8 steps or more
+    const long strips = l.hp / (16 * e), most = l.vp / 128;
     const long s = 1024 / strips < most ? 1024 / strips : most;
     l.splits = (int)(s < 1 ? 1 : s);
     long at = 0;
@@ -157,7 +158,6 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     l.z = take(4 * kFewTokens);
     l.xf = take(1024 * l.steps * l.nb);
     if (grad) {
-        l.lse_c = take(4 * kFewTokens);
         l.scale = take(4 * kFewTokens);
         l.weight = take(4 * kFewTokens);
         l.value = take(4L * T * K);
@@ -173,60 +173,64 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
 
 bool few(int T) { return T > 0 && T <= kFewTokens; }
 
+TokenArgs token_args(const Call& c, char* ws, float* z, long scale, long weight, long value, DForm form) {
+    return {c.e, c.T, c.V, c.H, c.alpha, c.X, c.W, c.ldx, c.ldw, z, c.lse, c.dloss, c.picked,
+            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form};
+}
+// Workgroups of four waves for the entries (forward) or the tokens (gradient).
+unsigned token_blocks(const Call& c) { return (unsigned)(up(c.grad ? c.T : (long)c.T * c.e.k, 4) / 4); }
+
 template <typename T, int NB>
 int run_few(const Call& c, const FewLayout& l) {
     typedef Chunk<T> Ch;
     char* ws = c.work;
     auto floats = [&](long at) { return (float*)(ws + at); };
     int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
-    const T *X = (const T*)c.X, *W = (const T*)c.W;
+    const T* W = (const T*)c.W;
     const hipStream_t st = c.stream;
     (void)hipGetLastError();
 
     const int xf_chunks = (int)(64 * l.steps * l.nb), xtf_chunks = c.grad && c.dW ? (int)(64 * l.hb * l.kt) : 0;
-    const FewPrepArgs prep{c.e, c.T, l.nb, l.kt, c.H, rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out,
-                           ws + l.xf, ws + l.xtf, xf_chunks, xtf_chunks};
-    vocab_few_prep_kernel<T><<<(xf_chunks + xtf_chunks + 255) / 256, 256, 0, st>>>(prep, X, c.ldx);
-    const float* z = c.picked;
-    if (!c.grad || !c.e.teacher) {
-        float* zo = c.e.teacher ? c.picked_out : floats(l.z);
-        vocab_pick_kernel<T><<<(unsigned)(up((long)c.T * c.e.k, 4) / 4), 256, 0, st>>>(
-            c.e, c.T, c.V, c.H, c.alpha, X, c.ldx, W, c.ldw, zo);
-        z = zo;
-    }
+    const int chunk_blocks = (xf_chunks + xtf_chunks + 255) / 256;
+    float* const z = c.e.teacher ? c.picked_out : floats(l.z);
+    const FewScanArgs scan{token_args(c, ws, z, l.scale, l.weight, l.value, D_WHOLE),
+                           {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
+                           l.nb, l.kt, ws + l.xf, ws + l.xtf, xf_chunks, xtf_chunks, chunk_blocks};
     if (c.grad)
-        vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
-            c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, floats(l.lse_c), floats(l.scale), floats(l.weight),
-            floats(l.value), D_WHOLE);
+        vocab_few_scan_kernel<T, true><<<chunk_blocks + token_blocks(c), 256, 0, st>>>(scan);
+    else
+        vocab_few_scan_kernel<T, false><<<chunk_blocks + token_blocks(c), 256, 0, st>>>(scan);
     const int per = few_rows(NB);
     int part = 0;
     for (int p = 0; p < l.pieces; ++p) {
         const int v0 = p * l.piece, vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
         const T* Wp = W + (size_t)v0 * c.ldw;
         const int groups = (int)up(vn, per) / per;
-        const FewArgs a{Wp, c.ldw, vn, c.H, ws + l.xf, count, c.alpha,
-                        (float2*)(ws + l.part) + (size_t)part * kFewTokens, floats(l.lse_c), floats(l.scale),
-                        floats(l.d), l.vp};
+        const FewArgs a{Wp, c.ldw, vn, c.H, ws + l.xf, count, rows, c.alpha,
+                        (float2*)(ws + l.part) + (size_t)part * kFewTokens, c.lse, floats(l.scale),
+                        c.e.teacher ? nullptr : c.e.index, floats(l.value), v0, floats(l.d), l.vp};
         if (!c.grad) {
             vocab_few_logits_kernel<T, NB, false><<<groups, 256, 0, st>>>(a);
             part += groups;
             continue;
         }
         vocab_few_logits_kernel<T, NB, true><<<groups, 256, 0, st>>>(a);
-        vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-            c.e, c.T, v0, vn, pos, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
+        if (c.e.teacher)
+            vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
+                c.e, c.T, v0, vn, pos, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
         if (c.dX) {
             const FewDxArgs x{Wp, c.ldw, vn, c.H, l.splits, count, floats(l.d), l.vp, floats(l.acc), (int)l.hp, p > 0};
             vocab_few_dx_kernel<T, NB><<<dim3((unsigned)(l.hp / (16 * Ch::E)), l.splits), 256, 0, st>>>(x);
         }
         if (c.dW) {
-            // 256 vocabulary rows and as many hidden blocks as leave two workgroups a compute unit
+            // 256 vocabulary rows and as many hidden blocks as leave eight workgroups a compute unit, but
+            // eight blocks or more: a wave reads its rows' D first
             const long row_groups = up(vn, 256) / 256;
-            const long cols = 512 / row_groups < 1 ? 1 : 512 / row_groups;
-            const int blocks = (int)((l.hb + cols - 1) / cols);
-            const int vec = c.H % 4 == 0 && c.lddw % 4 == 0 && (uintptr_t)c.dW % (4 * sizeof(T)) == 0;
+            const long cols = 2048 / row_groups < 1 ? 1 : 2048 / row_groups;
+            const long even = (l.hb + cols - 1) / cols;
+            const int blocks = (int)(even < 8 ? 8 : even);
             const FewDwArgs w{ws + l.xtf, count, floats(l.d), l.vp, vn, c.H, blocks,
-                              (T*)c.dW + (size_t)v0 * c.lddw, c.lddw, vec};
+                              (T*)c.dW + (size_t)v0 * c.lddw, c.lddw};
             vocab_few_dw_kernel<T, NB><<<dim3((unsigned)row_groups, (unsigned)((l.hb + blocks - 1) / blocks)), 256, 0,
                                         st>>>(w);
         }
@@ -236,7 +240,7 @@ int run_few(const Call& c, const FewLayout& l) {
                                                               kFewTokens, z, c.loss, c.lse_out);
     } else if (c.dX) {
         const DxCut cut{1, 16 * NB, l.splits, l.splits};
-        vocab_dx_out_kernel<T, 1><<<c.T, 256, 0, st>>>(pos, count, c.H, floats(l.acc), cut, (int)l.hp,
+        vocab_dx_out_kernel<T, 1><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(pos, count, c.H, floats(l.acc), cut, (int)l.hp,
                                                        floats(l.weight), nullptr, nullptr, (T*)c.dX, c.lddx);
     }
     return (int)hipGetLastError();
@@ -263,54 +267,43 @@ int run(const Call& c) {
     char* ws = c.work;
     auto floats = [&](long at) { return (float*)(ws + at); };
     int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
-    float* const x_most = P == 2 ? floats(l.maxima) : nullptr;
-    float* const x_unit = floats(l.x_unit);
-    const T *X = (const T*)c.X, *W = (const T*)c.W;
+    float *const x_unit = floats(l.x_unit), *const x_most = floats(l.x_most), *const w_unit = floats(l.w_unit);
+    const T* W = (const T*)c.W;
     const hipStream_t st = c.stream;
     const long x_pitch = Pl::pitch(l.hk), d_pitch = Pl::pitch(l.piece);
     const int slabs = l.hk / Pl::BK;
-    (void)hipGetLastError();
-
-    vocab_count_kernel<<<1, 1024, 0, st>>>(c.e, c.T, rows, pos, count, c.grad ? nullptr : c.loss,
-                                           c.grad ? nullptr : c.lse_out, (uint32_t*)(ws + l.maxima),
-                                           P == 2 ? l.pieces + 1 : 0);
-    // the logits of the named entries
-    const float* z = c.picked;
-    if (c.T > 0 && (!c.grad || !c.e.teacher)) {
-        float* zo = c.e.teacher ? c.picked_out : floats(l.z);
-        vocab_pick_kernel<T><<<(unsigned)(up((long)c.T * c.e.k, 4) / 4), 256, 0, st>>>(
-            c.e, c.T, c.V, c.H, c.alpha, X, c.ldx, W, c.ldw, zo);
-        z = zo;
-    }
-    if (c.grad && c.T > 0)
-        vocab_rows_kernel<<<(unsigned)(up(c.T, 4) / 4), 256, 0, st>>>(
-            c.e, c.T, c.V, c.alpha, pos, c.lse, c.dloss, z, floats(l.lse_c), floats(l.scale), floats(l.weight),
-            floats(l.value), P == 2 ? D_APART : D_PACKED);
-    // bf16 cross entropy multiplies dW with X times each token's weight (vocab_rows_kernel)
-    char* const xs = P == 1 && c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
-    vocab_pack_x_kernel<T, P><<<l.tp, 256, 0, st>>>(X, c.ldx, rows, count, c.H, ws + l.x, x_pitch, l.hk,
-                                                    floats(l.weight), xs, x_unit,
-                                                    c.grad ? (uint32_t*)x_most : nullptr);
-    const Operand x{ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
-    const Operand x_dw{xs ? xs : ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
-    const Operand d{ws + l.d, (uint32_t)d_pitch, (uint32_t)d_pitch, l.tp};
     // W is read in place when its rows are whole aligned slabs, else packed piece by piece
     const bool direct = P == 1 && c.H % Pl::BK == 0 && c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 &&
                         c.ldw < (1L << 22);
+    // bf16 cross entropy multiplies dW with X times each token's weight
+    char* const xs = P == 1 && c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
+    (void)hipGetLastError();
+
+    float* const z = c.e.teacher ? c.picked_out : floats(l.z);
+    const int max_blocks = P == 2 ? (int)(up(c.V, 4) / 4 < kMaxBlocks ? up(c.V, 4) / 4 : kMaxBlocks) : 0;
+    const ScanArgs scan{token_args(c, ws, z, l.scale, l.weight, l.value, P == 2 ? D_APART : D_PACKED),
+                        {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
+                        (int)token_blocks(c), floats(l.w_part), max_blocks, (uint32_t*)x_most};
+    const unsigned scan_blocks = 1 + token_blocks(c) + max_blocks;
+    if (c.grad)
+        vocab_scan_kernel<T, true><<<scan_blocks, 256, 0, st>>>(scan);
+    else
+        vocab_scan_kernel<T, false><<<scan_blocks, 256, 0, st>>>(scan);
+    const Operand x{ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
+    const Operand x_dw{xs ? xs : ws + l.x, (uint32_t)x_pitch, (uint32_t)x_pitch, l.tp};
+    const Operand d{ws + l.d, (uint32_t)d_pitch, (uint32_t)d_pitch, l.tp};
     int part = 0;
     for (int p = 0; p < l.pieces; ++p) {
         const int v0 = p * l.piece, vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
         const T* Wp = W + (size_t)v0 * c.ldw;
-        float* const w_unit = floats(l.w_unit) + p;
         Operand w{(const char*)Wp, (uint32_t)(c.ldw * 2), (uint32_t)(c.H * 2), vn};
-        if (!direct) {
-            uint32_t* const most = (uint32_t*)(ws + l.maxima) + 1 + p;
-            if (P == 2)
-                vocab_max_kernel<T><<<(unsigned)(vn < 8192 ? up(vn, 4) / 4 : 2048), 256, 0, st>>>(Wp, c.ldw, vn, c.H,
-                                                                                                 most);
-            vocab_pack_w_kernel<T, P><<<(unsigned)up(vn, 256), 256, 0, st>>>(Wp, c.ldw, vn, c.H, ws + l.w, x_pitch,
-                                                                           l.hk, most, w_unit);
-            w = Operand{ws + l.w, (uint32_t)x_pitch, (uint32_t)x_pitch, (int)up(vn, 256)};
+        if (!direct) w = Operand{ws + l.w, (uint32_t)x_pitch, (uint32_t)x_pitch, (int)up(vn, 256)};
+        if (p == 0 || !direct) {
+            const int x_blocks = p == 0 ? l.tp : 0;
+            const PackArgs pack{c.H, l.hk, x_pitch, c.X, c.ldx, rows, count, x_blocks, ws + l.x,
+                                c.grad ? floats(l.weight) : nullptr, xs, x_unit, (uint32_t*)x_most,
+                                Wp, c.ldw, vn, ws + l.w, floats(l.w_part), max_blocks, w_unit};
+            vocab_pack_kernel<T, P><<<x_blocks + (direct ? 0 : (unsigned)up(vn, 256) / kPackRows), 256, 0, st>>>(pack);
         }
         if (c.T == 0) {
             // only dW, which is 0, is left to do
@@ -329,12 +322,14 @@ int run(const Call& c) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
                 const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-                const GradArgs a{w, x, count, w_unit, x_unit, x_most, tm, tn, slabs, vn, c.alpha, floats(l.lse_c),
-                                 floats(l.scale), floats(l.weight), ws + l.d, d_pitch};
+                const GradArgs a{w, x, count, rows, w_unit, x_unit, x_most, tm, tn, slabs, vn, c.alpha, c.lse,
+                                 floats(l.scale), floats(l.weight), c.e.teacher ? nullptr : c.e.index,
+                                 floats(l.value), v0, ws + l.d, d_pitch};
                 vocab_grad_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
-            vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-                c.e, c.T, v0, vn, pos, floats(l.value), floats(l.weight), x_unit, x_most, ws + l.d, d_pitch);
+            if (c.e.teacher)
+                vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
+                    c.e, c.T, v0, vn, pos, floats(l.value), floats(l.weight), x_unit, x_most, ws + l.d, d_pitch);
             if (c.dX)
                 by_size<P>(l.dx_big, [&](auto* shape) {
                     using S = typename std::remove_pointer<decltype(shape)>::type;
@@ -347,8 +342,7 @@ int run(const Call& c) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(vn, S::kBN) / S::kBN;
                 T* out = (T*)c.dW + (size_t)v0 * c.lddw;
-                const int vec = c.H % 4 == 0 && c.lddw % 4 == 0 && (uintptr_t)c.dW % (4 * sizeof(T)) == 0;
-                const DwArgs a{x_dw, d, count, x_most, tm, tn, c.H, vn, out, c.lddw, vec};
+                    const DwArgs a{x_dw, d, count, x_most, tm, tn, c.H, vn, out, c.lddw};
                 vocab_dw_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
     }
@@ -356,7 +350,7 @@ int run(const Call& c) {
         vocab_loss_kernel<32><<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
                                                       c.loss, c.lse_out);
     else if (c.T > 0 && c.dX)
-        vocab_dx_out_kernel<T, P><<<c.T, 256, 0, st>>>(pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight),
+        vocab_dx_out_kernel<T, P><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight),
                                                        x_unit, x_most, (T*)c.dX, c.lddx);
     return (int)hipGetLastError();
 }

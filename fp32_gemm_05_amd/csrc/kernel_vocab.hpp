@@ -572,26 +572,41 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
     const int m0 = tm * T::kBM, n0 = tn * T::kBN;
     T t;
     t.template run<K_COL, K_COL>(lds, a.x, m0, a.d, n0, 0, (*a.count + T::BK - 1) / T::BK);
+    // 16 bytes a lane, at any alignment of O: two groups of four bf16 after the lane halves have traded
+    // (as in vocab_grad_kernel), or one of fp32
+    constexpr int E = 16 / sizeof(O), F = E / 4;
+    typedef O Row __attribute__((ext_vector_type(E), aligned(sizeof(O))));
     const float unit = T::kP == 2 ? *a.x_most / kDScale : 1.f;
+    const int h = (threadIdx.x & 63) >> 5;
+    const bool whole = m0 + T::kBM <= a.hidden;
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
-        if (n >= a.vocab) continue;
         O* out = (O*)a.out + (size_t)n * a.ld;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int m = m0 + t.row(i, 4 * g);
-                O v[4];
+            for (int g = 0; g < 4; g += F) {
+                O v[4 * F];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = (O)(t.acc[i][j][4 * g + q] * unit);
-                if (m + 4 <= a.hidden)
-                    __builtin_memcpy(out + m, v, sizeof(v));  // at any alignment of O
-                else
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 4 * F; ++q) v[q] = (O)(t.acc[i][j][4 * g + q] * unit);
+                int m = m0 + t.row(i, 4 * g);
+                u32x4 x;
+                __builtin_memcpy(&x, v, 16);
+                if constexpr (F == 2) {
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
+                    x = u32x4{s0[0], s1[0], s0[1], s1[1]};
+                    m += 4 * h;
+                }
+                if (n >= a.vocab) continue;
+                if (whole || m + E <= a.hidden) {
+                    *(Row*)(out + m) = __builtin_bit_cast(Row, x);
+                } else {
+                    __builtin_memcpy(v, &x, 16);
+                    for (int q = 0; q < E; ++q)
                         if (m + q < a.hidden) out[m + q] = v[q];
+                }
             }
     }
 }

@@ -41,9 +41,13 @@ struct Chunk {
             if (i < n) v[i] = p[i];
         return v;
     }
-    // A store of N consecutive values, at any alignment of T.
-    template <int N>
-    static __device__ inline void store(T* p, const T (&v)[N]) { __builtin_memcpy(p, v, N * sizeof(T)); }
+    typedef T Row __attribute__((ext_vector_type(E), aligned(sizeof(T))));  // E values in memory, at any alignment
+    // dW's hidden: rows 4 g + i of the F blocks of a group are hidden 16 F * group + 4 F g + 4 f + i, so
+    // that a lane ends with E consecutive ones.
+    static constexpr int F = E / 4;
+    static __host__ __device__ constexpr int hidden_of(int hb, int row) {
+        return 16 * F * (hb / F) + 4 * F * (row >> 2) + 4 * (hb % F) + (row & 3);
+    }
     // c[m][b] += a[m] b[b] over a step; the products of one c stand apart, none waits for the one before.
     template <int M, int B>
     static __device__ inline void mma(const V (&a)[M], const V (&b)[B], f32x4 (&c)[M][B]) {
@@ -77,7 +81,7 @@ struct FewScanArgs {
     Counted c;
     int nb, kt;
     char* xf;   // chunk (step * nb + b) * 64 + lane: token 16 b + lane % 16, hidden from step * STEP + lane / 16 * E
-    char* xtf;  // chunk (hb * kt + j) * 64 + lane: hidden 16 hb + lane % 16, tokens from j * STEP + lane / 16 * E
+    char* xtf;  // chunk (hb * kt + j) * 64 + lane: hidden `hidden_of(hb, lane % 16)`, tokens from j * STEP + lane / 16 * E
     int xf_chunks, xtf_chunks, chunk_blocks;
 };
 
@@ -93,8 +97,7 @@ __global__ void __launch_bounds__(256) vocab_few_scan_kernel(FewScanArgs a) {
     const Entries& e = a.t.e;
     if (threadIdx.x < 64) {
         const int t = threadIdx.x;
-        bool live = false;
-        for (int k = 0; k < e.k && t < a.t.tokens && !live; ++k) live = e.counts(e.index[(size_t)t * e.ld + k]);
+        const bool live = t < a.t.tokens && any_entry(e, t, 0);
         const unsigned long long m = __ballot(live);
         const int at = __popcll(m & ((1ull << t) - 1));
         if (live) rows[at] = t;
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(256) vocab_few_scan_kernel(FewScanArgs a) {
         *(typename C::V*)(a.xf + 16L * i) = v;
     } else if ((i -= a.xf_chunks) < a.xtf_chunks) {
         const int lane = i & 63, j = (i >> 6) % a.kt, hb = (i >> 6) / a.kt;
-        const int h = 16 * hb + (lane & 15), t = j * C::STEP + (lane >> 4) * C::E;
+        const int h = C::hidden_of(hb, lane & 15), t = j * C::STEP + (lane >> 4) * C::E;
 #pragma unroll
         for (int q = 0; q < C::E; ++q)
             if (t + q < n && h < a.t.hidden) v[q] = x[rows[t + q] * a.t.ldx + h];
@@ -265,13 +268,14 @@ struct FewDwArgs {
     const int* count;
     const float* d;
     long vp;
-    int vocab, hidden, blocks;  // blocks of 16 hidden per workgroup
+    int vocab, hidden, groups;  // groups of 128 bytes of a row per workgroup
     void* out;
     long ld;
 };
 
-// dW of 256 vocabulary rows, 64 a wave, and `blocks` blocks of 16 hidden: a wave holds D of its rows
-// and passes over the hidden blocks; bound by the stores.
+// dW of 256 vocabulary rows, 64 a wave, and `groups` groups of 128 bytes along them: a wave holds D of
+// its rows and passes over the groups.  Bound by the stores, which leave in whole lines at once: lines
+// that stay open while the next operand is loaded are more than the L2 holds.
 template <typename T, int NB>
 __global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
     typedef Chunk<T> C;
@@ -292,30 +296,39 @@ __global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
                 const int t = j * C::STEP + g * C::E + q, v = v0 + 16 * b + l;
                 Wide<T>::set(d[j][b], q, t < count && v < a.vocab ? a.d[t * a.vp + v] : 0.f);
             }
-    const int h_end = imin((int)(blockIdx.y + 1) * a.blocks, (a.hidden + 15) / 16);
-    for (int hb = blockIdx.y * a.blocks; hb < h_end; ++hb) {
-        f32x4 c[1][4] = {};
+    constexpr int F = C::F, HB = 2 * F;  // blocks of a group
+    const int first = blockIdx.y * a.groups, last = imin(first + a.groups, (a.hidden + 16 * HB - 1) / (16 * HB));
+    for (int q = first; q < last; ++q) {
+        V x[KT][HB];
+        f32x4 c[HB][4] = {};
 #pragma unroll
-        for (int j = 0; j < KT; ++j) {
-            const V x[1] = {((const V*)a.xtf)[(hb * KT + j) * 64 + lane]};
+        for (int j = 0; j < KT; ++j)
+#pragma unroll
+            for (int f = 0; f < HB; ++f) x[j][f] = ((const V*)a.xtf)[((q * HB + f) * KT + j) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < KT; ++j)
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
                 const V y[4] = {d[j][0][p], d[j][1][p], d[j][2][p], d[j][3][p]};
-                C::mma(x, y, c);
+                C::mma(x[j], y, c);
             }
-        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const int v = v0 + 16 * b + l, h = 16 * hb + 4 * g;
+            const int v = v0 + 16 * b + l;
             if (v >= a.vocab) continue;
-            T* out = (T*)a.out + (size_t)v * a.ld + h;
-            const T o[4] = {(T)c[0][b][0], (T)c[0][b][1], (T)c[0][b][2], (T)c[0][b][3]};
-            if (h + 4 <= a.hidden) {
-                C::store(out, o);
-            } else {
+            T* out = (T*)a.out + (size_t)v * a.ld;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (h + i < a.hidden) out[i] = o[i];
+            for (int s = 0; s < 2; ++s) {
+                const int h = 16 * F * (2 * q + s) + C::E * g;
+                typename C::Row o;
+#pragma unroll
+                for (int i = 0; i < C::E; ++i) o[i] = (T)c[s * F + i / 4][b][i % 4];
+                if (h + C::E <= a.hidden)
+                    *(typename C::Row*)(out + h) = o;
+                else
+#pragma unroll
+                    for (int i = 0; i < C::E; ++i)
+                        if (h + i < a.hidden) out[h + i] = o[i];
             }
         }
     }

@@ -24,6 +24,15 @@ struct Entries {
     __device__ bool counts(i64 v) const { return teacher ? v >= 0 : v != ignore; }
 };
 
+// Whether a token has an entry among its from-th and later ones; eight are looked at at once.
+__device__ inline bool any_entry(const Entries& e, long t, int from) {
+    bool any = false;
+    for (int k = from; k < e.k && !any; k += 8)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) any |= e.counts(e.index[t * e.ld + imin(k + q, e.k - 1)]);
+    return any;
+}
+
 // rows[0 .. *count): the tokens that count, in order; pos: a token's place in rows, or -1; loss and
 // lse (when given) of the others 0.  By one workgroup of 256, 4096 tokens at a time so that their
 // entries are read together.
@@ -41,14 +50,14 @@ __device__ inline void count_tokens(const Entries& e, int tokens, const Counted&
         unsigned long long m[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            // past the end the last token again, so that no load stands behind a branch
             const int t = t0 + r * 256 + threadIdx.x;
-            live[r] = t < tokens && e.counts(e.index[(size_t)t * e.ld]);
+            live[r] = e.counts(e.index[(size_t)imin(t, tokens - 1) * e.ld]) && t < tokens;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int t = t0 + r * 256 + threadIdx.x;
-            if (t < tokens)
-                for (int k = 1; k < e.k && !live[r]; ++k) live[r] = e.counts(e.index[(size_t)t * e.ld + k]);
+            if (t < tokens && !live[r]) live[r] = any_entry(e, t, 1);
             m[r] = __ballot(live[r]);
             if (lane == 0) waves[r][wave] = __popcll(m[r]);
         }
@@ -453,35 +462,36 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
     store1<P == 2 ? 2 : 1>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
 }
 
-// dX of every token: the sum of its product's parts, or 0 where it does not count.  A workgroup
-// takes 64 hidden of one token, its sixteen groups of threads every sixteenth part each.
-template <typename T, int P>
+// dX of every token: the sum of its product's parts, or 0 where it does not count.  TY groups of
+// threads take every TY-th part each: 16 for few tokens, whose product has many parts, 1 for others.
+template <typename T, int P, int TY>
 __global__ void __launch_bounds__(256) vocab_dx_out_kernel(const int* pos, const int* count, int hidden,
                                                            const float* acc, DxCut cut, int hp, const float* weight,
                                                            const float* x_unit, const float* x_most, T* dx, long ld) {
-    __shared__ f32x4 part[16][16];
+    constexpr int TX = 256 / TY;
+    typedef T Row __attribute__((ext_vector_type(4), aligned(sizeof(T))));
     const int t = blockIdx.x, i = pos[t], splits = cut.splits(*count);
     const size_t rows = cut.rows(*count);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, h = blockIdx.y * 64 + tx * 4;
+    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, h = (blockIdx.y * TX + tx) * 4;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0 && h < hidden)
 #pragma unroll 4
-        for (int z = ty; z < splits; z += 16) v += *(const f32x4*)(acc + (z * rows + i) * hp + h);
-    if (splits > 1) {
+        for (int z = ty; z < splits; z += TY) v += *(const f32x4*)(acc + (z * rows + i) * hp + h);
+    if constexpr (TY > 1) {
+        __shared__ f32x4 part[TY][TX];
         part[ty][tx] = v;
         __syncthreads();
-        if (ty > 0) return;
-        for (int y = 1; y < 16; ++y) v += part[y][tx];
+        for (int y = 1; y < TY; ++y) v += part[y][tx];
     }
     if (ty > 0 || h >= hidden) return;
     float s = 0.f;
     if (i >= 0) s = P == 1 ? weight[t] : *x_most / (x_unit[i] * kDScale);
-    T o[4];
+    Row o;
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = (T)(i < 0 ? 0.f : v[q] * s);
     T* out = dx + (size_t)t * ld + h;
     if (h + 4 <= hidden)
-        __builtin_memcpy(out, o, sizeof(o));
+        *(Row*)out = o;
     else
         for (int q = 0; h + q < hidden; ++q) out[q] = o[q];
 }

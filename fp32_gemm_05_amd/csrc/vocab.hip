@@ -136,7 +136,7 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     l.nb = T > 32 ? 4 : T > 16 ? 2 : 1;
     l.kt = (int)up(16 * l.nb, 4 * e) / (4 * e);
     l.steps = up(H, 4 * e) / (4 * e);
-    l.hb = up(H, 16) / 16;
+    l.hb = up(H, 8 * e) / 16;  // dW's groups are 128 bytes of hidden
     l.hp = up(H, 16 * e);
     const long vp = up(V, 64);
     l.piece = (int)(vp < 1L << 21 ? vp : 1L << 21);
@@ -223,15 +223,15 @@ int run_few(const Call& c, const FewLayout& l) {
             vocab_few_dx_kernel<T, NB><<<dim3((unsigned)(l.hp / (16 * Ch::E)), l.splits), 256, 0, st>>>(x);
         }
         if (c.dW) {
-            // 256 vocabulary rows and as many hidden blocks as leave eight workgroups a compute unit, but
-            // eight blocks or more: a wave reads its rows' D first
-            const long row_groups = up(vn, 256) / 256;
+            // 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but four
+            // groups or more: a wave reads its rows' D first
+            const long row_groups = up(vn, 256) / 256, all = up(c.H, 8 * Ch::E) / (8 * Ch::E);
             const long cols = 2048 / row_groups < 1 ? 1 : 2048 / row_groups;
-            const long even = (l.hb + cols - 1) / cols;
-            const int blocks = (int)(even < 8 ? 8 : even);
-            const FewDwArgs w{ws + l.xtf, count, floats(l.d), l.vp, vn, c.H, blocks,
+            const long even = (all + cols - 1) / cols;
+            const int groups = (int)(even < 4 ? 4 : even);
+            const FewDwArgs w{ws + l.xtf, count, floats(l.d), l.vp, vn, c.H, groups,
                               (T*)c.dW + (size_t)v0 * c.lddw, c.lddw};
-            vocab_few_dw_kernel<T, NB><<<dim3((unsigned)row_groups, (unsigned)((l.hb + blocks - 1) / blocks)), 256, 0,
+            vocab_few_dw_kernel<T, NB><<<dim3((unsigned)row_groups, (unsigned)((all + groups - 1) / groups)), 256, 0,
                                         st>>>(w);
         }
     }
@@ -240,7 +240,7 @@ int run_few(const Call& c, const FewLayout& l) {
                                                               kFewTokens, z, c.loss, c.lse_out);
     } else if (c.dX) {
         const DxCut cut{1, 16 * NB, l.splits, l.splits};
-        vocab_dx_out_kernel<T, 1><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(pos, count, c.H, floats(l.acc), cut, (int)l.hp,
+        vocab_dx_out_kernel<T, 1, 16><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(pos, count, c.H, floats(l.acc), cut, (int)l.hp,
                                                        floats(l.weight), nullptr, nullptr, (T*)c.dX, c.lddx);
     }
     return (int)hipGetLastError();
@@ -349,9 +349,16 @@ int run(const Call& c) {
     if (!c.grad)
         vocab_loss_kernel<32><<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
                                                       c.loss, c.lse_out);
-    else if (c.T > 0 && c.dX)
-        vocab_dx_out_kernel<T, P><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight),
-                                                       x_unit, x_most, (T*)c.dX, c.lddx);
+    else if (c.T > 0 && c.dX) {
+        auto out = [&](auto kernel, long cols) {
+            kernel<<<dim3(c.T, (unsigned)(up(c.H, cols) / cols)), 256, 0, st>>>(
+                pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight), x_unit, x_most, (T*)c.dX, c.lddx);
+        };
+        if (c.T < 512)
+            out(vocab_dx_out_kernel<T, P, 16>, 64);
+        else
+            out(vocab_dx_out_kernel<T, P, 1>, 1024);
+    }
     return (int)hipGetLastError();
 }
 

@@ -2,8 +2,8 @@
 //
 // With few tokens every product is one pass over W (or dW): 2 * tokens / sizeof(W) operations a
 // byte.  So W goes from memory straight into the MFMA operands, whatever its alignment, with no
-// packing pass; the tokens' side, a few hundred KB at most, comes from the caches in the order in
-// which the lanes want it.  bf16 is multiplied with v_mfma_f32_16x16x32_bf16, fp32 with
+// packing pass; the tokens' side, a few hundred KB at most, comes from the caches.  Tokens that do not
+// count keep their place: their columns are computed and left out at the end.  bf16 is multiplied with v_mfma_f32_16x16x32_bf16, fp32 with
 // v_mfma_f32_16x16x4_f32: at 64 tokens the fp32 rate and the memory's are about even, below that
 // memory bounds both.  D is kept in fp32, and with bf16 operands enters its products as the sum of
 // two bf16 values (16 bits), which costs no time here.
@@ -76,75 +76,46 @@ struct Wide {
     }
 };
 
-struct FewScanArgs {
-    TokenArgs t;
-    Counted c;
-    int nb, kt;
-    char* xf;   // chunk (step * nb + b) * 64 + lane: token 16 b + lane % 16, hidden from step * STEP + lane / 16 * E
-    char* xtf;  // chunk (hb * kt + j) * 64 + lane: hidden `hidden_of(hb, lane % 16)`, tokens from j * STEP + lane / 16 * E
-    int xf_chunks, xtf_chunks, chunk_blocks;
-};
-
-// All that reads the inputs alone, in one launch: chunk_blocks workgroups put the counted tokens' rows
-// of X into the two orders of chunks above (each finds out by itself which count), the rest look at
-// four entries or tokens each.
+// Distillation's work on the entries, four waves a workgroup (token_wave).
 template <typename T, bool GRAD>
-__global__ void __launch_bounds__(256) vocab_few_scan_kernel(FewScanArgs a) {
-    typedef Chunk<T> C;
-    if ((int)blockIdx.x >= a.chunk_blocks)
-        return token_wave<T, GRAD>(a.t, (long)(blockIdx.x - a.chunk_blocks) * 4 + (threadIdx.x >> 6));
-    __shared__ int rows[kFewTokens], counted;
-    const Entries& e = a.t.e;
-    if (threadIdx.x < 64) {
-        const int t = threadIdx.x;
-        const bool live = t < a.t.tokens && any_entry(e, t, 0);
-        const unsigned long long m = __ballot(live);
-        const int at = __popcll(m & ((1ull << t) - 1));
-        if (live) rows[at] = t;
-        if (t == 0) counted = __popcll(m);
-        if (blockIdx.x == 0) {
-            if (t < a.t.tokens) a.c.pos[t] = live ? at : -1;
-            if (live) a.c.rows[at] = t;
-            if (t == 0) *a.c.count = __popcll(m);
-            if (a.c.loss && t < a.t.tokens && !live) a.c.loss[t] = a.c.lse[t] = 0.f;
-        }
-    }
-    __syncthreads();
-    const int n = counted;
-    const T* x = (const T*)a.t.x;
-    int i = blockIdx.x * 256 + threadIdx.x;
-    typename C::V v = {};
-    if (i < a.xf_chunks) {
-        const int lane = i & 63, b = (i >> 6) % a.nb, step = (i >> 6) / a.nb;
-        const int t = 16 * b + (lane & 15), k = step * C::STEP + (lane >> 4) * C::E;
-        if (t < n && k < a.t.hidden) v = C::load(x + rows[t] * a.t.ldx + k, a.t.hidden - k);
-        *(typename C::V*)(a.xf + 16L * i) = v;
-    } else if ((i -= a.xf_chunks) < a.xtf_chunks) {
-        const int lane = i & 63, j = (i >> 6) % a.kt, hb = (i >> 6) / a.kt;
-        const int h = C::hidden_of(hb, lane & 15), t = j * C::STEP + (lane >> 4) * C::E;
-#pragma unroll
-        for (int q = 0; q < C::E; ++q)
-            if (t + q < n && h < a.t.hidden) v[q] = x[rows[t + q] * a.t.ldx + h];
-        *(typename C::V*)(a.xtf + 16L * i) = v;
-    }
+__global__ void __launch_bounds__(256) vocab_few_token_kernel(TokenArgs a) {
+    token_wave<T, GRAD>(a, (long)blockIdx.x * 4 + (threadIdx.x >> 6));
 }
 
 struct FewArgs {
-    const void* w;
-    long ldw;
-    int vocab, hidden;
-    const char* xf;
-    const int *count, *rows;
+    Entries e;
+    int tokens;
+    const void *x, *w;
+    long ldx, ldw;
+    int vocab, hidden, groups;  // of this piece; workgroups for its logits
+    int whole_vocab;
     float alpha;
-    float2* part;        // forward: [workgroup][kFewTokens]
-    // gradient, as in GradArgs
-    const float *lse, *scale;
-    const i64* target;
-    const float* value;
-    i64 v0;
-    float* d;            // [counted token][vp]
+    i64 v0;                     // first vocabulary row of this piece
+    float2* part;               // forward: [workgroup][kFewTokens]
+    float* z;                   // forward, cross entropy: the target's logit
+    // gradient, per token: D = exp(z - lse) * scale; cross entropy: scale = alpha * dloss
+    const float *lse, *dloss, *scale;
+    float* d;                   // [token][vp]
     long vp;
+    // gradient, dW wanted, first piece: X in the order in which dW's product takes it, chunk
+    // (hb * kt + j) * 64 + lane: hidden_of(hb, lane % 16), tokens from j * STEP + lane / 16 * E
+    char* xtf;
+    int kt, xtf_chunks;
 };
+
+// One chunk of xtf; the tokens that do not count are zeros.
+template <typename T>
+__device__ inline void few_transpose(const FewArgs& a, int i) {
+    typedef Chunk<T> C;
+    if (i >= a.xtf_chunks) return;
+    const int lane = i & 63, j = (i >> 6) % a.kt, hb = (i >> 6) / a.kt;
+    const int h = C::hidden_of(hb, lane & 15), t = j * C::STEP + (lane >> 4) * C::E;
+    typename C::V v = {};
+#pragma unroll
+    for (int q = 0; q < C::E; ++q)
+        if (t + q < a.tokens && h < a.hidden && any_entry(a.e, t + q, 0)) v[q] = ((const T*)a.x)[(t + q) * a.ldx + h];
+    *(typename C::V*)(a.xtf + 16L * i) = v;
+}
 
 // z of 16 MR vocabulary rows and all tokens.  The four waves of a workgroup take every fourth U steps
 // of the hidden size each, so that even a small vocabulary keeps many loads in flight, and add up in
@@ -158,15 +129,17 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
     // of NB > 1 do better with loads between them
     constexpr bool HOLD = sizeof(T) == 2 || NB == 1;
     __shared__ f32x4 sums[4][NB][64];
-    const int count = *a.count;
-    if (count == 0) return;
+    if (GRAD && (int)blockIdx.x >= a.groups)
+        return few_transpose<T>(a, ((int)blockIdx.x - a.groups) * 256 + (int)threadIdx.x);
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
     const int wave = (int)uniform_u32(threadIdx.x >> 6);
     const int r0 = blockIdx.x * 16 * MR;
     const T* w[MR];
 #pragma unroll
     for (int m = 0; m < MR; ++m) w[m] = (const T*)a.w + (size_t)imin(r0 + 16 * m + l, a.vocab - 1) * a.ldw + g * C::E;
-    const V* xf = (const V*)a.xf + lane;
+    const T* x[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x[b] = (const T*)a.x + imin(16 * b + l, a.tokens - 1) * a.ldx + g * C::E;
     f32x4 acc[MR][NB];
 #pragma unroll
     for (int m = 0; m < MR; ++m)
@@ -182,11 +155,12 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
 #pragma unroll
             for (int u = 0; u < U; ++u) vw[u][m] = C::load(p + u * C::STEP);
         }
-        const V* x = xf + (size_t)q * U * NB * 64;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int b = 0; b < NB; ++b) {
+            const T* p = x[b] + (size_t)q * U * C::STEP;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) vx[u][b] = x[(u * NB + b) * 64];
+            for (int u = 0; u < U; ++u) vx[u][b] = C::load(p + u * C::STEP);
+        }
         if (HOLD) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; ++u) C::mma(vw[u], vx[u], acc);
@@ -196,7 +170,7 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
 #pragma unroll
         for (int m = 0; m < MR; ++m) vw[m] = C::load(w[m] + (size_t)s * C::STEP);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) vx[b] = xf[(s * NB + b) * 64];
+        for (int b = 0; b < NB; ++b) vx[b] = C::load(x[b] + (size_t)s * C::STEP);
         C::mma(vw, vx, acc);
     }
     if (full * C::STEP < a.hidden && wave == 3) {
@@ -205,7 +179,7 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
 #pragma unroll
         for (int m = 0; m < MR; ++m) vw[m] = C::load(w[m] + (size_t)full * C::STEP, n);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) vx[b] = xf[(full * NB + b) * 64];
+        for (int b = 0; b < NB; ++b) vx[b] = C::load(x[b] + (size_t)full * C::STEP, n);
         C::mma(vw, vx, acc);
     }
     // wave b gets the sums of tokens 16 b + l, vocabulary rows r0 + 16 m + 4 g + i
@@ -220,20 +194,30 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
     }
     if (wave >= NB) return;
     const int n = 16 * wave + l;
+    if (n >= a.tokens && !GRAD) return;
+    const bool live = n < a.tokens && any_entry(a.e, n, 0);
+    // cross entropy: the target's row of this piece, or a row that none has
+    i64 entry = -1;
+    if (!a.e.teacher && live) {
+        entry = a.e.index[n] - a.v0;
+        if (entry < 0 || entry >= a.vocab) entry = -1;
+    }
     if constexpr (GRAD) {
-        const bool live = n < count;
-        const int token = live ? a.rows[n] : 0;
-        const float lse = live ? a.lse[token] : 0.f, scale = live ? a.scale[token] : 0.f;
-        const i64 entry = a.target && live ? a.target[token] - a.v0 : -1;
-        const float value = a.target && live ? a.value[token] : 0.f;
+        float lse = 0.f, scale = 0.f;
+        if (live) {
+            lse = a.lse[n];
+            scale = a.e.teacher ? a.scale[n] : a.alpha * a.dloss[n];
+            // a target outside the vocabulary: NaN, as its loss is
+            if (!a.e.teacher && (a.e.index[n] < 0 || a.e.index[n] >= a.whole_vocab)) scale = NAN;
+        }
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
             const int v = r0 + 16 * m + 4 * g;
             f32x4 d;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                d[i] = live && v + i < a.vocab ? __expf(z[m][i] * a.alpha - lse) * scale : 0.f;
-                if (v + i == entry && v + i < a.vocab) d[i] = value;
+                const float y = z[m][i] * a.alpha - lse;
+                d[i] = live && v + i < a.vocab ? (v + i == entry ? expm1f(y) : __expf(y)) * scale : 0.f;
             }
             *(f32x4*)(a.d + n * a.vp + v) = d;
         }
@@ -246,6 +230,7 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
                 const float x = r0 + 16 * m + 4 * g + i < a.vocab ? z[m][i] * a.alpha : -INFINITY;
                 z[m][i] = x;
                 top = x > top || x != x ? x : top;  // a NaN stays
+                if (r0 + 16 * m + 4 * g + i == entry) a.z[n] = x;
             }
 #pragma unroll
         for (int o = 16; o < 64; o *= 2) {
@@ -263,12 +248,19 @@ __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
     }
 }
 
-struct FewDwArgs {
-    const char* xtf;
-    const int* count;
+struct FewGradArgs {
     const float* d;
     long vp;
-    int vocab, hidden, groups;  // groups of 128 bytes of a row per workgroup
+    int tokens, vocab, hidden;
+    // dX: `strips` of 16 E hidden, each in `splits` parts of the vocabulary
+    const void* w;
+    long ldw;
+    int strips, splits;
+    float* acc;  // [splits][16 NB][hp]
+    int hp, add;
+    // dW: workgroups of 256 vocabulary rows by `groups` groups of 128 bytes of them
+    const char* xtf;
+    int groups, row_groups;
     void* out;
     long ld;
 };
@@ -277,14 +269,13 @@ struct FewDwArgs {
 // its rows and passes over the groups.  Bound by the stores, which leave in whole lines at once: lines
 // that stay open while the next operand is loaded are more than the L2 holds.
 template <typename T, int NB>
-__global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
+__device__ inline void few_dw(const FewGradArgs& a, int block) {
     typedef Chunk<T> C;
     typedef typename C::V V;
     constexpr int KT = (16 * NB + C::STEP - 1) / C::STEP;
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-    const int v0 = blockIdx.x * 256 + (threadIdx.x >> 6) * 64;
+    const int v0 = block % a.row_groups * 256 + (threadIdx.x >> 6) * 64;
     if (v0 >= a.vocab) return;
-    const int count = *a.count;
     constexpr int PARTS = Wide<T>::PARTS;
     V d[KT][4][PARTS];
 #pragma unroll
@@ -294,10 +285,10 @@ __global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
 #pragma unroll
             for (int q = 0; q < C::E; ++q) {
                 const int t = j * C::STEP + g * C::E + q, v = v0 + 16 * b + l;
-                Wide<T>::set(d[j][b], q, t < count && v < a.vocab ? a.d[t * a.vp + v] : 0.f);
+                Wide<T>::set(d[j][b], q, t < a.tokens && v < a.vocab ? a.d[t * a.vp + v] : 0.f);
             }
     constexpr int F = C::F, HB = 2 * F;  // blocks of a group
-    const int first = blockIdx.y * a.groups, last = imin(first + a.groups, (a.hidden + 16 * HB - 1) / (16 * HB));
+    const int first = block / a.row_groups * a.groups, last = imin(first + a.groups, (a.hidden + 16 * HB - 1) / (16 * HB));
     for (int q = first; q < last; ++q) {
         V x[KT][HB];
         f32x4 c[HB][4] = {};
@@ -334,31 +325,19 @@ __global__ void __launch_bounds__(256) vocab_few_dw_kernel(FewDwArgs a) {
     }
 }
 
-struct FewDxArgs {
-    const void* w;
-    long ldw;
-    int vocab, hidden, splits;
-    const int* count;
-    const float* d;
-    long vp;
-    float* acc;  // [splits][16 NB][hp]
-    int hp, add;
-};
-
 // dX of 16 E hidden over a part of the vocabulary.  A lane's chunks are E consecutive hidden of E
 // rows of W; element e of the chunks makes the operand of the e-th 16 hidden, h0 + E * (lane % 16) + e.
 // The four waves take every fourth step of the part and add up in LDS.
 template <typename T, int NB>
-__global__ void __launch_bounds__(256) vocab_few_dx_kernel(FewDxArgs a) {
+__device__ inline void few_dx(const FewGradArgs& a, int block) {
     typedef Chunk<T> C;
     typedef typename C::V V;
     constexpr int E = C::E;
     __shared__ f32x4 sums[4][E][64];
-    if (*a.count == 0) return;
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
     const int wave = (int)uniform_u32(threadIdx.x >> 6);
-    const int h0 = blockIdx.x * 16 * E, h = h0 + l * E, n = a.hidden - h;
-    const int steps = (a.vocab + C::STEP - 1) / C::STEP, z = blockIdx.y;
+    const int h0 = block % a.strips * 16 * E, h = h0 + l * E, n = a.hidden - h;
+    const int steps = (a.vocab + C::STEP - 1) / C::STEP, z = block / a.strips;
     const int first = (int)((long)steps * z / a.splits), last = (int)((long)steps * (z + 1) / a.splits);
     constexpr int PARTS = Wide<T>::PARTS, U = 8 / E;
     f32x4 acc[E][NB] = {};
@@ -431,6 +410,16 @@ __global__ void __launch_bounds__(256) vocab_few_dx_kernel(FewDxArgs a) {
             }
         }
     }
+}
+
+// Both gradients' products, in one launch: they need D alone.  strips = 0: no dX.
+template <typename T, int NB>
+__global__ void __launch_bounds__(256) vocab_few_grad_kernel(FewGradArgs a) {
+    const int dx = a.strips * a.splits;
+    if ((int)blockIdx.x < dx)
+        few_dx<T, NB>(a, blockIdx.x);
+    else
+        few_dw<T, NB>(a, (int)blockIdx.x - dx);
 }
 
 }  // namespace vocab

@@ -150,7 +150,8 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
 // entries.  D_PACKED (bf16): times s, with X and the product as they are, so that dW's factors are
 // rounded once (D) and not twice; D_APART (fp32): s is the weight of X and the product.
 //
-// D_WHOLE, for few tokens, whose D is kept wide: both operators' rows are s * (p - y), weight 1.
+// D_WHOLE, for few tokens, whose D is kept wide: s * (p - y), weight 1 (only distillation's is made
+// here).
 enum DForm { D_PACKED, D_APART, D_WHOLE };
 
 struct TokenArgs {
@@ -194,9 +195,9 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
             if (!e.counts(v)) return;
             const float c = fmaxf(-expm1f(entry_logit<T>(a, t, 0) - l), 0x1p-25f);
             const bool good = v >= 0 && v < a.vocab;
-            scale = !good ? NAN : a.form == D_WHOLE ? s : 1.f / c;
-            weight = !good ? NAN : a.form == D_WHOLE ? 1.f : s * c;
-            if (lane == 0) a.value[t] = a.form == D_WHOLE ? -s * c : -1.f;
+            scale = good ? 1.f / c : NAN;
+            weight = good ? s * c : NAN;
+            if (lane == 0) a.value[t] = -1.f;
         } else {
             bool good = true;
             float top, log_total;
@@ -378,14 +379,15 @@ __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
 
 // lse of each counted token from its partial maxima and sums, then its loss.  A workgroup takes TX
 // tokens, TY threads each: once through the maxima, once through the sums, so that no load waits
-// for an exponential.
+// for an exponential.  rows null: a token's partials stand at its own place, whether it counts or
+// not, and z of a target that names no row of the vocabulary has not been written.
 template <int TX>
-__global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* rows, const int* count,
-                                                          const float2* part, int parts, int tp, const float* z,
-                                                          float* loss, float* lse) {
+__global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* rows, const int* count, int tokens,
+                                                          int vocab, const float2* part, int parts, int tp,
+                                                          const float* z, float* loss, float* lse) {
     constexpr int TY = 1024 / TX;
     __shared__ float slot[16][TX], lses[TX];
-    const int n = *count, tx = threadIdx.x % TX, ty = threadIdx.x / TX, i0 = blockIdx.x * TX, i = i0 + tx;
+    const int n = rows ? *count : tokens, tx = threadIdx.x % TX, ty = threadIdx.x / TX, i0 = blockIdx.x * TX, i = i0 + tx;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (i0 >= n) return;
     const auto larger = [](float a, float b) { return b > a || b != b ? b : a; };  // a NaN stays
@@ -416,17 +418,25 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
 #pragma unroll
         for (int y = 0; y < 16; ++y) sum += slot[y][tx];
         const float l = top + logf(sum);
-        const int t = rows[i];
+        const int t = rows ? rows[i] : i;
+        const bool live = rows || any_entry(e, t, 0);
         lses[tx] = l;
-        lse[t] = l;
-        if (!e.teacher) loss[t] = l - z[t];
+        lse[t] = live ? l : 0.f;
+        if (!e.teacher) {
+            const bool named = rows || (e.index[t] >= 0 && e.index[t] < vocab);
+            loss[t] = !live ? 0.f : named ? l - z[t] : NAN;
+        }
     }
     if (!e.teacher) return;
     __syncthreads();
     for (int y = wave; y < TX; y += 16) {
         if (i0 + y >= n) break;
-        const int t = rows[i0 + y];
+        const int t = rows ? rows[i0 + y] : i0 + y;
         const float l = lses[y];
+        if (!rows && !any_entry(e, t, 0)) {
+            if (lane == 0) loss[t] = 0.f;
+            continue;
+        }
         float top_t, log_total, s = 0.f;
         teacher_stats(e, t, top_t, log_total);
         for (int k = lane; k < e.k; k += 64) {
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
     const long j = (long)blockIdx.x * 256 + threadIdx.x;
     if (j >= (long)tokens * e.k) return;
     const long t = j / e.k, k = j - t * e.k;
-    const int i = pos[t];
+    const int i = P == 0 ? (int)t : pos[t];
     const i64 v = e.index[t * e.ld + k];
     if (i < 0 || !e.counts(v) || v < v0 || v >= v0 + vocab) return;
     if constexpr (P == 0) {
@@ -464,14 +474,16 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
 
 // dX of every token: the sum of its product's parts, or 0 where it does not count.  TY groups of
 // threads take every TY-th part each: 16 for few tokens, whose product has many parts, 1 for others.
+// P = 0: a token's parts stand at its own place and need no scale.
 template <typename T, int P, int TY>
-__global__ void __launch_bounds__(256) vocab_dx_out_kernel(const int* pos, const int* count, int hidden,
+__global__ void __launch_bounds__(256) vocab_dx_out_kernel(Entries e, const int* pos, const int* count, int hidden,
                                                            const float* acc, DxCut cut, int hp, const float* weight,
                                                            const float* x_unit, const float* x_most, T* dx, long ld) {
     constexpr int TX = 256 / TY;
     typedef T Row __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-    const int t = blockIdx.x, i = pos[t], splits = cut.splits(*count);
-    const size_t rows = cut.rows(*count);
+    const int t = blockIdx.x, i = P > 0 ? pos[t] : any_entry(e, t, 0) ? t : -1;
+    const int splits = P > 0 ? cut.splits(*count) : cut.groups;
+    const size_t rows = P > 0 ? cut.rows(*count) : cut.bn;
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, h = (blockIdx.y * TX + tx) * 4;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0 && h < hidden)
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(256) vocab_dx_out_kernel(const int* pos, const
     }
     if (ty > 0 || h >= hidden) return;
     float s = 0.f;
-    if (i >= 0) s = P == 1 ? weight[t] : *x_most / (x_unit[i] * kDScale);
+    if (i >= 0) s = P == 0 ? 1.f : P == 1 ? weight[t] : *x_most / (x_unit[i] * kDScale);
     Row o;
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = (T)(i < 0 ? 0.f : v[q] * s);

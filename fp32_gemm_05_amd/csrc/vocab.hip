@@ -125,7 +125,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
 // At most kFewTokens tokens (kernel_vocab_few.hpp).  nb: blocks of 16 tokens.
 struct FewLayout {
     int nb, kt, piece, pieces, splits;
-    long steps, hb, hp, vp, count, rows, pos, z, scale, weight, value, xf, xtf, d, part, acc, bytes;
+    long hb, hp, vp, z, scale, weight, value, xtf, d, part, acc, bytes;
 };
 
 int few_rows(int nb) { return nb == 4 ? 64 : 32; }  // vocabulary rows of a workgroup
@@ -135,7 +135,6 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     const int e = f32 ? 4 : 8;
     l.nb = T > 32 ? 4 : T > 16 ? 2 : 1;
     l.kt = (int)up(16 * l.nb, 4 * e) / (4 * e);
-    l.steps = up(H, 4 * e) / (4 * e);
     l.hb = up(H, 8 * e) / 16;  // dW's groups are 128 bytes of hidden
     l.hp = up(H, 16 * e);
     const long vp = up(V, 64);
@@ -152,11 +151,7 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
         at = up(at + bytes, 1024);
         return o;
     };
-    l.count = take(4);
-    l.rows = take(4 * kFewTokens);
-    l.pos = take(4 * kFewTokens);
     l.z = take(4 * kFewTokens);
-    l.xf = take(1024 * l.steps * l.nb);
     if (grad) {
         l.scale = take(4 * kFewTokens);
         l.weight = take(4 * kFewTokens);
@@ -185,63 +180,55 @@ int run_few(const Call& c, const FewLayout& l) {
     typedef Chunk<T> Ch;
     char* ws = c.work;
     auto floats = [&](long at) { return (float*)(ws + at); };
-    int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
     const T* W = (const T*)c.W;
     const hipStream_t st = c.stream;
+    const int per = few_rows(NB);
     (void)hipGetLastError();
 
-    const int xf_chunks = (int)(64 * l.steps * l.nb), xtf_chunks = c.grad && c.dW ? (int)(64 * l.hb * l.kt) : 0;
-    const int chunk_blocks = (xf_chunks + xtf_chunks + 255) / 256;
     float* const z = c.e.teacher ? c.picked_out : floats(l.z);
-    const FewScanArgs scan{token_args(c, ws, z, l.scale, l.weight, l.value, D_WHOLE),
-                           {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
-                           l.nb, l.kt, ws + l.xf, ws + l.xtf, xf_chunks, xtf_chunks, chunk_blocks};
-    if (c.grad)
-        vocab_few_scan_kernel<T, true><<<chunk_blocks + token_blocks(c), 256, 0, st>>>(scan);
-    else
-        vocab_few_scan_kernel<T, false><<<chunk_blocks + token_blocks(c), 256, 0, st>>>(scan);
-    const int per = few_rows(NB);
+    if (c.e.teacher) {
+        const TokenArgs t = token_args(c, ws, z, l.scale, l.weight, l.value, D_WHOLE);
+        if (c.grad)
+            vocab_few_token_kernel<T, true><<<token_blocks(c), 256, 0, st>>>(t);
+        else
+            vocab_few_token_kernel<T, false><<<token_blocks(c), 256, 0, st>>>(t);
+    }
     int part = 0;
     for (int p = 0; p < l.pieces; ++p) {
         const int v0 = p * l.piece, vn = c.V - v0 < l.piece ? c.V - v0 : l.piece;
         const T* Wp = W + (size_t)v0 * c.ldw;
-        const int groups = (int)up(vn, per) / per;
-        const FewArgs a{Wp, c.ldw, vn, c.H, ws + l.xf, count, rows, c.alpha,
-                        (float2*)(ws + l.part) + (size_t)part * kFewTokens, c.lse, floats(l.scale),
-                        c.e.teacher ? nullptr : c.e.index, floats(l.value), v0, floats(l.d), l.vp};
+        const int groups = (int)(up(vn, per) / per);
+        const int chunks = c.grad && c.dW && p == 0 ? (int)(64 * l.hb * l.kt) : 0;
+        const FewArgs a{c.e, c.T, c.X, Wp, c.ldx, c.ldw, vn, c.H, groups, c.V, c.alpha, v0,
+                        (float2*)(ws + l.part) + (size_t)part * kFewTokens, z, c.lse, c.dloss, floats(l.scale),
+                        floats(l.d), l.vp, ws + l.xtf, l.kt, chunks};
         if (!c.grad) {
             vocab_few_logits_kernel<T, NB, false><<<groups, 256, 0, st>>>(a);
             part += groups;
             continue;
         }
-        vocab_few_logits_kernel<T, NB, true><<<groups, 256, 0, st>>>(a);
+        vocab_few_logits_kernel<T, NB, true><<<groups + (chunks + 255) / 256, 256, 0, st>>>(a);
         if (c.e.teacher)
             vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-                c.e, c.T, v0, vn, pos, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
-        if (c.dX) {
-            const FewDxArgs x{Wp, c.ldw, vn, c.H, l.splits, count, floats(l.d), l.vp, floats(l.acc), (int)l.hp, p > 0};
-            vocab_few_dx_kernel<T, NB><<<dim3((unsigned)(l.hp / (16 * Ch::E)), l.splits), 256, 0, st>>>(x);
-        }
-        if (c.dW) {
-            // 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but four
-            // groups or more: a wave reads its rows' D first
-            const long row_groups = up(vn, 256) / 256, all = up(c.H, 8 * Ch::E) / (8 * Ch::E);
-            const long cols = 2048 / row_groups < 1 ? 1 : 2048 / row_groups;
-            const long even = (all + cols - 1) / cols;
-            const int groups = (int)(even < 4 ? 4 : even);
-            const FewDwArgs w{ws + l.xtf, count, floats(l.d), l.vp, vn, c.H, groups,
-                              (T*)c.dW + (size_t)v0 * c.lddw, c.lddw};
-            vocab_few_dw_kernel<T, NB><<<dim3((unsigned)row_groups, (unsigned)((all + groups - 1) / groups)), 256, 0,
-                                        st>>>(w);
-        }
+                c.e, c.T, v0, vn, nullptr, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
+        // dW: 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but four
+        // groups or more: a wave reads its rows' D first
+        const long row_groups = up(vn, 256) / 256, all = up(c.H, 8 * Ch::E) / (8 * Ch::E);
+        const long cols = 2048 / row_groups < 1 ? 1 : 2048 / row_groups;
+        const long even = (all + cols - 1) / cols, own = even < 4 ? 4 : even;
+        const int strips = c.dX ? (int)(l.hp / (16 * Ch::E)) : 0;
+        const FewGradArgs g{floats(l.d), l.vp, c.T, vn, c.H, Wp, c.ldw, strips, l.splits, floats(l.acc), (int)l.hp,
+                            p > 0, ws + l.xtf, (int)own, (int)row_groups, (T*)c.dW + (size_t)v0 * c.lddw, c.lddw};
+        const long dw_blocks = c.dW ? row_groups * ((all + own - 1) / own) : 0;
+        vocab_few_grad_kernel<T, NB><<<(unsigned)(strips * l.splits + dw_blocks), 256, 0, st>>>(g);
     }
     if (!c.grad) {
-        vocab_loss_kernel<4><<<(unsigned)(up(c.T, 4) / 4), 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part,
-                                                              kFewTokens, z, c.loss, c.lse_out);
+        vocab_loss_kernel<4><<<(unsigned)(up(c.T, 4) / 4), 1024, 0, st>>>(
+            c.e, nullptr, nullptr, c.T, c.V, (const float2*)(ws + l.part), part, kFewTokens, z, c.loss, c.lse_out);
     } else if (c.dX) {
         const DxCut cut{1, 16 * NB, l.splits, l.splits};
-        vocab_dx_out_kernel<T, 1, 16><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(pos, count, c.H, floats(l.acc), cut, (int)l.hp,
-                                                       floats(l.weight), nullptr, nullptr, (T*)c.dX, c.lddx);
+        vocab_dx_out_kernel<T, 0, 16><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(
+            c.e, nullptr, nullptr, c.H, floats(l.acc), cut, (int)l.hp, nullptr, nullptr, nullptr, (T*)c.dX, c.lddx);
     }
     return (int)hipGetLastError();
 }
@@ -347,12 +334,12 @@ int run(const Call& c) {
             });
     }
     if (!c.grad)
-        vocab_loss_kernel<32><<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, (const float2*)(ws + l.part), part, l.tp, z,
-                                                      c.loss, c.lse_out);
+        vocab_loss_kernel<32><<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, c.T, c.V, (const float2*)(ws + l.part), part,
+                                                          l.tp, z, c.loss, c.lse_out);
     else if (c.T > 0 && c.dX) {
         auto out = [&](auto kernel, long cols) {
             kernel<<<dim3(c.T, (unsigned)(up(c.H, cols) / cols)), 256, 0, st>>>(
-                pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight), x_unit, x_most, (T*)c.dX, c.lddx);
+                c.e, pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight), x_unit, x_most, (T*)c.dX, c.lddx);
         };
         if (c.T < 512)
             out(vocab_dx_out_kernel<T, P, 16>, 64);

@@ -104,29 +104,48 @@ def _vector(t, name, dtype, n):
         raise ValueError(f"{name} must be contiguous")
 
 
+# torch.cuda.current_stream makes a Stream object first, 20 times the time of the handle alone
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Problem:
     """The checked operands that every call has, and what they share."""
 
     def __init__(self, X, W, alpha, stream, entries=0):
-        self.ldx, self.ldw = _matrix(X, "X"), _matrix(W, "W", X.dtype)
-        if X.shape[1] != W.shape[1]:
+        ldx, ldw = _matrix(X, "X"), _matrix(W, "W", X.dtype if isinstance(X, torch.Tensor) else None)
+        self.T, self.H = X.shape
+        self.V, H = W.shape
+        if self.H != H:
             raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
-        if W.shape[0] < 1 or W.shape[1] < 1:
+        if self.V < 1 or H < 1:
             raise ValueError(f"W {tuple(W.shape)} has no element")
-        self.T, self.H, self.V = X.shape[0], X.shape[1], W.shape[0]
         self.K = entries
         self.dtype, self.device = X.dtype, X.device
         self.head = (_TYPES[X.dtype], self.T, self.V, self.H)
-        self.matrices = (X.data_ptr(), self.ldx, W.data_ptr(), self.ldw)
+        self.matrices = (X.data_ptr(), ldx, W.data_ptr(), ldw)
         self.alpha = float(alpha)
-        # results and workspace are allocated on the stream that uses them
-        if stream is None:
-            self.stream = torch.cuda.current_stream(self.device)
-        elif isinstance(stream, int):
-            self.stream = torch.cuda.ExternalStream(stream, device=self.device)
-        else:
-            self.stream = stream
-        self.handle = self.stream.cuda_stream
+        self.stream = stream
+        self.same_device((W, "W"))
+
+    def __enter__(self):
+        """Results and workspace are allocated on the stream that uses them."""
+        self.context = None
+        stream, index = self.stream, self.device.index
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.device)
+            self.context = torch.cuda.stream(stream)
+        elif index != torch.cuda.current_device():
+            self.context = torch.cuda.device(self.device)
+        if self.context is not None:
+            self.context.__enter__()
+        self.handle = _current_handle(index)
+        return self
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
 
     def same_device(self, *named):
         for t, name in named:
@@ -144,7 +163,7 @@ class _Problem:
 def _ce(X, W, target, alpha, stream):
     p = _Problem(X, W, alpha, stream)
     _vector(target, "target", torch.int64, p.T)
-    p.same_device((W, "W"), (target, "target"))
+    p.same_device((target, "target"))
     return p
 
 
@@ -154,7 +173,7 @@ def vocab_ce(X, W, target, alpha: float = 1.0, ignore_index: int = -100, stream=
     Tokens whose target is ignore_index have loss 0 and lse 0; a target outside the vocabulary
     gives NaN."""
     p = _ce(X, W, target, alpha, stream)
-    with torch.cuda.stream(p.stream):
+    with p:
         loss, lse = p.new(p.T), p.new(p.T)
         work, n = p.workspace(False)
         _call("vocab_ce", *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index), loss.data_ptr(),
@@ -182,7 +201,7 @@ def vocab_ce_grad(X, W, target, lse, dloss, alpha: float = 1.0, ignore_index: in
     _vector(lse, "lse", torch.float32, p.T)
     _vector(dloss, "dloss", torch.float32, p.T)
     p.same_device((lse, "lse"), (dloss, "dloss"))
-    with torch.cuda.stream(p.stream):
+    with p:
         dX, dW = _outputs(p, want_dx, want_dw)
         work, n = p.workspace(True)
         _call("vocab_ce_grad", *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index), lse.data_ptr(),
@@ -199,7 +218,7 @@ def _distill(X, W, index, teacher, alpha, stream):
     p = _Problem(X, W, alpha, stream, index.shape[1])
     if index.shape[0] != p.T:
         raise ValueError(f"index has {index.shape[0]} rows for {p.T} tokens")
-    p.same_device((W, "W"), (index, "index"), (teacher, "teacher"))
+    p.same_device((index, "index"), (teacher, "teacher"))
     return p, (index.data_ptr(), ldi, teacher.data_ptr(), ldt)
 
 
@@ -210,7 +229,7 @@ def vocab_distill(X, W, index, teacher, alpha: float = 1.0, teacher_alpha: float
     no entry, and a token without entries has loss 0.  picked (T x K) holds the student's logits at
     the entries, which the gradient takes back."""
     p, entries = _distill(X, W, index, teacher, alpha, stream)
-    with torch.cuda.stream(p.stream):
+    with p:
         loss, lse, picked = p.new(p.T), p.new(p.T), p.new(p.T, p.K)
         work, n = p.workspace(False)
         _call("vocab_distill", *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries, loss.data_ptr(),
@@ -227,7 +246,7 @@ def vocab_distill_grad(X, W, index, teacher, lse, picked, dloss, alpha: float = 
     if _matrix(picked, "picked", torch.float32) != p.K or tuple(picked.shape) != (p.T, p.K):
         raise ValueError("picked must be the contiguous T x K tensor of vocab_distill")
     p.same_device((lse, "lse"), (dloss, "dloss"), (picked, "picked"))
-    with torch.cuda.stream(p.stream):
+    with p:
         dX, dW = _outputs(p, want_dx, want_dw)
         work, n = p.workspace(True)
         _call("vocab_distill_grad", *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries,

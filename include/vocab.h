@@ -20,8 +20,8 @@
  * twice).  They recompute the logits in pieces of the vocabulary, from the forward call's lse.
  *
  * Tokens that do not count -- target == ignore_index, or no index >= 0 -- have loss 0, lse 0 and
- * gradient 0, whatever X, dloss and teacher hold there (NaN and infinities included), and cost no
- * product.  A target or an index >= V (or a target < 0 that is not ignore_index) cannot be refused
+ * gradient 0, whatever X, dloss and teacher hold there (NaN and infinities included); among more
+ * than 64 tokens they cost no product either.  A target or an index >= V (or a target < 0 that is not ignore_index) cannot be refused
  * without waiting for the device: nothing is read for it, and the token's loss and the gradients
  * that it enters are NaN.  Teacher entries of -infinity have q = 0 and add nothing.
  *

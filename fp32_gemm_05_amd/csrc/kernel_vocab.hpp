@@ -90,6 +90,21 @@ __device__ inline f32x16 mfma(typename Planes<P>::Half8 a, typename Planes<P>::H
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+__device__ inline float wave_sum(float s) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    return s;
+}
+__device__ inline float wave_max(float s) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s = fmaxf(s, __shfl_xor(s, o));
+    return s;
+}
+// A maximum that many workgroups raise, in 64 words (one word would take their atomics one after the
+// other: 10 us a thousand); read by whole waves.
+constexpr int kMostSlots = 64;
+__device__ inline float most_of(const float* slots) { return wave_max(slots[threadIdx.x & 63]); }
+
 // The scale of P = 2 operands: the power of two that brings a largest value m into [2^14, 2^15).
 // m of 0 (or nothing finite) gives 1; an m so small or large that the power would leave fp32's
 // range gives the nearest that does not.
@@ -414,7 +429,7 @@ struct GradArgs {
     Operand w, x;
     const int *count, *rows;       // the counted tokens
     const float *w_unit, *x_unit;  // P = 2, as in LseArgs
-    const float* x_most;           // P = 2: the largest |weight * x_unit| of a counted token
+    const float* x_most;           // P = 2: the largest |weight * x_unit| of a counted token (most_of)
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;
     const float *lse, *scale, *weight;  // per token: D = exp(z - lse) * scale; its weight in dX and dW
@@ -443,6 +458,7 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     if (n0 >= count) return;
     T t;
     t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
+    const float x_most = T::kP == 2 ? most_of(a.x_most) : 0.f;
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
@@ -457,7 +473,7 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
             value = a.value[token];
         }
         if (T::kP == 2 && live) {
-            const float unit = a.x_unit[n], f = d_factor(a.weight[token], unit, *a.x_most);
+            const float unit = a.x_unit[n], f = d_factor(a.weight[token], unit, x_most);
             alpha *= *a.w_unit * unit;
             scale *= f;
             value *= f;
@@ -576,7 +592,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
     // (as in vocab_grad_kernel), or one of fp32
     constexpr int E = 16 / sizeof(O), F = E / 4;
     typedef O Row __attribute__((ext_vector_type(E), aligned(sizeof(O))));
-    const float unit = T::kP == 2 ? *a.x_most / kDScale : 1.f;
+    const float unit = T::kP == 2 ? most_of(a.x_most) / kDScale : 1.f;
     const int h = (threadIdx.x & 63) >> 5;
     const bool whole = m0 + T::kBM <= a.hidden;
 #pragma unroll

@@ -112,17 +112,6 @@ __device__ inline float wave_dot(const T* x, const T* w, int n) {
     for (int o = 32; o > 0; o >>= 1) t += __shfl_xor(t, o);
     return t;
 }
-__device__ inline float wave_sum(float s) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    return s;
-}
-__device__ inline float wave_max(float s) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s = fmaxf(s, __shfl_xor(s, o));
-    return s;
-}
-
 // The teacher's softmax over a token's entries, by one wave: maximum and log of the sum.
 __device__ inline void teacher_stats(const Entries& e, long t, float& top, float& log_total) {
     const int lane = threadIdx.x & 63;
@@ -242,7 +231,7 @@ struct ScanArgs {
     int token_blocks;
     float* w_part;    // max_blocks maxima of |W|'s finite values
     int max_blocks;
-    uint32_t* x_most; // cleared for vocab_pack_kernel
+    uint32_t* x_most; // kMostSlots, cleared for vocab_pack_kernel
 };
 
 // All that reads the inputs alone, in one launch: workgroup 0 counts, the next token_blocks look at
@@ -251,7 +240,7 @@ template <typename T, bool GRAD>
 __global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
     int b = blockIdx.x;
     if (b == 0) {
-        if (threadIdx.x == 0) *a.x_most = 0;
+        if (threadIdx.x < kMostSlots) a.x_most[threadIdx.x] = 0;
         count_tokens(a.t.e, a.t.tokens, a.c);
         return;
     }
@@ -296,7 +285,7 @@ struct PackArgs {
     const float* weight;  // per token
     char* scaled;         // P = 1, when wanted: the rows times their weight
     float* x_unit;        // P = 2: each row in its own power of two, x_unit what a packed unit stands for
-    uint32_t* x_most;     // P = 2: the largest |weight| * x_unit, in a gradient's call (weight given)
+    uint32_t* x_most;     // P = 2: kMostSlots maxima of |weight| * x_unit, in a gradient's call (weight given)
     // W: `vocab` rows, and zero rows to the next multiple of 256
     const void* w;
     long ldw;
@@ -330,7 +319,8 @@ __device__ inline void pack_x(const PackArgs& a, int i) {
                 const float u = ldexpf(1.f, -e);
                 a.x_unit[i] = u;
                 const float w = a.weight ? fabsf(a.weight[t] * u) : 0.f;
-                if (w > 0.f) atomicMax(a.x_most, __float_as_uint(w));  // a maximum: the order does not matter
+                // a maximum: the order does not matter
+                if (w > 0.f) atomicMax(a.x_most + i % kMostSlots, __float_as_uint(w));
             }
         }
     } else if (a.scaled && s) {
@@ -363,16 +353,24 @@ __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
         f = ldexpf(1.f, e);
         if (b == 0 && threadIdx.x == 0) *a.w_unit = ldexpf(1.f, -e);
     }
+    const bool whole = (b + 1) * kPackRows <= a.vocab;
+    const T* s = (const T*)a.w + (size_t)b * kPackRows * a.ldw;
     for (int k = threadIdx.x * 4; k < a.kp; k += 1024) {
+        float v[kPackRows][4];
+        if (whole && k + 4 <= a.cols) {  // all rows' loads together
+#pragma unroll
+            for (int r = 0; r < kPackRows; ++r) load(s + r * a.ldw + k, v[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < kPackRows; ++r)
+                load_row(b * kPackRows + r < a.vocab ? s + r * a.ldw : nullptr, k, a.cols, v[r]);
+        }
 #pragma unroll
         for (int r = 0; r < kPackRows; ++r) {
-            const int i = b * kPackRows + r;
-            float v[4];
-            load_row(i < a.vocab ? (const T*)a.w + (size_t)i * a.ldw : nullptr, k, a.cols, v);
             if constexpr (P == 2)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] *= f;
-            store4<P>(a.w_out + (size_t)i * a.pitch, k, v);
+                for (int q = 0; q < 4; ++q) v[r][q] *= f;
+            store4<P>(a.w_out + (size_t)(b * kPackRows + r) * a.pitch, k, v[r]);
         }
     }
 }
@@ -459,6 +457,7 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
                                                           const float* x_unit, const float* x_most, char* d,
                                                           long d_pitch) {
     const long j = (long)blockIdx.x * 256 + threadIdx.x;
+    const float most = P == 2 ? most_of(x_most) : 0.f;
     if (j >= (long)tokens * e.k) return;
     const long t = j / e.k, k = j - t * e.k;
     const int i = P == 0 ? (int)t : pos[t];
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
         ((float*)(d + (size_t)i * d_pitch))[v - v0] = value[j];
         return;
     }
-    const float f = P == 2 ? d_factor(weight[t], x_unit[i], *x_most) : 1.f;
+    const float f = P == 2 ? d_factor(weight[t], x_unit[i], most) : 1.f;
     store1<P == 2 ? 2 : 1>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
 }
 
@@ -485,6 +484,7 @@ __global__ void __launch_bounds__(256) vocab_dx_out_kernel(Entries e, const int*
     const int splits = P > 0 ? cut.splits(*count) : cut.groups;
     const size_t rows = P > 0 ? cut.rows(*count) : cut.bn;
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, h = (blockIdx.y * TX + tx) * 4;
+    const float most = P == 2 ? most_of(x_most) : 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0 && h < hidden)
 #pragma unroll 4
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(256) vocab_dx_out_kernel(Entries e, const int*
     }
     if (ty > 0 || h >= hidden) return;
     float s = 0.f;
-    if (i >= 0) s = P == 0 ? 1.f : P == 1 ? weight[t] : *x_most / (x_unit[i] * kDScale);
+    if (i >= 0) s = P == 0 ? 1.f : P == 1 ? weight[t] : most / (x_unit[i] * kDScale);
     Row o;
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = (T)(i < 0 ? 0.f : v[q] * s);

@@ -86,12 +86,16 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     l.piece = (int)up((vp + pieces - 1) / pieces, 256);
     l.pieces = (int)((vp + l.piece - 1) / l.piece);
     // dX's workgroups: its tiles, or about as many as the chip has places for (one large tile a
-    // compute unit, two small ones)
-    l.dx_big = T > 128 && H > 128;
-    const int bm = l.dx_big ? Big<1>::kBM : Small<1>::kBM, bn = l.dx_big ? Big<1>::kBN : Small<1>::kBN;
-    const int tiles_m = (int)(up(H, bm) / bm), tiles = tiles_m * (int)(up(l.tp, bn) / bn);
-    const int places = l.dx_big ? 256 : 512, slabs = l.piece / bk;
-    l.cut = {tiles_m, bn, tiles > places ? tiles : places / tiles * tiles, slabs / 8 > 1 ? slabs / 8 : 1};
+    // compute unit, two small ones), with 8 slabs or more each; large tiles if they fill most places
+    const int slabs = l.piece / bk, most_cuts = slabs / 8 > 1 ? slabs / 8 : 1;
+    auto cut = [&](int bm, int bn, int places) {
+        const int tiles_m = (int)(up(H, bm) / bm), tiles = tiles_m * (int)(up(l.tp, bn) / bn);
+        return DxCut{tiles_m, bn, tiles > places ? tiles : places / tiles * tiles, most_cuts};
+    };
+    l.cut = cut(Big<1>::kBM, Big<1>::kBN, 256);
+    const long filled = up(H, Big<1>::kBM) / Big<1>::kBM * (up(T, Big<1>::kBN) / Big<1>::kBN) * most_cuts;
+    l.dx_big = T > 128 && H > 128 && filled >= 192;
+    if (!l.dx_big) l.cut = cut(Small<1>::kBM, Small<1>::kBN, 512);
     long at = 0;
     auto take = [&](long bytes) {
         const long o = at;
@@ -103,7 +107,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     l.pos = take(4L * l.tp);
     if (!teacher) l.z = take(4L * l.tp);
     l.x_unit = take(4L * l.tp);
-    l.x_most = take(4);
+    l.x_most = take(4L * kMostSlots);
     l.w_unit = take(4);
     l.w_part = take(4L * kMaxBlocks);
     l.x = take(element * l.hk * l.tp);
@@ -114,7 +118,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
         l.value = take(4L * T * K);
         if (P == 1 && !teacher) l.xs = take(element * l.hk * l.tp);
         l.d = take(element * l.tp * l.piece);
-        l.acc = take(4L * l.hp * ((long)l.cut.groups / tiles_m * bn));
+        l.acc = take(4L * l.hp * ((long)l.cut.groups / l.cut.tiles_m * l.cut.bn));
     } else {
         l.part = take(8L * (vp / kPartRows) * l.tp);
     }

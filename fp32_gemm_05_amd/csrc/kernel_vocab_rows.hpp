@@ -205,6 +205,8 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
                 }
                 a.value[t * e.k + k] = d;
             }
+            if (!__all(good))  // an entry past the vocabulary: the whole row is NaN, as the loss is
+                for (int k = lane; k < e.k; k += 64) a.value[t * e.k + k] = NAN;
             scale = __all(good) ? (a.form == D_APART ? 1.f : s) : NAN;
             weight = a.form == D_APART ? s : 1.f;
         }

@@ -17,7 +17,8 @@
 //
 // P is the number of 16-bit planes an operand is held in.  P = 1: bf16 operands, as they are.
 // P = 2: fp32 operands as the sum of two fp16 values, a row stored in blocks of 32 k as [32 high]
-// [32 low].  The operand is scaled by a power of two first, so that its largest value lies in
+// [32 low].  The operand -- a row of X, a row of W in the forward call, the whole of W in the gradient's,
+// whose dX sums over its rows -- is scaled by a power of two first, so that its largest value lies in
 // [2^14, 2^15); high + low then holds every value down to 2^-16 of the largest to one fp32 rounding
 // (2^-24 of itself) and smaller ones to 2^-40 of the largest.  Three products (hl, lh, hh) are
 // accumulated in fp32; the one left out, ll, is below 2^-24 of the whole.  Three fp16 MFMAs do the
@@ -378,8 +379,7 @@ struct Tile {
 struct LseArgs {
     Operand w, x;          // vocabulary rows of this piece, counted tokens
     const int* count;      // number of counted tokens
-    const float* w_unit;   // P = 2: what a packed unit of W, and of each token's row of X, stands for
-    const float* x_unit;
+    const float *w_unit, *x_unit;  // P = 2: what a packed unit of each row of W, of X stands for
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;
     float2* part;          // [vocabulary pieces of WM rows][tp]: maximum and sum of exp(z - maximum)
@@ -402,15 +402,22 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
         float alpha = a.alpha;
-        if (T::kP == 2) alpha *= *a.w_unit * (n < count ? a.x_unit[n] : 0.f);
+        if (T::kP == 2) alpha *= n < count ? a.x_unit[n] : 0.f;
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float z = m0 + t.row(i, e) < a.vocab ? t.acc[i][j][e] * alpha : -INFINITY;
-                t.acc[i][j][e] = z;
-                top = z > top || z != z ? z : top;  // a NaN stays
+            for (int g = 0; g < 4; ++g) {
+                const int m = m0 + t.row(i, 4 * g);
+                f32x4 unit = {1.f, 1.f, 1.f, 1.f};
+                if (T::kP == 2) unit = *(const f32x4*)(a.w_unit + m);  // to the end of the tile, as the rows
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int e = 4 * g + q;
+                    const float z = m + q < a.vocab ? t.acc[i][j][e] * (alpha * unit[q]) : -INFINITY;
+                    t.acc[i][j][e] = z;
+                    top = z > top || z != z ? z : top;  // a NaN stays
+                }
             }
         const float other = __shfl_xor(top, 32);
         top = other > top || other != other ? other : top;
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
 struct GradArgs {
     Operand w, x;
     const int *count, *rows;       // the counted tokens
-    const float *w_unit, *x_unit;  // P = 2, as in LseArgs
+    const float *w_unit, *x_unit;  // P = 2: what a packed unit of W, of each row of X stands for
     const float* x_most;           // P = 2: the largest |weight * x_unit| of a counted token (most_of)
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;

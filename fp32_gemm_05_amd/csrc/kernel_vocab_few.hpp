@@ -469,18 +469,17 @@ __device__ inline void few_dx(const FewGradArgs& a, int block) {
 #pragma unroll
         for (int e = 0; e < HE; ++e) sums[wave][e][lane] = acc[e][b];
         __syncthreads();
-        // element i of block e: token 16 b + l, hidden h0 + HE * (4 g + i) + e
-        float* out = a.acc + ((size_t)z * 16 * NB + 16 * b + l) * a.hp + h0 + HE * 4 * g;
+        // element i of block e: token 16 b + l, hidden h0 + HE * (4 g + i) + e; wave i takes its HE in a row
+        f32x4* out = (f32x4*)(a.acc + ((size_t)z * 16 * NB + 16 * b + l) * a.hp + h0 + HE * (4 * g + wave));
 #pragma unroll
-        for (int e = wave; e < HE; e += 4) {
-            f32x4 c = sums[0][e][lane];
+        for (int e = 0; e < HE; e += 4) {
+            f32x4 c;
 #pragma unroll
-            for (int y = 1; y < 4; ++y) c += sums[y][e][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float* p = out + HE * i + e;
-                *p = a.add ? *p + c[i] : c[i];
+            for (int q = 0; q < 4; ++q) {
+                const float* p = (const float*)&sums[0][e + q][lane] + wave;
+                c[q] = p[0] + p[HE * 256] + p[2 * HE * 256] + p[3 * HE * 256];
             }
+            out[e / 4] = a.add ? out[e / 4] + c : c;
         }
     }
 }

@@ -293,7 +293,9 @@ struct PackArgs {
     long ldw;
     int vocab;
     char* w_out;
-    const float* w_part;  // P = 2: the power of two of its largest value
+    // P = 2: in the power of two of its largest value (w_parts maxima), w_unit[0] what a packed unit
+    // stands for; w_parts 0: each row in its own, w_unit[row]
+    const float* w_part;
     int w_parts;
     float* w_unit;
 };
@@ -341,6 +343,52 @@ __device__ inline void pack_x(const PackArgs& a, int i) {
     }
 }
 
+// Row i of W by one wave, in its own power of two.  The row is read once: up to kHeld chunks of 256 stay
+// in registers between the search for its largest value and the stores.
+template <typename T>
+__device__ inline void pack_w_row(const PackArgs& a, int i) {
+    constexpr int kHeld = 8;
+    const int lane = threadIdx.x & 63;
+    const T* s = i < a.vocab ? (const T*)a.w + (size_t)i * a.ldw : nullptr;
+    char* out = a.w_out + (size_t)i * a.pitch;
+    float v[kHeld][4], m = 0.f;
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) {
+        const int k = c * 256 + lane * 4;
+        if (k < a.kp) load_row(s, k, a.cols, v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c)
+        if (c * 256 + lane * 4 < a.kp)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = finite_max(m, v[c][q]);
+    for (int k = kHeld * 256 + lane * 4; k < a.cols; k += 256) {
+        float w[4];
+        load_row(s, k, a.cols, w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m = finite_max(m, w[q]);
+    }
+    m = wave_max(m);
+    const int e = scale_exponent(m);
+    const float f = ldexpf(1.f, e);
+#pragma unroll
+    for (int c = 0; c < kHeld; ++c) {
+        const int k = c * 256 + lane * 4;
+        if (k >= a.kp) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[c][q] *= f;
+        store4<2>(out, k, v[c]);
+    }
+    for (int k = kHeld * 256 + lane * 4; k < a.kp; k += 256) {
+        float w[4];
+        load_row(s, k, a.cols, w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] *= f;
+        store4<2>(out, k, w);
+    }
+    if (lane == 0) a.w_unit[i] = ldexpf(1.f, -e);
+}
+
 // The packed operands, in one launch: x_blocks workgroups take a row of X each, the rest kPackRows
 // rows of W.
 template <typename T, int P>
@@ -349,6 +397,10 @@ __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
     const int b = blockIdx.x - a.x_blocks;
     float f = 1.f;
     if constexpr (P == 2) {
+        if (a.w_parts == 0) {
+            for (int r = threadIdx.x >> 6; r < kPackRows; r += 4) pack_w_row<T>(a, b * kPackRows + r);
+            return;
+        }
         float m = 0.f;
         for (int i = threadIdx.x; i < a.w_parts; i += 256) m = fmaxf(m, a.w_part[i]);
         const int e = scale_exponent(block_max(m));

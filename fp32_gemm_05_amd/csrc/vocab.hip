@@ -108,7 +108,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     if (!teacher) l.z = take(4L * l.tp);
     l.x_unit = take(4L * l.tp);
     l.x_most = take(4L * kMostSlots);
-    l.w_unit = take(4);
+    l.w_unit = take(4L * l.piece);
     l.w_part = take(4L * kMaxBlocks);
     l.x = take(element * l.hk * l.tp);
     l.w = take(element * l.hk * l.piece);
@@ -273,7 +273,8 @@ int run(const Call& c) {
     (void)hipGetLastError();
 
     float* const z = c.e.teacher ? c.picked_out : floats(l.z);
-    const int max_blocks = P == 2 ? (int)(up(c.V, 4) / 4 < kMaxBlocks ? up(c.V, 4) / 4 : kMaxBlocks) : 0;
+    // the gradient's W is packed in one power of two, that of its largest value
+    const int max_blocks = P == 2 && c.grad ? (int)(up(c.V, 4) / 4 < kMaxBlocks ? up(c.V, 4) / 4 : kMaxBlocks) : 0;
     const ScanArgs scan{token_args(c, ws, z, l.scale, l.weight, l.value, P == 2 ? D_APART : D_PACKED),
                         {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
                         (int)token_blocks(c), floats(l.w_part), max_blocks, (uint32_t*)x_most};

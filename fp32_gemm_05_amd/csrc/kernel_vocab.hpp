@@ -386,23 +386,19 @@ struct LseArgs {
     int part0, tp;
 };
 
-template <class T>
-__global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
-    __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
-    int tm, tn;
-    tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
-    const int m0 = tm * T::kBM, n0 = tn * T::kBN;
-    const int count = *a.count;
-    if (n0 >= count) return;
-    T t;
-    t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
-    const int h = (threadIdx.x & 63) >> 5;
-    const int piece = a.part0 + tm * T::WAVES_M + (threadIdx.x >> 6) / T::WAVES_N;
+constexpr float kLog2E = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+
+// The tile's maxima and sums.  Its exponentials cost as much as 10 slabs of products if each value is
+// masked, compared and rescaled; PLAIN, for a tile of valid rows and alpha >= 0, takes the maximum of the
+// accumulators as they are and one fma, one v_exp_f32 and one add for each.  A NaN may be missed by the
+// maximum, but not by the sum.
+template <bool PLAIN, class T>
+__device__ inline void lse_tile(T& t, const LseArgs& a, int m0, int n0, int count, int piece) {
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
-        float alpha = a.alpha;
-        if (T::kP == 2) alpha *= n < count ? a.x_unit[n] : 0.f;
+        float c = a.alpha * kLog2E;
+        if (T::kP == 2) c *= n < count ? a.x_unit[n] : 0.f;
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
@@ -413,23 +409,43 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
                 if (T::kP == 2) unit = *(const f32x4*)(a.w_unit + m);  // to the end of the tile, as the rows
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int e = 4 * g + q;
-                    const float z = m + q < a.vocab ? t.acc[i][j][e] * (alpha * unit[q]) : -INFINITY;
-                    t.acc[i][j][e] = z;
-                    top = z > top || z != z ? z : top;  // a NaN stays
+                    float z = t.acc[i][j][4 * g + q];
+                    if (T::kP == 2) z *= unit[q];
+                    if (!PLAIN) z = m + q < a.vocab ? z * c : -INFINITY;
+                    top = fmaxf(top, z);
+                    t.acc[i][j][4 * g + q] = z;
                 }
             }
-        const float other = __shfl_xor(top, 32);
-        top = other > top || other != other ? other : top;
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // z * log2(e) of the largest; nothing but -inf here: the sum is 0
+        const float ref = top == -INFINITY ? 0.f : PLAIN ? top * c : top;
         float sum = 0.f;
-        const float ref = top == -INFINITY ? 0.f : top;  // nothing but -inf here: the sum is 0
 #pragma unroll
         for (int i = 0; i < T::MB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum += __expf(t.acc[i][j][e] - ref);
+            for (int e = 0; e < 16; ++e)
+                sum += __builtin_amdgcn_exp2f(PLAIN ? __builtin_fmaf(t.acc[i][j][e], c, -ref) : t.acc[i][j][e] - ref);
         sum += __shfl_xor(sum, 32);
-        if (h == 0) a.part[(size_t)piece * a.tp + n] = make_float2(top, sum);
+        if ((threadIdx.x & 63) < 32)
+            a.part[(size_t)piece * a.tp + n] = make_float2(top == -INFINITY ? top : ref * kLn2, sum);
     }
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
+    __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
+    int tm, tn;
+    tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
+    const int m0 = tm * T::kBM, n0 = tn * T::kBN;
+    const int count = *a.count;
+    if (n0 >= count) return;
+    T t;
+    t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
+    const int piece = a.part0 + tm * T::WAVES_M + (threadIdx.x >> 6) / T::WAVES_N;
+    if (m0 + T::kBM <= a.vocab && a.alpha >= 0.f)
+        lse_tile<true>(t, a, m0, n0, count, piece);
+    else
+        lse_tile<false>(t, a, m0, n0, count, piece);
 }
 
 struct GradArgs {
@@ -453,10 +469,56 @@ __device__ inline float d_factor(float weight, float x_unit, float x_most) {
     return x_most > 0.f ? weight * x_unit / x_most * kDScale : 0.f;
 }
 
-template <class T>
-__global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
+// D of a token's column in this wave, stored.  PLAIN: no row past the vocabulary and no target among
+// these, as nearly everywhere: a fma, an exponential, a product and the rounding of each are left.
+template <bool PLAIN, class T>
+__device__ inline void grad_column(const T& t, const GradArgs& a, int j, int n, int m0, float lse, float scale,
+                                   float alpha, int entry, float value) {
     typedef typename Planes<T::kP>::Half Half;
     typedef typename Planes<T::kP>::Half4 Half4;
+    const int h = (threadIdx.x & 63) >> 5;
+    char* out = a.d + (size_t)n * a.d_pitch;
+    const float c = alpha * kLog2E, l = lse * kLog2E;
+#pragma unroll
+    for (int i = 0; i < T::MB; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+            Half4 v[2][T::kP];
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int e = 4 * (g + f) + q, m = m0 + t.row(i, e);
+                    // with one rounding less where D keeps 22 bits
+                    float x = T::kP == 2 ? __builtin_fmaf(t.acc[i][j][e], alpha, -lse) * kLog2E
+                                         : __builtin_fmaf(t.acc[i][j][e], c, -l);
+                    x = __builtin_amdgcn_exp2f(x) * scale;
+                    if (!PLAIN) {
+                        // rows past the vocabulary are the zeros that dX's product runs over
+                        x = m < a.vocab ? x : 0.f;
+                        x = m == entry ? value : x;
+                    }
+                    // one x for the high part that is stored and for the one that the low part is measured
+                    // from: a product drawn into one of the two conversions rounds once, the other twice
+                    if (T::kP == 2) asm("" : "+v"(x));
+                    v[f][0][q] = (Half)x;
+                    if constexpr (T::kP == 2) v[f][1][q] = (Half)(x - (float)v[f][0][q]);
+                }
+            // the lane halves hold entries 0-3, 8-11 and 4-7, 12-15 of sixteen: they trade, so that
+            // each stores eight in a row
+            const int m = m0 + t.row(i, 4 * g) + 4 * h;
+#pragma unroll
+            for (int p = 0; p < T::kP; ++p) {
+                const u32x2 x = __builtin_bit_cast(u32x2, v[0][p]), y = __builtin_bit_cast(u32x2, v[1][p]);
+                const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
+                const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
+                *(u32x4*)(out + Planes<T::kP>::at(m, p)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+            }
+        }
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     int tm, tn;
     tile_of(blockIdx.x, a.tiles_m * a.tiles_n, a.tiles_m, a.tiles_n, 4, tm, tn);
@@ -471,8 +533,8 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
         const int n = n0 + t.col(j);
         const bool live = n < count;
         const int token = live ? a.rows[n] : 0;
-        const float lse = live ? a.lse[token] : 0.f;
-        float scale = live ? a.scale[token] : 0.f, alpha = a.alpha, value = 0.f;
+        // a token past the count has a row of zeros for X: its entries come out as 0 by their scale
+        float lse = live ? a.lse[token] : 0.f, scale = live ? a.scale[token] : 0.f, alpha = a.alpha, value = 0.f;
         int entry = -1;  // the target's place in this piece
         if (a.target && live) {
             const long long v = a.target[token] - a.v0;
@@ -485,38 +547,12 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
             scale *= f;
             value *= f;
         }
-        char* out = a.d + (size_t)n * a.d_pitch;
-#pragma unroll
-        for (int i = 0; i < T::MB; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; g += 2) {
-                Half4 v[2][T::kP];
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int e = 4 * (g + f) + q;
-                        // entries past the vocabulary and tokens past the count are the zeros that the
-                        // products of D run over
-                        const int m = m0 + t.row(i, e);
-                        float x = live && m < a.vocab ? __expf(t.acc[i][j][e] * alpha - lse) * scale : 0.f;
-                        x = m == entry ? value : x;
-                        Half x_p[T::kP];
-                        split<T::kP>(x, x_p);
-#pragma unroll
-                        for (int p = 0; p < T::kP; ++p) v[f][p][q] = x_p[p];
-                    }
-                // the lane halves hold entries 0-3, 8-11 and 4-7, 12-15 of sixteen: they trade, so that
-                // each stores eight in a row
-                const int m = m0 + t.row(i, 4 * g) + 4 * h;
-#pragma unroll
-                for (int p = 0; p < T::kP; ++p) {
-                    const u32x2 x = __builtin_bit_cast(u32x2, v[0][p]), y = __builtin_bit_cast(u32x2, v[1][p]);
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(x[0], y[0], false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(x[1], y[1], false, false);
-                    *(u32x4*)(out + Planes<T::kP>::at(m, p)) = u32x4{s0[0], s1[0], s0[1], s1[1]};
-                }
-            }
+        const int first = m0 + t.row(0, 0) - 4 * h;  // of this wave's rows
+        const bool plain = first + T::kWM <= a.vocab && !__any(entry >= first && entry < first + T::kWM);
+        if (plain)
+            grad_column<true>(t, a, j, n, m0, lse, scale, alpha, entry, value);
+        else
+            grad_column<false>(t, a, j, n, m0, lse, scale, alpha, entry, value);
     }
 }
 

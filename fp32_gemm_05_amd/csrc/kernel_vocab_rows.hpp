@@ -442,24 +442,24 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
     const int n = rows ? *count : tokens, tx = threadIdx.x % TX, ty = threadIdx.x / TX, i0 = blockIdx.x * TX, i = i0 + tx;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (i0 >= n) return;
-    const auto larger = [](float a, float b) { return b > a || b != b ? b : a; };  // a NaN stays
     float top = -INFINITY;
     if (i < n)
 #pragma unroll 8
-        for (int p = ty; p < parts; p += TY) top = larger(top, part[(size_t)p * tp + i].x);
+        for (int p = ty; p < parts; p += TY) top = fmaxf(top, part[(size_t)p * tp + i].x);
 #pragma unroll
-    for (int o = TX; o < 64; o *= 2) top = larger(top, __shfl_xor(top, o));
+    for (int o = TX; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
     if (lane < TX) slot[wave][tx] = top;
     __syncthreads();
 #pragma unroll
-    for (int y = 0; y < 16; ++y) top = larger(top, slot[y][tx]);
+    for (int y = 0; y < 16; ++y) top = fmaxf(top, slot[y][tx]);
     __syncthreads();
+    const float ref = top == -INFINITY ? 0.f : top;  // nothing but -inf: the sum is 0, or a NaN among its parts
     float sum = 0.f;
-    if (i < n && top != -INFINITY)
+    if (i < n)
 #pragma unroll 8
         for (int p = ty; p < parts; p += TY) {
             const float2 v = part[(size_t)p * tp + i];
-            sum += v.y * expf(v.x - top);
+            sum += v.y * expf(v.x - ref);
         }
 #pragma unroll
     for (int o = TX; o < 64; o *= 2) sum += __shfl_xor(sum, o);

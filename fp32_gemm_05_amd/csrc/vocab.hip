@@ -55,15 +55,32 @@ struct Layout {
 constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
-// Tile shapes: the large one when it fills the chip, else the small one.
+// Tile shapes.  The large one has a compute unit to itself, of the others two share one.
 template <int P>
 using Big = Tile<P, 256, 256, 128, 64, 3, 2>;
 template <int P>
+using Mid = Tile<P, 128, 128, 64, 32, 2, 2>;
+template <int P>
 using Small = Tile<P, 128, 64, 64, 32, 3, 3>;
+enum Shape { SMALL, MID, BIG };
 
-template <class B>
-bool fills(long rows_m, long rows_n) {
-    return up(rows_m, B::kBM) / B::kBM * (up(rows_n, B::kBN) / B::kBN) >= 192;
+// The shape for a product of rows_m x rows_n: the one whose rounds over the chip's 256 compute units
+// take least.  A round costs the area that a compute unit works on over the rate that the shape reaches
+// in long products (2048 tokens, 32768 x 2048: the middle one 0.92 of the large one's in fp32 and 0.82
+// in bf16, the small one 0.77 and 0.68); a last round that leaves each unit one tile of two takes 0.6
+// of a round's time.  Measured (fp32, forward product, us, small/middle/large): 1362 tokens, 15116 x 444:
+// 68, 60, 70; 500 tokens, 60000 x 256: 60, 52, 49; 300 tokens, 20000 x 1000: 55, 53, 74; 2142 tokens,
+// 576 x 3392: 50, 77, -.
+Shape shape_of(int P, long rows_m, long rows_n) {
+    auto cost = [&](long bm, long bn, int places, double rate) {
+        const long tiles = up(rows_m, bm) / bm * (up(rows_n, bn) / bn), slots = 256L * places;
+        const long full = tiles / slots, rest = tiles - full * slots;
+        const double last = rest == 0 ? 0 : places > 1 && rest <= 256 ? 0.6 : 1;
+        return (full + last) * places * bm * bn / rate;
+    };
+    const double small = cost(128, 64, 2, P == 2 ? 0.77 : 0.68), mid = cost(128, 128, 2, P == 2 ? 0.92 : 0.82);
+    const double big = cost(256, 256, 1, 1);
+    return big <= mid && big <= small ? BIG : mid < small ? MID : SMALL;
 }
 
 Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
@@ -246,9 +263,11 @@ int run_few(const Call& c) {
 }
 
 template <int P, class F>
-void by_size(bool big, F f) {
-    if (big)
+void by_shape(Shape shape, F f) {
+    if (shape == BIG)
         f((Big<P>*)nullptr);
+    else if (shape == MID)
+        f((Mid<P>*)nullptr);
     else
         f((Small<P>*)nullptr);
 }
@@ -302,7 +321,7 @@ int run(const Call& c) {
         if (c.T == 0) {
             // only dW, which is 0, is left to do
         } else if (!c.grad) {
-            by_size<P>(fills<Big<P>>(vn, c.T), [&](auto* shape) {
+            by_shape<P>(shape_of(P, vn, c.T), [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(vn, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
                 const LseArgs a{w, x, count, w_unit, x_unit, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part,
@@ -312,7 +331,7 @@ int run(const Call& c) {
             });
             continue;
         } else {
-            by_size<P>(fills<Big<P>>(vn, c.T), [&](auto* shape) {
+            by_shape<P>(shape_of(P, vn, c.T), [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
                 const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
@@ -324,15 +343,16 @@ int run(const Call& c) {
             if (c.e.teacher)
                 vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
                     c.e, c.T, v0, vn, pos, floats(l.value), floats(l.weight), x_unit, x_most, ws + l.d, d_pitch);
-            if (c.dX)
-                by_size<P>(l.dx_big, [&](auto* shape) {
-                    using S = typename std::remove_pointer<decltype(shape)>::type;
-                    const DxArgs a{w, d, count, w_unit, l.cut, (int)up(vn, Pl::BK) / Pl::BK, floats(l.acc), l.hp, p > 0};
-                    vocab_dx_kernel<S><<<l.cut.groups, S::NT, 0, st>>>(a);
-                });
+            if (c.dX) {
+                const DxArgs a{w, d, count, w_unit, l.cut, (int)up(vn, Pl::BK) / Pl::BK, floats(l.acc), l.hp, p > 0};
+                if (l.dx_big)
+                    vocab_dx_kernel<Big<P>><<<l.cut.groups, Big<P>::NT, 0, st>>>(a);
+                else
+                    vocab_dx_kernel<Small<P>><<<l.cut.groups, Small<P>::NT, 0, st>>>(a);
+            }
         }
         if (c.dW)
-            by_size<P>(fills<Big<P>>(c.H, vn), [&](auto* shape) {
+            by_shape<P>(shape_of(P, c.H, vn), [&](auto* shape) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(vn, S::kBN) / S::kBN;
                 T* out = (T*)c.dW + (size_t)v0 * c.lddw;

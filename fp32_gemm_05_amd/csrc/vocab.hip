@@ -162,8 +162,8 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     l.piece = (int)(vp < 1L << 21 ? vp : 1L << 21);
     l.pieces = (int)((vp + l.piece - 1) / l.piece);
     l.vp = l.piece;
-    // dX's pass over W in enough parts to fill the chip four times, each of 4 or 8 steps or more
-    const long strips = l.hp / (16 * he), most = l.vp / 128;
+    // dX's pass over W in enough parts to fill the chip four times, each of 8 or 16 steps or more
+    const long strips = l.hp / (16 * he), most = l.vp / 256;
     const long s = 1024 / strips < most ? 1024 / strips : most;
     l.splits = (int)(s < 1 ? 1 : s);
     long at = 0;
@@ -232,11 +232,11 @@ int run_few(const Call& c, const FewLayout& l) {
         if (c.e.teacher)
             vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
                 c.e, c.T, v0, vn, nullptr, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
-        // dW: 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but four
+        // dW: 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but two
         // groups or more: a wave reads its rows' D first
         const long row_groups = up(vn, 256) / 256, all = up(c.H, 8 * C::HE) / (8 * C::HE);
         const long cols = 2048 / row_groups < 1 ? 1 : 2048 / row_groups;
-        const long even = (all + cols - 1) / cols, own = even < 4 ? 4 : even;
+        const long even = (all + cols - 1) / cols, own = even < 2 ? 2 : even;
         const int strips = c.dX ? (int)(l.hp / (16 * C::HE)) : 0;
         const FewGradArgs g{floats(l.d), l.vp, c.T, vn, c.H, Wp, c.ldw, strips, l.splits, floats(l.acc), (int)l.hp,
                             p > 0, ws + l.xtf, (int)own, (int)row_groups, (T*)c.dW + (size_t)v0 * c.lddw, c.lddw};

@@ -13,6 +13,7 @@ contiguous copy is asked for where rows overlap).  ``vocab_cross_entropy`` and
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -61,35 +62,40 @@ def _raise(code, name):
     raise error
 
 
-def _call(name, *args):
-    rc = _entry(name)(*args)
-    if rc != 0:
-        _raise(rc, name)
-
-
 def vocab_workspace(dtype, grad: bool, T: int, V: int, H: int, K: int = 0) -> int:
     """Bytes of workspace of a call (K = 0: cross entropy, else the teacher's entries per token)."""
-    n = _entry("vocab_workspace")(_TYPES[dtype], int(grad), int(T), int(V), int(H), int(K))
+    return _workspace(dtype, bool(grad), int(T), int(V), int(H), int(K))
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(dtype, grad, T, V, H, K):
+    n = _entry("vocab_workspace")(_TYPES[dtype], grad, T, V, H, K)
     if n < 0:
         _raise(n, "vocab_workspace")
     return n
 
 
+# The checks and calls below take about as long as two kernel launches, which is what a small problem
+# takes in all: attributes are read once, and no stream or device context is entered without need.
+
 def _matrix(t, name, dtype=None):
+    """Checks a 2-D device tensor with unit column stride; returns (rows, columns, leading dimension)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dim() != 2 or (t.dtype not in _TYPES if dtype is None else t.dtype != dtype):
         want = "float32 or bfloat16" if dtype is None else str(dtype).replace("torch.", "")
         raise TypeError(f"{name} must be a 2-D {want} tensor")
     _require_device(t, name)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and unit != 1:
         raise ValueError(f"{name} must be row-major with unit column stride")
-    if t.shape[0] <= 1 or t.shape[1] == 0:
-        return max(1, t.shape[1])  # one row, or no element: no stride is addressed
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} has row stride {t.stride(0)} below its row length {t.shape[1]} "
+    if rows <= 1 or cols == 0:
+        ld = cols if cols > 1 else 1  # one row, or no element: no stride is addressed
+    elif ld < cols:
+        raise ValueError(f"{name} has row stride {ld} below its row length {cols} "
                          f"(a broadcast or overlapping view); pass a contiguous copy")
-    return t.stride(0)
+    return rows, cols, ld
 
 
 def _vector(t, name, dtype, n):
@@ -112,59 +118,58 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 class _Problem:
     """The checked operands that every call has, and what they share."""
 
+    __slots__ = ("T", "V", "H", "K", "dtype", "device", "head", "matrices", "alpha", "context")
+
     def __init__(self, X, W, alpha, stream, entries=0):
-        ldx, ldw = _matrix(X, "X"), _matrix(W, "W", X.dtype if isinstance(X, torch.Tensor) else None)
-        self.T, self.H = X.shape
-        self.V, H = W.shape
+        self.T, self.H, ldx = _matrix(X, "X")
+        self.dtype = X.dtype
+        self.V, H, ldw = _matrix(W, "W", self.dtype)
         if self.H != H:
             raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
         if self.V < 1 or H < 1:
             raise ValueError(f"W {tuple(W.shape)} has no element")
         self.K = entries
-        self.dtype, self.device = X.dtype, X.device
-        self.head = (_TYPES[X.dtype], self.T, self.V, self.H)
+        self.device = X.device
+        self.head = (_TYPES[self.dtype], self.T, self.V, H)
         self.matrices = (X.data_ptr(), ldx, W.data_ptr(), ldw)
         self.alpha = float(alpha)
-        self.stream = stream
-        self.same_device((W, "W"))
-
-    def __enter__(self):
-        """Results and workspace are allocated on the stream that uses them."""
+        self.same_device(W, "W")
+        # results and workspace are allocated on the stream that uses them
         self.context = None
-        stream, index = self.stream, self.device.index
         if stream is not None:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device=self.device)
             self.context = torch.cuda.stream(stream)
-        elif index != torch.cuda.current_device():
+        elif self.device.index != torch.cuda.current_device():
             self.context = torch.cuda.device(self.device)
-        if self.context is not None:
-            self.context.__enter__()
-        self.handle = _current_handle(index)
-        return self
 
-    def __exit__(self, *exc):
-        if self.context is not None:
-            self.context.__exit__(*exc)
+    def same_device(self, t, name):
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, X on {self.device}")
 
-    def same_device(self, *named):
-        for t, name in named:
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, X on {self.device}")
+    def vector(self, t, name, dtype=torch.float32):
+        _vector(t, name, dtype, self.T)
+        self.same_device(t, name)
+
+    def run(self, body):
+        if self.context is None:
+            return body()
+        with self.context:
+            return body()
 
     def new(self, *shape, dtype=torch.float32):
         return torch.empty(shape, dtype=dtype, device=self.device)
 
     def workspace(self, grad):
+        """Kept by the caller until the call has enqueued its work; the stream's own pool takes it back."""
         n = vocab_workspace(self.dtype, grad, self.T, self.V, self.H, self.K)
-        return self.new(n, dtype=torch.uint8), n
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
 
-
-def _ce(X, W, target, alpha, stream):
-    p = _Problem(X, W, alpha, stream)
-    _vector(target, "target", torch.int64, p.T)
-    p.same_device((target, "target"))
-    return p
+    def call(self, name, work, *args):
+        rc = (_entries.get(name) or _entry(name))(*args, work.data_ptr(), work.numel(),
+                                                  _current_handle(self.device.index))
+        if rc != 0:
+            _raise(rc, name)
 
 
 def vocab_ce(X, W, target, alpha: float = 1.0, ignore_index: int = -100, stream=None):
@@ -172,53 +177,55 @@ def vocab_ce(X, W, target, alpha: float = 1.0, ignore_index: int = -100, stream=
 
     Tokens whose target is ignore_index have loss 0 and lse 0; a target outside the vocabulary
     gives NaN."""
-    p = _ce(X, W, target, alpha, stream)
-    with p:
+    p = _Problem(X, W, alpha, stream)
+    p.vector(target, "target", torch.int64)
+
+    def body():
         loss, lse = p.new(p.T), p.new(p.T)
-        work, n = p.workspace(False)
-        _call("vocab_ce", *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index), loss.data_ptr(),
-              lse.data_ptr(), work.data_ptr(), n, p.handle)
-    return loss, lse
+        p.call("vocab_ce", p.workspace(False), *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index),
+               loss.data_ptr(), lse.data_ptr())
+        return loss, lse
+    return p.run(body)
 
 
-def _outputs(p, want_dx, want_dw):
+def _gradients(p, want_dx, want_dw, name, *args):
+    """Allocates the wanted gradients, and calls `name` with args and them."""
     if not (want_dx or want_dw):
         raise ValueError("neither dX nor dW is wanted")
-    return (p.new(p.T, p.H, dtype=p.dtype) if want_dx else None,
-            p.new(p.V, p.H, dtype=p.dtype) if want_dw else None)
 
-
-def _out_args(p, dX, dW, work, n):
-    return (None if dX is None else dX.data_ptr(), p.H, None if dW is None else dW.data_ptr(), p.H,
-            work.data_ptr(), n, p.handle)
+    def body():
+        dX = p.new(p.T, p.H, dtype=p.dtype) if want_dx else None
+        dW = p.new(p.V, p.H, dtype=p.dtype) if want_dw else None
+        p.call(name, p.workspace(True), *args, None if dX is None else dX.data_ptr(), p.H,
+               None if dW is None else dW.data_ptr(), p.H)
+        return dX, dW
+    return p.run(body)
 
 
 def vocab_ce_grad(X, W, target, lse, dloss, alpha: float = 1.0, ignore_index: int = -100, want_dx: bool = True,
                   want_dw: bool = True, stream=None):
     """Gradients (dX, dW) of sum(dloss * loss), from the lse of vocab_ce; one that is not wanted is None
     and costs no product."""
-    p = _ce(X, W, target, alpha, stream)
-    _vector(lse, "lse", torch.float32, p.T)
-    _vector(dloss, "dloss", torch.float32, p.T)
-    p.same_device((lse, "lse"), (dloss, "dloss"))
-    with p:
-        dX, dW = _outputs(p, want_dx, want_dw)
-        work, n = p.workspace(True)
-        _call("vocab_ce_grad", *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index), lse.data_ptr(),
-              dloss.data_ptr(), *_out_args(p, dX, dW, work, n))
-    return dX, dW
+    p = _Problem(X, W, alpha, stream)
+    p.vector(target, "target", torch.int64)
+    p.vector(lse, "lse")
+    p.vector(dloss, "dloss")
+    return _gradients(p, want_dx, want_dw, "vocab_ce_grad", *p.head, p.alpha, *p.matrices, target.data_ptr(),
+                      int(ignore_index), lse.data_ptr(), dloss.data_ptr())
 
 
 def _distill(X, W, index, teacher, alpha, stream):
-    ldi, ldt = _matrix(index, "index", torch.int64), _matrix(teacher, "teacher", torch.float32)
-    if index.shape != teacher.shape:
+    rows, k, ldi = _matrix(index, "index", torch.int64)
+    rows_t, k_t, ldt = _matrix(teacher, "teacher", torch.float32)
+    if (rows, k) != (rows_t, k_t):
         raise ValueError(f"shape mismatch: index {tuple(index.shape)}, teacher {tuple(teacher.shape)}")
-    if index.shape[1] < 1:
+    if k < 1:
         raise ValueError("index has no entry")
-    p = _Problem(X, W, alpha, stream, index.shape[1])
-    if index.shape[0] != p.T:
-        raise ValueError(f"index has {index.shape[0]} rows for {p.T} tokens")
-    p.same_device((index, "index"), (teacher, "teacher"))
+    p = _Problem(X, W, alpha, stream, k)
+    if rows != p.T:
+        raise ValueError(f"index has {rows} rows for {p.T} tokens")
+    p.same_device(index, "index")
+    p.same_device(teacher, "teacher")
     return p, (index.data_ptr(), ldi, teacher.data_ptr(), ldt)
 
 
@@ -229,29 +236,26 @@ def vocab_distill(X, W, index, teacher, alpha: float = 1.0, teacher_alpha: float
     no entry, and a token without entries has loss 0.  picked (T x K) holds the student's logits at
     the entries, which the gradient takes back."""
     p, entries = _distill(X, W, index, teacher, alpha, stream)
-    with p:
+
+    def body():
         loss, lse, picked = p.new(p.T), p.new(p.T), p.new(p.T, p.K)
-        work, n = p.workspace(False)
-        _call("vocab_distill", *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries, loss.data_ptr(),
-              lse.data_ptr(), picked.data_ptr(), work.data_ptr(), n, p.handle)
-    return loss, lse, picked
+        p.call("vocab_distill", p.workspace(False), *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries,
+               loss.data_ptr(), lse.data_ptr(), picked.data_ptr())
+        return loss, lse, picked
+    return p.run(body)
 
 
 def vocab_distill_grad(X, W, index, teacher, lse, picked, dloss, alpha: float = 1.0, teacher_alpha: float = 1.0,
                        want_dx: bool = True, want_dw: bool = True, stream=None):
     """Gradients (dX, dW) of sum(dloss * loss), from the lse and picked of vocab_distill."""
     p, entries = _distill(X, W, index, teacher, alpha, stream)
-    _vector(lse, "lse", torch.float32, p.T)
-    _vector(dloss, "dloss", torch.float32, p.T)
-    if _matrix(picked, "picked", torch.float32) != p.K or tuple(picked.shape) != (p.T, p.K):
+    p.vector(lse, "lse")
+    p.vector(dloss, "dloss")
+    if _matrix(picked, "picked", torch.float32) != (p.T, p.K, p.K):
         raise ValueError("picked must be the contiguous T x K tensor of vocab_distill")
-    p.same_device((lse, "lse"), (dloss, "dloss"), (picked, "picked"))
-    with p:
-        dX, dW = _outputs(p, want_dx, want_dw)
-        work, n = p.workspace(True)
-        _call("vocab_distill_grad", *p.head, p.K, p.alpha, float(teacher_alpha), *p.matrices, *entries,
-              lse.data_ptr(), picked.data_ptr(), dloss.data_ptr(), *_out_args(p, dX, dW, work, n))
-    return dX, dW
+    p.same_device(picked, "picked")
+    return _gradients(p, want_dx, want_dw, "vocab_distill_grad", *p.head, p.K, p.alpha, float(teacher_alpha),
+                      *p.matrices, *entries, lse.data_ptr(), picked.data_ptr(), dloss.data_ptr())
 
 
 class _CrossEntropy(torch.autograd.Function):

@@ -178,12 +178,13 @@ __device__ inline void few_transpose(const FewArgs& a, int i) {
 // z of 16 MR vocabulary rows and all tokens.  The four waves of a workgroup take every fourth U steps
 // of the hidden size each, so that even a small vocabulary keeps many loads in flight, and add up in
 // LDS; 16 B chunks of a row make 64-byte runs a step, U of them in a row.
-template <class C, int NB, bool GRAD>
+template <class C, int NB, int MR, bool GRAD>
 __global__ void __launch_bounds__(256) vocab_few_logits_kernel(FewArgs a) {
     typedef typename C::T T;
     typedef typename C::Raw Raw;
     typedef typename C::Part Part;
-    constexpr int MR = NB == 4 ? 4 : 2, U = C::P == 3 ? 1 : NB == 4 ? 2 : 4;
+    // steps whose loads are held in registers at once
+    constexpr int U = C::P == 3 ? (NB == 4 && MR == 2 ? 2 : 1) : MR == 4 ? 2 : 4;
     // all loads before the first MFMA, where the compiler would keep too few in flight; the long fp32 runs
     // of NB > 1 do better with loads between them
     constexpr bool HOLD = sizeof(T) == 2 || NB == 1;

@@ -149,8 +149,6 @@ struct FewLayout {
     long hb, hp, vp, z, scale, weight, value, xtf, d, part, acc, bytes;
 };
 
-int few_rows(int nb) { return nb == 4 ? 64 : 32; }  // vocabulary rows of a workgroup
-
 FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     FewLayout l{};
     l.nb = T > 32 ? 4 : T > 16 ? 2 : 1;
@@ -203,7 +201,11 @@ int run_few(const Call& c, const FewLayout& l) {
     auto floats = [&](long at) { return (float*)(ws + at); };
     const T* W = (const T*)c.W;
     const hipStream_t st = c.stream;
-    const int per = few_rows(NB);
+    // vocabulary rows of a workgroup's logits: 64 where three in four compute units get one (40 tokens,
+    // fp32 20000 x 2000: 67 us against 88 us with 32, as the tokens' side is read and cut half as often),
+    // 32 where they do not (40 tokens, fp32 2000 x 300: 13 us against 8 us)
+    const bool wide = NB == 4 && c.V >= 64 * 192;
+    const int per = wide ? 64 : 32;
     (void)hipGetLastError();
 
     float* const z = c.e.teacher ? c.picked_out : floats(l.z);
@@ -223,12 +225,19 @@ int run_few(const Call& c, const FewLayout& l) {
         const FewArgs a{c.e, c.T, c.X, Wp, c.ldx, c.ldw, vn, c.H, groups, c.V, c.alpha, v0,
                         (float2*)(ws + l.part) + (size_t)part * kFewTokens, z, c.lse, c.dloss, floats(l.scale),
                         floats(l.d), l.vp, ws + l.xtf, l.kt, chunks};
+        const unsigned blocks = groups + (chunks + 255) / 256;
+        if (c.grad && wide)
+            vocab_few_logits_kernel<C, NB, NB == 4 ? 4 : 2, true><<<blocks, 256, 0, st>>>(a);
+        else if (c.grad)
+            vocab_few_logits_kernel<C, NB, 2, true><<<blocks, 256, 0, st>>>(a);
+        else if (wide)
+            vocab_few_logits_kernel<C, NB, NB == 4 ? 4 : 2, false><<<blocks, 256, 0, st>>>(a);
+        else
+            vocab_few_logits_kernel<C, NB, 2, false><<<blocks, 256, 0, st>>>(a);
         if (!c.grad) {
-            vocab_few_logits_kernel<C, NB, false><<<groups, 256, 0, st>>>(a);
             part += groups;
             continue;
         }
-        vocab_few_logits_kernel<C, NB, true><<<groups + (chunks + 255) / 256, 256, 0, st>>>(a);
         if (c.e.teacher)
             vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
                 c.e, c.T, v0, vn, nullptr, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);

@@ -42,19 +42,6 @@ struct Call {
 
 long up(long x, long to) { return (x + to - 1) / to * to; }
 
-// The workspace: byte offsets of its arrays for a call's sizes (the pointers of the call are not
-// looked at, so that its size can be asked for beforehand).
-struct Layout {
-    int tp, hk, hp;     // padded tokens, hidden as a product's k, hidden as a product's rows
-    int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces
-    DxCut cut;
-    bool dx_big;
-    long count, rows, pos, z, scale, weight, x_unit, x_most, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
-};
-
-constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
-constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
-
 // Tile shapes.  The large one has a compute unit to itself, of the others two share one.
 template <int P>
 using Big = Tile<P, 256, 256, 128, 64, 3, 2>;
@@ -63,6 +50,19 @@ using Mid = Tile<P, 128, 128, 64, 32, 2, 2>;
 template <int P>
 using Small = Tile<P, 128, 64, 64, 32, 3, 3>;
 enum Shape { SMALL, MID, BIG };
+
+// The workspace: byte offsets of its arrays for a call's sizes (the pointers of the call are not
+// looked at, so that its size can be asked for beforehand).
+struct Layout {
+    int tp, hk, hp;     // padded tokens, hidden as a product's k, hidden as a product's rows
+    int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces
+    DxCut cut;
+    Shape dx_shape;
+    long count, rows, pos, z, scale, weight, x_unit, x_most, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
+};
+
+constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
+constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
 // The shape for a product of rows_m x rows_n: the one whose rounds over the chip's 256 compute units
 // take least.  A round costs the area that a compute unit works on over the rate that the shape reaches
@@ -103,16 +103,24 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     l.piece = (int)up((vp + pieces - 1) / pieces, 256);
     l.pieces = (int)((vp + l.piece - 1) / l.piece);
     // dX's workgroups: its tiles, or about as many as the chip has places for (one large tile a
-    // compute unit, two small ones), with 8 slabs or more each; large tiles if they fill most places
+    // compute unit, two of the others), with 8 slabs or more each.  Large tiles if they fill most places
+    // and cover no more than the middle ones do; these if each place gets 600 vocabulary rows of a tile
+    // or more, as the small ones have less to fill and to sum at the ends.  Measured (dX and its sum,
+    // fp32, us, small/middle/large): 1001 tokens, 50021 x 1000: 342, 292, 271; 500 tokens, 60000 x 256:
+    // 98, 86, 71; 777 tokens, 5003 x 1001: 40, 42, 52; 300 tokens, 20000 x 1000: 73, 68, 80; 128 tokens,
+    // 30000 x 2048: 89, 78, -; 1340 tokens, 3070 x 174: 18, 22, -.
     const int slabs = l.piece / bk, most_cuts = slabs / 8 > 1 ? slabs / 8 : 1;
     auto cut = [&](int bm, int bn, int places) {
         const int tiles_m = (int)(up(H, bm) / bm), tiles = tiles_m * (int)(up(l.tp, bn) / bn);
         return DxCut{tiles_m, bn, tiles > places ? tiles : places / tiles * tiles, most_cuts};
     };
-    l.cut = cut(Big<1>::kBM, Big<1>::kBN, 256);
-    const long filled = up(H, Big<1>::kBM) / Big<1>::kBM * (up(T, Big<1>::kBN) / Big<1>::kBN) * most_cuts;
-    l.dx_big = T > 128 && H > 128 && filled >= 192;
-    if (!l.dx_big) l.cut = cut(Small<1>::kBM, Small<1>::kBN, 512);
+    const long large = up(H, 256) * up(T, 256), middle = up(H, 128) * up(T, 128);
+    if (T > 128 && H > 128 && large / (256 * 256) * most_cuts >= 192 && middle * 10 > large * 9)
+        l.dx_shape = BIG, l.cut = cut(256, 256, 256);
+    else if ((double)middle * l.piece >= 600. * 512 * 128 * 128)
+        l.dx_shape = MID, l.cut = cut(128, 128, 512);
+    else
+        l.dx_shape = SMALL, l.cut = cut(128, 64, 512);
     long at = 0;
     auto take = [&](long bytes) {
         const long o = at;
@@ -354,10 +362,10 @@ int run(const Call& c) {
                     c.e, c.T, v0, vn, pos, floats(l.value), floats(l.weight), x_unit, x_most, ws + l.d, d_pitch);
             if (c.dX) {
                 const DxArgs a{w, d, count, w_unit, l.cut, (int)up(vn, Pl::BK) / Pl::BK, floats(l.acc), l.hp, p > 0};
-                if (l.dx_big)
-                    vocab_dx_kernel<Big<P>><<<l.cut.groups, Big<P>::NT, 0, st>>>(a);
-                else
-                    vocab_dx_kernel<Small<P>><<<l.cut.groups, Small<P>::NT, 0, st>>>(a);
+                by_shape<P>(l.dx_shape, [&](auto* shape) {
+                    using S = typename std::remove_pointer<decltype(shape)>::type;
+                    vocab_dx_kernel<S><<<l.cut.groups, S::NT, 0, st>>>(a);
+                });
             }
         }
         if (c.dW)
@@ -365,7 +373,7 @@ int run(const Call& c) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 const int tm = (int)up(c.H, S::kBM) / S::kBM, tn = (int)up(vn, S::kBN) / S::kBN;
                 T* out = (T*)c.dW + (size_t)v0 * c.lddw;
-                    const DwArgs a{x_dw, d, count, x_most, tm, tn, c.H, vn, out, c.lddw};
+                const DwArgs a{x_dw, d, count, x_most, tm, tn, c.H, vn, out, c.lddw};
                 vocab_dw_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
     }

@@ -186,6 +186,15 @@ def test_several_pieces_of_the_vocabulary(dtype, T, V, H):
     run_distill(X, W, index, teacher, dloss, 0.5, 0.8, dtype)
 
 
+# few whole large tiles, and enough vocabulary for middle ones in dX: in one piece, and in two
+@pytest.mark.parametrize("dtype,T,V,H", [("bf16", 300, 20000, 1000), ("f32", 300, 20000, 1000),
+                                         ("bf16", 1100, 300001, 100), ("f32", 1100, 150001, 100)])
+def test_dx_in_middle_tiles(dtype, T, V, H):
+    X, W, target, dloss, g = inputs(T, V, H, dtype, 21)
+    target[torch.rand(T, generator=g, device="cuda") < 0.3] = -100
+    run_ce(X, W, target, dloss, 1.0, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [7, 100])
 def test_offsets_past_32_bits(dtype, T):

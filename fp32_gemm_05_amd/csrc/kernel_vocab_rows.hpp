@@ -267,12 +267,12 @@ __global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
     if (threadIdx.x == 0) a.w_part[b] = m;
 }
 
-// Four values of a row that has `cols`, zero past them (and where there is no row).
-template <typename T>
-__device__ inline void load_row(const T* s, int k, int cols, float (&v)[4]) {
-    if (s && k + 4 <= cols) return load(s + k, v);
+// N values of a row that has `cols`, zero past them (and where there is no row).
+template <typename T, int N>
+__device__ inline void load_row(const T* s, int k, int cols, float (&v)[N]) {
+    if (s && k + N <= cols) return load(s + k, v);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = s && k + q < cols ? (float)s[k + q] : 0.f;
+    for (int q = 0; q < N; ++q) v[q] = s && k + q < cols ? (float)s[k + q] : 0.f;
 }
 
 struct PackArgs {
@@ -291,15 +291,14 @@ struct PackArgs {
     // W: `vocab` rows, and zero rows to the next multiple of 256
     const void* w;
     long ldw;
-    int vocab;
+    int vocab, w_rows;    // w_rows of them by one workgroup
     char* w_out;
     // P = 2: in the power of two of its largest value (w_parts maxima), w_unit[0] what a packed unit
-    // stands for; w_parts 0: each row in its own, w_unit[row]
+    // stands for; by row: each row in its own, w_unit[row]
     const float* w_part;
     int w_parts;
     float* w_unit;
 };
-constexpr int kPackRows = 8;  // of W by one workgroup
 
 template <typename T, int P>
 __device__ inline void pack_x(const PackArgs& a, int i) {
@@ -389,43 +388,80 @@ __device__ inline void pack_w_row(const PackArgs& a, int i) {
     if (lane == 0) a.w_unit[i] = ldexpf(1.f, -e);
 }
 
-// The packed operands, in one launch: x_blocks workgroups take a row of X each, the rest kPackRows
-// rows of W.
-template <typename T, int P>
+// Rows of W for one workgroup: 4, in bf16 as many as give each thread 8 values (a power of two; 400
+// tokens, 60000 x 100: 15 us, with 4 rows 23).  In fp32 that many are no faster (45 us either way), and
+// a number that the kernel does not know costs it 28 us of 137 (1001 tokens, 50021 x 1000).
+constexpr int kPackRows = 4;
+template <int P>
+__host__ inline int pack_rows(int kp) {
+    int rows = kPackRows;
+    while (P == 1 && rows < 32 && 2 * rows * kp <= 2048) rows *= 2;
+    return rows;
+}
+
+// The packed operands, in one launch: x_blocks workgroups take a row of X each, the rest w_rows rows
+// of W.  Bound by memory: 200 MB read and 200 MB written (1001 tokens, 50021 x 1000, fp32) take 135 us
+// where a copy of that size, after kernels that left the caches full of results, takes 96.
+template <typename T, int P, bool BY_ROW>
 __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
     if ((int)blockIdx.x < a.x_blocks) return pack_x<T, P>(a, blockIdx.x);
-    const int b = blockIdx.x - a.x_blocks;
+    const int w_rows = P == 2 ? kPackRows : a.w_rows, row0 = (blockIdx.x - a.x_blocks) * w_rows;
+    if constexpr (BY_ROW) {
+        static_assert(kPackRows == 4, "a wave a row");
+        pack_w_row<T>(a, row0 + (threadIdx.x >> 6));
+        return;
+    }
+    // the workgroup's rows as one line of chunks of 8 values, the first chunk read before the search
+    // for the unit
+    const uint32_t per = (uint32_t)a.kp / 8, chunks = per * w_rows;
+    const T* s = (const T*)a.w + (size_t)row0 * a.ldw;
+    char* out = a.w_out + (size_t)row0 * a.pitch;
+    float v[8];
+    uint32_t at = 0;
+    auto fetch = [&](uint32_t i) {
+        const int r = (int)(i / per), k = (int)(i - r * per) * 8;
+        at = (uint32_t)(r * a.pitch) + (uint32_t)Planes<P>::at(k, 0);
+        load_row(row0 + r < a.vocab ? s + r * a.ldw : nullptr, k, a.cols, v);
+    };
+    uint32_t i = threadIdx.x;
+    if (i < chunks) fetch(i);
     float f = 1.f;
     if constexpr (P == 2) {
-        if (a.w_parts == 0) {
-            for (int r = threadIdx.x >> 6; r < kPackRows; r += 4) pack_w_row<T>(a, b * kPackRows + r);
-            return;
-        }
         float m = 0.f;
-        for (int i = threadIdx.x; i < a.w_parts; i += 256) m = fmaxf(m, a.w_part[i]);
+        for (int j = threadIdx.x; j < a.w_parts; j += 256) m = fmaxf(m, a.w_part[j]);
         const int e = scale_exponent(block_max(m));
         f = ldexpf(1.f, e);
-        if (b == 0 && threadIdx.x == 0) *a.w_unit = ldexpf(1.f, -e);
+        if (row0 == 0 && threadIdx.x == 0) *a.w_unit = ldexpf(1.f, -e);
     }
-    const bool whole = (b + 1) * kPackRows <= a.vocab;
-    const T* s = (const T*)a.w + (size_t)b * kPackRows * a.ldw;
-    for (int k = threadIdx.x * 4; k < a.kp; k += 1024) {
-        float v[kPackRows][4];
-        if (whole && k + 4 <= a.cols) {  // all rows' loads together
+    for (;;) {
+        if (i >= chunks) break;
+        typename Planes<P>::Half8 o[P];
 #pragma unroll
-            for (int r = 0; r < kPackRows; ++r) load(s + r * a.ldw + k, v[r]);
+        for (int j = 0; j < 8; ++j) {
+            typename Planes<P>::Half x[P];
+            split<P>(P == 2 ? v[j] * f : v[j], x);
+#pragma unroll
+            for (int p = 0; p < P; ++p) o[p][j] = x[p];
+        }
+        if constexpr (P == 1) {
+            *(typename Planes<P>::Half8*)(out + at) = o[0];
         } else {
+            // Four lanes hold the two planes of a slab: with the next four they trade halves, so that
+            // each store writes whole lines of 128 bytes.  chunks is a multiple of 8: both have one.
+            // Stored past the caches: the products read it from memory either way (135 us; cached 141).
+            typedef int Int4 __attribute__((ext_vector_type(4)));
+            const bool odd = threadIdx.x & 4;
+            const Int4 hi = __builtin_bit_cast(Int4, o[0]), lo = __builtin_bit_cast(Int4, o[P - 1]);
+            Int4 other;
 #pragma unroll
-            for (int r = 0; r < kPackRows; ++r)
-                load_row(b * kPackRows + r < a.vocab ? s + r * a.ldw : nullptr, k, a.cols, v[r]);
+            for (int j = 0; j < 4; ++j) other[j] = __shfl_xor(odd ? hi[j] : lo[j], 4);
+            const uint32_t from = __shfl_xor((int)at, 4);
+            __builtin_nontemporal_store(odd ? other : hi, (Int4*)(out + (odd ? from + 64 : at)));
+            __builtin_nontemporal_store(odd ? lo : other, (Int4*)(out + (odd ? at + 64 : from)));
         }
-#pragma unroll
-        for (int r = 0; r < kPackRows; ++r) {
-            if constexpr (P == 2)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[r][q] *= f;
-            store4<P>(a.w_out + (size_t)(b * kPackRows + r) * a.pitch, k, v[r]);
-        }
+        i += 256;
+        if (i >= chunks) break;
+        fetch(i);
     }
 }
 

@@ -330,10 +330,15 @@ int run(const Call& c) {
         if (!direct) w = Operand{ws + l.w, (uint32_t)x_pitch, (uint32_t)x_pitch, (int)up(vn, 256)};
         if (p == 0 || !direct) {
             const int x_blocks = p == 0 ? l.tp : 0;
+            const int w_rows = pack_rows<P>(l.hk);
             const PackArgs pack{c.H, l.hk, x_pitch, c.X, c.ldx, rows, count, x_blocks, ws + l.x,
                                 c.grad ? floats(l.weight) : nullptr, xs, x_unit, (uint32_t*)x_most,
-                                Wp, c.ldw, vn, ws + l.w, floats(l.w_part), max_blocks, w_unit};
-            vocab_pack_kernel<T, P><<<x_blocks + (direct ? 0 : (unsigned)up(vn, 256) / kPackRows), 256, 0, st>>>(pack);
+                                Wp, c.ldw, vn, w_rows, ws + l.w, floats(l.w_part), max_blocks, w_unit};
+            const unsigned blocks = x_blocks + (direct ? 0 : (unsigned)up(vn, 256) / w_rows);
+            if (P == 2 && !c.grad)
+                vocab_pack_kernel<T, P, P == 2><<<blocks, 256, 0, st>>>(pack);
+            else
+                vocab_pack_kernel<T, P, false><<<blocks, 256, 0, st>>>(pack);
         }
         if (c.T == 0) {
             // only dW, which is 0, is left to do

@@ -116,16 +116,16 @@ __device__ inline int scale_exponent(float m) {
 }
 constexpr float kDScale = 0x1p15f;  // of D, whose entries are at most 1 in magnitude
 
-// A product operand, stored with k along its rows (K_ROW: A[m][k]) or down its columns (K_COL:
-// A[k][m]); rows past `rows` read as its last row, quads past row_bytes as its last quad.  Neither
-// kind of stand-in reaches a result: past-the-end m or n are never stored, past-the-end k meet
-// zeros of the other operand.
+// A product operand, stored with k along its rows (K_ROW: A[m][k], the rows whole slabs; K_ENDS: rows
+// that may end inside one) or down its columns (K_COL: A[k][m]); rows past `rows` read as its last row,
+// quads past row_bytes as the row's last quad.  Neither kind of stand-in reaches a result: past-the-end
+// m or n are never stored, past-the-end k meet zeros of the other operand.
 struct Operand {
     const char* base;
     uint32_t pitch, row_bytes;
     int rows;
 };
-enum Order { K_ROW, K_COL };
+enum Order { K_ROW, K_ENDS, K_COL };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -135,7 +135,7 @@ template <int P, Order O, int R, int W, int NT>
 struct Side {
     static constexpr int BK = Planes<P>::BK, NW = NT / 64;
     static constexpr int BYTES = R * BK * 2 * P;                            // of a slab in LDS
-    static constexpr int QUADS = O == K_ROW ? Planes<P>::QR : R * P / 8;    // per stored row
+    static constexpr int QUADS = O != K_COL ? Planes<P>::QR : R * P / 8;    // per stored row
     static constexpr int ROW = QUADS * 16;
     static constexpr int L = BYTES / 16 / NT;                               // loads per thread
     static constexpr int B = W / 32;                                        // 32-row blocks of a wave
@@ -146,23 +146,24 @@ struct Side {
     // 64-bit read is served in passes of 32 lanes, which read one chunk each of four consecutive
     // rows: the flips put those on the four different quarters of the 64 banks.
     static constexpr int CHUNKS = R * P / 32;
-    static_assert(O == K_ROW || CHUNKS % 2 == 0, "chunks pair up");
+    static_assert(O != K_COL || CHUNKS % 2 == 0, "chunks pair up");
     __host__ __device__ static constexpr int flip(int r) { return CHUNKS % 4 == 0 ? (r & 3) : ((r >> 1) & 1); }
     __host__ __device__ static constexpr int source_quad(int r, int u) {
-        return O == K_ROW ? Planes<P>::swz(r, u) : (u ^ (flip(r) << 2));
+        return O != K_COL ? Planes<P>::swz(r, u) : (u ^ (flip(r) << 2));
     }
 
     const char* at;       // next slab
     size_t step;          // bytes from slab to slab
     uint32_t off[L];
+    uint32_t end[O == K_ENDS ? L : 1];  // its row's last quad
     int left;             // K_COL: rows from `at` to the operand's end
-    uint32_t lane_at[O == K_ROW ? KK * P : B * P];  // LDS offsets of this lane's fragments
+    uint32_t lane_at[O != K_COL ? KK * P : B * P];  // LDS offsets of this lane's fragments
     int frag;             // wave's part of them
 
     __device__ inline void init(const Operand& o, int row0, int k0, int wave, int lane, int wave_at) {
-        if (O == K_ROW) {
-            at = o.base + (size_t)first_row(o, row0) * o.pitch + (size_t)k0 * ROW;
-            step = ROW;
+        if (O != K_COL) {
+            at = o.base + (size_t)first_row(o, row0) * o.pitch + (O == K_ENDS ? 0 : (size_t)k0 * ROW);
+            step = O == K_ENDS ? 0 : ROW;
             left = 0;
         } else {
             at = o.base + (size_t)k0 * BK * o.pitch + (size_t)row0 * 2 * P;
@@ -170,8 +171,9 @@ struct Side {
             left = o.rows - k0 * BK;
         }
         set_offsets(o, row0, wave, lane);
+        if (O == K_ENDS) advance(k0 * ROW);
         const int l = lane & 31, h = lane >> 5;
-        if (O == K_ROW) {
+        if (O != K_COL) {
             // row l of a block, quad 2 * kk + h of plane p
             frag = wave_at * W * ROW;
 #pragma unroll
@@ -196,15 +198,22 @@ struct Side {
         for (int j = 0; j < L; ++j) {
             const int i = (j * NW + wave) * 64 + lane;
             const int r = i / QUADS, u = i - r * QUADS;
-            if (O == K_ROW) {
+            if (O != K_COL) {
                 const int row = imin(row0 + r, o.rows - 1) - first_row(o, row0);
-                off[j] = (uint32_t)row * o.pitch + (uint32_t)(source_quad(r, u) * 16);
+                const uint32_t quad = source_quad(r, u) * 16, last = o.row_bytes - 16;
+                off[j] = (uint32_t)row * o.pitch + (O == K_ENDS && quad > last ? last : quad);
+                if (O == K_ENDS) end[j] = (uint32_t)row * o.pitch + last;
             } else {
                 const uint32_t q = (uint32_t)row0 * 2 * P + (uint32_t)(source_quad(r, u) * 16);
                 const uint32_t last = o.row_bytes - 16;
                 off[j] = (uint32_t)imin(r, left - 1) * o.pitch + (q < last ? q : last) - (uint32_t)row0 * 2 * P;
             }
         }
+    }
+    // K_ENDS: the loads' places `bytes` further on, their row's last quad at most.
+    __device__ inline void advance(uint32_t bytes) {
+#pragma unroll
+        for (int j = 0; j < L; ++j) off[j] = off[j] + bytes < end[j] ? off[j] + bytes : end[j];
     }
     // Requests loads [from, to) of the next slab into LDS at `lds`.
     __device__ inline void issue(uint32_t lds, int from, int to) const {
@@ -213,6 +222,7 @@ struct Side {
             if (j >= from && j < to) dl_load<16>(at, off[j], lds + j * NW * 1024);
     }
     __device__ inline void next(const Operand& o, int row0, int wave, int lane) {
+        if (O == K_ENDS) return advance(ROW);
         at += step;
         if (O == K_COL) {
             left -= BK;
@@ -226,7 +236,7 @@ struct Side {
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                if (O == K_ROW) {
+                if (O != K_COL) {
                     v[p][b] = *(const Half8*)(slab + frag + b * 32 * ROW + lane_at[p * KK + kk]);
                 } else {
                     const char* a = slab + lane_at[b * P + p] + kk * 16 * ROW;
@@ -431,7 +441,7 @@ __device__ inline void lse_tile(T& t, const LseArgs& a, int m0, int n0, int coun
     }
 }
 
-template <class T>
+template <class T, Order W>
 __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     int tm, tn;
@@ -440,7 +450,7 @@ __global__ void __launch_bounds__(T::NT) vocab_lse_kernel(LseArgs a) {
     const int count = *a.count;
     if (n0 >= count) return;
     T t;
-    t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
+    t.template run<W, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
     const int piece = a.part0 + tm * T::WAVES_M + (threadIdx.x >> 6) / T::WAVES_N;
     if (m0 + T::kBM <= a.vocab && a.alpha >= 0.f)
         lse_tile<true>(t, a, m0, n0, count, piece);
@@ -517,7 +527,7 @@ __device__ inline void grad_column(const T& t, const GradArgs& a, int j, int n, 
         }
 }
 
-template <class T>
+template <class T, Order W>
 __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     int tm, tn;
@@ -526,7 +536,7 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     const int count = *a.count, h = (threadIdx.x & 63) >> 5;
     if (n0 >= count) return;
     T t;
-    t.template run<K_ROW, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
+    t.template run<W, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
     const float x_most = T::kP == 2 ? most_of(a.x_most) : 0.f;
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {

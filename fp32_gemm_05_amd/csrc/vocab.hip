@@ -301,9 +301,14 @@ int run(const Call& c) {
     const hipStream_t st = c.stream;
     const long x_pitch = Pl::pitch(l.hk), d_pitch = Pl::pitch(l.piece);
     const int slabs = l.hk / Pl::BK;
-    // W is read in place when its rows are whole aligned slabs, else packed piece by piece
-    const bool direct = P == 1 && c.H % Pl::BK == 0 && c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 &&
-                        c.ldw < (1L << 22);
+    // W is read in place when its rows are whole aligned slabs, or whole aligned quads and the products
+    // are short: rows that end inside a slab, and so between two lines of memory, slow those by 8 %, and
+    // packing W costs most where it is large (a bf16 step, us, packed/in place: 300 tokens, 20000 x 1000:
+    // 152, 138; 1001 tokens, 50021 x 1000: 574, 529; 777 tokens, 5003 x 1000: 111, 114; 3000 tokens,
+    // 8000 x 504: 188, 193)
+    const bool direct = P == 1 && (c.H % Pl::BK == 0 || (c.H % 8 == 0 && (long)c.V * c.H >= 16384L * c.T)) &&
+                        c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 && c.ldw < (1L << 22);
+    const bool ends = direct && c.H % Pl::BK != 0;  // kernels of their own: the others take 2 % less time
     // bf16 cross entropy multiplies dW with X times each token's weight
     char* const xs = P == 1 && c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
     (void)hipGetLastError();
@@ -348,7 +353,10 @@ int run(const Call& c) {
                 const int tm = (int)up(vn, S::kBM) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
                 const LseArgs a{w, x, count, w_unit, x_unit, tm, tn, slabs, vn, c.alpha, (float2*)(ws + l.part), part,
                                 l.tp};
-                vocab_lse_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
+                if (P == 1 && ends)
+                    vocab_lse_kernel<S, P == 1 ? K_ENDS : K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
+                else
+                    vocab_lse_kernel<S, K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
                 part += tm * S::WAVES_M;
             });
             continue;
@@ -360,7 +368,10 @@ int run(const Call& c) {
                 const GradArgs a{w, x, count, rows, w_unit, x_unit, x_most, tm, tn, slabs, vn, c.alpha, c.lse,
                                  floats(l.scale), floats(l.weight), c.e.teacher ? nullptr : c.e.index,
                                  floats(l.value), v0, ws + l.d, d_pitch};
-                vocab_grad_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
+                if (P == 1 && ends)
+                    vocab_grad_kernel<S, P == 1 ? K_ENDS : K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
+                else
+                    vocab_grad_kernel<S, K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
             });
             if (c.e.teacher)
                 vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(

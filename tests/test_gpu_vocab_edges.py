@@ -195,6 +195,20 @@ def test_dx_in_middle_tiles(dtype, T, V, H):
     run_ce(X, W, target, dloss, 1.0, dtype)
 
 
+# rows that end inside a slab: NaN stand behind them in the padding, and behind the last row's end
+@pytest.mark.parametrize("pad", [0, 8])
+@pytest.mark.parametrize("T,V,H", [(70, 144000, 8), (300, 70001, 72), (700, 13000, 1000), (1100, 140000, 136),
+                                   (300, 2000, 72)])
+def test_rows_that_end_inside_a_slab(T, V, H, pad):
+    X, W, target, dloss, g = inputs(T, V, H, "bf16", 22, pad)
+    memory = torch.full((V * W.stride(0) + 4096,), float("nan"), device="cuda", dtype=W.dtype)
+    W = memory[:V * W.stride(0)].view(V, W.stride(0))[:, :H].copy_(W)
+    target[torch.rand(T, generator=g, device="cuda") < 0.3] = -100
+    run_ce(X, W, target, dloss, 1.0, "bf16")
+    index, teacher = entries(T, V, 3, g)
+    run_distill(X, W, index, teacher, dloss, 0.5, 0.8, "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [7, 100])
 def test_offsets_past_32_bits(dtype, T):

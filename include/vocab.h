@@ -21,9 +21,10 @@
  *
  * Tokens that do not count -- target == ignore_index, or no index >= 0 -- have loss 0, lse 0 and
  * gradient 0, whatever X, dloss and teacher hold there (NaN and infinities included); among more
- * than 64 tokens they cost no product either.  A target or an index >= V (or a target < 0 that is not ignore_index) cannot be refused
- * without waiting for the device: nothing is read for it, and the token's loss and the gradients
- * that it enters are NaN.  Teacher entries of -infinity have q = 0 and add nothing.
+ * than 64 tokens they cost no product either.  A target or an index >= V (or a target < 0 that is
+ * not ignore_index) cannot be refused without waiting for the device: nothing is read for it, and
+ * the token's loss and the gradients that it enters are NaN.  Teacher entries of -infinity have
+ * q = 0 and add nothing.
  *
  * Memory and streams: device pointers owned by the caller, work enqueued on `stream`, no wait, no
  * allocation, no memset; calls may be captured into a HIP graph.  `work` is scratch memory of at
@@ -32,12 +33,15 @@
  * gives the same bits.
  *
  * Precision: loss, lse, picked, dloss and teacher are fp32, as are all sums and softmax
- * statistics.  fp32 X and W are multiplied as two fp16 parts each, scaled by a power of two (a
- * token's own for X, one for up to 2^21 rows of W): values down to 2^-16 of the largest keep their
- * 24 bits, smaller ones are held to 2^-40 of the largest, D to 2^-40 of its largest possible entry.
- * An infinity in W makes NaN of every logit of its row.  With bf16 X and W, D is rounded to bf16
- * for the two gradient products (cross entropy scales a token's row so that its target's entry is
- * exact), and dX and dW are rounded to bf16 at the end.
+ * statistics.  fp32 X and W of more than 64 tokens are multiplied as two fp16 parts each, scaled by
+ * a power of two (a token's own for X; for W a row's own in the forward calls, one for up to 2^21
+ * rows in the gradients): values down to 2^-16 of the largest keep their 24 bits, smaller ones are
+ * held to 2^-40 of the largest, D to 2^-40 of its largest possible entry.  Of 17 to 64 tokens they
+ * are three bf16 parts each, 24 bits at any magnitude; with up to 16 the products are fp32's own.
+ * An infinity in W may make NaN of every logit of its row, and a teacher's row of -infinities alone
+ * makes its token NaN.  With bf16 X and W, D is rounded to bf16 for the two gradient products (cross
+ * entropy scales a token's row so that its target's entry is exact), and dX and dW are rounded to
+ * bf16 at the end.
  *
  * Return codes as in sgemm.h: 0, -i for argument i, +hipError_t from a launch.  T = 0 is a quick
  * return (dW, when wanted, is set to 0).

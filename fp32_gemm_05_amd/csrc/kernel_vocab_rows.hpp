@@ -388,9 +388,10 @@ __device__ inline void pack_w_row(const PackArgs& a, int i) {
     if (lane == 0) a.w_unit[i] = ldexpf(1.f, -e);
 }
 
-// Rows of W for one workgroup: 4, in bf16 as many as give each thread 8 values (a power of two; 400
-// tokens, 60000 x 100: 15 us, with 4 rows 23).  In fp32 that many are no faster (45 us either way), and
-// a number that the kernel does not know costs it 28 us of 137 (1001 tokens, 50021 x 1000).
+// Rows of W for one workgroup: 4, in bf16 as many as give each thread 8 values (a power of two; both
+// packings of a step, 400 tokens, 60000 x 100: 15 us, with 4 rows 23).  In fp32 that many are no faster
+// (45 us either way), and a number that the kernel does not know costs both 28 us of 137 (1001 tokens,
+// 50021 x 1000).
 constexpr int kPackRows = 4;
 template <int P>
 __host__ inline int pack_rows(int kp) {
@@ -400,8 +401,8 @@ __host__ inline int pack_rows(int kp) {
 }
 
 // The packed operands, in one launch: x_blocks workgroups take a row of X each, the rest w_rows rows
-// of W.  Bound by memory: 200 MB read and 200 MB written (1001 tokens, 50021 x 1000, fp32) take 135 us
-// where a copy of that size, after kernels that left the caches full of results, takes 96.
+// of W.  Bound by memory: 200 MB read and 200 MB written (1001 tokens, 50021 x 1000, fp32) take 68 us,
+// where a copy of that size takes 74, and 96 after kernels that left the caches full of results.
 template <typename T, int P, bool BY_ROW>
 __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
     if ((int)blockIdx.x < a.x_blocks) return pack_x<T, P>(a, blockIdx.x);
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
         } else {
             // Four lanes hold the two planes of a slab: with the next four they trade halves, so that
             // each store writes whole lines of 128 bytes.  chunks is a multiple of 8: both have one.
-            // Stored past the caches: the products read it from memory either way (135 us; cached 141).
+            // Stored past the caches: the products read it from memory either way (a step's two: 135 us; cached 141).
             typedef int Int4 __attribute__((ext_vector_type(4)));
             const bool odd = threadIdx.x & 4;
             const Int4 hi = __builtin_bit_cast(Int4, o[0]), lo = __builtin_bit_cast(Int4, o[P - 1]);

@@ -211,8 +211,10 @@ int run_few(const Call& c, const FewLayout& l) {
     const hipStream_t st = c.stream;
     // vocabulary rows of a workgroup's logits: 64 where three in four compute units get one (40 tokens,
     // fp32 20000 x 2000: 67 us against 88 us with 32, as the tokens' side is read and cut half as often),
-    // 32 where they do not (40 tokens, fp32 2000 x 300: 13 us against 8 us)
-    const bool wide = NB == 4 && c.V >= 64 * 192;
+    // 32 where they do not (40 tokens, fp32 2000 x 300: 13 us against 8 us).  fp32's 32 in three parts have a
+    // compute unit to themselves, so there 64 are taken once 32 would need a second round (60 tokens,
+    // 12000 x 1000: 25 us against 33; 50 tokens, 8300 x 1000: 24 against 31)
+    const bool wide = NB == 4 && c.V >= (C::P == 3 ? 32 * 256 + 1 : 64 * 192);
     const int per = wide ? 64 : 32;
     (void)hipGetLastError();
 

@@ -209,6 +209,17 @@ def test_rows_that_end_inside_a_slab(T, V, H, pad):
     run_distill(X, W, index, teacher, dloss, 0.5, 0.8, "bf16")
 
 
+# few tokens against 32 and against 64 vocabulary rows a workgroup, on both sides of the change
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,H", [(40, 8192, 130), (40, 8193, 130), (61, 12287, 77), (64, 12288, 512), (33, 20001, 64)])
+def test_few_tokens_and_many_rows(T, V, H, dtype):
+    X, W, target, dloss, g = inputs(T, V, H, dtype, 23, 3)
+    target[torch.rand(T, generator=g, device="cuda") < 0.3] = -100
+    run_ce(X, W, target, dloss, 1.0, dtype)
+    index, teacher = entries(T, V, 5, g)
+    run_distill(X, W, index, teacher, dloss, 0.5, 0.8, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [7, 100])
 def test_offsets_past_32_bits(dtype, T):

@@ -467,8 +467,9 @@ __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
 }
 
 // lse of each counted token from its partial maxima and sums, then its loss.  A workgroup takes TX
-// tokens, TY threads each: once through the maxima, once through the sums, so that no load waits
-// for an exponential.  rows null: a token's partials stand at its own place, whether it counts or
+// tokens, TY threads each: the first kHeld partials of a thread are read once, all together, and those
+// past them once for the maxima and once for the sums, so that no load waits for an exponential.  Bound
+// by the latency of its few dependent loads.  rows null: a token's partials stand at its own place, whether it counts or
 // not, and z of a target that names no row of the vocabulary has not been written.
 template <int TX>
 __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* rows, const int* count, int tokens,
@@ -479,10 +480,19 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
     const int n = rows ? *count : tokens, tx = threadIdx.x % TX, ty = threadIdx.x / TX, i0 = blockIdx.x * TX, i = i0 + tx;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (i0 >= n) return;
+    constexpr int kHeld = 8;
+    float2 held[kHeld];
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+        const int p = ty + r * TY;
+        held[r] = i < n && p < parts ? part[(size_t)p * tp + i] : make_float2(-INFINITY, 0.f);
+    }
     float top = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) top = fmaxf(top, held[r].x);
     if (i < n)
 #pragma unroll 8
-        for (int p = ty; p < parts; p += TY) top = fmaxf(top, part[(size_t)p * tp + i].x);
+        for (int p = ty + kHeld * TY; p < parts; p += TY) top = fmaxf(top, part[(size_t)p * tp + i].x);
 #pragma unroll
     for (int o = TX; o < 64; o *= 2) top = fmaxf(top, __shfl_xor(top, o));
     if (lane < TX) slot[wave][tx] = top;
@@ -492,9 +502,11 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
     __syncthreads();
     const float ref = top == -INFINITY ? 0.f : top;  // nothing but -inf: the sum is 0, or a NaN among its parts
     float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) sum += held[r].y * expf(held[r].x - ref);
     if (i < n)
 #pragma unroll 8
-        for (int p = ty; p < parts; p += TY) {
+        for (int p = ty + kHeld * TY; p < parts; p += TY) {
             const float2 v = part[(size_t)p * tp + i];
             sum += v.y * expf(v.x - ref);
         }

@@ -263,7 +263,7 @@ int run_few(const Call& c, const FewLayout& l) {
         vocab_few_grad_kernel<C, NB><<<(unsigned)(strips * l.splits + dw_blocks), 256, 0, st>>>(g);
     }
     if (!c.grad) {
-        vocab_loss_kernel<4><<<(unsigned)(up(c.T, 4) / 4), 1024, 0, st>>>(
+        vocab_loss_kernel<2><<<(unsigned)(up(c.T, 2) / 2), 1024, 0, st>>>(
             c.e, nullptr, nullptr, c.T, c.V, (const float2*)(ws + l.part), part, kFewTokens, z, c.loss, c.lse_out);
     } else if (c.dX) {
         const DxCut cut{1, 16 * NB, l.splits, l.splits};

@@ -197,10 +197,13 @@ bool few(int T) { return T > 0 && T <= kFewTokens; }
 
 TokenArgs token_args(const Call& c, char* ws, float* z, long scale, long weight, long value, DForm form) {
     return {c.e, c.T, c.V, c.H, c.alpha, c.X, c.W, c.ldx, c.ldw, z, c.lse, c.dloss, c.picked,
-            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form};
+            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form, entries_per_wave(c.T, c.e.k)};
 }
 // Workgroups of four waves for the entries (forward) or the tokens (gradient).
-unsigned token_blocks(const Call& c) { return (unsigned)(up(c.grad ? c.T : (long)c.T * c.e.k, 4) / 4); }
+unsigned token_blocks(const Call& c) {
+    const int per = entries_per_wave(c.T, c.e.k);
+    return (unsigned)(up(c.grad ? c.T : c.T * (up(c.e.k, per) / per), 4) / 4);
+}
 
 template <class C, int NB>
 int run_few(const Call& c, const FewLayout& l) {

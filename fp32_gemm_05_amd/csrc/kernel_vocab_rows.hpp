@@ -156,7 +156,8 @@ struct TokenArgs {
     int per;                     // forward: a wave's entries, 1 or kPerWave
 };
 // Entries of one token that a wave takes together where there are enough for all waves: they share the
-// reads of X and the waits (4096 tokens of 64 entries, 65536 x 4096 bf16: 298 us one by one, 224; 8000 x 512: 77, 58).
+// reads of X and the waits (4096 tokens of 64 entries, 65536 x 4096 bf16: 298 us one by one, 224; 8000 x 512:
+// 77, 58).
 constexpr int kPerWave = 4;
 __host__ inline int entries_per_wave(long tokens, long k) { return k >= kPerWave && tokens * k >= 32768 ? kPerWave : 1; }
 

@@ -398,10 +398,18 @@ int run(const Call& c) {
                 vocab_dw_kernel<S><<<tm * tn, S::NT, 0, st>>>(a);
             });
     }
-    if (!c.grad)
-        vocab_loss_kernel<32><<<l.tp / 32, 1024, 0, st>>>(c.e, rows, count, c.T, c.V, (const float2*)(ws + l.part), part,
-                                                          l.tp, z, c.loss, c.lse_out);
-    else if (c.T > 0 && c.dX) {
+    if (!c.grad) {
+        // fewer tokens a workgroup until every compute unit has one (100 tokens, 131072 rows: 17.6 us with
+        // 32, 8.9 with 8; 2048 tokens: 10.9, 8.1)
+        auto loss = [&](auto kernel, int tokens) {
+            kernel<<<l.tp / tokens, 1024, 0, st>>>(c.e, rows, count, c.T, c.V, (const float2*)(ws + l.part), part, l.tp,
+                                                   z, c.loss, c.lse_out);
+        };
+        if (c.T <= 2048)
+            loss(vocab_loss_kernel<8>, 8);
+        else
+            loss(vocab_loss_kernel<32>, 32);
+    } else if (c.T > 0 && c.dX) {
         auto out = [&](auto kernel, long cols) {
             kernel<<<dim3(c.T, (unsigned)(up(c.H, cols) / cols)), 256, 0, st>>>(
                 c.e, pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight), x_unit, x_most, (T*)c.dX, c.lddx);

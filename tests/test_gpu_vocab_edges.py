@@ -220,6 +220,16 @@ def test_few_tokens_and_many_rows(T, V, H, dtype):
     run_distill(X, W, index, teacher, dloss, 0.5, 0.8, dtype)
 
 
+# entries taken four to a wave, and added up over more lanes than a wave has
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,H,K", [(60, 3000, 100, 701), (700, 2000, 77, 50), (2, 40, 33, 200)])
+def test_many_entries(T, V, H, K, dtype):
+    X, W, _, dloss, g = inputs(T, V, H, dtype, 24, 3)
+    index, teacher = entries(T, V, K, g)
+    index[1::7] = -1
+    run_distill(X, W, index, teacher, dloss, 0.5, 0.8, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T", [7, 100])
 def test_offsets_past_32_bits(dtype, T):

@@ -114,7 +114,9 @@ __device__ inline int scale_exponent(float m) {
     const int e = 14 - ilogbf(m);
     return e > 126 ? 126 : e < -126 ? -126 : e;
 }
-constexpr float kDScale = 0x1p15f;  // of D, whose entries are at most 1 in magnitude
+// Of D, whose entries are at most 1 in magnitude, but for the error of z - lse.  That is of any size where
+// logits are: past kDMost, which fp16 still holds, an entry is cut off there, by no more than that error.
+constexpr float kDScale = 0x1p15f, kDMost = 0x1.fp0f;
 
 // A product operand, stored with k along its rows (K_ROW: A[m][k], the rows whole slabs; K_ENDS: rows
 // that may end inside one) or down its columns (K_COL: A[k][m]); rows past `rows` read as its last row,
@@ -481,9 +483,10 @@ __device__ inline float d_factor(float weight, float x_unit, float x_most) {
 
 // D of a token's column in this wave, stored.  PLAIN: no row past the vocabulary and no target among
 // these, as nearly everywhere: a fma, an exponential, a product and the rounding of each are left.
+// most (P = 2): of the exponent, that of kDMost (the minimum keeps a NaN).
 template <bool PLAIN, class T>
 __device__ inline void grad_column(const T& t, const GradArgs& a, int j, int n, int m0, float lse, float scale,
-                                   float alpha, int entry, float value) {
+                                   float alpha, float most, int entry, float value) {
     typedef typename Planes<T::kP>::Half Half;
     typedef typename Planes<T::kP>::Half4 Half4;
     const int h = (threadIdx.x & 63) >> 5;
@@ -502,6 +505,7 @@ __device__ inline void grad_column(const T& t, const GradArgs& a, int j, int n, 
                     // with one rounding less where D keeps 22 bits
                     float x = T::kP == 2 ? __builtin_fmaf(t.acc[i][j][e], alpha, -lse) * kLog2E
                                          : __builtin_fmaf(t.acc[i][j][e], c, -l);
+                    if (T::kP == 2) x = __builtin_elementwise_minimum(x, most);
                     x = __builtin_amdgcn_exp2f(x) * scale;
                     if (!PLAIN) {
                         // rows past the vocabulary are the zeros that dX's product runs over
@@ -551,6 +555,7 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
             entry = v >= 0 && v < a.vocab ? (int)v : -1;
             value = a.value[token];
         }
+        const float most = T::kP == 2 && live ? log2f(kDMost / scale) : 0.f;
         if (T::kP == 2 && live) {
             const float unit = a.x_unit[n], f = d_factor(a.weight[token], unit, x_most);
             alpha *= *a.w_unit * unit;
@@ -560,9 +565,9 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
         const int first = m0 + t.row(0, 0) - 4 * h;  // of this wave's rows
         const bool plain = first + T::kWM <= a.vocab && !__any(entry >= first && entry < first + T::kWM);
         if (plain)
-            grad_column<true>(t, a, j, n, m0, lse, scale, alpha, entry, value);
+            grad_column<true>(t, a, j, n, m0, lse, scale, alpha, most, entry, value);
         else
-            grad_column<false>(t, a, j, n, m0, lse, scale, alpha, entry, value);
+            grad_column<false>(t, a, j, n, m0, lse, scale, alpha, most, entry, value);
     }
 }
 

@@ -132,8 +132,10 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
 // Cross entropy: with s = alpha * dloss, p the softmax and c = 1 - p[target].  D_PACKED, D_APART: p / c
 // with -1 at the target, and s * c is X's weight in dW and the product's in dX.  The target's entry
 // carries most of the gradient: as -1 it is exact in bf16, where s * (p - 1) would be rounded.  c
-// comes from expm1, so a p close to 1 costs no digits; a c below 2^-25, where fp32 cannot tell p from
-// 1, is raised to it.
+// comes from expm1, so a p close to 1 costs no digits.  A c below 2^-25, where fp32 cannot tell p from
+// 1, is raised to it; in D_APART, whose fp16 planes hold no entry of 2 or more, one below c_floor, the
+// error that z - lse may have: a c that came out too small by it would make the other entries p / c too
+// large.  The target's entry is then less than 1 in magnitude, and s * c times D what it was.
 //
 // Distillation: p, and p - (sum of q over the entries that name the same vocabulary row) at the
 // entries.  D_PACKED (bf16): times s, with X and the product as they are, so that dW's factors are
@@ -142,6 +144,8 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
 // D_WHOLE, for few tokens, whose D is kept wide: s * (p - y), weight 1 (only distillation's is made
 // here).
 enum DForm { D_PACKED, D_APART, D_WHOLE };
+// z and lse are sums of their own: 16 roundings of lse's size between them are ordinary.
+__device__ inline float c_floor(float lse) { return 0x1p-20f * (1.f + fabsf(lse)); }
 
 struct TokenArgs {
     Entries e;
@@ -239,11 +243,12 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
         if (!e.teacher) {
             const i64 v = e.index[t * e.ld];
             if (!e.counts(v)) return;
-            const float c = fmaxf(-expm1f(entry_logit<T>(a, t, 0) - l), 0x1p-25f);
+            const float own = fmaxf(-expm1f(entry_logit<T>(a, t, 0) - l), 0.f);
+            const float c = fmaxf(own, a.form == D_APART ? c_floor(l) : 0x1p-25f);
             const bool good = v >= 0 && v < a.vocab;
             scale = good ? 1.f / c : NAN;
             weight = good ? s * c : NAN;
-            if (lane == 0) a.value[t] = -1.f;
+            if (lane == 0) a.value[t] = a.form == D_APART ? -own / c : -1.f;
         } else {
             bool good = true;
             float top, log_total;
@@ -271,7 +276,9 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
                 float d = 0.f;
                 if (v >= 0) {
                     good = good && v < a.vocab;
-                    d = (a.form == D_APART ? 1.f : s) * (expf(a.picked[t * e.k + k] - l) - q);
+                    float y = a.picked[t * e.k + k] - l;
+                    if (a.form == D_APART) y = y > 0.f ? 0.f : y;  // p <= 1, for its fp16 planes
+                    d = (a.form == D_APART ? 1.f : s) * (expf(y) - q);
                 }
                 if (k < e.k) a.value[t * e.k + k] = d;
             }

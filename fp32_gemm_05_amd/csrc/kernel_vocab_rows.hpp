@@ -399,8 +399,8 @@ __device__ inline void pack_x(const PackArgs& a, int i) {
                 const float u = ldexpf(1.f, -e);
                 a.x_unit[i] = u;
                 const float w = a.weight ? fabsf(a.weight[t] * u) : 0.f;
-                // a maximum: the order does not matter
-                if (w > 0.f) atomicMax(a.x_most + i % kMostSlots, __float_as_uint(w));
+                // a maximum: the order does not matter; a weight that is no number stays its token's own
+                if (w > 0.f && __builtin_isfinite(w)) atomicMax(a.x_most + i % kMostSlots, __float_as_uint(w));
             }
         }
     } else if (a.scaled && s) {

@@ -77,3 +77,36 @@ def test_logits_beyond_what_fp32_tells_apart(T, V, H, alpha):
         X, W, index, torch.zeros(T, 3, device="cuda"), lse, picked, dloss, alpha=alpha)
     for name in got:
         assert bool(torch.isfinite(got[name]).all()), name
+
+
+PATHS = [(5, 700, 96), (40, 700, 96), (150, 1500, 96), (900, 20000, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,H", PATHS)
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_one_tokens_upstream_gradient_stays_its_own(T, V, H, dtype, value):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    t = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    X = torch.randn(T, H, generator=g, device="cuda").to(t)
+    W = (torch.randn(V, H, generator=g, device="cuda") * (1.5 / H ** 0.5)).to(t)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    index = torch.randint(0, V, (T, 3), generator=g, device="cuda")
+    teacher = torch.randn(T, 3, generator=g, device="cuda")
+    bad = T // 2
+    others = torch.arange(T, device="cuda") != bad
+    dloss[bad] = value
+    loss, lse = sg.vocab_ce(X, W, target)
+    ce = sg.vocab_ce_grad(X, W, target, lse, dloss)[0]
+    _, lse, picked = sg.vocab_distill(X, W, index, teacher)
+    distill = sg.vocab_distill_grad(X, W, index, teacher, lse, picked, dloss)[0]
+    dloss[bad] = 1.0
+    _, lse_ce = sg.vocab_ce(X, W, target)
+    clean = sg.vocab_ce_grad(X, W, target, lse_ce, dloss)[0], \
+        sg.vocab_distill_grad(X, W, index, teacher, lse, picked, dloss)[0]
+    for got, want in zip((ce, distill), clean):
+        assert bool(torch.isfinite(got[others]).all())
+        assert not bool(torch.isfinite(got[bad]).all())
+        # what the other tokens are rounded in may follow the largest weight
+        vc.rows_within("dX", got[others], want[others], 2.0 ** -18 * want[others].double().abs())

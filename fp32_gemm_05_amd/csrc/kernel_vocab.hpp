@@ -101,10 +101,6 @@ __device__ inline float wave_max(float s) {
     for (int o = 32; o > 0; o >>= 1) s = fmaxf(s, __shfl_xor(s, o));
     return s;
 }
-// A maximum that many workgroups raise, in 64 words (one word would take their atomics one after the
-// other: 10 us a thousand); read by whole waves.
-constexpr int kMostSlots = 64;
-__device__ inline float most_of(const float* slots) { return wave_max(slots[threadIdx.x & 63]); }
 
 // The scale of P = 2 operands: the power of two that brings a largest value m into [2^14, 2^15).
 // m of 0 (or nothing finite) gives 1; an m so small or large that the power would leave fp32's
@@ -464,22 +460,15 @@ struct GradArgs {
     Operand w, x;
     const int *count, *rows;       // the counted tokens
     const float *w_unit, *x_unit;  // P = 2: what a packed unit of W, of each row of X stands for
-    const float* x_most;           // P = 2: the largest |weight * x_unit| of a counted token (most_of)
     int tiles_m, tiles_n, slabs, vocab;
     float alpha;
-    const float *lse, *scale, *weight;  // per token: D = exp(z - lse) * scale; its weight in dX and dW
+    const float *lse, *scale;      // per token: D = exp(z - lse) * scale
     const long long* target;       // cross entropy: the entries that take `value`, per token
     const float* value;
     long long v0;                  // first vocabulary row of this piece
     char* d;                       // [counted token][vocabulary piece], planes
     long d_pitch;
 };
-
-// P = 2: what D's row of a token is stored in: its weight relative to the largest one, which makes
-// dW's sum over tokens uniform, times kDScale.
-__device__ inline float d_factor(float weight, float x_unit, float x_most) {
-    return x_most > 0.f ? weight * x_unit / x_most * kDScale : 0.f;
-}
 
 // D of a token's column in this wave, stored.  PLAIN: no row past the vocabulary and no target among
 // these, as nearly everywhere: a fma, an exponential, a product and the rounding of each are left.
@@ -541,7 +530,6 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
     if (n0 >= count) return;
     T t;
     t.template run<W, K_ROW>(lds, a.w, m0, a.x, n0, 0, a.slabs);
-    const float x_most = T::kP == 2 ? most_of(a.x_most) : 0.f;
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
         const int n = n0 + t.col(j);
@@ -557,10 +545,9 @@ __global__ void __launch_bounds__(T::NT) vocab_grad_kernel(GradArgs a) {
         }
         const float most = T::kP == 2 && live ? log2f(kDMost / scale) : 0.f;
         if (T::kP == 2 && live) {
-            const float unit = a.x_unit[n], f = d_factor(a.weight[token], unit, x_most);
-            alpha *= *a.w_unit * unit;
-            scale *= f;
-            value *= f;
+            alpha *= *a.w_unit * a.x_unit[n];
+            scale *= kDScale;
+            value *= kDScale;
         }
         const int first = m0 + t.row(0, 0) - 4 * h;  // of this wave's rows
         const bool plain = first + T::kWM <= a.vocab && !__any(entry >= first && entry < first + T::kWM);
@@ -631,7 +618,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dx_kernel(DxArgs a) {
 struct DwArgs {
     Operand x, d;      // [token][hidden]; [token][vocabulary piece]
     const int* count;
-    const float* x_most;
+    const float* x_most;  // P = 2: what a packed unit of X stands for
     int tiles_m, tiles_n, hidden, vocab;
     void* out;         // [vocabulary piece][hidden] in the operands' type
     long ld;
@@ -650,7 +637,7 @@ __global__ void __launch_bounds__(T::NT) vocab_dw_kernel(DwArgs a) {
     // (as in vocab_grad_kernel), or one of fp32
     constexpr int E = 16 / sizeof(O), F = E / 4;
     typedef O Row __attribute__((ext_vector_type(E), aligned(sizeof(O))));
-    const float unit = T::kP == 2 ? most_of(a.x_most) / kDScale : 1.f;
+    const float unit = T::kP == 2 ? *a.x_most / kDScale : 1.f;
     const int h = (threadIdx.x & 63) >> 5;
     const bool whole = m0 + T::kBM <= a.hidden;
 #pragma unroll

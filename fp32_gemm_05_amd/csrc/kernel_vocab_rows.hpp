@@ -140,6 +140,8 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
 // Distillation: p, and p - (sum of q over the entries that name the same vocabulary row) at the
 // entries.  D_PACKED (bf16): times s, with X and the product as they are, so that dW's factors are
 // rounded once (D) and not twice; D_APART (fp32): s is the weight of X and the product.
+// So D's entries stay within 1 whatever a token's weight, and a token's dX is its own matter; X times the
+// weights is packed apart for dW, in one power of two, since that sums over tokens.
 //
 // D_WHOLE, for few tokens, whose D is kept wide: s * (p - y), weight 1 (only distillation's is made
 // here).
@@ -222,27 +224,30 @@ __device__ inline void entry_logits(const TokenArgs& a, long t, long k0) {
 }
 
 // The work of wave i: forward, the logits of `per` entries; gradient, one token's scale, weight, values.
+// Returns that weight, 0 for a token that does not count.
 template <typename T, bool GRAD>
-__device__ inline void token_wave(const TokenArgs& a, long i) {
+__device__ inline float token_wave(const TokenArgs& a, long i) {
     const int lane = threadIdx.x & 63;
     const Entries& e = a.e;
     if constexpr (!GRAD) {
         if (a.per > 1) {
             const long groups = (e.k + kPerWave - 1) / kPerWave;
             if (i < a.tokens * groups) entry_logits<T>(a, i / groups, i % groups * kPerWave);
-            return;
+            return 0.f;
         }
-        if (i >= (long)a.tokens * e.k) return;
+        if (i >= (long)a.tokens * e.k) return 0.f;
         const float z = entry_logit<T>(a, i / e.k, i % e.k);
         if (lane == 0) a.z[i] = z;
+        return 0.f;
     } else {
         const long t = i;
-        if (t >= a.tokens) return;
+        if (t >= a.tokens) return 0.f;
         const float s = a.alpha * a.dloss[t], l = a.lse[t];
         float scale, weight;
+        bool counts = true;
         if (!e.teacher) {
             const i64 v = e.index[t * e.ld];
-            if (!e.counts(v)) return;
+            if (!e.counts(v)) return 0.f;
             const float own = fmaxf(-expm1f(entry_logit<T>(a, t, 0) - l), 0.f);
             const float c = fmaxf(own, a.form == D_APART ? c_floor(l) : 0x1p-25f);
             const bool good = v >= 0 && v < a.vocab;
@@ -250,7 +255,7 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
             weight = good ? s * c : NAN;
             if (lane == 0) a.value[t] = a.form == D_APART ? -own / c : -1.f;
         } else {
-            bool good = true;
+            bool good = true, any = false;
             float top, log_total;
             teacher_stats(e, t, top, log_total);
             const i64* index = e.index + t * e.ld;
@@ -275,6 +280,7 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
                 }
                 float d = 0.f;
                 if (v >= 0) {
+                    any = true;
                     good = good && v < a.vocab;
                     float y = a.picked[t * e.k + k] - l;
                     if (a.form == D_APART) y = y > 0.f ? 0.f : y;  // p <= 1, for its fp16 planes
@@ -286,17 +292,20 @@ __device__ inline void token_wave(const TokenArgs& a, long i) {
                 for (int k = lane; k < e.k; k += 64) a.value[t * e.k + k] = NAN;
             scale = __all(good) ? (a.form == D_APART ? 1.f : s) : NAN;
             weight = a.form == D_APART ? s : 1.f;
+            counts = __any(any);
         }
         if (lane == 0) {
             a.scale[t] = scale;
             a.weight[t] = weight;
         }
+        return counts ? weight : 0.f;
     }
 }
 
 // The largest finite |x|.
 __device__ inline float finite_max(float m, float x) { return __builtin_isfinite(x) ? fmaxf(m, fabsf(x)) : m; }
-__device__ inline float block_max(float m) {  // of 256 threads
+template <int I = 0>
+__device__ inline float block_max(float m) {  // of 256 threads; each I once in a kernel
     __shared__ float part[4];
     m = wave_max(m);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
@@ -308,39 +317,54 @@ struct ScanArgs {
     TokenArgs t;
     Counted c;
     int token_blocks;
+    float* x_part;    // when wanted (gradient): token_blocks maxima of |weight * X|'s finite values
     float* w_part;    // max_blocks maxima of |W|'s finite values
     int max_blocks;
-    uint32_t* x_most; // kMostSlots, cleared for vocab_pack_kernel
 };
 
+// One wave's part of the largest finite |x * f|, four values of a row a lane.
+template <typename T>
+__device__ inline float row_max(const T* s, int n, float f, float m) {
+    int k = (threadIdx.x & 63) * 4;
+#pragma unroll 4
+    for (; k + 4 <= n; k += 256) {
+        float v[4];
+        load(s + k, v);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m = finite_max(m, v[q] * f);
+    }
+    for (; k < n; ++k) m = finite_max(m, (float)s[k] * f);
+    return m;
+}
+
 // All that reads the inputs alone, in one launch: workgroup 0 counts, the next token_blocks look at
-// four entries or tokens each, the rest (fp32) at W's magnitude.
+// four entries or tokens at a time each, the rest (fp32) at W's magnitude.
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
     int b = blockIdx.x;
-    if (b == 0) {
-        if (threadIdx.x < kMostSlots) a.x_most[threadIdx.x] = 0;
-        count_tokens(a.t.e, a.t.tokens, a.c);
+    if (b == 0) return count_tokens(a.t.e, a.t.tokens, a.c);
+    b -= 1;
+    const int wave = threadIdx.x >> 6;
+    if (b < a.token_blocks) {
+        if constexpr (!GRAD) {
+            token_wave<T, GRAD>(a.t, (long)b * 4 + wave);
+        } else {
+            float m = 0.f;
+            for (long t = (long)b * 4 + wave; t < a.t.tokens; t += (long)a.token_blocks * 4) {
+                const float weight = token_wave<T, GRAD>(a.t, t);
+                if (a.x_part) m = row_max((const T*)a.t.x + t * a.t.ldx, a.t.hidden, weight, m);
+            }
+            if (!a.x_part) return;
+            m = block_max(m);
+            if (threadIdx.x == 0) a.x_part[b] = m;
+        }
         return;
     }
-    b -= 1;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    if (b < a.token_blocks) return token_wave<T, GRAD>(a.t, (long)b * 4 + wave);
     b -= a.token_blocks;
     float m = 0.f;
-    for (int r = b * 4 + wave; r < a.t.vocab; r += a.max_blocks * 4) {
-        const T* s = (const T*)a.t.w + (size_t)r * a.t.ldw;
-        int k = lane * 4;
-#pragma unroll 4
-        for (; k + 4 <= a.t.hidden; k += 256) {
-            float v[4];
-            load(s + k, v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m = finite_max(m, v[q]);
-        }
-        for (; k < a.t.hidden; ++k) m = finite_max(m, (float)s[k]);
-    }
-    m = block_max(m);
+    for (int r = b * 4 + wave; r < a.t.vocab; r += a.max_blocks * 4)
+        m = row_max((const T*)a.t.w + (size_t)r * a.t.ldw, a.t.hidden, 1.f, m);
+    m = block_max<1>(m);
     if (threadIdx.x == 0) a.w_part[b] = m;
 }
 
@@ -362,9 +386,13 @@ struct PackArgs {
     int x_blocks;
     char* x_out;
     const float* weight;  // per token
-    char* scaled;         // P = 1, when wanted: the rows times their weight
+    char* scaled;         // when wanted: the rows times their weight
     float* x_unit;        // P = 2: each row in its own power of two, x_unit what a packed unit stands for
-    uint32_t* x_most;     // P = 2: kMostSlots maxima of |weight| * x_unit, in a gradient's call (weight given)
+    // P = 2, `scaled`: in the power of two of their largest value (x_parts maxima), x_most what a packed
+    // unit stands for
+    const float* x_part;
+    int x_parts;
+    float* x_most;
     // W: `vocab` rows, and zero rows to the next multiple of 256
     const void* w;
     long ldw;
@@ -380,10 +408,11 @@ struct PackArgs {
 template <typename T, int P>
 __device__ inline void pack_x(const PackArgs& a, int i) {
     const int n = *a.count;
-    if (i >= (n + 255) / 256 * 256) return;
+    if (i > 0 && i >= (n + 255) / 256 * 256) return;  // the first says what x_most is, whatever n
     const int t = i < n ? a.rows[i] : 0;
     const T* s = i < n ? (const T*)a.x + (size_t)t * a.ldx : nullptr;
-    float f = 1.f;
+    const float weight = a.scaled && s ? a.weight[t] : 0.f;
+    float f = 1.f, g = 1.f;
     if constexpr (P == 2) {
         if (s) {
             float m = 0.f;
@@ -395,27 +424,26 @@ __device__ inline void pack_x(const PackArgs& a, int i) {
             }
             const int e = scale_exponent(block_max(m));
             f = ldexpf(1.f, e);
-            if (threadIdx.x == 0) {
-                const float u = ldexpf(1.f, -e);
-                a.x_unit[i] = u;
-                const float w = a.weight ? fabsf(a.weight[t] * u) : 0.f;
-                // a maximum: the order does not matter; a weight that is no number stays its token's own
-                if (w > 0.f && __builtin_isfinite(w)) atomicMax(a.x_most + i % kMostSlots, __float_as_uint(w));
-            }
+            if (threadIdx.x == 0) a.x_unit[i] = ldexpf(1.f, -e);
         }
-    } else if (a.scaled && s) {
-        f = a.weight[t];
+        if (a.scaled) {
+            float m = 0.f;
+            for (int j = threadIdx.x; j < a.x_parts; j += 256) m = fmaxf(m, a.x_part[j]);
+            const int e = scale_exponent(block_max<1>(m));
+            g = ldexpf(1.f, e);
+            if (i == 0 && threadIdx.x == 0) *a.x_most = ldexpf(1.f, -e);
+        }
     }
     for (int k = threadIdx.x * 4; k < a.kp; k += 1024) {
-        float v[4];
+        float v[4], x[4];
         load_row(s, k, a.cols, v);
-        if constexpr (P == 1) {
-            store4<P>(a.x_out + (size_t)i * a.pitch, k, v);
-            if (!a.scaled) continue;
-        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] *= f;
-        store4<P>((P == 1 ? a.scaled : a.x_out) + (size_t)i * a.pitch, k, v);
+        for (int q = 0; q < 4; ++q) x[q] = v[q] * f;
+        store4<P>(a.x_out + (size_t)i * a.pitch, k, x);
+        if (!a.scaled) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = v[q] * weight * g;
+        store4<P>(a.scaled + (size_t)i * a.pitch, k, x);
     }
 }
 
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(256) vocab_pack_kernel(PackArgs a) {
     if constexpr (P == 2) {
         float m = 0.f;
         for (int j = threadIdx.x; j < a.w_parts; j += 256) m = fmaxf(m, a.w_part[j]);
-        const int e = scale_exponent(block_max(m));
+        const int e = scale_exponent(block_max<2>(m));
         f = ldexpf(1.f, e);
         if (row0 == 0 && threadIdx.x == 0) *a.w_unit = ldexpf(1.f, -e);
     }
@@ -633,11 +661,8 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
 // Puts the values of a teacher's entries into D where they fall into this piece (P = 0: a D in fp32).
 template <int P>
 __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens, int v0, int vocab, const int* pos,
-                                                          const float* value, const float* weight,
-                                                          const float* x_unit, const float* x_most, char* d,
-                                                          long d_pitch) {
+                                                          const float* value, char* d, long d_pitch) {
     const long j = (long)blockIdx.x * 256 + threadIdx.x;
-    const float most = P == 2 ? most_of(x_most) : 0.f;
     if (j >= (long)tokens * e.k) return;
     const long t = j / e.k, k = j - t * e.k;
     const int i = P == 0 ? (int)t : pos[t];
@@ -647,8 +672,7 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
         ((float*)(d + (size_t)i * d_pitch))[v - v0] = value[j];
         return;
     }
-    const float f = P == 2 ? d_factor(weight[t], x_unit[i], most) : 1.f;
-    store1<P == 2 ? 2 : 1>(d + (size_t)i * d_pitch, v - v0, value[j] * f);
+    store1<P == 2 ? 2 : 1>(d + (size_t)i * d_pitch, v - v0, P == 2 ? value[j] * kDScale : value[j]);
 }
 
 // dX of every token: the sum of its product's parts, or 0 where it does not count.  TY groups of
@@ -657,14 +681,13 @@ __global__ void __launch_bounds__(256) vocab_patch_kernel(Entries e, int tokens,
 template <typename T, int P, int TY>
 __global__ void __launch_bounds__(256) vocab_dx_out_kernel(Entries e, const int* pos, const int* count, int hidden,
                                                            const float* acc, DxCut cut, int hp, const float* weight,
-                                                           const float* x_unit, const float* x_most, T* dx, long ld) {
+                                                           T* dx, long ld) {
     constexpr int TX = 256 / TY;
     typedef T Row __attribute__((ext_vector_type(4), aligned(sizeof(T))));
     const int t = blockIdx.x, i = P > 0 ? pos[t] : any_entry(e, t, 0) ? t : -1;
     const int splits = P > 0 ? cut.splits(*count) : cut.groups;
     const size_t rows = P > 0 ? cut.rows(*count) : cut.bn;
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, h = (blockIdx.y * TX + tx) * 4;
-    const float most = P == 2 ? most_of(x_most) : 0.f;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (i >= 0 && h < hidden)
 #pragma unroll 4
@@ -677,7 +700,7 @@ __global__ void __launch_bounds__(256) vocab_dx_out_kernel(Entries e, const int*
     }
     if (ty > 0 || h >= hidden) return;
     float s = 0.f;
-    if (i >= 0) s = P == 0 ? 1.f : P == 1 ? weight[t] : most / (x_unit[i] * kDScale);
+    if (i >= 0) s = P == 0 ? 1.f : P == 1 ? weight[t] : weight[t] / kDScale;
     Row o;
 #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = (T)(i < 0 ? 0.f : v[q] * s);

@@ -58,10 +58,11 @@ struct Layout {
     int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces
     DxCut cut;
     Shape dx_shape;
-    long count, rows, pos, z, scale, weight, x_unit, x_most, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
+    long count, rows, pos, z, scale, weight, x_unit, x_most, x_part, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
 };
 
 constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
+constexpr int kMostTokenBlocks = 2048;  // and that look at the tokens in a gradient call
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
 // The shape for a product of rows_m x rows_n: the one whose rounds over the chip's 256 compute units
@@ -132,7 +133,6 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     l.pos = take(4L * l.tp);
     if (!teacher) l.z = take(4L * l.tp);
     l.x_unit = take(4L * l.tp);
-    l.x_most = take(4L * kMostSlots);
     l.w_unit = take(4L * l.piece);
     l.w_part = take(4L * kMaxBlocks);
     l.x = take(element * l.hk * l.tp);
@@ -141,7 +141,8 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
         l.scale = take(4L * l.tp);
         l.weight = take(4L * l.tp);
         l.value = take(4L * T * K);
-        if (P == 1 && !teacher) l.xs = take(element * l.hk * l.tp);
+        if (P == 2) l.x_most = take(4), l.x_part = take(4L * kMostTokenBlocks);
+        if (P == 2 || !teacher) l.xs = take(element * l.hk * l.tp);
         l.d = take(element * l.tp * l.piece);
         l.acc = take(4L * l.hp * ((long)l.cut.groups / l.cut.tiles_m * l.cut.bn));
     } else {
@@ -253,7 +254,7 @@ int run_few(const Call& c, const FewLayout& l) {
         }
         if (c.e.teacher)
             vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-                c.e, c.T, v0, vn, nullptr, floats(l.value), nullptr, nullptr, nullptr, ws + l.d, l.vp * 4);
+                c.e, c.T, v0, vn, nullptr, floats(l.value), ws + l.d, l.vp * 4);
         // dW: 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but two
         // groups or more: a wave reads its rows' D first
         const long row_groups = up(vn, 256) / 256, all = up(c.H, 8 * C::HE) / (8 * C::HE);
@@ -271,7 +272,7 @@ int run_few(const Call& c, const FewLayout& l) {
     } else if (c.dX) {
         const DxCut cut{1, 16 * NB, l.splits, l.splits};
         vocab_dx_out_kernel<T, 0, 16><<<dim3(c.T, (unsigned)(up(c.H, 64) / 64)), 256, 0, st>>>(
-            c.e, nullptr, nullptr, c.H, floats(l.acc), cut, (int)l.hp, nullptr, nullptr, nullptr, (T*)c.dX, c.lddx);
+            c.e, nullptr, nullptr, c.H, floats(l.acc), cut, (int)l.hp, nullptr, (T*)c.dX, c.lddx);
     }
     return (int)hipGetLastError();
 }
@@ -314,17 +315,19 @@ int run(const Call& c) {
     const bool direct = P == 1 && (c.H % Pl::BK == 0 || (c.H % 8 == 0 && (long)c.V * c.H >= 16384L * c.T)) &&
                         c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 && c.ldw < (1L << 22);
     const bool ends = direct && c.H % Pl::BK != 0;  // kernels of their own: the others take 2 % less time
-    // bf16 cross entropy multiplies dW with X times each token's weight
-    char* const xs = P == 1 && c.grad && c.dW && !c.e.teacher ? ws + l.xs : nullptr;
+    // dW's product takes X times each token's weight, but for bf16 distillation, whose D has it
+    char* const xs = c.grad && c.dW && (P == 2 || !c.e.teacher) ? ws + l.xs : nullptr;
     (void)hipGetLastError();
 
     float* const z = c.e.teacher ? c.picked_out : floats(l.z);
     // the gradient's W is packed in one power of two, that of its largest value
     const int max_blocks = P == 2 && c.grad ? (int)(up(c.V, 4) / 4 < kMaxBlocks ? up(c.V, 4) / 4 : kMaxBlocks) : 0;
+    const unsigned blocks_of_tokens = token_blocks(c);
+    const int look = c.grad && blocks_of_tokens > kMostTokenBlocks ? kMostTokenBlocks : (int)blocks_of_tokens;
     const ScanArgs scan{token_args(c, ws, z, l.scale, l.weight, l.value, P == 2 ? D_APART : D_PACKED),
                         {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
-                        (int)token_blocks(c), floats(l.w_part), max_blocks, (uint32_t*)x_most};
-    const unsigned scan_blocks = 1 + token_blocks(c) + max_blocks;
+                        look, P == 2 && xs ? floats(l.x_part) : nullptr, floats(l.w_part), max_blocks};
+    const unsigned scan_blocks = 1 + look + max_blocks;
     if (c.grad)
         vocab_scan_kernel<T, true><<<scan_blocks, 256, 0, st>>>(scan);
     else
@@ -342,8 +345,8 @@ int run(const Call& c) {
             const int x_blocks = p == 0 ? l.tp : 0;
             const int w_rows = pack_rows<P>(l.hk);
             const PackArgs pack{c.H, l.hk, x_pitch, c.X, c.ldx, rows, count, x_blocks, ws + l.x,
-                                c.grad ? floats(l.weight) : nullptr, xs, x_unit, (uint32_t*)x_most,
-                                Wp, c.ldw, vn, w_rows, ws + l.w, floats(l.w_part), max_blocks, w_unit};
+                                floats(l.weight), xs, x_unit, floats(l.x_part), look, x_most, Wp, c.ldw, vn, w_rows,
+                                ws + l.w, floats(l.w_part), max_blocks, w_unit};
             const unsigned blocks = x_blocks + (direct ? 0 : (unsigned)up(vn, 256) / w_rows);
             if (P == 2 && !c.grad)
                 vocab_pack_kernel<T, P, P == 2><<<blocks, 256, 0, st>>>(pack);
@@ -370,9 +373,8 @@ int run(const Call& c) {
                 using S = typename std::remove_pointer<decltype(shape)>::type;
                 // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
                 const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
-                const GradArgs a{w, x, count, rows, w_unit, x_unit, x_most, tm, tn, slabs, vn, c.alpha, c.lse,
-                                 floats(l.scale), floats(l.weight), c.e.teacher ? nullptr : c.e.index,
-                                 floats(l.value), v0, ws + l.d, d_pitch};
+                const GradArgs a{w, x, count, rows, w_unit, x_unit, tm, tn, slabs, vn, c.alpha, c.lse, floats(l.scale),
+                                 c.e.teacher ? nullptr : c.e.index, floats(l.value), v0, ws + l.d, d_pitch};
                 if (P == 1 && ends)
                     vocab_grad_kernel<S, P == 1 ? K_ENDS : K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
                 else
@@ -380,7 +382,7 @@ int run(const Call& c) {
             });
             if (c.e.teacher)
                 vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
-                    c.e, c.T, v0, vn, pos, floats(l.value), floats(l.weight), x_unit, x_most, ws + l.d, d_pitch);
+                    c.e, c.T, v0, vn, pos, floats(l.value), ws + l.d, d_pitch);
             if (c.dX) {
                 const DxArgs a{w, d, count, w_unit, l.cut, (int)up(vn, Pl::BK) / Pl::BK, floats(l.acc), l.hp, p > 0};
                 by_shape<P>(l.dx_shape, [&](auto* shape) {
@@ -412,7 +414,7 @@ int run(const Call& c) {
     } else if (c.T > 0 && c.dX) {
         auto out = [&](auto kernel, long cols) {
             kernel<<<dim3(c.T, (unsigned)(up(c.H, cols) / cols)), 256, 0, st>>>(
-                c.e, pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight), x_unit, x_most, (T*)c.dX, c.lddx);
+                c.e, pos, count, c.H, floats(l.acc), l.cut, l.hp, floats(l.weight), (T*)c.dX, c.lddx);
         };
         if (c.T < 512)
             out(vocab_dx_out_kernel<T, P, 16>, 64);

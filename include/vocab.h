@@ -34,10 +34,11 @@
  *
  * Precision: loss, lse, picked, dloss and teacher are fp32, as are all sums and softmax
  * statistics.  fp32 X and W of more than 64 tokens are multiplied as two fp16 parts each, scaled by
- * a power of two (a token's own for X; for W a row's own in the forward calls, one for up to 2^21
- * rows in the gradients): values down to 2^-16 of the largest keep their 24 bits, smaller ones are
- * held to 2^-40 of the largest, D to 2^-40 of its largest possible entry.  Of 17 to 64 tokens they
- * are three bf16 parts each, 24 bits at any magnitude; with up to 16 the products are fp32's own.
+ * a power of two (a token's own for X; for W a row's own in the forward calls, one for the whole of W in
+ * the gradients): values down to 2^-16 of the largest keep 23 bits, smaller ones are held to 2^-40 of the
+ * largest.  Of D = s * (..), s = alpha * dloss, the part in brackets is held to 2^-40, in dX for every token
+ * by itself; dW takes s * X in one power of two, held to 2^-40 of its largest value.  Of 17 to 64 tokens
+ * the operands are three bf16 parts each, 24 bits; with up to 16 the products are fp32's own.
  * An infinity in W may make NaN of every logit of its row, and a teacher's row of -infinities alone
  * makes its token NaN.  With bf16 X and W, D is rounded to bf16 for the two gradient products (cross
  * entropy scales a token's row so that its target's entry is exact), and dX and dW are rounded to

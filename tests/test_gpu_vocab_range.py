@@ -110,3 +110,52 @@ def test_one_tokens_upstream_gradient_stays_its_own(T, V, H, dtype, value):
         assert not bool(torch.isfinite(got[bad]).all())
         # what the other tokens are rounded in may follow the largest weight
         vc.rows_within("dX", got[others], want[others], 2.0 ** -18 * want[others].double().abs())
+
+
+@pytest.mark.parametrize("T,V,H", [(100, 1500, 96), (777, 5003, 200), (200, 32768, 256)])
+@pytest.mark.parametrize("scale", [1.0, 1e-2, 1e-4])
+@pytest.mark.parametrize("small", [0.0, 1e-9])
+def test_a_row_of_zeros_among_others(T, V, H, scale, small):
+    # a counted row of zeros, or a very small one, takes nothing from the other tokens, and its own dX is as exact
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    X = torch.randn(T, H, generator=g, device="cuda") * scale
+    W = torch.randn(V, H, generator=g, device="cuda") * (1.5 / H ** 0.5)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    X[T // 3] *= small
+    vc.check_fp32_gradients(ce_definition(X, W, target, dloss), step(X, W, target, dloss))
+
+
+@pytest.mark.parametrize("T,V,H", [(100, 1500, 96), (777, 5003, 200)])
+def test_weights_far_apart(T, V, H):
+    # a token's dX is as exact beside upstream gradients 10^6 times its own
+    g = torch.Generator(device="cuda").manual_seed(T + 1)
+    X = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(V, H, generator=g, device="cuda") * (1.5 / H ** 0.5)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    dloss[::3] *= 1e6
+    dloss[1::3] *= -1e-3
+    vc.check_fp32_gradients(ce_definition(X, W, target, dloss), step(X, W, target, dloss))
+
+
+@pytest.mark.parametrize("T,V,H", PATHS)
+@pytest.mark.parametrize("value", [float("inf"), 1e38, 1e-30])
+def test_a_tokens_dx_does_not_depend_on_other_tokens(T, V, H, value):
+    g = torch.Generator(device="cuda").manual_seed(T + 2)
+    X = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(V, H, generator=g, device="cuda") * (1.5 / H ** 0.5)
+    index = torch.randint(0, V, (T, 3), generator=g, device="cuda")
+    teacher = torch.randn(T, 3, generator=g, device="cuda")
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    bad = T // 2
+    others = torch.arange(T, device="cuda") != bad
+    got = []
+    for change in (False, True):
+        if change:
+            dloss[bad] = value
+            X[bad] *= 1e-6
+        _, lse, picked = sg.vocab_distill(X, W, index, teacher)
+        got.append(torch.stack([step(X, W, index[:, 0].contiguous(), dloss)["dX"][others],
+                                sg.vocab_distill_grad(X, W, index, teacher, lse, picked, dloss)[0][others]]))
+    assert bool(torch.isfinite(got[0]).all()) and torch.equal(got[0], got[1])

@@ -127,6 +127,81 @@ __device__ inline void teacher_stats(const Entries& e, long t, float& top, float
     log_total = logf(wave_sum(s));
 }
 
+// Each entry's share of the teacher: the sum of q over the entries of its token that name the same row.  Up
+// to kPairs entries a wave compares each with each (token_wave); past that, as that time is the square of
+// their number, a workgroup sorts a token's entries by row and place and adds up the runs, in an order that
+// the entries alone decide.  Up to kSortInLds they are sorted in LDS, past that in `keys`.  Bound by the
+// barriers of the sort's passes.  Measured (a gradient call, 32768 x 16, us, compared/sorted): 2 tokens of 128
+// entries 44, 42; of 256 78, 44; of 16384 201828, 579; 1000 tokens of 128 138, 148; of 192 153, 153; of 256
+// 172, 155.
+constexpr int kPairs = 192, kSortInLds = 8192;
+template <bool IN_LDS>
+__global__ void __launch_bounds__(1024) vocab_shares_kernel(Entries e, int vocab, uint64_t* keys, float* shares) {
+    __shared__ uint64_t held[IN_LDS ? kSortInLds : 1];
+    __shared__ float part[2][16];
+    const long t = blockIdx.x;
+    const uint32_t n = e.k, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const i64* index = e.index + t * e.ld;
+    const float* teacher = e.teacher + t * e.ld_teacher;
+    uint64_t* const a = IN_LDS ? held : keys + (size_t)t * n;
+    float m = -INFINITY, s = 0.f;
+    for (uint32_t k = tid; k < n; k += 1024) {
+        const i64 v = index[k];
+        if (v >= 0) m = fmaxf(m, teacher[k] * e.teacher_alpha);
+        a[k] = v >= 0 && v < vocab ? (uint64_t)v << 32 | k : ~0ull;  // the others are read by nothing
+    }
+    m = wave_max(m);
+    if (lane == 0) part[0][wave] = m;
+    __syncthreads();
+    const float top = wave_max(part[0][lane & 15]);
+    for (uint32_t k = tid; k < n; k += 1024)
+        if (index[k] >= 0) s += expf(teacher[k] * e.teacher_alpha - top);
+    s = wave_sum(s);
+    if (lane == 0) part[1][wave] = s;
+    __syncthreads();
+    const float log_total = logf(wave_sum(lane < 16 ? part[1][lane] : 0.f));
+    // a bitonic network of ascending comparisons alone, for which entries past n are the largest
+    int log_n = 0;
+    while ((1ull << log_n) < n) ++log_n;
+    for (int size = 1; size <= log_n; ++size)
+        for (int step = size; step > 0; --step) {
+            const uint32_t width = 1u << (step - 1);
+            for (uint32_t p = tid; p < 1u << (log_n - 1); p += 1024) {
+                const uint32_t i = (p & ~(width - 1)) * 2 | (p & (width - 1));
+                const uint32_t j = step == size ? i ^ (2 * width - 1) : i + width;
+                if (j < n) {
+                    const uint64_t x = a[i], y = a[j];
+                    if (x > y) a[i] = y, a[j] = x;
+                }
+            }
+            __syncthreads();
+        }
+    // a lane adds up the run that starts at its place, up to kRun; a wave the longer ones together
+    constexpr uint32_t kRun = 64;
+    auto row = [&](uint32_t j) { return (uint32_t)(a[j] >> 32); };
+    auto share = [&](uint32_t j) { return expf(teacher[(uint32_t)a[j]] * e.teacher_alpha - top - log_total); };
+    for (uint32_t j0 = wave * 64; j0 < n; j0 += 1024) {
+        const uint32_t j = j0 + lane;
+        const uint32_t r = j < n ? row(j) : ~0u;
+        const bool head = r != ~0u && (j == 0 || row(j - 1) != r);
+        uint32_t end = j;
+        float q = 0.f;
+        if (head)
+            for (; end < n && end - j < kRun && row(end) == r; ++end) q += share(end);
+        const bool more = head && end < n && row(end) == r;
+        if (head && !more)
+            for (uint32_t i = j; i < end; ++i) shares[t * n + (uint32_t)a[i]] = q;
+        for (uint64_t runs = __ballot(more); runs; runs &= runs - 1) {
+            const uint32_t from = j0 + __builtin_ctzll(runs), its = row(from);
+            float sum = 0.f;
+            uint32_t i = from + lane;
+            for (; i < n && row(i) == its; i += 64) sum += share(i);
+            sum = wave_sum(sum);
+            for (i = from + lane; i < n && row(i) == its; i += 64) shares[t * n + (uint32_t)a[i]] = sum;
+        }
+    }
+}
+
 // What a token's row of D is held in.
 //
 // Cross entropy: with s = alpha * dloss, p the softmax and c = 1 - p[target].  D_PACKED, D_APART: p / c
@@ -159,6 +234,7 @@ struct TokenArgs {
     const float *lse, *dloss, *picked;
     float *scale, *weight, *value;  // gradient, per token (value: per entry): D = exp(z - lse) * scale
     DForm form;
+    bool shared;                 // gradient: value holds the entries' shares (vocab_shares_kernel)
     int per;                     // forward: a wave's entries, 1 or kPerWave
 };
 // Entries of one token that a wave takes together where there are enough for all waves: they share the
@@ -256,8 +332,8 @@ __device__ inline float token_wave(const TokenArgs& a, long i) {
             if (lane == 0) a.value[t] = a.form == D_APART ? -own / c : -1.f;
         } else {
             bool good = true, any = false;
-            float top, log_total;
-            teacher_stats(e, t, top, log_total);
+            float top = 0.f, log_total = 0.f;
+            if (!a.shared) teacher_stats(e, t, top, log_total);
             const i64* index = e.index + t * e.ld;
             const float* teacher = e.teacher + t * e.ld_teacher;
             for (int k0 = 0; k0 < e.k; k0 += 64) {
@@ -265,8 +341,8 @@ __device__ inline float token_wave(const TokenArgs& a, long i) {
                 const i64 v = k < e.k ? index[k] : -1;
                 // an entry's share of the teacher is that of all that name its row, 64 of them at a time
                 // in the lanes (one by one from memory: 14 us where this takes 6.6, 16 tokens of 64 entries)
-                float q = 0.f;
-                for (int o0 = 0; o0 < e.k; o0 += 64) {
+                float q = a.shared && v >= 0 ? a.value[t * e.k + k] : 0.f;
+                for (int o0 = 0; o0 < e.k && !a.shared; o0 += 64) {
                     const int o = o0 + lane;
                     const i64 row = o < e.k ? index[o] : -1;
                     const float share = row >= 0 ? expf(teacher[o] * e.teacher_alpha - top - log_total) : 0.f;

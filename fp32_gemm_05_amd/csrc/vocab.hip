@@ -42,6 +42,19 @@ struct Call {
 
 long up(long x, long to) { return (x + to - 1) / to * to; }
 
+// What the sort of the entries takes of the workspace, and its launch (distillation's gradient).
+long keys_bytes(int T, int K) { return K > kSortInLds ? 8L * T * K : 0; }
+bool shared(const Call& c) { return c.grad && c.e.teacher && c.e.k > kPairs && c.T > 0; }
+void launch_shares(const Call& c, long keys, long value) {
+    if (!shared(c)) return;
+    uint64_t* const k = (uint64_t*)(c.work + keys);
+    float* const v = (float*)(c.work + value);
+    if (c.e.k > kSortInLds)
+        vocab_shares_kernel<false><<<c.T, 1024, 0, c.stream>>>(c.e, c.V, k, v);
+    else
+        vocab_shares_kernel<true><<<c.T, 1024, 0, c.stream>>>(c.e, c.V, k, v);
+}
+
 // Tile shapes.  The large one has a compute unit to itself, of the others two share one.
 template <int P>
 using Big = Tile<P, 256, 256, 128, 64, 3, 2>;
@@ -58,7 +71,7 @@ struct Layout {
     int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces
     DxCut cut;
     Shape dx_shape;
-    long count, rows, pos, z, scale, weight, x_unit, x_most, x_part, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
+    long count, rows, pos, z, scale, weight, keys, x_unit, x_most, x_part, w_part, w_unit, value, x, xs, w, d, part, acc, bytes;
 };
 
 constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
@@ -140,6 +153,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
     if (grad) {
         l.scale = take(4L * l.tp);
         l.weight = take(4L * l.tp);
+        l.keys = take(keys_bytes(T, K));
         l.value = take(4L * T * K);
         if (P == 2) l.x_most = take(4), l.x_part = take(4L * kMostTokenBlocks);
         if (P == 2 || !teacher) l.xs = take(element * l.hk * l.tp);
@@ -155,7 +169,7 @@ Layout layout(int P, bool grad, int T, int V, int H, int K, bool teacher) {
 // At most kFewTokens tokens (kernel_vocab_few.hpp).  nb: blocks of 16 tokens.
 struct FewLayout {
     int nb, kt, piece, pieces, splits;
-    long hb, hp, vp, z, scale, weight, value, xtf, d, part, acc, bytes;
+    long hb, hp, vp, z, scale, weight, keys, value, xtf, d, part, acc, bytes;
 };
 
 FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
@@ -183,6 +197,7 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
     if (grad) {
         l.scale = take(4 * kFewTokens);
         l.weight = take(4 * kFewTokens);
+        l.keys = take(keys_bytes(T, K));
         l.value = take(4L * T * K);
         l.xtf = take(64L * e * (f32 ? 4 : 2) * l.hb * l.kt);
         l.d = take(4L * 16 * l.nb * l.vp);
@@ -198,7 +213,8 @@ bool few(int T) { return T > 0 && T <= kFewTokens; }
 
 TokenArgs token_args(const Call& c, char* ws, float* z, long scale, long weight, long value, DForm form) {
     return {c.e, c.T, c.V, c.H, c.alpha, c.X, c.W, c.ldx, c.ldw, z, c.lse, c.dloss, c.picked,
-            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form, entries_per_wave(c.T, c.e.k)};
+            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form, shared(c),
+            entries_per_wave(c.T, c.e.k)};
 }
 // Workgroups of four waves for the entries (forward) or the tokens (gradient).
 unsigned token_blocks(const Call& c) {
@@ -224,6 +240,7 @@ int run_few(const Call& c, const FewLayout& l) {
 
     float* const z = c.e.teacher ? c.picked_out : floats(l.z);
     if (c.e.teacher) {
+        launch_shares(c, l.keys, l.value);
         const TokenArgs t = token_args(c, ws, z, l.scale, l.weight, l.value, D_WHOLE);
         if (c.grad)
             vocab_few_token_kernel<T, true><<<token_blocks(c), 256, 0, st>>>(t);
@@ -328,6 +345,7 @@ int run(const Call& c) {
                         {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
                         look, P == 2 && xs ? floats(l.x_part) : nullptr, floats(l.w_part), max_blocks};
     const unsigned scan_blocks = 1 + look + max_blocks;
+    launch_shares(c, l.keys, l.value);
     if (c.grad)
         vocab_scan_kernel<T, true><<<scan_blocks, 256, 0, st>>>(scan);
     else

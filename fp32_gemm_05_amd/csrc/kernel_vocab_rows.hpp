@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
     }
     b -= a.token_blocks;
     float m = 0.f;
-    for (int r = b * 4 + wave; r < a.t.vocab; r += a.max_blocks * 4)
+    for (long r = b * 4 + wave; r < a.t.vocab; r += a.max_blocks * 4)  // long: a step past the last row
         m = row_max((const T*)a.t.w + (size_t)r * a.t.ldw, a.t.hidden, 1.f, m);
     m = block_max<1>(m);
     if (threadIdx.x == 0) a.w_part[b] = m;

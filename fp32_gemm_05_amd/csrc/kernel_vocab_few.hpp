@@ -137,7 +137,7 @@ __device__ inline void few_mma_t(const typename M::Part (&a)[PA], const typename
 // Distillation's work on the entries, four waves a workgroup (token_wave).
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(256) vocab_few_token_kernel(TokenArgs a) {
-    token_wave<T, GRAD>(a, (long)blockIdx.x * 4 + (threadIdx.x >> 6));
+    for (long i = (long)blockIdx.x * 4 + (threadIdx.x >> 6); i < a.waves; i += (long)gridDim.x * 4) token_wave<T, GRAD>(a, i);
 }
 
 struct FewArgs {

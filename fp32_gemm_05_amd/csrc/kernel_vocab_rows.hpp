@@ -236,6 +236,7 @@ struct TokenArgs {
     DForm form;
     bool shared;                 // gradient: value holds the entries' shares (vocab_shares_kernel)
     int per;                     // forward: a wave's entries, 1 or kPerWave
+    long waves;                  // of token_wave
 };
 // Entries of one token that a wave takes together where there are enough for all waves: they share the
 // reads of X and the waits (4096 tokens of 64 entries, 65536 x 4096 bf16: 298 us one by one, 224; 8000 x 512:
@@ -308,16 +309,14 @@ __device__ inline float token_wave(const TokenArgs& a, long i) {
     if constexpr (!GRAD) {
         if (a.per > 1) {
             const long groups = (e.k + kPerWave - 1) / kPerWave;
-            if (i < a.tokens * groups) entry_logits<T>(a, i / groups, i % groups * kPerWave);
+            entry_logits<T>(a, i / groups, i % groups * kPerWave);
             return 0.f;
         }
-        if (i >= (long)a.tokens * e.k) return 0.f;
         const float z = entry_logit<T>(a, i / e.k, i % e.k);
         if (lane == 0) a.z[i] = z;
         return 0.f;
     } else {
         const long t = i;
-        if (t >= a.tokens) return 0.f;
         const float s = a.alpha * a.dloss[t], l = a.lse[t];
         float scale, weight;
         bool counts = true;
@@ -422,18 +421,14 @@ __global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
     b -= 1;
     const int wave = threadIdx.x >> 6;
     if (b < a.token_blocks) {
-        if constexpr (!GRAD) {
-            token_wave<T, GRAD>(a.t, (long)b * 4 + wave);
-        } else {
-            float m = 0.f;
-            for (long t = (long)b * 4 + wave; t < a.t.tokens; t += (long)a.token_blocks * 4) {
-                const float weight = token_wave<T, GRAD>(a.t, t);
-                if (a.x_part) m = row_max((const T*)a.t.x + t * a.t.ldx, a.t.hidden, weight, m);
-            }
-            if (!a.x_part) return;
-            m = block_max(m);
-            if (threadIdx.x == 0) a.x_part[b] = m;
+        float m = 0.f;
+        for (long i = (long)b * 4 + wave; i < a.t.waves; i += (long)a.token_blocks * 4) {
+            const float weight = token_wave<T, GRAD>(a.t, i);
+            if (GRAD && a.x_part) m = row_max((const T*)a.t.x + i * a.t.ldx, a.t.hidden, weight, m);
         }
+        if (!GRAD || !a.x_part) return;
+        m = block_max(m);
+        if (threadIdx.x == 0) a.x_part[b] = m;
         return;
     }
     b -= a.token_blocks;

@@ -75,7 +75,9 @@ struct Layout {
 };
 
 constexpr int kMaxBlocks = 1024;  // workgroups that look for W's largest value
-constexpr int kMostTokenBlocks = 2048;  // and that look at the tokens in a gradient call
+// and at the tokens or entries: in a gradient call so many that their maxima are few, in a forward call all
+// that a grid of less than 2^32 threads holds with room to spare
+constexpr int kMostTokenBlocks = 2048, kMostEntryBlocks = 1 << 20;
 constexpr int kPartRows = 64;  // the fewest vocabulary rows behind one partial sum
 
 // The shape for a product of rows_m x rows_n: the one whose rounds over the chip's 256 compute units
@@ -212,14 +214,15 @@ FewLayout few_layout(bool f32, bool grad, int T, int V, int H, int K) {
 bool few(int T) { return T > 0 && T <= kFewTokens; }
 
 TokenArgs token_args(const Call& c, char* ws, float* z, long scale, long weight, long value, DForm form) {
+    const int per = entries_per_wave(c.T, c.e.k);
     return {c.e, c.T, c.V, c.H, c.alpha, c.X, c.W, c.ldx, c.ldw, z, c.lse, c.dloss, c.picked,
-            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form, shared(c),
-            entries_per_wave(c.T, c.e.k)};
+            (float*)(ws + scale), (float*)(ws + weight), (float*)(ws + value), form, shared(c), per,
+            c.grad ? c.T : c.T * (up(c.e.k, per) / per)};
 }
 // Workgroups of four waves for the entries (forward) or the tokens (gradient).
-unsigned token_blocks(const Call& c) {
-    const int per = entries_per_wave(c.T, c.e.k);
-    return (unsigned)(up(c.grad ? c.T : c.T * (up(c.e.k, per) / per), 4) / 4);
+unsigned token_blocks(const Call& c, const TokenArgs& t) {
+    const long blocks = up(t.waves, 4) / 4, most = c.grad ? kMostTokenBlocks : kMostEntryBlocks;
+    return (unsigned)(blocks < most ? blocks : most);
 }
 
 template <class C, int NB>
@@ -243,9 +246,9 @@ int run_few(const Call& c, const FewLayout& l) {
         launch_shares(c, l.keys, l.value);
         const TokenArgs t = token_args(c, ws, z, l.scale, l.weight, l.value, D_WHOLE);
         if (c.grad)
-            vocab_few_token_kernel<T, true><<<token_blocks(c), 256, 0, st>>>(t);
+            vocab_few_token_kernel<T, true><<<token_blocks(c, t), 256, 0, st>>>(t);
         else
-            vocab_few_token_kernel<T, false><<<token_blocks(c), 256, 0, st>>>(t);
+            vocab_few_token_kernel<T, false><<<token_blocks(c, t), 256, 0, st>>>(t);
     }
     int part = 0;
     for (int p = 0; p < l.pieces; ++p) {
@@ -339,9 +342,9 @@ int run(const Call& c) {
     float* const z = c.e.teacher ? c.picked_out : floats(l.z);
     // the gradient's W is packed in one power of two, that of its largest value
     const int max_blocks = P == 2 && c.grad ? (int)(up(c.V, 4) / 4 < kMaxBlocks ? up(c.V, 4) / 4 : kMaxBlocks) : 0;
-    const unsigned blocks_of_tokens = token_blocks(c);
-    const int look = c.grad && blocks_of_tokens > kMostTokenBlocks ? kMostTokenBlocks : (int)blocks_of_tokens;
-    const ScanArgs scan{token_args(c, ws, z, l.scale, l.weight, l.value, P == 2 ? D_APART : D_PACKED),
+    const TokenArgs tokens = token_args(c, ws, z, l.scale, l.weight, l.value, P == 2 ? D_APART : D_PACKED);
+    const int look = (int)token_blocks(c, tokens);
+    const ScanArgs scan{tokens,
                         {rows, pos, count, c.grad ? nullptr : c.loss, c.lse_out},
                         look, P == 2 && xs ? floats(l.x_part) : nullptr, floats(l.w_part), max_blocks};
     const unsigned scan_blocks = 1 + look + max_blocks;

@@ -27,3 +27,29 @@ def test_largest_vocabulary_fp32_gradient():
     # sum_v p W = 4 e / V: 5e-9 of W; lse and exp are off by a few 2^-24 of 21
     want = torch.where(torch.arange(T, device="cuda") == 4, 0.0, -dloss.double())[:, None]
     assert bool(((dX.double() - want).abs() <= 1e-5).all()), float((dX.double() - want).abs().max())
+
+
+# one wave for four entries would be more than 2^32 threads
+@pytest.mark.parametrize("T,K", [(4096, 2 ** 16 + 60), (64, 2 ** 22 + 60)])
+def test_entries_past_a_grids_threads(T, K):
+    V, H = 300, 16
+    assert T * (K // 4) * 64 > 2 ** 32
+    g = torch.Generator(device="cuda").manual_seed(T)
+    X = torch.randn(T, H, generator=g, device="cuda")
+    W = torch.randn(V, H, generator=g, device="cuda") / 4
+    few = torch.randint(0, V, (T, 2), generator=g, device="cuda")
+    few_teacher = torch.randn(T, 2, generator=g, device="cuda")
+    dloss = torch.rand(T, generator=g, device="cuda") + 0.5
+    index = torch.full((T, K), -1, device="cuda")
+    teacher = torch.full((T, K), float("nan"), device="cuda")
+    index[:, 0], index[:, -1] = few[:, 0], few[:, 1]
+    teacher[:, 0], teacher[:, -1] = few_teacher[:, 0], few_teacher[:, 1]
+    want = sg.vocab_distill(X, W, few, few_teacher)
+    got = sg.vocab_distill(X, W, index, teacher)
+    # the same two entries, in the same order
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[2][:, 0], want[2][:, 0]) and torch.equal(got[2][:, -1], want[2][:, 1])
+    assert not bool(got[2][:, 1:-1].any())
+    want = sg.vocab_distill_grad(X, W, few, few_teacher, *want[1:], dloss)
+    got = sg.vocab_distill_grad(X, W, index, teacher, *got[1:], dloss)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -39,6 +39,7 @@ _KINDS = {"alpha": ctypes.c_float, "teacher_alpha": ctypes.c_float, "ignore_inde
           **dict.fromkeys(["X", "W", "target", "index", "teacher", "loss", "lse", "picked", "dloss", "dX", "dW",
                            "work", "stream"], ctypes.c_void_p)}
 _entries = {}
+_MOST = 2 ** 31 - 1  # of a size or a row stride: ctypes would pass on the low 32 bits of a larger one
 
 
 def _entry(name):
@@ -69,6 +70,9 @@ def vocab_workspace(dtype, grad: bool, T: int, V: int, H: int, K: int = 0) -> in
 
 @functools.lru_cache(maxsize=256)
 def _workspace(dtype, grad, T, V, H, K):
+    for i, n in enumerate((T, V, H, K)):
+        if abs(n) > _MOST:
+            _raise(-3 - i, "vocab_workspace")
     n = _entry("vocab_workspace")(_TYPES[dtype], grad, T, V, H, K)
     if n < 0:
         _raise(n, "vocab_workspace")
@@ -95,7 +99,16 @@ def _matrix(t, name, dtype=None):
     elif ld < cols:
         raise ValueError(f"{name} has row stride {ld} below its row length {cols} "
                          f"(a broadcast or overlapping view); pass a contiguous copy")
+    if rows > _MOST or ld > _MOST:
+        raise ValueError(f"{name} has {rows} rows with stride {ld}: neither may be above {_MOST}")
     return rows, cols, ld
+
+
+def _ignored(index):
+    index = int(index)
+    if not -2 ** 63 <= index < 2 ** 63:
+        raise ValueError(f"ignore_index {index} is no int64")
+    return index
 
 
 def _vector(t, name, dtype, n):
@@ -182,7 +195,7 @@ def vocab_ce(X, W, target, alpha: float = 1.0, ignore_index: int = -100, stream=
 
     def body():
         loss, lse = p.new(p.T), p.new(p.T)
-        p.call("vocab_ce", p.workspace(False), *p.head, p.alpha, *p.matrices, target.data_ptr(), int(ignore_index),
+        p.call("vocab_ce", p.workspace(False), *p.head, p.alpha, *p.matrices, target.data_ptr(), _ignored(ignore_index),
                loss.data_ptr(), lse.data_ptr())
         return loss, lse
     return p.run(body)
@@ -211,7 +224,7 @@ def vocab_ce_grad(X, W, target, lse, dloss, alpha: float = 1.0, ignore_index: in
     p.vector(lse, "lse")
     p.vector(dloss, "dloss")
     return _gradients(p, want_dx, want_dw, "vocab_ce_grad", *p.head, p.alpha, *p.matrices, target.data_ptr(),
-                      int(ignore_index), lse.data_ptr(), dloss.data_ptr())
+                      _ignored(ignore_index), lse.data_ptr(), dloss.data_ptr())
 
 
 def _distill(X, W, index, teacher, alpha, stream):

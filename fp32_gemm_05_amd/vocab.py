@@ -128,6 +128,15 @@ _current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _on_device(stream, device):
+    """The torch stream of a handle or stream, which has to be `device`'s."""
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, X on {device}")
+    return stream
+
+
 class _Problem:
     """The checked operands that every call has, and what they share."""
 
@@ -150,9 +159,7 @@ class _Problem:
         # results and workspace are allocated on the stream that uses them
         self.context = None
         if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self.device)
-            self.context = torch.cuda.stream(stream)
+            self.context = torch.cuda.stream(_on_device(stream, self.device))
         elif self.device.index != torch.cuda.current_device():
             self.context = torch.cuda.device(self.device)
 

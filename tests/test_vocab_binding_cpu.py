@@ -1,4 +1,7 @@
-"""CPU checks of the vocabulary head's binding: what does not fit the C ABI's integers."""
+"""CPU checks of the vocabulary head's binding: what does not fit the C ABI's integers, streams of
+other devices."""
+import types
+
 import pytest
 import torch
 
@@ -37,3 +40,19 @@ def test_ignored_target_past_64_bits_is_refused():
     for index in (2 ** 63, 2 ** 64 - 100, -2 ** 63 - 1):
         with pytest.raises(ValueError, match="no int64"):
             binding._ignored(index)
+
+
+def test_stream_of_another_device_is_refused():
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1))
+    assert binding._on_device(stream, torch.device("cuda", 1)) is stream
+    with pytest.raises(ValueError, match="stream is on cuda:1, X on cuda:0"):
+        binding._on_device(stream, torch.device("cuda", 0))
+
+
+def test_stream_of_another_device_is_refused_by_a_call(any_device, monkeypatch):
+    entered = []
+    monkeypatch.setattr(torch.cuda, "stream", entered.append)
+    X = torch.empty(3, 8, device="meta")
+    with pytest.raises(ValueError, match="stream is on cuda:1, X on meta"):
+        binding._Problem(X, torch.empty(5, 8, device="meta"), 1.0, types.SimpleNamespace(device=torch.device("cuda", 1)))
+    assert not entered

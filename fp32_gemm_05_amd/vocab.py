@@ -140,7 +140,7 @@ def _on_device(stream, device):
 class _Problem:
     """The checked operands that every call has, and what they share."""
 
-    __slots__ = ("T", "V", "H", "K", "dtype", "device", "head", "matrices", "alpha", "context")
+    __slots__ = ("T", "V", "H", "K", "dtype", "device", "head", "matrices", "alpha", "context", "stream", "read")
 
     def __init__(self, X, W, alpha, stream, entries=0):
         self.T, self.H, ldx = _matrix(X, "X")
@@ -155,17 +155,21 @@ class _Problem:
         self.head = (_TYPES[self.dtype], self.T, self.V, H)
         self.matrices = (X.data_ptr(), ldx, W.data_ptr(), ldw)
         self.alpha = float(alpha)
+        self.read = [X]
         self.same_device(W, "W")
-        # results and workspace are allocated on the stream that uses them
-        self.context = None
+        # results and workspace are allocated on the stream that uses them; the operands are told of it, so
+        # that their memory is not given out again before it has read them
+        self.context = self.stream = None
         if stream is not None:
-            self.context = torch.cuda.stream(_on_device(stream, self.device))
+            self.stream = _on_device(stream, self.device)
+            self.context = torch.cuda.stream(self.stream)
         elif self.device.index != torch.cuda.current_device():
             self.context = torch.cuda.device(self.device)
 
     def same_device(self, t, name):
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, X on {self.device}")
+        self.read.append(t)
 
     def vector(self, t, name, dtype=torch.float32):
         _vector(t, name, dtype, self.T)
@@ -175,7 +179,12 @@ class _Problem:
         if self.context is None:
             return body()
         with self.context:
-            return body()
+            try:
+                return body()
+            finally:
+                if self.stream is not None:
+                    for t in self.read:
+                        t.record_stream(self.stream)
 
     def new(self, *shape, dtype=torch.float32):
         return torch.empty(shape, dtype=dtype, device=self.device)

@@ -41,7 +41,10 @@ def definition(X, W, alpha, index, q, counts, dloss, dtype=torch.float64):
     e = 4 * (X.shape[1] + 16) ** 0.5 * U * (z.abs().max(1).values + lse.abs() + 4 * r + 2)
     zero = torch.zeros((), dtype=dtype, device=X.device)
     sx = (s * x).abs()
-    return {"loss": torch.where(counts, loss, zero), "lse": torch.where(counts, lse, zero), "p": p, "d": d, "s": s,
+    scale = r + z.abs().max(1).values + lse.abs() + 2
+    return {"scale": scale, "SX": scale[:, None] * (a @ w.abs()), "SW": (a * scale[:, None]).t() @ x.abs(),
+            "QX": (d.square() @ w.square()).sqrt(), "QW": (d.square().t() @ x.square()).sqrt(),
+            "loss": torch.where(counts, loss, zero), "lse": torch.where(counts, lse, zero), "p": p, "d": d, "s": s,
             "E": e, "dX": d @ w, "dW": d.t() @ x, "AX": a @ w.abs(), "AW": a.t() @ x.abs(),
             # the part of dX's and dW's terms that a token's own E enters
             "EX": e[:, None] * (a @ w.abs()), "EW": (a * e[:, None]).t() @ x.abs(),
@@ -65,3 +68,33 @@ def check_fp32_gradients(r, got, tokens=slice(None), vocabulary=slice(None)):
         of = name[1]
         bound = r["E" + of] + (4 * n ** 0.5 + 8) * U * r["A" + of] + r["G" + of]
         rows_within(name, got[name][rows], r[name][rows], bound[rows])
+
+
+def block_norms(x, rows=64):
+    """The root mean square of blocks of `rows` values."""
+    n = -(-x.shape[0] // rows)
+    return torch.nn.functional.pad(x, (0, n * rows - x.shape[0])).view(n, rows).square().sum(1).sqrt()
+
+
+def check_digits(r, plain, got, dtype, names=("loss", "lse", "dX", "dW")):
+    """Errors as small as the arithmetic's own, so that a lost low part of an operand shows: twice the plain
+    float32 form's (`plain`), and 16 u of the scale of what a value is computed from -- R, the largest logit and lse
+    for the exponents, and that times a gradient's terms.  The planes' roundings make 1 u of R of a logit in
+    the mean, those of exp, log and their arguments 3 u; a row of dW may hang on one logit, of which one in 10^6 is off by
+    four times the mean.  (fp16 alone, without a low part, is off by 2000 u of R.)  In bf16, D and s X are
+    rounded, each by at most b = 2^-8 and independently, so their n terms' errors add up like their squares
+    (Q), and the result is rounded once: b (2 Q + |result|) more.  In norm by row; loss and lse by blocks of 64
+    tokens."""
+    b = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    for name in names:
+        err = got[name].double() - r[name].double()
+        own = (plain[name].double() - r[name].double()).abs()
+        if name in ("loss", "lse"):
+            err, own, rest = (block_norms(v) for v in (err.abs(), own, 16 * U * r["scale"].double()))
+        else:
+            of = name[1]
+            rest = 16 * U * r["S" + of] + b * (2 * r["Q" + of] + r[name].abs()) + r["G" + of]
+            err, own, rest = (v.double().norm(dim=-1) for v in (err, own, rest))
+        bad = ~(err <= 2 * own + rest + 1e-37)
+        assert not bool(bad.any()), (name, int(bad.sum()), bad.nonzero()[:4].flatten().tolist(),
+                                     float((err / (2 * own + rest + 1e-300)).nan_to_num(float("inf")).max()))

@@ -23,6 +23,7 @@ constexpr long kPieceBytes = 768L << 20;           // workspace of one piece of 
 
 struct Call {
     bool f32, grad;
+    bool distill;  // not e.teacher: of no tokens that may be null
     int T, V, H;
     Entries e;
     float alpha;
@@ -44,7 +45,7 @@ long up(long x, long to) { return (x + to - 1) / to * to; }
 
 // What the sort of the entries takes of the workspace, and its launch (distillation's gradient).
 long keys_bytes(int T, int K) { return K > kSortInLds ? 8L * T * K : 0; }
-bool shared(const Call& c) { return c.grad && c.e.teacher && c.e.k > kPairs && c.T > 0; }
+bool shared(const Call& c) { return c.grad && c.distill && c.e.k > kPairs && c.T > 0; }
 void launch_shares(const Call& c, long keys, long value) {
     if (!shared(c)) return;
     uint64_t* const k = (uint64_t*)(c.work + keys);
@@ -241,8 +242,8 @@ int run_few(const Call& c, const FewLayout& l) {
     const int per = wide ? 64 : 32;
     (void)hipGetLastError();
 
-    float* const z = c.e.teacher ? c.picked_out : floats(l.z);
-    if (c.e.teacher) {
+    float* const z = c.distill ? c.picked_out : floats(l.z);
+    if (c.distill) {
         launch_shares(c, l.keys, l.value);
         const TokenArgs t = token_args(c, ws, z, l.scale, l.weight, l.value, D_WHOLE);
         if (c.grad)
@@ -272,7 +273,7 @@ int run_few(const Call& c, const FewLayout& l) {
             part += groups;
             continue;
         }
-        if (c.e.teacher)
+        if (c.distill)
             vocab_patch_kernel<0><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
                 c.e, c.T, v0, vn, nullptr, floats(l.value), ws + l.d, l.vp * 4);
         // dW: 256 vocabulary rows and as many groups as leave eight workgroups a compute unit, but two
@@ -318,7 +319,7 @@ void by_shape(Shape shape, F f) {
 template <typename T, int P>
 int run(const Call& c) {
     using Pl = Planes<P>;
-    const Layout l = layout(P, c.grad, c.T, c.V, c.H, c.e.k, c.e.teacher != nullptr);
+    const Layout l = layout(P, c.grad, c.T, c.V, c.H, c.e.k, c.distill);
     char* ws = c.work;
     auto floats = [&](long at) { return (float*)(ws + at); };
     int *count = (int*)(ws + l.count), *rows = (int*)(ws + l.rows), *pos = (int*)(ws + l.pos);
@@ -336,10 +337,10 @@ int run(const Call& c) {
                         c.ldw % 8 == 0 && (uintptr_t)c.W % 16 == 0 && c.ldw < (1L << 22);
     const bool ends = direct && c.H % Pl::BK != 0;  // kernels of their own: the others take 2 % less time
     // dW's product takes X times each token's weight, but for bf16 distillation, whose D has it
-    char* const xs = c.grad && c.dW && (P == 2 || !c.e.teacher) ? ws + l.xs : nullptr;
+    char* const xs = c.grad && c.dW && (P == 2 || !c.distill) ? ws + l.xs : nullptr;
     (void)hipGetLastError();
 
-    float* const z = c.e.teacher ? c.picked_out : floats(l.z);
+    float* const z = c.distill ? c.picked_out : floats(l.z);
     // the gradient's W is packed in one power of two, that of its largest value
     const int max_blocks = P == 2 && c.grad ? (int)(up(c.V, 4) / 4 < kMaxBlocks ? up(c.V, 4) / 4 : kMaxBlocks) : 0;
     const TokenArgs tokens = token_args(c, ws, z, l.scale, l.weight, l.value, P == 2 ? D_APART : D_PACKED);
@@ -395,13 +396,13 @@ int run(const Call& c) {
                 // whole 256-row tiles of D, so that the products find zeros, not old values, past vn
                 const int tm = (int)up(vn, 256) / S::kBM, tn = (int)up(c.T, S::kBN) / S::kBN;
                 const GradArgs a{w, x, count, rows, w_unit, x_unit, tm, tn, slabs, vn, c.alpha, c.lse, floats(l.scale),
-                                 c.e.teacher ? nullptr : c.e.index, floats(l.value), v0, ws + l.d, d_pitch};
+                                 c.distill ? nullptr : c.e.index, floats(l.value), v0, ws + l.d, d_pitch};
                 if (P == 1 && ends)
                     vocab_grad_kernel<S, P == 1 ? K_ENDS : K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
                 else
                     vocab_grad_kernel<S, K_ROW><<<tm * tn, S::NT, 0, st>>>(a);
             });
-            if (c.e.teacher)
+            if (c.distill)
                 vocab_patch_kernel<P><<<(unsigned)(up((long)c.T * c.e.k, 256) / 256), 256, 0, st>>>(
                     c.e, c.T, v0, vn, pos, floats(l.value), ws + l.d, d_pitch);
             if (c.dX) {
@@ -577,7 +578,7 @@ int vocab_distill(int dtype, int T, int V, int H, int K, float alpha, float teac
     Call c{};
     c.f32 = dtype == VOCAB_F32;
     c.T = T, c.V = V, c.H = H, c.alpha = alpha;
-    c.e = {index, ldi, K, 0, teacher, ldt, teacher_alpha};
+    c.e = {index, ldi, K, 0, teacher, ldt, teacher_alpha}, c.distill = true;
     c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
     c.loss = loss, c.lse_out = lse, c.picked_out = picked;
     c.work = (char*)work, c.stream = stream;
@@ -613,7 +614,7 @@ int vocab_distill_grad(int dtype, int T, int V, int H, int K, float alpha, float
     Call c{};
     c.f32 = dtype == VOCAB_F32, c.grad = true;
     c.T = T, c.V = V, c.H = H, c.alpha = alpha;
-    c.e = {index, ldi, K, 0, teacher, ldt, teacher_alpha};
+    c.e = {index, ldi, K, 0, teacher, ldt, teacher_alpha}, c.distill = true;
     c.X = X, c.ldx = ldx, c.W = W, c.ldw = ldw;
     c.lse = lse, c.picked = picked, c.dloss = dloss;
     c.dX = dX, c.lddx = lddx, c.dW = dW, c.lddw = lddw;

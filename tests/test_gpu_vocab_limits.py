@@ -53,3 +53,25 @@ def test_entries_past_a_grids_threads(T, K):
     want = sg.vocab_distill_grad(X, W, few, few_teacher, *want[1:], dloss)
     got = sg.vocab_distill_grad(X, W, index, teacher, *got[1:], dloss)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H", [64, 1000])
+def test_no_tokens_to_distill(dtype, H):
+    # the gradient of nothing: dW is set to 0, in the workspace that the call asked for
+    from fp32_gemm_05_amd import vocab as binding
+    V, K = 700, 5
+    W = torch.randn(V, H, device="cuda").to(dtype)
+    n = sg.vocab_workspace(dtype, True, 0, V, H, K)
+    memory = torch.full((n + 2 ** 20,), 77, dtype=torch.uint8, device="cuda")
+    dW = torch.full((V, H), float("nan"), device="cuda", dtype=dtype)
+    binding._Problem(torch.empty(0, H, device="cuda", dtype=dtype), W, 1.0, None, K).call(
+        "vocab_distill_grad", memory[:n], binding._TYPES[dtype], 0, V, H, K, 1.0, 1.0, None, H, W.data_ptr(), H, None, K,
+        None, K, None, None, None, None, H, dW.data_ptr(), H)
+    torch.cuda.synchronize()
+    assert not bool(dW.any()) and bool((memory[n:] == 77).all())
+    none = torch.empty(0, K, dtype=torch.int64, device="cuda")
+    X = torch.empty(0, H, device="cuda", dtype=dtype)
+    loss, lse, picked = sg.vocab_distill(X, W, none, none.float())
+    dX, dW = sg.vocab_distill_grad(X, W, none, none.float(), lse, picked, loss)
+    assert loss.shape == lse.shape == (0,) and picked.shape == (0, K) and dX.shape == (0, H) and not bool(dW.any())

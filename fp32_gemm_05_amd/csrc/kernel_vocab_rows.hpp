@@ -701,7 +701,9 @@ __global__ void __launch_bounds__(1024) vocab_loss_kernel(Entries e, const int* 
         lse[t] = live ? l : 0.f;
         if (!e.teacher) {
             const bool named = rows || (e.index[t] >= 0 && e.index[t] < vocab);
-            loss[t] = !live ? 0.f : named ? l - z[t] : NAN;
+            // z and l are sums of their own: of a confident token the difference may come out below 0
+            const float d = l - (named ? z[t] : NAN);
+            loss[t] = !live || d < 0.f ? 0.f : d;
         }
     }
     if (!e.teacher) return;

@@ -61,6 +61,21 @@ def test_confident_tokens(T, V, H, counted, top):
     vc.rows_within("rival", got["dW"][v:v + 1], r["dW"][v:v + 1], bound)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,V,H", [(40, 3000, 256), (100, 3000, 256), (900, 20000, 300)])
+@pytest.mark.parametrize("top", [25.0, 40.0])
+def test_cross_entropy_is_not_negative(T, V, H, top, dtype):
+    X, W, target, dloss = confident(T, V, H, [12.0, 14.0, 16.0, 18.0, 20.0], top, 5 + T)
+    X, W = X.to(dtype), W.to(dtype)
+    loss, _ = sg.vocab_ce(X, W, target)
+    r = ce_definition(X, W, target, dloss)
+    assert bool((loss >= 0).all()), float(loss.min())
+    # lse and z are off by E / 4 each at most but for one in 10^4, and their difference by what both are
+    assert bool(((loss.double() - r["loss"]).abs() <= r["E"]).all())
+    target[::2] = V  # outside the vocabulary: still NaN
+    assert bool(torch.isnan(sg.vocab_ce(X, W, target)[0][::2]).all())
+
+
 @pytest.mark.parametrize("T,V,H", [(100, 1500, 96), (300, 20000, 200)])
 @pytest.mark.parametrize("alpha", [1e5, -1e6, 1e7])
 def test_logits_beyond_what_fp32_tells_apart(T, V, H, alpha):

@@ -1,6 +1,6 @@
 """Train a small language-model head with the library's own products: hidden states are a GEMM of the
 inputs, the head's loss is cross entropy plus distillation from a teacher's top logits, and the gradient
-goes back through the head into the GEMM's weights.  The T x V logits are never in memory.
+goes back through the head into the GEMM's weights.  The T x V logits are not kept.
 
     python examples/vocab_head.py [--steps 30] [--dtype f32|bf16] [--tokens 512] [--vocab 4000] [--hidden 256]
 """

@@ -19,10 +19,11 @@
 // P = 2: fp32 operands as the sum of two fp16 values, a row stored in blocks of 32 k as [32 high]
 // [32 low].  The operand -- a row of X, a row of W in the forward call, the whole of W in the gradient's,
 // whose dX sums over its rows -- is scaled by a power of two first, so that its largest value lies in
-// [2^14, 2^15); high + low then holds every value down to 2^-16 of the largest to one fp32 rounding
-// (2^-24 of itself) and smaller ones to 2^-40 of the largest.  Three products (hl, lh, hh) are
-// accumulated in fp32; the one left out, ll, is below 2^-24 of the whole.  Three fp16 MFMAs do the
-// work of an fp32 product at 16/3 of the fp32 MFMA rate, from operands of the same size.
+// [2^14, 2^15); high + low then holds every value down to 2^-16 of the largest to 2^-23 of itself (23 bits:
+// a quarter of all fp32 values are off by their last one) and smaller ones to 2^-40 of the largest.  Three
+// products (hl, lh, hh) are accumulated in fp32; the one left out, ll, is up to 2^-22 of the whole, 2^-25 in
+// the mean and of either sign.  Three fp16 MFMAs do the work of an fp32 product at 16/3 of the fp32 MFMA
+// rate, from operands of the same size.
 #pragma once
 
 #include "kernel_common.hpp"

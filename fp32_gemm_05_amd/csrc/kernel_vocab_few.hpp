@@ -8,7 +8,8 @@
 // Three ways to multiply.  Bf16: v_mfma_f32_16x16x32_bf16; D, kept in fp32, enters its products as two
 // bf16 values (16 bits), which costs no time here.  Fp32: v_mfma_f32_16x16x4_f32, exact products; at
 // more than 16 tokens its rate, not the memory's, would bound, so there Fp32Split cuts each value into
-// three bf16 parts on the way (24 bits) and takes the six products above 2^-24 of the whole: 384 cycles
+// three bf16 parts on the way (24 bits; of values from 2^-110 to 2^127, where the parts neither vanish nor
+// round up to infinity) and takes the six products above 2^-24 of the whole: 384 cycles
 // a 2 KB of W instead of 1024.
 //
 // A "chunk" is E consecutive elements along k in one lane.  A step is the 4 E elements that the four

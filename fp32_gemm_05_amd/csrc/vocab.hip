@@ -2,9 +2,9 @@
 // the logits z = alpha * X W^T, forward and gradient, without the T x V logits in memory.
 //
 // Forward: one product whose tiles end as per-token maxima and sums of exponentials (log-sum-exp),
-// and one dot product per named entry.  Gradient: the vocabulary is taken in pieces; a piece's
-// logits are recomputed into D = d(loss)/dz (bf16, or two fp16 planes for fp32), from which
-// dX += D W and dW = D^T X follow.  The tokens that do not count are left out at the start: the
+// and one dot product per named entry.  Gradient: the vocabulary is taken in pieces (one, where it fits
+// kPieceBytes); a piece's logits are recomputed into D = d(loss)/dz (bf16, or two fp16 planes for fp32),
+// from which dX += D W and dW = D^T X follow.  The tokens that do not count are left out at the start: the
 // others are packed together, so they cost no product, and whatever their rows hold reaches no
 // gradient.
 #include <limits.h>
@@ -66,7 +66,8 @@ using Small = Tile<P, 128, 64, 64, 32, 3, 3>;
 enum Shape { SMALL, MID, BIG };
 
 // The workspace: byte offsets of its arrays for a call's sizes (the pointers of the call are not
-// looked at, so that its size can be asked for beforehand).
+// looked at, so that its size can be asked for beforehand; so a packed W has its place also where bf16 W will
+// be read as it stands).
 struct Layout {
     int tp, hk, hp;     // padded tokens, hidden as a product's k, hidden as a product's rows
     int piece, pieces;  // vocabulary rows of a piece (a multiple of 256), number of pieces

@@ -8,7 +8,13 @@ workspace, and the call.  No arithmetic happens here.
 
 X (T x H) and W (V x H) are both float32 or both bfloat16, row-major with any row stride (a
 contiguous copy is asked for where rows overlap).  ``vocab_cross_entropy`` and
-``vocab_distillation`` are the same operators for torch's autograd.
+``vocab_distillation`` are the same operators for torch's autograd, which gives gradients of the losses
+alone; the four functions above are no part of it: their results carry no gradient, also where X or W
+requires one.
+
+``stream`` (a torch stream of X's device, or a handle) is where a call runs and where its results and its
+workspace are allocated; the caller orders it behind what made the operands, which are kept until it
+has read them.
 """
 from __future__ import annotations
 

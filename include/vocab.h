@@ -19,6 +19,8 @@
  * y the one-hot target, or the teacher's q added up per vocabulary row (an entry may be named
  * twice).  They recompute the logits in pieces of the vocabulary, from the forward call's lse.
  *
+ * A piece's D is a workspace array of at most about 768 MB; one piece may be the whole vocabulary.
+ *
  * Tokens that do not count -- target == ignore_index, or no index >= 0 -- have loss 0, lse 0 and
  * gradient 0, whatever X, dloss and teacher hold there (NaN and infinities included); among more
  * than 64 tokens they cost no product either.  A target or an index >= V (or a target < 0 that is
@@ -37,12 +39,16 @@
  * a power of two (a token's own for X; for W a row's own in the forward calls, one for the whole of W in
  * the gradients): values down to 2^-16 of the largest keep 23 bits, smaller ones are held to 2^-40 of the
  * largest.  Of D = s * (..), s = alpha * dloss, the part in brackets is held to 2^-40, in dX for every token
- * by itself; dW takes s * X in one power of two, held to 2^-40 of its largest value.  Of 17 to 64 tokens
- * the operands are three bf16 parts each, 24 bits; with up to 16 the products are fp32's own.
- * An infinity in W may make NaN of every logit of its row, and a teacher's row of -infinities alone
- * makes its token NaN.  With bf16 X and W, D is rounded to bf16 for the two gradient products (cross
- * entropy scales a token's row so that its target's entry is exact), and dX and dW are rounded to
- * bf16 at the end.
+ * by itself; dW takes s * X in one power of two, held to 2^-40 of its largest value.  Values of W above
+ * 2^90 may overflow.  Of 17 to 64 tokens the operands are three bf16 parts each, 24 bits; with up to 16 the
+ * products are fp32's own.  An infinity in W may make NaN of every logit of its row, and a teacher's row of
+ * -infinities alone makes its token NaN.  With bf16 X and W, D is rounded for the two gradient products: to
+ * bf16 (cross entropy scales a token's row so that its target's entry is exact), or of up to 64 tokens to two
+ * bf16 parts; dX and dW are rounded to bf16 at the end.
+ *
+ * A loss is a difference of lse and logits that were summed apart (of up to 64 tokens' cross entropy,
+ * together), each off by a few roundings of its size: up to 3e-5 at a logit of 40, which is all of a confident
+ * token's loss.  Cross entropy is not below 0.
  *
  * Return codes as in sgemm.h: 0, -i for argument i, +hipError_t from a launch.  T = 0 is a quick
  * return (dW, when wanted, is set to 0).
@@ -59,7 +65,11 @@ extern "C" {
 enum { VOCAB_F32 = 0, VOCAB_BF16 = 1 }; /* the type of X, W, dX and dW */
 
 /* Bytes of workspace of a call: grad 0 for the forward entry points, 1 for the gradients; K = 0 for
- * cross entropy, else the teacher's entries per token.  Limits of every call: T <= 2^21,
+ * cross entropy, else the teacher's entries per token.  Of more than 64 tokens it holds about 768 MB at
+ * most for a piece of the vocabulary, of 256 rows or more (packed W, also where bf16 W needs no packing, and D); X packed, in a gradient
+ * twice, and dX in fp32 once for each part that its product is cut into; and T V / 8 bytes of
+ * maxima and sums in a forward call.  A gradient from more than 8192 entries a token takes 8 T K bytes to
+ * sort them.  Limits of every call: T <= 2^21,
  * V <= 2^31 - 1025, H <= 2^20, K * T < 2^31.  Negative: -i for argument i. */
 SGEMM_API long long vocab_workspace(int dtype, int grad, int T, int V, int H, int K);
 

@@ -70,3 +70,30 @@ def test_time_grows_with_the_entries_not_their_square(T):
     small, large = us(2048), us(16384)
     print(f"T={T}: {small:.0f} us with 2048 entries, {large:.0f} us with 16384")
     assert large < 24 * small
+
+
+@pytest.mark.parametrize("T", [5, 80])
+@pytest.mark.parametrize("K", [300, 9000])
+def test_graph_replays(T, K):
+    X, W, index, teacher, dloss = problem(T, 2000, 40, K, T + K)
+
+    def run():
+        return gradients(X, W, index, teacher, dloss)
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        run()
+    torch.cuda.current_stream().wait_stream(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for i in range(4):
+        index.copy_(index.roll(1, 0))
+        index[i % T] = index[i % T].sort().values.flip(0)
+        teacher.mul_(0.9)
+        eager = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(eager[n], captured[n]) for n in eager), i

@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(256) vocab_scan_kernel(ScanArgs a) {
         float m = 0.f;
         for (long i = (long)b * 4 + wave; i < a.t.waves; i += (long)a.token_blocks * 4) {
             const float weight = token_wave<T, GRAD>(a.t, i);
-            if (GRAD && a.x_part) m = row_max((const T*)a.t.x + i * a.t.ldx, a.t.hidden, weight, m);
+            if (GRAD && a.x_part && weight != 0.f) m = row_max((const T*)a.t.x + i * a.t.ldx, a.t.hidden, weight, m);
         }
         if (!GRAD || !a.x_part) return;
         m = block_max(m);

@@ -30,13 +30,19 @@ from ._binding import (  # noqa: F401
     tile_order,
 )
 
-_VOCAB = ("vocab_ce", "vocab_ce_grad", "vocab_distill", "vocab_distill_grad", "vocab_workspace",
-          "vocab_cross_entropy", "vocab_distillation")
+# the operators' modules, imported at the first use of one of their names
+_OPERATORS = {
+    "vocab": ("vocab_ce", "vocab_ce_grad", "vocab_distill", "vocab_distill_grad", "vocab_workspace",
+              "vocab_cross_entropy", "vocab_distillation"),
+    "linear": ("linear_act", "linear_act_grad", "linear_workspace", "linear_layer"),
+}
+_MODULE_OF = {name: module for module, names in _OPERATORS.items() for name in names}
 
 
 def __getattr__(name):
-    if name not in _VOCAB:
+    if name not in _MODULE_OF:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import vocab
-    globals().update({n: getattr(vocab, n) for n in _VOCAB})
+    import importlib
+    module = importlib.import_module("." + _MODULE_OF[name], __name__)
+    globals().update({n: getattr(module, n) for n in _OPERATORS[_MODULE_OF[name]]})
     return globals()[name]

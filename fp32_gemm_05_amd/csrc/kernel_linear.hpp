@@ -1,0 +1,469 @@
+// kernel_linear.hpp -- the kernels of the linear layer with an epilogue (gfx950):
+//
+//   Z = X W^T + bias,  Y = act(Z) + residual;   dZ = dY act'(Z),  dX = dZ W,  dW = dZ^T X,  dbias = sum_t dZ.
+//
+// More than kFewTokens tokens: the tile loop of kernel_vocab.hpp, fp32 operands on the fp32 MFMA (P = 0: no
+// operand is cut into parts, so infinities, NaN and values of any scale come out as an fp32 sum gives them),
+// bf16 on the bf16 MFMA.  Output features are the M side of Z, hidden that of dX and dW, so that a lane holds
+// four consecutive elements of one row of the result.  Operands are read in place where their rows are whole
+// 16-byte quads, k that ends inside a slab included; others are packed first.
+//
+// At most kFewTokens tokens: one pass over W, straight from memory into the MFMA operands at any alignment
+// (the modes of kernel_vocab_few.hpp).
+#pragma once
+
+#include "kernel_vocab_few.hpp"
+
+namespace libsgemm {
+namespace linear {
+
+using vocab::K_COL;
+using vocab::K_ENDS;
+using vocab::K_ROW;
+using vocab::Operand;
+using vocab::Order;
+using vocab::Planes;
+using vocab::Tile;
+using vocab::u32x4;
+
+enum Act { NONE = 0, RELU = 1, GELU = 2, GELU_TANH = 3, SILU = 4 };
+
+// Four values of T at any alignment of T; the first n of them.
+template <typename T>
+__device__ inline f32x4 load4(const T* p, int n = 4) {
+    T v[4] = {};
+    if (n >= 4)
+        __builtin_memcpy(v, p, sizeof(v));
+    else
+        for (int i = 0; i < 3; ++i)
+            if (i < n) v[i] = p[i];
+    return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+template <typename T>
+__device__ inline void store4(T* p, f32x4 x, int n = 4) {
+    const T v[4] = {(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
+    if (n >= 4)
+        __builtin_memcpy(p, v, sizeof(v));
+    else
+        for (int i = 0; i < 3; ++i)
+            if (i < n) p[i] = v[i];
+}
+
+// The normal distribution's upper tail Q(t) = erfc(t / sqrt 2) / 2 for t >= 0 as k P(k) exp(-t^2 / 2), k = 1 /
+// (1 + 0.375 t): P of degree 8 fitted to the least largest relative error, 2.3e-7 (with fp32's roundings 5e-7),
+// so that the far negative side of gelu keeps its digits, which 1 + erf loses.  bell: exp(-t^2 / 2).
+__device__ inline float upper_tail(float t, float& bell) {
+    bell = __builtin_amdgcn_exp2f(-0.72134752044448170f * t * t);
+    const float k = __builtin_amdgcn_rcpf(__builtin_fmaf(0.375f, t, 1.f));
+    float p = -0.0329474956f;
+    p = __builtin_fmaf(p, k, 0.137030736f);
+    p = __builtin_fmaf(p, k, -0.186776593f);
+    p = __builtin_fmaf(p, k, 0.0508598723f);
+    p = __builtin_fmaf(p, k, 0.0155141391f);
+    p = __builtin_fmaf(p, k, 0.0886697173f);
+    p = __builtin_fmaf(p, k, 0.128441304f);
+    p = __builtin_fmaf(p, k, 0.149604827f);
+    p = __builtin_fmaf(p, k, 0.149603382f);
+    return p * k * bell;
+}
+__device__ inline float sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
+}
+constexpr float kTanhA = 0.79788456080286536f, kTanhB = 0.044715f;  // sqrt(2 / pi)
+
+template <int ACT>
+__device__ inline float act(float z) {
+    if constexpr (ACT == RELU) return z < 0.f ? 0.f : z;  // a NaN stays
+    if constexpr (ACT == GELU) {
+        float bell;
+        const float t = fminf(fabsf(z), 20.f);  // Q is 0 in fp32 from 14 on
+        return (z < 0.f ? 0.f : z) - t * upper_tail(t, bell);
+    }
+    // (1 + tanh(w)) / 2 = sigmoid(2 w)
+    if constexpr (ACT == GELU_TANH) return z * sigmoid(2.f * kTanhA * z * __builtin_fmaf(kTanhB * z, z, 1.f));
+    if constexpr (ACT == SILU) return z * sigmoid(z);
+    return z;
+}
+template <int ACT>
+__device__ inline float slope(float z) {
+    if constexpr (ACT == RELU) return z > 0.f ? 1.f : z != z ? z : 0.f;
+    // past 20 each of these slopes is 0 or 1 in fp32, and z^2 below stays finite
+    const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(z, 20.f), -20.f);
+    if constexpr (ACT == GELU) {
+        float bell;
+        const float q = upper_tail(fabsf(c), bell);
+        return __builtin_fmaf(c * 0.39894228040143268f, bell, c < 0.f ? q : 1.f - q);
+    }
+    if constexpr (ACT == GELU_TANH) {
+        const float s = sigmoid(2.f * kTanhA * c * __builtin_fmaf(kTanhB * c, c, 1.f));
+        return __builtin_fmaf(2.f * kTanhA * c * __builtin_fmaf(3.f * kTanhB * c, c, 1.f), s * (1.f - s), s);
+    }
+    if constexpr (ACT == SILU) {
+        const float s = sigmoid(c);
+        return s * __builtin_fmaf(c, 1.f - s, 1.f);
+    }
+    return 1.f;
+}
+// f(integral_constant) for the activation of a call; uniform.
+template <class F>
+__device__ inline void by_act(int a, F f) {
+    switch (a) {
+        case RELU: return f(std::integral_constant<int, RELU>{});
+        case GELU: return f(std::integral_constant<int, GELU>{});
+        case GELU_TANH: return f(std::integral_constant<int, GELU_TANH>{});
+        case SILU: return f(std::integral_constant<int, SILU>{});
+        default: return f(std::integral_constant<int, NONE>{});
+    }
+}
+
+// What becomes of a finished row of sums: rows of `n` tokens or of dW, columns of `m`.
+struct Finish {
+    int n, m;           // rows and columns of the result
+    int act, wide;      // wide: out and residual are fp32 beside bf16 operands
+    const void* bias;   // [m] or null
+    const void* residual;
+    long ld_residual;
+    void* z;            // null: not kept
+    long ld_z;
+    void* out;
+    long ld;
+};
+
+// N groups of four consecutive columns of a row, STEP columns apart.  FORWARD: not, the sums are stored as they are.
+template <bool FORWARD, typename T, int N, int STEP = 8>
+__device__ inline void finish_block(const Finish& f, long row, int col, f32x4 (&v)[N]) {
+    auto each = [&](auto body) {
+#pragma unroll
+        for (int g = 0; g < N; ++g)
+            if (col + g * STEP < f.m) body(v[g], col + g * STEP, f.m - col - g * STEP);
+    };
+    if constexpr (FORWARD) {
+        if (f.bias) each([&](f32x4& x, int c, int left) { x += load4((const T*)f.bias + c, left); });
+        if (f.z) each([&](f32x4& x, int c, int left) { store4((T*)f.z + row * f.ld_z + c, x, left); });
+        by_act(f.act, [&](auto which) {
+#pragma unroll
+            for (int g = 0; g < N; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[g][i] = act<decltype(which)::value>(v[g][i]);
+        });
+        if (sizeof(T) == 2 && f.wide) {
+            if (f.residual)
+                each([&](f32x4& x, int c, int left) { x += load4((const float*)f.residual + row * f.ld_residual + c, left); });
+            each([&](f32x4& x, int c, int left) { store4((float*)f.out + row * f.ld + c, x, left); });
+            return;
+        }
+        if (f.residual)
+            each([&](f32x4& x, int c, int left) { x += load4((const T*)f.residual + row * f.ld_residual + c, left); });
+    }
+    each([&](f32x4& x, int c, int left) { store4((T*)f.out + row * f.ld + c, x, left); });
+}
+
+struct ProductArgs {
+    Operand a, b;          // M side, N side
+    int tiles_m, tiles_n;
+    int k, slabs, splits;  // of the long axis, cut into `splits` parts of whole slabs
+    float* part;           // splits > 1: [split][row of whole tiles][pitch], summed by linear_sum_kernel
+    long rows, pitch;
+    Finish f;
+};
+
+// One product.  With few tiles the long axis is cut, so that the chip is filled, and the parts are
+// summed in a fixed order.
+template <class T, Order OA, Order OB, bool TAIL, bool FORWARD>
+__global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
+    typedef typename Planes<T::kP>::Half E;
+    __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
+    const int tiles = a.tiles_m * a.tiles_n, z = blockIdx.x / tiles;
+    int tm, tn;
+    tile_of(blockIdx.x - z * tiles, tiles, a.tiles_m, a.tiles_n, 4, tm, tn);
+    const int m0 = tm * T::kBM, n0 = tn * T::kBN;
+    const int first = (int)((long)a.slabs * z / a.splits), last = (int)((long)a.slabs * (z + 1) / a.splits);
+    T t;
+    t.template run<OA, OB, TAIL>(lds, a.a, m0, a.b, n0, first, last - first, a.k - (last - 1) * T::BK);
+    if (a.splits > 1) {
+#pragma unroll
+        for (int j = 0; j < T::NB; ++j) {
+            float* out = a.part + (z * a.rows + n0 + t.col(j)) * a.pitch + m0;
+#pragma unroll
+            for (int i = 0; i < T::MB; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *(f32x4*)(out + t.row(i, 4 * g)) = f32x4{t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1],
+                                                             t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
+        }
+        return;
+    }
+    // a block's values leave the accumulators before anything is done to them, and a block ends before the next
+    // begins: all of them together would spill
+#pragma unroll
+    for (int j = 0; j < T::NB; ++j) {
+#pragma unroll
+        for (int i = 0; i < T::MB; ++i) {
+            // anew for each block: as values of the whole kernel they and the addresses made of them would spill
+            int n = n0 + t.col(j), m = m0 + t.row(i, 0);
+            asm volatile("" : "+v"(n), "+v"(m));
+            f32x4 v[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                v[g] = f32x4{t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1], t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
+            if (n < a.f.n) finish_block<FORWARD, E>(a.f, n, m, v);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+// The sum of a product's parts, finished.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_sum_kernel(const float* part, int splits, long rows, long pitch, Finish f) {
+    const int n = blockIdx.x, m = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (m >= f.m) return;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int z = 0; z < splits; ++z) v += *(const f32x4*)(part + (z * rows + n) * pitch + m);
+    f32x4 one[1] = {v};
+    finish_block<true, T>(f, n, m, one);
+}
+
+// Rows of an operand that cannot be read in place, copied to rows of whole slabs, 16-byte aligned, zeros at
+// their ends.  One workgroup a row.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_pack_kernel(const T* in, long ld, int cols, T* out, long pitch) {
+    constexpr int V = 16 / sizeof(T);
+    const T* src = in + (size_t)blockIdx.x * ld;
+    T* dst = out + (size_t)blockIdx.x * pitch;
+    for (int c = threadIdx.x * V; c < pitch; c += 256 * V) {
+        T v[V] = {};
+        if (c + V <= cols)
+            __builtin_memcpy(v, src + c, 16);
+        else
+            for (int i = 0; i < V; ++i)
+                if (c + i < cols) v[i] = src[c + i];
+        *(u32x4*)(dst + c) = *(const u32x4*)v;
+    }
+}
+
+struct SlopeArgs {
+    const void *dy, *z;  // z null: no activation
+    long ld_dy, ld_z;
+    int rows, cols, act;
+    int per;             // rows of a workgroup
+    void* dz;            // null: dY is read in place by the products, only its sums are wanted
+    long pitch;          // whole 16 bytes
+    float* sums;         // [workgroup of rows][pitch], null: not wanted
+};
+
+// dZ = dY act'(Z), in the operands' type for the products, and its column sums over `per` rows, of
+// the values before they are rounded.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_slope_kernel(SlopeArgs a) {
+    constexpr int V = 16 / sizeof(T);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int c = (blockIdx.x * 64 + lane) * V, left = a.cols - c;
+    const int r0 = blockIdx.y * a.per, r1 = imin(r0 + a.per, a.rows);
+    float sum[V] = {};
+    if (c < a.pitch)
+        by_act(a.z ? a.act : NONE, [&](auto which) {
+            constexpr int ACT = decltype(which)::value;
+#pragma unroll 2
+            for (int r = r0 + wave; r < r1; r += 4) {
+                f32x4 d[V / 4];
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) {
+                    d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    const int n = left - 4 * q;
+                    if (n > 0) d[q] = load4((const T*)a.dy + r * a.ld_dy + c + 4 * q, n);
+                    if (ACT != NONE && n > 0) {
+                        const f32x4 z = load4((const T*)a.z + r * a.ld_z + c + 4 * q, n);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[q][i] = i < n ? d[q][i] * slope<ACT>(z[i]) : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[4 * q + i] += d[q][i];
+                }
+                if (a.dz) {
+                    T v[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] = (T)d[i / 4][i % 4];
+                    *(u32x4*)((T*)a.dz + r * a.pitch + c) = *(const u32x4*)v;
+                }
+            }
+        });
+    if (!a.sums) return;
+    __shared__ float all[4][64][V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) all[wave][lane][i] = sum[i];
+    __syncthreads();
+    if (wave > 0 || c >= a.pitch) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        a.sums[(size_t)blockIdx.y * a.pitch + c + i] = all[0][lane][i] + all[1][lane][i] + all[2][lane][i] + all[3][lane][i];
+}
+
+// dbias from the partial sums of `parts` workgroups: 64 columns a workgroup, 16 parts at a time.
+template <typename T>
+__global__ void __launch_bounds__(1024) linear_bias_kernel(const float* sums, int parts, long pitch, int cols, T* out) {
+    __shared__ float all[16][64];
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6, c = blockIdx.x * 64 + x;
+    float s = 0.f;
+    if (c < cols)
+        for (int p = y; p < parts; p += 16) s += sums[(size_t)p * pitch + c];
+    all[y][x] = s;
+    __syncthreads();
+    if (y > 0 || c >= cols) return;
+    for (int i = 1; i < 16; ++i) s += all[i][x];
+    out[c] = (T)s;
+}
+
+// A result of no tokens: zeros.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_zero_kernel(T* out, long ld, int cols) {
+    for (int c = blockIdx.y * 256 + threadIdx.x; c < cols; c += gridDim.y * 256) out[(size_t)blockIdx.x * ld + c] = (T)0.f;
+}
+
+// ---- at most kFewTokens tokens -----------------------------------------------------------------------
+
+struct FewArgs {
+    int tokens, outs, hidden;
+    const void *x, *w;
+    long ldx, ldw;
+    Finish f;
+};
+
+// Z of 16 MR output features and all tokens.  The NW waves of a workgroup take every NW-th group of U steps
+// of the hidden size each and add up in LDS.
+template <class C, int NB, int MR, int NW>
+__global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
+    typedef typename C::T T;
+    typedef typename C::Raw Raw;
+    typedef typename C::Part Part;
+    constexpr int U = C::P == 3 ? (NB == 4 && MR == 2 ? 2 : 1) : MR == 4 ? 2 : 4;  // steps held in registers
+    constexpr bool HOLD = sizeof(T) == 2 || NB == 1;
+    static_assert(NW >= NB, "a wave for each block of tokens");
+    __shared__ f32x4 sums[NW][NB][64];
+    const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+    const int wave = (int)uniform_u32(threadIdx.x >> 6);
+    const int r0 = blockIdx.x * 16 * MR;
+    const T *w[MR], *x[NB];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) w[m] = (const T*)a.w + (size_t)imin(r0 + 16 * m + l, a.outs - 1) * a.ldw + g * C::E;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) x[b] = (const T*)a.x + (size_t)imin(16 * b + l, a.tokens - 1) * a.ldx + g * C::E;
+    f32x4 acc[MR][NB] = {};
+    auto multiply = [&](const Raw (&vw)[MR], const Raw (&vx)[NB]) {
+        Part pw[MR][C::P];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) C::parts(vw[m], pw[m]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            Part px[C::P];
+            C::parts(vx[b], px);
+            f32x4* c[MR];
+#pragma unroll
+            for (int m = 0; m < MR; ++m) c[m] = &acc[m][b];
+            vocab::few_mma<C>(pw, px, c);
+        }
+    };
+    const int full = a.hidden / C::STEP, groups = full / U;
+    for (int q = wave; q < groups; q += NW) {
+        Raw vw[U][MR], vx[U][NB];
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int u = 0; u < U; ++u) vw[u][m] = C::template load<Raw>(w[m] + (size_t)(q * U + u) * C::STEP);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int u = 0; u < U; ++u) vx[u][b] = C::template load<Raw>(x[b] + (size_t)(q * U + u) * C::STEP);
+        if (HOLD) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(vw[u], vx[u]);
+    }
+    const int steps = (a.hidden + C::STEP - 1) / C::STEP;
+    for (int s = groups * U + wave; s < steps; s += NW) {
+        const int n = a.hidden - s * C::STEP - g * C::E;  // elements of this lane's chunk, maybe none
+        Raw vw[MR], vx[NB];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) vw[m] = C::template load<Raw>(w[m] + (size_t)s * C::STEP, n);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vx[b] = C::template load<Raw>(x[b] + (size_t)s * C::STEP, n);
+        multiply(vw, vx);
+    }
+    // wave b gets tokens 16 b + l, output features r0 + 16 m + 4 g + i
+    f32x4 z[MR];
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+        if (m > 0) __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[m][b];
+        __syncthreads();
+        if (wave < NB) {
+            z[m] = sums[0][wave][lane];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) z[m] += sums[i][wave][lane];
+        }
+    }
+    const int n = 16 * wave + l;
+    if (wave >= NB || n >= a.tokens) return;
+    finish_block<true, T, MR, 16>(a.f, n, r0 + 4 * g, z);
+}
+
+struct FewSlopeArgs {
+    const void *dy, *z, *x;
+    long ld_dy, ld_z, ldx;
+    int tokens, outs, hidden, act;
+    int groups;      // workgroups of 64 output features
+    float* d;        // [16 NB][pitch]: dZ, zeros past the tokens and the output features
+    long pitch;
+    void* dbias;     // null: not wanted
+    char* xt;        // X in the order of vocab_few_grad_kernel, `chunks` of them
+    int kt, chunks;
+};
+
+// dZ and dbias of few tokens, 64 output features a workgroup; the workgroups after those put X in the order
+// that dW's product takes.
+template <class C, int NB>
+__global__ void __launch_bounds__(256) linear_few_slope_kernel(FewSlopeArgs a) {
+    typedef typename C::T T;
+    if ((int)blockIdx.x >= a.groups) {
+        const int i = ((int)blockIdx.x - a.groups) * 256 + (int)threadIdx.x;
+        if (i >= a.chunks) return;
+        const int lane = i & 63, j = (i >> 6) % a.kt, hb = (i >> 6) / a.kt;
+        const int h = C::hidden_of(hb, lane & 15), t = j * C::STEP + (lane >> 4) * C::E;
+        typename C::Raw v = {};
+#pragma unroll
+        for (int q = 0; q < C::E; ++q)
+            if (t + q < a.tokens && h < a.hidden) v[q] = ((const T*)a.x)[(t + q) * a.ldx + h];
+        ((typename C::Raw*)a.xt)[i] = v;
+        return;
+    }
+    __shared__ f32x4 all[16][16];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = blockIdx.x * 64 + 4 * tx, left = a.outs - c;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    by_act(a.z ? a.act : NONE, [&](auto which) {
+        constexpr int ACT = decltype(which)::value;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int t = 16 * b + ty;
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            if (t < a.tokens && left > 0) {
+                d = load4((const T*)a.dy + t * a.ld_dy + c, left);
+                if (ACT != NONE) {
+                    const f32x4 z = load4((const T*)a.z + t * a.ld_z + c, left);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = i < left ? d[i] * slope<ACT>(z[i]) : 0.f;
+                }
+            }
+            *(f32x4*)(a.d + t * a.pitch + c) = d;
+            sum += d;
+        }
+    });
+    if (!a.dbias) return;
+    all[ty][tx] = sum;
+    __syncthreads();
+    if (ty > 0 || left <= 0) return;
+    for (int i = 1; i < 16; ++i) sum += all[i][tx];
+    store4((T*)a.dbias + c, sum, left);
+}
+
+}  // namespace linear
+}  // namespace libsgemm

@@ -23,7 +23,8 @@
 // a quarter of all fp32 values are off by their last one) and smaller ones to 2^-40 of the largest.  Three
 // products (hl, lh, hh) are accumulated in fp32; the one left out, ll, is up to 2^-22 of the whole, 2^-25 in
 // the mean and of either sign.  Three fp16 MFMAs do the work of an fp32 product at 16/3 of the fp32 MFMA
-// rate, from operands of the same size.
+// rate, from operands of the same size.  P = 0: fp32 as it is, on v_mfma_f32_32x32x2_f32; the products of
+// kernel_linear.hpp alone take it.
 #pragma once
 
 #include "kernel_common.hpp"
@@ -37,11 +38,14 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int P>
 struct Planes {
-    static_assert(P == 1 || P == 2, "bf16, or fp32 as two fp16 planes");
-    typedef typename std::conditional<P == 1, __bf16, _Float16>::type Half;
-    typedef Half Half8 __attribute__((ext_vector_type(8)));
+    static_assert(P >= 0 && P <= 2, "fp32, bf16, or fp32 as two fp16 planes");
+    typedef typename std::conditional<P == 0, float, typename std::conditional<P == 1, __bf16, _Float16>::type>::type Half;
+    typedef Half Half8 __attribute__((ext_vector_type(P == 0 ? 4 : 8)));  // a fragment: 16 bytes
     typedef Half Half4 __attribute__((ext_vector_type(4)));
-    static constexpr int BK = 64 / P;    // k per slab
+    static constexpr int N = P == 0 ? 1 : P;        // planes
+    static constexpr int SIZE = P == 0 ? 4 : 2 * P;  // bytes of an element in them
+    static constexpr int STEP = P == 0 ? 8 : 16;    // k of a step: the lane halves hold a fragment each
+    static constexpr int BK = 128 / SIZE;           // k per slab
     static constexpr int QR = 8;         // 16-byte quads per row and slab
     static constexpr int ROW = QR * 16;  // bytes per row and slab
     // LDS quad u of row r holds the row's quad swz(r, u), an involution.  A 128-bit read is served
@@ -50,10 +54,10 @@ struct Planes {
     __host__ __device__ static constexpr int swz(int r, int u) { return u ^ ((r >> 1) & 7); }
     // Byte offset of plane p of element k within a row.
     __host__ __device__ static constexpr long at(long k, int p) {
-        return P == 1 ? 2 * k : (k >> 5) * 128 + p * 64 + (k & 31) * 2;
+        return P <= 1 ? SIZE * k : (k >> 5) * 128 + p * 64 + (k & 31) * 2;
     }
     // Bytes of a row of kp elements (kp a multiple of BK).
-    __host__ __device__ static constexpr long pitch(long kp) { return 2L * P * kp; }
+    __host__ __device__ static constexpr long pitch(long kp) { return (long)SIZE * kp; }
 };
 
 // x as P values; infinities and NaN have no low part.
@@ -86,6 +90,7 @@ __device__ inline void store4(char* row, long k, const float (&x)[4]) {
 }
 template <int P>
 __device__ inline f32x16 mfma(typename Planes<P>::Half8 a, typename Planes<P>::Half8 b, f32x16 c) {
+    static_assert(P > 0, "fp32 steps are four products");
     if constexpr (P == 1)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     else
@@ -133,22 +138,25 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 template <int P, Order O, int R, int W, int NT>
 struct Side {
     static constexpr int BK = Planes<P>::BK, NW = NT / 64;
-    static constexpr int BYTES = R * BK * 2 * P;                            // of a slab in LDS
-    static constexpr int QUADS = O != K_COL ? Planes<P>::QR : R * P / 8;    // per stored row
+    static constexpr int SIZE = Planes<P>::SIZE, NP = Planes<P>::N;
+    static constexpr int BYTES = R * BK * SIZE;                             // of a slab in LDS
+    static constexpr int QUADS = O != K_COL ? Planes<P>::QR : R * SIZE / 16;  // per stored row
     static constexpr int ROW = QUADS * 16;
     static constexpr int L = BYTES / 16 / NT;                               // loads per thread
     static constexpr int B = W / 32;                                        // 32-row blocks of a wave
-    static constexpr int KK = BK / 16;
+    static constexpr int KK = BK / Planes<P>::STEP;
     static_assert(BYTES / 16 % NT == 0, "whole loads per thread");
 
     // K_COL: chunk c (64 bytes: 32 m of one plane) of LDS row r holds chunk c ^ flip(r).  A transposed
     // 64-bit read is served in passes of 32 lanes, which read one chunk each of four consecutive
     // rows: the flips put those on the four different quarters of the 64 banks.
-    static constexpr int CHUNKS = R * P / 32;
-    static_assert(O != K_COL || CHUNKS % 2 == 0, "chunks pair up");
+    // fp32 (P = 0) is read 32 bits a lane, the lane halves 32 m each of rows 4 apart: the rows of one half
+    // have their halves of 64 m traded.
+    static constexpr int CHUNKS = R * SIZE / 64;
+    static_assert(O != K_COL || CHUNKS % (P == 0 ? 4 : 2) == 0, "chunks pair up");
     __host__ __device__ static constexpr int flip(int r) { return CHUNKS % 4 == 0 ? (r & 3) : ((r >> 1) & 1); }
     __host__ __device__ static constexpr int source_quad(int r, int u) {
-        return O != K_COL ? Planes<P>::swz(r, u) : (u ^ (flip(r) << 2));
+        return O != K_COL ? Planes<P>::swz(r, u) : P == 0 ? u ^ (((r >> 2) & 1) << 3) : u ^ (flip(r) << 2);
     }
 
     const char* at;       // next slab
@@ -156,7 +164,7 @@ struct Side {
     uint32_t off[L];
     uint32_t end[O == K_ENDS ? L : 1];  // its row's last quad
     int left;             // K_COL: rows from `at` to the operand's end
-    uint32_t lane_at[O != K_COL ? KK * P : B * P];  // LDS offsets of this lane's fragments
+    uint32_t lane_at[O != K_COL ? KK * NP : B * NP];  // LDS offsets of this lane's fragments
     int frag;             // wave's part of them
 
     __device__ inline void init(const Operand& o, int row0, int k0, int wave, int lane, int wave_at) {
@@ -165,7 +173,7 @@ struct Side {
             step = O == K_ENDS ? 0 : ROW;
             left = 0;
         } else {
-            at = o.base + (size_t)k0 * BK * o.pitch + (size_t)row0 * 2 * P;
+            at = o.base + (size_t)k0 * BK * o.pitch + (size_t)row0 * SIZE;
             step = (size_t)BK * o.pitch;
             left = o.rows - k0 * BK;
         }
@@ -176,7 +184,12 @@ struct Side {
             // row l of a block, quad 2 * kk + h of plane p
             frag = wave_at * W * ROW;
 #pragma unroll
-            for (int q = 0; q < KK * P; ++q) lane_at[q] = l * ROW + Planes<P>::swz(l, 2 * q + h) * 16;
+            for (int q = 0; q < KK * NP; ++q) lane_at[q] = l * ROW + Planes<P>::swz(l, 2 * q + h) * 16;
+        } else if (P == 0) {
+            // k = 4 h .. 4 h + 3 of m = l
+            frag = 0;
+#pragma unroll
+            for (int b = 0; b < B; ++b) lane_at[b] = 4 * h * ROW + (((wave_at * W + b * 32 + l) * 4) ^ (h << 7));
         } else {
             // lane i of a group of 16 points at k = i / 4, m = 4 * (i % 4) and gets k = 0 .. 3 of m = i
             const int i = lane & 15, r = 8 * h + (i >> 2), f = flip(i >> 2);
@@ -203,9 +216,9 @@ struct Side {
                 off[j] = (uint32_t)row * o.pitch + (O == K_ENDS && quad > last ? last : quad);
                 if (O == K_ENDS) end[j] = (uint32_t)row * o.pitch + last;
             } else {
-                const uint32_t q = (uint32_t)row0 * 2 * P + (uint32_t)(source_quad(r, u) * 16);
+                const uint32_t q = (uint32_t)row0 * SIZE + (uint32_t)(source_quad(r, u) * 16);
                 const uint32_t last = o.row_bytes - 16;
-                off[j] = (uint32_t)imin(r, left - 1) * o.pitch + (q < last ? q : last) - (uint32_t)row0 * 2 * P;
+                off[j] = (uint32_t)imin(r, left - 1) * o.pitch + (q < last ? q : last) - (uint32_t)row0 * SIZE;
             }
         }
     }
@@ -228,17 +241,30 @@ struct Side {
             if (left < BK && left > 0) set_offsets(o, row0, wave, lane);
         }
     }
-    // The fragments of k-step kk: of a lane, 8 consecutive k of its row in each block and plane.
-    __device__ inline void read(const char* slab, int kk, typename Planes<P>::Half8 (&v)[P][B]) const {
+    // Zeros for the k of a slab past its first `valid`, in the places that this thread has filled.
+    __device__ inline void zero_past(char* slab, int valid, int wave, int lane) const {
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+            const int i = (j * NW + wave) * 64 + lane;
+            const int r = i / QUADS, u = i - r * QUADS;
+            if ((O != K_COL ? source_quad(r, u) * (16 / SIZE) : r) >= valid) *(u32x4*)(slab + (size_t)i * 16) = u32x4{0, 0, 0, 0};
+        }
+    }
+    // The fragments of k-step kk: of a lane, 8 consecutive k (fp32: 4) of its row in each block and plane.
+    __device__ inline void read(const char* slab, int kk, typename Planes<P>::Half8 (&v)[NP][B]) const {
         typedef typename Planes<P>::Half8 Half8;
 #pragma unroll
-        for (int p = 0; p < P; ++p)
+        for (int p = 0; p < NP; ++p)
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                if (O != K_COL) {
+                if constexpr (O != K_COL) {
                     v[p][b] = *(const Half8*)(slab + frag + b * 32 * ROW + lane_at[p * KK + kk]);
+                } else if constexpr (P == 0) {
+                    const char* a = slab + lane_at[b] + kk * 8 * ROW;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) v[p][b][t] = *(const float*)(a + t * ROW);
                 } else {
-                    const char* a = slab + lane_at[b * P + p] + kk * 16 * ROW;
+                    const char* a = slab + lane_at[b * NP + p] + kk * 16 * ROW;
                     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
                     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * ROW));
                     v[p][b] = __builtin_bit_cast(Half8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -259,18 +285,21 @@ struct Tile {
     static constexpr int kP = P, kBM = BM, kBN = BN, kWM = WM, kWN = WN;
     static constexpr int WAVES_M = BM / WM, WAVES_N = BN / WN, NW = WAVES_M * WAVES_N, NT = NW * 64;
     static constexpr int MB = WM / 32, NB = WN / 32;
-    static constexpr int BK = Planes<P>::BK, KK = BK / 16;
-    static constexpr int BYTES_A = BM * BK * 2 * P, BYTES_B = BN * BK * 2 * P;
+    static constexpr int BK = Planes<P>::BK, KK = BK / Planes<P>::STEP, NP = Planes<P>::N;
+    static constexpr int BYTES_A = BM * BK * Planes<P>::SIZE, BYTES_B = BN * BK * Planes<P>::SIZE;
     static constexpr int LDS_BYTES = BYTES_A * SA + BYTES_B * SB;
-    static constexpr int MFMAS = MB * NB * (P == 2 ? 3 : 1);  // per k-step
+    static constexpr int MFMAS = MB * NB * (P == 2 ? 3 : P == 0 ? 4 : 1);  // per k-step
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
     static_assert(SB >= 2 && (SA == SB || SA == SB + 1), "stages");
 
     f32x16 acc[MB][NB];
 
-    // Multiplies slabs [k0, k0 + slabs) of A rows m0.. and B rows n0..; lds: LDS_BYTES.
-    template <Order OA, Order OB>
-    __device__ inline void run(char* lds, const Operand& a, int m0, const Operand& b, int n0, int k0, int slabs) {
+    // Multiplies slabs [k0, k0 + slabs) of A rows m0.. and B rows n0..; lds: LDS_BYTES.  TAIL: the last of them
+    // may hold fewer than BK k, `last_k`; both operands' others are made zeros once they have landed, so that
+    // what stands in for them (infinities and NaN too) adds nothing.
+    template <Order OA, Order OB, bool TAIL = false>
+    __device__ inline void run(char* lds, const Operand& a, int m0, const Operand& b, int n0, int k0, int slabs,
+                               int last_k = BK) {
         using A = Side<P, OA, BM, WM, NT>;
         using B = Side<P, OB, BN, WN, NT>;
         constexpr int LA = A::L, LB = B::L;
@@ -290,10 +319,34 @@ struct Tile {
         sb.init(b, n0, k0, wave, lane, wave % WAVES_N);
         char* const lds_b = lds + SA * BYTES_A;
         const uint32_t base_a = lds_addr((const float*)lds) + wave * 1024, base_b = base_a + SA * BYTES_A;
-        typename Planes<P>::Half8 va[2][P][MB], vb[2][P][NB];
+        typename Planes<P>::Half8 va[2][NP][MB], vb[2][NP][NB];
         // the MFMAs of k-step kk, `loads` calls of issue(0 ..) spread between them if there is `more`
         auto multiply = [&](int kk, bool more, int loads, auto issue) {
             int x = 0, q = 0;
+            auto between = [&]() {
+                ++x;
+                if (loads > 0) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (; q < loads && q * MFMAS < x * loads; ++q)
+                        if (more) issue(q);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            if constexpr (P == 0) {
+                // element t of every lane's fragment: k = 4 h + t of the step
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < MB; ++i)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(va[kk & 1][0][i][t], vb[kk & 1][0][j][t],
+                                                                             acc[i][j], 0, 0, 0);
+                            between();
+                        }
+                return;
+            } else
 #pragma unroll
             for (int w = P - 1; w >= 0; --w)  // planes of total weight w, the smallest terms first
 #pragma unroll
@@ -303,15 +356,14 @@ struct Tile {
 #pragma unroll
                         for (int j = 0; j < NB; ++j) {
                             acc[i][j] = mfma<P>(va[kk & 1][p][i], vb[kk & 1][w - p][j], acc[i][j]);
-                            ++x;
-                            if (loads > 0) {
-                                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                                for (; q < loads && q * MFMAS < x * loads; ++q)
-                                    if (more) issue(q);
-                                __builtin_amdgcn_sched_barrier(0);
-                            }
+                            between();
                         }
+        };
+        // the last slab has landed (no load is in flight by then): its end is made zeros
+        auto end_slab = [&](int ta, int tb) {
+            sa.zero_past(lds + ta * BYTES_A, last_k, wave, lane);
+            sb.zero_past(lds_b + tb * BYTES_B, last_k, wave, lane);
+            wait_vm_lgkm0<0>();
         };
         constexpr int SMAX = SA > SB ? SA : SB;
 #pragma unroll
@@ -330,6 +382,7 @@ struct Tile {
             wait_vm_lgkm0<LA*(SA - 1) + LB*(SB - 1)>();
         else
             wait_vm_lgkm0<0>();
+        if (TAIL && slabs == 1 && last_k < BK) end_slab(0, 0);
         dl_barrier();
         sa.read(lds, 0, va[0]);
         sb.read(lds_b, 0, vb[0]);
@@ -354,6 +407,7 @@ struct Tile {
                     wait_vm_lgkm0<LA*(SA - 2) + LB*(SB - 2)>();
                 else
                     wait_vm_lgkm0<0>();
+                if (TAIL && s + 2 == slabs && last_k < BK) end_slab(ta1, tb1);
                 dl_barrier();
                 sa.read(lds + ta1 * BYTES_A, 0, va[0]);
                 sb.read(lds_b + tb1 * BYTES_B, 0, vb[0]);

@@ -35,6 +35,8 @@ _OPERATORS = {
     "vocab": ("vocab_ce", "vocab_ce_grad", "vocab_distill", "vocab_distill_grad", "vocab_workspace",
               "vocab_cross_entropy", "vocab_distillation"),
     "linear": ("linear_act", "linear_act_grad", "linear_workspace", "linear_layer"),
+    "sample": ("vocab_sample", "vocab_sample_workspace"),
+    "grads": ("grad_norm", "clip_grad_norm", "grad_workspace"),
 }
 _MODULE_OF = {name: module for module, names in _OPERATORS.items() for name in names}
 

@@ -9,14 +9,14 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsgemm.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("sgemm.hip", "vocab.hip", "linear.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("sgemm.hip", "vocab.hip", "linear.hip", "sample.hip", "grads.hip")]
 KERNEL_HEADERS = ("kernel_common.hpp", "kernel_mfma.hpp", "kernel_pipe.hpp", "kernel_deep.hpp", "kernel_splitk.hpp",
                   "kernel_direct.hpp", "kernel_dl.hpp", "kernel_valu.hpp")
 VOCAB_HEADERS = ("kernel_vocab.hpp", "kernel_vocab_rows.hpp", "kernel_vocab_few.hpp")
-OPERATOR_HEADERS = ("kernel_linear.hpp",)
+OPERATOR_HEADERS = ("kernel_linear.hpp", "kernel_sample.hpp", "kernel_grads.hpp")
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("sgemm_kernels.hpp", "sgemm_launch.hpp", "tuned_table.inc")
                      + KERNEL_HEADERS + VOCAB_HEADERS + OPERATOR_HEADERS] + [
-    os.path.join(os.path.dirname(HERE), "include", f) for f in ("sgemm.h", "vocab.h", "linear.h")]
+    os.path.join(os.path.dirname(HERE), "include", f) for f in ("sgemm.h", "vocab.h", "linear.h", "sample.h", "grads.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

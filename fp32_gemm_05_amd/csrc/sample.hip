@@ -1,0 +1,54 @@
+// sample.hip -- entry points of the drawing of tokens: argument checks, workspace, launches.
+#include "../../include/sample.h"
+#include "kernel_sample.hpp"
+
+namespace libsgemm {
+namespace sample {
+namespace {
+
+constexpr int kMaxRows = 1 << 21, kMaxVocab = 1 << 23;  // 2^23 probabilities of 2^40 are below 2^64
+
+int run(int dtype, int rows, const Args& a, hipStream_t stream) {
+    (void)hipGetLastError();
+    if (dtype == SAMPLE_F32)
+        sample_row_kernel<float><<<rows, kThreads, 0, stream>>>(a);
+    else
+        sample_row_kernel<__bf16><<<rows, kThreads, 0, stream>>>(a);
+    return (int)hipGetLastError();
+}
+
+}  // namespace
+}  // namespace sample
+}  // namespace libsgemm
+
+extern "C" {
+
+long long vocab_sample_workspace(int dtype, int T, int V) {
+    if (dtype != SAMPLE_F32 && dtype != SAMPLE_BF16) return -1;
+    if (T < 0 || T > libsgemm::sample::kMaxRows) return -2;
+    if (V < 1 || V > libsgemm::sample::kMaxVocab) return -3;
+    return 0;
+}
+
+int vocab_sample(int dtype, int T, int V, const void* logits, int ld, const float* u, float temperature,
+                 const float* temperatures, long long top_k, const long long* top_ks, float top_p, const float* top_ps,
+                 float min_p, const float* min_ps, long long* token, void* work, long long work_bytes,
+                 hipStream_t stream) {
+    const long need = vocab_sample_workspace(dtype, T, V);
+    if (need < 0) return (int)need;
+    if (ld < V) return -5;
+    if (T == 0) return 0;
+    if (!logits || (uintptr_t)logits % (dtype == SAMPLE_F32 ? 4 : 2)) return -4;
+    if (!u) return -6;
+    if (!temperatures && !(temperature >= 0.f && temperature < INFINITY)) return -7;
+    if (!top_ps && top_p != top_p) return -11;
+    if (!min_ps && min_p != min_p) return -13;
+    if (!token) return -15;
+    if (need > 0 && (!work || (uintptr_t)work % 16)) return -16;
+    if (work_bytes < need) return -17;
+    const libsgemm::sample::Args a{logits, ld, V, u, temperatures, temperature, top_ks, top_k, top_ps, top_p,
+                                   min_ps, min_p, token};
+    return libsgemm::sample::run(dtype, T, a, stream);
+}
+
+}  // extern "C"

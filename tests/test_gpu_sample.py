@@ -1,0 +1,99 @@
+"""GPU checks of the drawing of tokens against a plain implementation in 64 bits (sample_reference.py)."""
+import math
+
+import pytest
+import torch
+
+import fp32_gemm_05_amd as sg
+from sample_reference import check
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def rows(T, V, dtype, seed=0, spread=2.0, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + T + V)
+    wide = torch.full((T, V + pad), float("nan"), device="cuda", dtype=DT[dtype])
+    wide[:, :V] = torch.randn(T, V, generator=g, device="cuda") * spread
+    return wide[:, :V], torch.rand(T, generator=g, device="cuda"), g
+
+
+SETTINGS = [dict(), dict(temperature=0.0), dict(temperature=0.3), dict(top_k=1), dict(top_k=7), dict(top_p=0.9),
+            dict(top_p=0.1, temperature=2.0), dict(min_p=0.05), dict(top_k=40, top_p=0.95, min_p=0.01, temperature=0.7),
+            dict(top_p=0.0), dict(min_p=1.0), dict(min_p=2.0), dict(top_p=0.999999), dict(top_k=10 ** 9)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,pad", [(1, 1, 0), (3, 2, 1), (5, 63, 0), (4, 64, 3), (6, 1000, 0), (9, 1025, 5), (3, 5003, 3),
+                                     (2, 40000, 0), (2, 131072, 0), (1, 300001, 1)])
+def test_settings(T, V, pad, dtype):
+    logits, u, _ = rows(T, V, dtype, pad=pad)
+    for s in SETTINGS:
+        check(logits, u, sg.vocab_sample(logits, u, **s), **s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(40, 500), (300, 2000), (64, 20001)])
+def test_settings_of_each_row(T, V, dtype):
+    logits, u, g = rows(T, V, dtype, pad=3)
+
+    def pick(values, kind=torch.float32):
+        return torch.tensor(values, device="cuda", dtype=kind)[torch.randint(0, len(values), (T,), generator=g, device="cuda")]
+
+    s = dict(temperature=pick([0.0, 0.5, 1.0, 1.7]), top_k=pick([0, 1, 2, 50, V - 1, V, 10 ** 12, -3], torch.int64),
+             top_p=pick([0.2, 0.9, 0.99, 1.0, 1.5]), min_p=pick([0.0, 0.01, 0.3, -1.0]))
+    check(logits, u, sg.vocab_sample(logits, u, **s), **s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("values", [1, 2, 5])
+def test_ties(values, dtype):
+    """Few distinct logits, so that the borders fall inside runs of equal ones: lower indexes first."""
+    T, V = 24, 9000
+    g = torch.Generator(device="cuda").manual_seed(values)
+    logits = (torch.randint(0, values, (T, V), generator=g, device="cuda") * 0.5).to(DT[dtype])
+    logits[:, ::7] *= -0.0  # -0 and 0 are one value
+    u = torch.rand(T, generator=g, device="cuda")
+    for s in SETTINGS + [dict(top_k=8000), dict(top_k=4000, top_p=0.5)]:
+        check(logits, u, sg.vocab_sample(logits, u, **s), **s)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_masks_and_what_is_no_distribution(dtype):
+    T, V = 16, 3001
+    logits, u, g = rows(T, V, dtype)
+    lowest = torch.finfo(DT[dtype]).min
+    logits[0] = -math.inf                     # nothing left
+    logits[1, torch.arange(V, device="cuda") != 17] = -math.inf
+    logits[2, 5] = math.nan
+    logits[3, 5] = math.inf
+    logits[4] = lowest                        # all of the type's lowest value: equal
+    logits[5, 1000:] = lowest
+    logits[6, 10:] = -math.inf                # fewer than top_k
+    logits[7] = torch.finfo(DT[dtype]).max    # all of the largest
+    logits[8, 3], logits[8, 4] = torch.finfo(DT[dtype]).max, lowest
+    logits[9] = 0.0
+    logits[10, ::2] = -math.inf
+    u[11], u[12], u[13], u[14] = 0.0, 1.0, -1.0, 1 - 2.0 ** -24
+    u[15] = math.nan
+    for s in SETTINGS:
+        check(logits, u, sg.vocab_sample(logits, u, **s), **s)
+    bad = torch.full((T,), 0.5, device="cuda")
+    bad[0:4] = torch.tensor([-1.0, math.nan, math.inf, -math.inf], device="cuda")
+    clean, u2, _ = rows(T, V, dtype, seed=3)
+    check(clean, u2, sg.vocab_sample(clean, u2, temperature=bad), temperature=bad)
+    assert sg.vocab_sample(clean, u2, temperature=bad)[:4].tolist() == [-1] * 4
+    bad = torch.full((T,), 0.5, device="cuda")
+    bad[3] = math.nan
+    assert sg.vocab_sample(clean, u2, top_p=bad).tolist()[3] == -1
+    assert sg.vocab_sample(clean, u2, min_p=bad).tolist()[3] == -1
+
+
+def test_distribution():
+    """Evenly spaced u give each token its share."""
+    n = 4096
+    row = torch.tensor([0.0, 1.0, -1.0, 2.0, -20.0], device="cuda")
+    u = (torch.arange(n, device="cuda") + 0.5) / n
+    token = sg.vocab_sample(row.expand(n, 5).contiguous(), u)
+    share = torch.bincount(token, minlength=5).double() / n
+    assert float((share - torch.softmax(row.double(), 0)).abs().max()) <= 2 / n

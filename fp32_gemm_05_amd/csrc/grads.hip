@@ -12,7 +12,6 @@ namespace {
 
 constexpr int kMaxTensors = 1 << 20;
 constexpr long kMaxElements = 1L << 40;
-constexpr long kFactorAt = 0, kSumsAt = 256;  // of the workspace
 
 long size_of(const GradTensor& t) { return t.dtype == GRADS_F32 ? 4 : 2; }
 bool empty(const GradTensor& t) { return t.rows == 0 || t.cols == 0; }
@@ -40,46 +39,49 @@ long piece_size(int count, const GradTensor* t, long& pieces) {
     }
 }
 
-// f(table, first piece, pieces) for the tensors, kTable at a time, from the last to the first where `back`.
-template <class F>
-void tables(int count, const GradTensor* tensors, long piece, bool back, F f) {
-    long first = 0;
-    int i = back ? count - 1 : 0;
-    while (back ? i >= 0 : i < count) {
-        Table t;
-        t.count = 0;
-        t.piece = (uint32_t)piece;
-        t.bf16[0] = t.bf16[1] = t.bf16[2] = 0;
-        long last = 0;
-        for (; (back ? i >= 0 : i < count) && t.count < kTable; back ? --i : ++i) {
-            const GradTensor& g = tensors[i];
-            if (empty(g)) continue;
-            last += pieces_of(g.rows, g.cols, piece);
-            const int n = t.count++;
-            t.e[n] = {g.x, g.out, (long)g.cols, (uint32_t)g.rows, (uint32_t)g.ld, (uint32_t)g.ld_out, (uint32_t)last};
-            if (g.dtype == GRADS_BF16) t.bf16[n >> 5] |= 1u << (n & 31);
-        }
-        if (t.count == 0) break;
-        f(t, first, (unsigned)last);
-        first += last;
-    }
+// The workspace: byte offsets of its arrays.
+struct Layout {
+    long piece, pieces, entries, tensor_of, sums, bytes;
+};
+Layout layout(int count, const GradTensor* t) {
+    Layout l{};
+    l.piece = piece_size(count, t, l.pieces);
+    auto up = [](long x) { return (x + 255) / 256 * 256; };
+    l.entries = 256;  // the factor stands before them
+    l.tensor_of = l.entries + up((long)sizeof(Entry) * count);
+    l.sums = l.tensor_of + up(4 * l.pieces);
+    l.bytes = l.sums + 8 * l.pieces;
+    return l;
 }
 
 int launch(int count, const GradTensor* tensors, bool clip, float max_norm, float eps, float* norm, char* work,
            hipStream_t stream) {
     (void)hipGetLastError();
-    long pieces = 0;
-    const long piece = piece_size(count, tensors, pieces);
-    double* const sums = (double*)(work + kSumsAt);
-    float* const factor = clip ? (float*)(work + kFactorAt) : nullptr;
-    tables(count, tensors, piece, false, [&](const Table& t, long first, unsigned n) {
-        grads_squares_kernel<<<n, 256, 0, stream>>>(t, sums + first);
-    });
-    grads_norm_kernel<<<1, 1024, 0, stream>>>(sums, pieces, norm, factor, max_norm, eps);
-    if (clip)
-        tables(count, tensors, piece, true, [&](const Table& t, long, unsigned n) {
-            grads_scale_kernel<<<n, 256, 0, stream>>>(t, factor);
-        });
+    const Layout l = layout(count, tensors);
+    double* const sums = (double*)(work + l.sums);
+    float* const factor = clip ? (float*)work : nullptr;
+    Entry* const entries = (Entry*)(work + l.entries);
+    uint32_t* const tensor_of = (uint32_t*)(work + l.tensor_of);
+    long first = 0;
+    uint32_t sent = 0;
+    for (int i = 0; i < count;) {
+        Table t;
+        uint32_t n = 0;
+        for (; i < count && n < kTable; ++i) {
+            const GradTensor& g = tensors[i];
+            if (empty(g)) continue;
+            const long own = pieces_of(g.rows, g.cols, l.piece);
+            t.e[n++] = {g.x, g.out, (long)g.cols, (uint32_t)g.rows, (uint32_t)g.ld, (uint32_t)g.ld_out, (uint32_t)first,
+                        (uint32_t)own, g.dtype == GRADS_BF16};
+            first += own;
+        }
+        if (n > 0) grads_table_kernel<<<n, 256, 0, stream>>>(t, sent, entries, tensor_of);
+        sent += n;
+    }
+    if (l.pieces > 0) grads_squares_kernel<<<(unsigned)l.pieces, 256, 0, stream>>>(entries, tensor_of, (uint32_t)l.piece, sums);
+    grads_norm_kernel<<<1, 1024, 0, stream>>>(sums, l.pieces, norm, factor, max_norm, eps);
+    if (clip && l.pieces > 0)
+        grads_scale_kernel<<<(unsigned)l.pieces, 256, 0, stream>>>(entries, tensor_of, (uint32_t)l.piece, factor);
     return (int)hipGetLastError();
 }
 
@@ -147,9 +149,8 @@ long long grad_workspace(int count, const GradTensor* tensors) {
     if (count > 0 && !tensors) return -2;
     for (int i = 0; i < count; ++i)
         if (!sizes_ok(tensors[i])) return -2;
-    long pieces = 0;
-    if (piece_size(count, tensors, pieces) == 0) return -2;
-    return kSumsAt + 8 * pieces;
+    const Layout l = layout(count, tensors);
+    return l.piece == 0 ? -2 : l.bytes;
 }
 
 int grad_norm(int count, const GradTensor* tensors, float* norm, void* work, long long work_bytes, hipStream_t stream) {

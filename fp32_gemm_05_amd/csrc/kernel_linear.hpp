@@ -28,25 +28,44 @@ using vocab::u32x4;
 
 enum Act { NONE = 0, RELU = 1, GELU = 2, GELU_TANH = 3, SILU = 4 };
 
-// Four values of T at any alignment of T; the first n of them.
-template <typename T>
-__device__ inline f32x4 load4(const T* p, int n = 4) {
-    T v[4] = {};
-    if (n >= 4)
-        __builtin_memcpy(v, p, sizeof(v));
+// N4 groups of four values of T at any alignment of T, in accesses of up to 16 bytes; the first `left` of them.
+template <typename T, int N4>
+__device__ inline void load(const T* p, int left, f32x4 (&v)[N4]) {
+    T x[4 * N4] = {};
+    if (left >= 4 * N4)
+        __builtin_memcpy(x, p, sizeof(x));
     else
-        for (int i = 0; i < 3; ++i)
-            if (i < n) v[i] = p[i];
-    return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+#pragma unroll
+        for (int i = 0; i < 4 * N4 - 1; ++i)
+            if (i < left) x[i] = p[i];
+#pragma unroll
+    for (int i = 0; i < 4 * N4; ++i) v[i / 4][i % 4] = (float)x[i];
+}
+template <typename T, int N4>
+__device__ inline void add(const void* p, long row, long ld, int col, int left, f32x4 (&v)[N4]) {
+    f32x4 x[N4];
+    load((const T*)p + row * ld + col, left, x);
+#pragma unroll
+    for (int g = 0; g < N4; ++g) v[g] += x[g];
+}
+template <typename T, int N4>
+__device__ inline void leave(void* p, long row, long ld, int col, int left, const f32x4 (&v)[N4]) {
+    T x[4 * N4];
+#pragma unroll
+    for (int i = 0; i < 4 * N4; ++i) x[i] = (T)v[i / 4][i % 4];
+    T* out = (T*)p + row * ld + col;
+    if (left >= 4 * N4)
+        __builtin_memcpy(out, x, sizeof(x));
+    else
+#pragma unroll
+        for (int i = 0; i < 4 * N4 - 1; ++i)
+            if (i < left) out[i] = x[i];
 }
 template <typename T>
-__device__ inline void store4(T* p, f32x4 x, int n = 4) {
-    const T v[4] = {(T)x[0], (T)x[1], (T)x[2], (T)x[3]};
-    if (n >= 4)
-        __builtin_memcpy(p, v, sizeof(v));
-    else
-        for (int i = 0; i < 3; ++i)
-            if (i < n) p[i] = v[i];
+__device__ inline f32x4 load4(const T* p, int n = 4) {
+    f32x4 v[1];
+    load(p, n, v);
+    return v[0];
 }
 
 // The normal distribution's upper tail Q(t) = erfc(t / sqrt 2) / 2 for t >= 0 as k P(k) exp(-t^2 / 2), k = 1 /
@@ -129,33 +148,29 @@ struct Finish {
     long ld;
 };
 
-// N groups of four consecutive columns of a row, STEP columns apart.  FORWARD: not, the sums are stored as they are.
-template <bool FORWARD, typename T, int N, int STEP = 8>
-__device__ inline void finish_block(const Finish& f, long row, int col, f32x4 (&v)[N]) {
+// 4 N consecutive columns of a row, `left` of which exist.  FORWARD: not, the sums are stored as they are.
+template <bool FORWARD, typename T, int N>
+__device__ inline void finish(const Finish& f, long row, int col, int left, f32x4 (&v)[N]) {
     auto each = [&](auto body) {
 #pragma unroll
-        for (int g = 0; g < N; ++g)
-            if (col + g * STEP < f.m) body(v[g], col + g * STEP, f.m - col - g * STEP);
+        for (int g = 0; g < N; ++g) body(v[g], col + 4 * g, left - 4 * g);
     };
     if constexpr (FORWARD) {
-        if (f.bias) each([&](f32x4& x, int c, int left) { x += load4((const T*)f.bias + c, left); });
-        if (f.z) each([&](f32x4& x, int c, int left) { store4((T*)f.z + row * f.ld_z + c, x, left); });
+        if (f.bias) add<T>(f.bias, 0, 0, col, left, v);
+        if (f.z) leave<T>(f.z, row, f.ld_z, col, left, v);
         by_act(f.act, [&](auto which) {
+            each([&](f32x4& x, int, int) {
 #pragma unroll
-            for (int g = 0; g < N; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[g][i] = act<decltype(which)::value>(v[g][i]);
+                for (int i = 0; i < 4; ++i) x[i] = act<decltype(which)::value>(x[i]);
+            });
         });
         if (sizeof(T) == 2 && f.wide) {
-            if (f.residual)
-                each([&](f32x4& x, int c, int left) { x += load4((const float*)f.residual + row * f.ld_residual + c, left); });
-            each([&](f32x4& x, int c, int left) { store4((float*)f.out + row * f.ld + c, x, left); });
-            return;
+            if (f.residual) add<float>(f.residual, row, f.ld_residual, col, left, v);
+            return leave<float>(f.out, row, f.ld, col, left, v);
         }
-        if (f.residual)
-            each([&](f32x4& x, int c, int left) { x += load4((const T*)f.residual + row * f.ld_residual + c, left); });
+        if (f.residual) add<T>(f.residual, row, f.ld_residual, col, left, v);
     }
-    each([&](f32x4& x, int c, int left) { store4((T*)f.out + row * f.ld + c, x, left); });
+    leave<T>(f.out, row, f.ld, col, left, v);
 }
 
 struct ProductArgs {
@@ -180,35 +195,42 @@ __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
     const int first = (int)((long)a.slabs * z / a.splits), last = (int)((long)a.slabs * (z + 1) / a.splits);
     T t;
     t.template run<OA, OB, TAIL>(lds, a.a, m0, a.b, n0, first, last - first, a.k - (last - 1) * T::BK);
-    if (a.splits > 1) {
-#pragma unroll
-        for (int j = 0; j < T::NB; ++j) {
-            float* out = a.part + (z * a.rows + n0 + t.col(j)) * a.pitch + m0;
-#pragma unroll
-            for (int i = 0; i < T::MB; ++i)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *(f32x4*)(out + t.row(i, 4 * g)) = f32x4{t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1],
-                                                             t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
-        }
-        return;
-    }
-    // a block's values leave the accumulators before anything is done to them, and a block ends before the next
-    // begins: all of them together would spill
+    // The tile leaves through LDS, 32 rows of the result at a time and wave by wave: a lane's accumulators are four
+    // columns of 32 rows, and stored from there a line of memory would be written in eight pieces (8192 x 8192 x 4096
+    // bf16 with Z kept: 677 us, so 490).  Row r holds its quad q at q ^ r: writes of 16 rows at one quad and
+    // reads of a row's quads in a row are both spread over the banks.
+    constexpr int WM = T::kWM, QUADS = WM / 4, N4 = sizeof(E) == 2 ? 2 : 1, LANES = QUADS / N4, ROWS = 64 / LANES;
+    static_assert(T::NW * 32 * WM * 4 <= T::LDS_BYTES, "a place for each wave");
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 31, h = lane >> 5;
+    f32x4* const own = (f32x4*)lds + wave * 32 * QUADS;
+    const int m = m0 + (wave / T::WAVES_N) * WM + lane % LANES * 4 * N4, q0 = lane % LANES * N4;
+    const int n_wave = n0 + (wave % T::WAVES_N) * T::kWN;
+    wait_vm_lgkm0<0>();
+    dl_barrier();  // every wave has read its last slab
 #pragma unroll
     for (int j = 0; j < T::NB; ++j) {
 #pragma unroll
-        for (int i = 0; i < T::MB; ++i) {
-            // anew for each block: as values of the whole kernel they and the addresses made of them would spill
-            int n = n0 + t.col(j), m = m0 + t.row(i, 0);
-            asm volatile("" : "+v"(n), "+v"(m));
-            f32x4 v[4];
+        for (int i = 0; i < T::MB; ++i)
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-                v[g] = f32x4{t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1], t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
-            if (n < a.f.n) finish_block<FORWARD, E>(a.f, n, m, v);
-            __builtin_amdgcn_sched_barrier(0);
+                own[l * QUADS + ((8 * i + 2 * g + h) ^ (l & (QUADS - 1)))] =
+                    f32x4{t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1], t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
+        wait_vm_lgkm0<0>();  // a wave's own writes before its reads; it shares them with no other wave
+#pragma unroll 1
+        for (int r = lane / LANES; r < 32; r += ROWS) {
+            const int n = n_wave + j * 32 + r;
+            f32x4 v[N4];
+#pragma unroll
+            for (int q = 0; q < N4; ++q) v[q] = own[r * QUADS + ((q0 + q) ^ (r & (QUADS - 1)))];
+            if (a.splits > 1) {
+                float* out = a.part + (z * a.rows + n) * a.pitch + m;
+#pragma unroll
+                for (int q = 0; q < N4; ++q) *(f32x4*)(out + 4 * q) = v[q];
+            } else if (n < a.f.n && m < a.f.m) {
+                finish<FORWARD, E>(a.f, n, m, a.f.m - m, v);
+            }
         }
+        wait_vm_lgkm0<0>();
     }
 }
 
@@ -221,7 +243,7 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const float* part, int 
 #pragma unroll 4
     for (int z = 0; z < splits; ++z) v += *(const f32x4*)(part + (z * rows + n) * pitch + m);
     f32x4 one[1] = {v};
-    finish_block<true, T>(f, n, m, one);
+    finish<true, T>(f, n, m, f.m - m, one);
 }
 
 // Rows of an operand that cannot be read in place, copied to rows of whole slabs, 16-byte aligned, zeros at
@@ -404,7 +426,12 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
     }
     const int n = 16 * wave + l;
     if (wave >= NB || n >= a.tokens) return;
-    finish_block<true, T, MR, 16>(a.f, n, r0 + 4 * g, z);
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+        const int v = r0 + 16 * m + 4 * g;
+        f32x4 one[1] = {z[m]};
+        if (v < a.outs) finish<true, T>(a.f, n, v, a.outs - v, one);
+    }
 }
 
 struct FewSlopeArgs {
@@ -462,7 +489,8 @@ __global__ void __launch_bounds__(256) linear_few_slope_kernel(FewSlopeArgs a) {
     __syncthreads();
     if (ty > 0 || left <= 0) return;
     for (int i = 1; i < 16; ++i) sum += all[i][tx];
-    store4((T*)a.dbias + c, sum, left);
+    const f32x4 one[1] = {sum};
+    leave<T>(a.dbias, 0, 0, c, left, one);
 }
 
 }  // namespace linear

@@ -42,46 +42,78 @@ __host__ inline long pieces_of(long rows, long cols, long piece) {
     return (rows + per - 1) / per;
 }
 
-// f(row, column, elements) for a piece's vectors of 16 bytes.  A row's last vector, where it is not whole, is
-// given as a whole one that ends with the row, `elements` of whose last were not in the one before it; a row shorter
-// than a vector is given as it is, with a column of 0.
-template <typename T, class F>
-__device__ inline void each(const Entry& e, uint32_t i, uint32_t piece, F f) {
+// load(slot, row, column, elements) and then use(the same) for a piece's vectors of 16 bytes, U of them on their way
+// at once.  A row's last vector, where it is not whole, is given as a whole one that ends with the row, `elements` of
+// whose last were not in the one before it; a row shorter than a vector is given as it is, with a column of 0.
+template <typename T, int U, class L, class F>
+__device__ inline void each(const Entry& e, uint32_t i, uint32_t piece, L load, F use) {
     constexpr int N = 16 / sizeof(T);
+    const int x = threadIdx.x;
     if (e.cols >= piece) {
         const uint32_t parts = (uint32_t)((e.cols + piece - 1) / piece), r = i / parts;
         const long c0 = (long)(i - r * parts) * piece, c1 = c0 + piece < e.cols ? c0 + piece : e.cols;
+        long c = c0 + x * N;
+        for (; c + (256 * (U - 1) + 1) * N <= c1; c += 256 * U * N) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) load(u, r, c + 256 * u * N, N);
+#pragma unroll
+            for (int u = 0; u < U; ++u) use(u, r, c + 256 * u * N, N);
+        }
         // (a last part shorter than a vector reaches back into the part before it)
-#pragma unroll 4
-        for (long c = c0 + threadIdx.x * N; c < c1; c += 256 * N) f(r, c + N <= c1 ? c : c1 - N, c + N <= c1 ? N : (int)(c1 - c));
+        for (; c < c1; c += 256 * N) {
+            const bool whole = c + N <= c1;
+            load(0, r, whole ? c : c1 - N, whole ? N : (int)(c1 - c));
+            use(0, r, whole ? c : c1 - N, whole ? N : (int)(c1 - c));
+        }
         return;
     }
     const uint32_t cols = (uint32_t)e.cols, per = piece / cols, r0 = i * per;
-    const uint32_t rows = r0 + per < e.rows ? per : e.rows - r0, each_row = (cols + N - 1) / N;
-#pragma unroll 4
-    for (uint32_t v = threadIdx.x; v < rows * each_row; v += 256) {
-        const uint32_t r = v / each_row, c = (v - r * each_row) * N;
-        f(r0 + r, (long)(c + N <= cols ? c : cols < N ? 0 : cols - N), (int)(c + N <= cols ? N : cols - c));
+    const uint32_t rows = r0 + per < e.rows ? per : e.rows - r0, each_row = (cols + N - 1) / N, all = rows * each_row;
+    for (uint32_t v = x; v < all; v += 256 * U) {
+        uint32_t row[U], col[U];
+        int n[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w = v + 256 * u, r = w / each_row, c = (w - r * each_row) * N;
+            row[u] = r0 + r;
+            col[u] = c + N <= cols ? c : cols < N ? 0 : cols - N;
+            n[u] = w >= all ? 0 : c + N <= cols ? N : (int)(cols - c);
+            if (n[u] > 0) load(u, row[u], (long)col[u], n[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (n[u] > 0) use(u, row[u], (long)col[u], n[u]);
     }
+}
+
+template <typename T, int N>
+struct Vec {
+    T v[N];
+};
+// A vector of `each`; of a row shorter than one its n elements, at the end, behind zeros.
+template <typename T, int N>
+__device__ inline void fetch(Vec<T, N>& v, const T* p, long cols, int n) {
+    if (cols >= N)
+        __builtin_memcpy(v.v, p, 16);
+    else
+#pragma unroll
+        for (int q = 0; q < N; ++q) v.v[q] = q >= N - n ? p[q - (N - n)] : (T)0.f;
 }
 
 template <typename T>
 __device__ inline double squares(const Entry& e, uint32_t i, uint32_t piece) {
-    constexpr int N = 16 / sizeof(T);
+    constexpr int N = 16 / sizeof(T), U = 4;
     double s = 0;
-    each<T>(e, i, piece, [&](uint32_t r, long c, int n) {
-        const T* p = (const T*)e.x + (size_t)r * e.ld + c;
-        T v[N] = {};
-        if (e.cols >= N)
-            __builtin_memcpy(v, p, 16);
-        else
-            for (int q = 0; q < n; ++q) v[N - n + q] = p[q];
+    Vec<T, N> v[U];
+    each<T, U>(
+        e, i, piece, [&](int u, uint32_t r, long c, int n) { fetch(v[u], (const T*)e.x + (size_t)r * e.ld + c, e.cols, n); },
+        [&](int u, uint32_t, long, int n) {
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-            const double x = q >= N - n ? (double)(float)v[q] : 0.;
-            s = __builtin_fma(x, x, s);
-        }
-    });
+            for (int q = 0; q < N; ++q) {
+                const double x = q >= N - n ? (double)(float)v[u].v[q] : 0.;
+                s = __builtin_fma(x, x, s);
+            }
+        });
     return s;
 }
 
@@ -122,22 +154,26 @@ __global__ void __launch_bounds__(1024) grads_norm_kernel(const double* sums, lo
 
 template <typename T>
 __device__ inline void scale(const Entry& e, uint32_t i, uint32_t piece, float f) {
-    constexpr int N = 16 / sizeof(T);
+    constexpr int N = 16 / sizeof(T), U = 4;
     const bool in_place = e.out == e.x;
-    each<T>(e, i, piece, [&](uint32_t r, long c, int n) {
-        const T* p = (const T*)e.x + (size_t)r * e.ld + c;
-        T* o = (T*)e.out + (size_t)r * e.ld_out + c;
-        // in place an element is read and written by one lane alone
-        if (n == N || (e.cols >= N && !in_place)) {
-            T v[N];
-            __builtin_memcpy(v, p, 16);
+    Vec<T, N> v[U];
+    each<T, U>(
+        e, i, piece, [&](int u, uint32_t r, long c, int n) { fetch(v[u], (const T*)e.x + (size_t)r * e.ld + c, e.cols, n); },
+        [&](int u, uint32_t r, long c, int n) {
+            T* o = (T*)e.out + (size_t)r * e.ld_out + c;
 #pragma unroll
-            for (int q = 0; q < N; ++q) v[q] = (T)((float)v[q] * f);
-            __builtin_memcpy(o, v, 16);
-        } else {
-            for (int q = e.cols >= N ? N - n : 0, end = q + n; q < end; ++q) o[q] = (T)((float)p[q] * f);
-        }
-    });
+            for (int q = 0; q < N; ++q) v[u].v[q] = (T)((float)v[u].v[q] * f);
+            // the elements that two vectors share get the same values twice, but in place, where one lane
+            // alone may read and write an element
+            if (n == N || (e.cols >= N && !in_place)) {
+                __builtin_memcpy(o, v[u].v, 16);
+                return;
+            }
+            if (e.cols < N) o -= N - n;
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (q >= N - n) o[q] = v[u].v[q];
+        });
 }
 
 // From the last piece to the first: what the norm's pass has read last is still in the caches.

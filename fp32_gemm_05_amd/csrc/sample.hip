@@ -8,12 +8,26 @@ namespace {
 
 constexpr int kMaxRows = 1 << 21, kMaxVocab = 1 << 23;  // 2^23 probabilities of 2^40 are below 2^64
 
+template <typename T>
+void launch(int rows, const Args& a, hipStream_t stream) {
+    constexpr int N = 16 / sizeof(T);
+    const int vectors = (a.vocab + kThreads * N - 1) / (kThreads * N);
+    if (vectors <= 4)
+        sample_row_kernel<T, 4><<<rows, kThreads, 0, stream>>>(a);
+    else if (vectors <= 8)
+        sample_row_kernel<T, 8><<<rows, kThreads, 0, stream>>>(a);
+    else if (vectors <= 16)
+        sample_row_kernel<T, 16><<<rows, kThreads, 0, stream>>>(a);
+    else
+        sample_row_kernel<T, 0><<<rows, kThreads, 0, stream>>>(a);
+}
+
 int run(int dtype, int rows, const Args& a, hipStream_t stream) {
     (void)hipGetLastError();
     if (dtype == SAMPLE_F32)
-        sample_row_kernel<float><<<rows, kThreads, 0, stream>>>(a);
+        launch<float>(rows, a, stream);
     else
-        sample_row_kernel<__bf16><<<rows, kThreads, 0, stream>>>(a);
+        launch<__bf16>(rows, a, stream);
     return (int)hipGetLastError();
 }
 

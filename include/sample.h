@@ -16,8 +16,8 @@
  * NaN, or a NaN for u, top_p or min_p.
  *
  * Probabilities are added up as whole multiples of 2^-40 of the largest one, in 64 bits, so that a token does not
- * depend on timing or on how the work is cut; exponentials are off by less than 2^-31 of themselves.  A token whose
- * probability is below 2^-41 of the largest one's is not drawn.
+ * depend on timing or on how the work is cut.  exp(-x) of the distance x from the largest logit is off by up to
+ * 2^-22 + 2^-24 x of itself.  A token whose probability is below 2^-41 of the largest one's is not drawn.
  *
  * temperature, top_k, top_p and min_p are one value for all rows, or with a pointer (device memory) one for each.
  *

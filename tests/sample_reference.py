@@ -1,7 +1,8 @@
 """Drawing tokens from rows of logits in 64 bits, row by row, and which tokens are right.  Runs on any device.
 
-The kernels' exponentials are off by less than 2^-31 of themselves and their probabilities by half of 2^-40 of the
-largest one's, so a row's sums are off by less than (2^-31 + V 2^-41) of the whole, and this reference's by V 2^-53.
+The kernels' exponentials exp(-x) are off by up to 2^-22 (their own last place and a product) + 2^-24 x (the rounding of
+the logits' difference) of themselves, and their probabilities by half of 2^-40 of the largest one's.  The mean of x
+weighted by exp(-x) is at most 1 + log(V) < 15, so a row's sums are off by less than 2^-20 + V 2^-41 of the whole.
 Where a border (top_p's, min_p's, u's) lies nearer to a sum than `near` of the whole, either side of it is right:
 `allowed` gives every token that is.
 """
@@ -27,7 +28,7 @@ def allowed(row, u, temperature, top_k, top_p, min_p):
         return {-1}
     if temperature == 0:
         return {int((row == top).nonzero()[0])}
-    near = 2.0 ** -31 + V * 2.0 ** -40
+    near = 2.0 ** -20 + V * 2.0 ** -41
     # -0 and 0 are equal; a stable sort keeps the lower index first
     order = torch.sort(-(row + 0.0), stable=True).indices
     p = ((row[order] - top) / temperature).exp()

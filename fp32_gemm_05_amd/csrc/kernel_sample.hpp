@@ -1,11 +1,17 @@
 // kernel_sample.hpp -- drawing tokens from rows of logits (gfx950).
 //
 // What stays of a row is a prefix of its order (falling logit, then rising index) whatever filters are set, so it
-// is described by the key of the last logit that stays and how many of the logits equal to it do, from the lowest
-// index on.  Keys are the fp32 values' bits in an order that compares as unsigned integers.
+// is described by the last logit that stays and the index up to which logits equal to it do.
 //
 // Probabilities are whole multiples of 2^-40 of the largest, so their sums are exact in 64 bits and the same in any
 // order: atomics and any cut of the row give one result.
+//
+// A workgroup has a row, in registers up to 256 KB of it.  It reads the row once from memory; what bounds it then is
+// its own passes over the registers (131072 bf16 logits: 2.9 us for the largest, 12 us for a pass of exponentials)
+// and a dozen steps of all threads together (0.3 - 1 us each).  So it avoids passes: top_p and a large top_k look for
+// the cut in counts of bins of the exponent, from which masses follow to 1 % of what lies on the lighter side, and order
+// only the few logits at the border; a small top_k needs no counts (1024 threads' own largest bound it); what
+// stays is listed where it is short, and only the listed weighed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -15,6 +21,15 @@ namespace libsgemm {
 namespace sample {
 
 typedef unsigned long long u64;
+
+// A value that all lanes have, in a scalar register.
+__device__ inline float uniform(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
+}
+__device__ inline int uniform(int x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
 
 struct Args {
     const void* logits;
@@ -42,35 +57,50 @@ __device__ inline float value_of(uint32_t key) {
     return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// exp((x - top) / temperature) as a multiple of 2^-40: log2(e) / temperature = c + c_low.  The exponent is kept in two
-// parts, so that what is off is the exponential's own last place and x - top's rounding.
+// exp((x - top) / temperature) as a multiple of 2^-40: log2(e) / temperature = c + c_low, both kept, as an error of c
+// is one of all exponents in one direction.  What is left is the rounding of x - top, of the exponent and of the
+// exponential.  c is rounded down, so that both parts take -infinity to -infinity and not to NaN.
 struct Scale {
-    float top, c, c_low;
+    float top, c, c_low, bins;
+    __device__ Scale(float top_, float temperature) : top(top_) {
+        const double exact = fmin(1.4426950408889634 / (double)temperature, 0x1p120);  // no product with 0 is NaN
+        c = (float)exact;
+        if ((double)c > exact) c = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, c) - 1);
+        c_low = fmaxf((float)(exact - (double)c), c * 0x1p-40f);
+        c_low = uniform(c_low > 0.f ? c_low : 0x1p-149f);
+        bins = uniform(c * -64.f);
+        c = uniform(c);
+    }
 };
-__device__ inline float exponent_of(float x, const Scale& s) { return (x - s.top) * s.c; }
 __device__ inline float weight_of(float x, const Scale& s) {
-    const float d = x - s.top, t = d * s.c;
-    const float low = __builtin_fmaf(d, s.c_low, __builtin_fmaf(d, s.c, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    // (where t is -infinity, low is NaN)
-    const float w = t > -42.f ? __builtin_fmaf(e * 0.693147181f, low, e) : 0.f;
-    return (w + 0x1p-17f) - 0x1p-17f;
+    const float d = x - s.top;
+    const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(d, s.c, d * s.c_low));
+    return (e + 0x1p-17f) - 0x1p-17f;
 }
-// In units; sums of up to 2^12 weights are exact in 64-bit floating point, and all of a row's as integers.
-__device__ inline u64 units(double w) { return (u64)(w * 0x1p40); }
+// In units of 2^-40.  Below 2^12 sums of weights are exact in 64-bit floating point, and as integers all of a row's
+// are.
+__device__ inline u64 units(double w) { return __builtin_bit_cast(u64, w + 0x1p12) & ((1ull << 52) - 1); }
 
-// A row's elements: V vectors of 16 bytes a thread in registers (V = 0: read from memory each time, U vectors on
-// their way at once).  f(index, values) for each vector, of every thread together; past the row's end -infinity.
+// A row's elements: the first V vectors of 16 bytes a thread in registers, the others read from memory (the caches, after
+// the first time) in each pass, U on their way at once.  48 registers are what a thread can keep beside its work: 64
+// spilled, and each pass read the spilled ones again (131072 bf16 logits: 5.3 us for the largest, against 3).  f(index, values)
+// for each vector, of every thread together; past the row's end -infinity.
 template <typename T, int V>
 struct Row {
-    static constexpr int N = 16 / sizeof(T), U = 4, HELD = V > 0 ? V : 1;
+    static constexpr int N = 16 / sizeof(T), U = 2;
     const T* row;
     int size, used;  // used: vectors that hold something
     typedef uint32_t Vec __attribute__((ext_vector_type(4)));
-    Vec held[HELD];
+    Vec held[V];
 
+    // Of a thread's v-th vector, computed anew each time: kept for all vectors they spill.
+    static __device__ inline int index_of(int v) {
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));
+        return (v * kThreads + t) * N;
+    }
     __device__ inline Vec fetch(int v) const {
-        const int i = (v * kThreads + (int)threadIdx.x) * N;
+        const int i = index_of(v);
         Vec x;
         if (i + N <= size) {
             __builtin_memcpy(&x, row + i, 16);
@@ -84,9 +114,8 @@ struct Row {
     }
     __device__ inline void init(const T* at, int n) {
         row = at, size = n, used = (n + kThreads * N - 1) / (kThreads * N);
-        if (V > 0)
 #pragma unroll
-            for (int v = 0; v < HELD; ++v) held[v] = fetch(v);
+        for (int v = 0; v < V; ++v) held[v] = fetch(v);
     }
     template <class F>
     __device__ inline void use(int v, Vec x, F& f) const {
@@ -98,406 +127,636 @@ struct Row {
         float y[N];
 #pragma unroll
         for (int q = 0; q < N; ++q) y[q] = (float)z[q];
-        int at = (v * kThreads + (int)threadIdx.x) * N;
-        asm volatile("" : "+v"(at));
-        f(at, y);
+        f(index_of(v), y);
         __builtin_amdgcn_sched_barrier(0);
     }
     template <class F>
     __device__ inline void each(F f) const {
-        if constexpr (V > 0) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v < used) use(v, held[v], f);
-        } else {
-            for (int v = 0; v < used; v += U) {
-                Vec x[U];
+        for (int v = 0; v < V; ++v)
+            if (v < uniform(used)) use(v, held[v], f);
+        if (used <= V) return;
+        Vec x[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) x[u] = fetch(v + u);
+        for (int u = 0; u < U; ++u) x[u] = fetch(V + u);
+#pragma unroll 1
+        for (int v = V; v < used; v += U)
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (v + u < used) use(v + u, x[u], f);
+            for (int u = 0; u < U; ++u) {
+                const Vec y = x[u];
+                x[u] = fetch(v + u + U);  // (past the end nothing is read)
+                if (v + u < used) use(v + u, y, f);
             }
-        }
     }
 };
 
-__device__ inline u64 wave_scan(u64 v) {  // inclusive
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const u64 w = __shfl_up(v, o);
-        if (lane >= o) v += w;
-    }
-    return v;
+// v plus that of the lane that CTRL names, in the rows of ROWS.
+template <int CTRL, int ROWS>
+__device__ inline u64 plus_lane(u64 v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+    return v + ((u64)hi << 32 | lo);
+}
+// Inclusive sums over rows of 16 lanes, and over the wave.
+__device__ inline u64 row_scan(u64 v) {
+    v = plus_lane<0x111, 0xf>(v);  // row_shr: 1, 2, 4, 8
+    v = plus_lane<0x112, 0xf>(v);
+    v = plus_lane<0x114, 0xf>(v);
+    return plus_lane<0x118, 0xf>(v);
+}
+__device__ inline u64 wave_scan(u64 v) {
+    v = plus_lane<0x142, 0xa>(row_scan(v));  // row_bcast: 15 into rows 1 and 3, 31 into rows 2 and 3
+    return plus_lane<0x143, 0xc>(v);
+}
+__device__ inline u64 of_lane(u64 v, int lane) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32 | lo;
 }
 // Exclusive sums over the workgroup; `all` gets the whole.  parts: kWaves in LDS.
 __device__ inline u64 block_scan(u64 v, u64* parts, u64& all) {
-    const int wave = threadIdx.x >> 6;
+    static_assert(kWaves == 16, "a row of lanes");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const u64 own = wave_scan(v);
     __syncthreads();
-    if ((threadIdx.x & 63) == 63) parts[wave] = own;
+    if (lane == 63) parts[wave] = own;
     __syncthreads();
-    u64 before = 0;
-    all = 0;
-#pragma unroll 2
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) before += parts[w];
-        all += parts[w];
-    }
-    return before + own - v;
+    const u64 waves = row_scan(parts[lane & 15]);
+    all = of_lane(waves, 15);
+    return (wave > 0 ? of_lane(waves, wave - 1) : 0) + own - v;
 }
 
-// What stays: keys above `key`, and the first `equal` (by index) of those with it.
+// The largest value of a smaller key (that of -0 is no value's).
+__device__ inline float below(uint32_t key) { return value_of(key - (key == 0x80000000u ? 2 : 1)); }
+
+// What stays: logits above `edge`, and those equal to it up to index `last`.
 struct Cut {
-    uint32_t key, equal;
+    float edge;
+    int last;
+    __device__ bool keeps(float x, int i) const { return x > edge || (x == edge && i <= last); }
 };
-constexpr uint32_t kAll = 0xffffffffu;
 
 constexpr int kList = 2048;
 struct Shared {
     uint32_t count[kBins];
     u64 mass[kBins];
     u64 list[kList];
+    uint32_t rank[512];
     u64 parts[kWaves], found[4];
-    uint32_t keys[kWaves], bad[kWaves], listed;
+    float tops[kWaves];
+    uint32_t front, back, token;
 };
 
-// Bins of the exponent, from `from` below the top's on, `per` of them to a factor of two; those above it
-// are bin -1, those below the last kBins.
-struct Window {
-    float from, per;
-    __device__ int bin(float t) const {
-        const float b = (-t - from) * per;
-        return b < 0.f ? -1 : b < (float)kBins ? (int)b : kBins;
-    }
-};
-// What the logits and the masses spread over: 2^-16, down to 2^-48, and far logits that only top_k counts.
-__device__ inline Window window(int w) {
-    return w == 0 ? Window{0.f, 128.f} : w == 1 ? Window{16.f, 64.f} : Window{48.f, 16.f};
+// Bins of the exponent, 64 of them to a factor of two from the largest logit down; the last holds all below 2^-32.
+constexpr float kPerOctave = 64.f;
+__device__ inline uint32_t bin_of(float x, const Scale& s) {
+    return (uint32_t)fminf((x - s.top) * s.bins, (float)(kBins - 1));
 }
-constexpr int kWindows = 3;
+// The least finite value of the bins up to `bin`: the lanes of a wave try 64 keys at once.
+__device__ inline float least_of(uint32_t bin, const Scale& s) {
+    const uint32_t first = key_of(-INFINITY) + 1, last = key_of(s.top), lane = threadIdx.x & 63;
+    if (bin >= kBins - 1) return value_of(first);
+    uint32_t base = first - 1;  // lies below
+#pragma unroll
+    for (int shift = 26; shift >= -4; shift -= 6) {
+        const int sh = shift > 0 ? shift : 0;
+        const uint64_t at = (uint64_t)base + ((uint64_t)(lane + 1) << sh);
+        const bool below = at < last && bin_of(value_of((uint32_t)at), s) > bin;
+        base += (uint32_t)__popcll(__ballot(below)) << sh;
+    }
+    return value_of(base + 1);
+}
 
-// Counts, and where `weigh` the weights, of a window's bins.
-template <class R>
-__device__ inline void fill(const R& row, const Scale& sc, int w, bool weigh, Shared& s) {
-    const Window win = window(w);
+__device__ inline void clear(Shared& s) {
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
     __syncthreads();
-    row.each([&](int, const float (&x)[R::N]) {
-#pragma unroll
-        for (int q = 0; q < R::N; ++q) {
-            const int bin = win.bin(exponent_of(x[q], sc));
-            if (bin < 0 || bin >= kBins) continue;
+}
+
+// Counts of the bins, -infinities in the last; where `weigh`, a thread's mass.  The last bin's are counted in
+// registers: most of a row may lie there, and lanes that add to one place wait for each other (96 us, so 17).
+template <class R>
+__device__ inline u64 fill(const R& row, const Scale& sc, bool weigh, Shared& s) {
+    clear(s);
+    u64 mass = 0;
+    uint32_t far = 0;
+    auto add = [&](uint32_t bin) {
+        if (bin < kBins - 1)
             atomicAdd(&s.count[bin], 1u);
-            if (weigh) atomicAdd(&s.mass[bin], units(weight_of(x[q], sc)));
+        else
+            ++far;
+    };
+    if (weigh)
+        row.each([&](int, const float (&x)[R::N]) {
+            double sum = 0;
+#pragma unroll
+            for (int q = 0; q < R::N; ++q) {
+                add(bin_of(x[q], sc));
+                sum += (double)weight_of(x[q], sc);
+            }
+            mass += units(sum);
+        });
+    else
+        row.each([&](int, const float (&x)[R::N]) {
+#pragma unroll
+            for (int q = 0; q < R::N; ++q) add(bin_of(x[q], sc));
+        });
+    u64 all;
+    block_scan(far, s.parts, all);
+    if (threadIdx.x == 0) s.count[kBins - 1] = (uint32_t)all;
+    __syncthreads();
+    return mass;
+}
+
+// f(bin) of the first bin for which `is` turns true along the two bins of each thread, or -1 in none.  was: before
+// the thread's first bin.
+template <class F>
+__device__ inline int first_bin(bool was, bool is0, bool is1, int slot, F note, Shared& s) {
+    const int b0 = 2 * threadIdx.x;
+    if (threadIdx.x == 0) s.found[slot] = (u64)-1;
+    __syncthreads();
+    if (!was && is0)
+        s.found[slot] = b0, note(0);
+    else if (!is0 && is1)
+        s.found[slot] = b0 + 1, note(1);
+    __syncthreads();
+    return (int)s.found[slot];
+}
+
+// The bin in which the sum of counts from the top on reaches want > 0, and the sum before it, or -1.
+__device__ inline int reach(u64 want, u64& before, Shared& s) {
+    const int b0 = 2 * threadIdx.x, b1 = b0 + 1;
+    const u64 v0 = s.count[b0], v1 = s.count[b1];
+    u64 all;
+    const u64 at = block_scan(v0 + v1, s.parts, all);
+    const int bin = first_bin(at >= want, at + v0 >= want, at + v0 + v1 >= want, 0,
+                              [&](int second) { s.found[1] = second ? at + v0 : at; }, s);
+    before = s.found[1];
+    return bin;
+}
+
+// The bins [lo, hi] in one of which the sum of masses from the top on reaches want <= total, from the counts.  A bin's
+// mass lies between its count times the weights at its ends, 2^(1/64) apart; and so does what lies below a bin,
+// which is the row's mass less the sum up to it.  counted: of the bins before lo, between: of lo to hi.
+__device__ inline void reach_mass(u64 want, u64 total, int& lo, int& hi, u64& counted, u64& between, Shared& s) {
+    const int b0 = 2 * threadIdx.x, b1 = b0 + 1;
+    const u64 c0 = s.count[b0], c1 = s.count[b1];
+    // 2^-16 more and less than the ends: an exponent's own rounding, and a weight's to units
+    auto least = [&](int b, u64 c) -> u64 {
+        const double w = (double)__builtin_amdgcn_exp2f(-(float)(b + 1) / kPerOctave) * (0x1p40 * (1 - 0x1p-16)) - 1.;
+        return b < kBins - 1 && w > 0. ? (u64)(w * (double)c) : 0;
+    };
+    auto most = [&](int b, u64 c) -> u64 {
+        return (u64)(((double)__builtin_amdgcn_exp2f(-(float)b / kPerOctave) * (0x1p40 * (1 + 0x1p-16)) + 2.) * (double)c);
+    };
+    const u64 l0 = least(b0, c0), l1 = least(b1, c1), m0 = most(b0, c0), m1 = most(b1, c1);
+    u64 all_l, all_m, all_c;
+    const u64 low = block_scan(l0 + l1, s.parts, all_l), high = block_scan(m0 + m1, s.parts, all_m);
+    const u64 count = block_scan(c0 + c1, s.parts, all_c);
+    auto at_least = [&](u64 l, u64 m) {
+        const u64 below = all_m - m, rest = total > below ? total - below : 0;
+        return l > rest ? l : rest;
+    };
+    auto at_most = [&](u64 l, u64 m) {
+        const u64 below = all_l - l, rest = total > below ? total - below : 0;
+        return m < rest ? m : rest;
+    };
+    lo = first_bin(at_most(low, high) >= want && b0 > 0, at_most(low + l0, high + m0) >= want,
+                   at_most(low + l0 + l1, high + m0 + m1) >= want, 0, [&](int second) { s.found[1] = second ? count + c0 : count; }, s);
+    hi = first_bin(at_least(low, high) >= want && b0 > 0, at_least(low + l0, high + m0) >= want,
+                   at_least(low + l0 + l1, high + m0 + m1) >= want, 2,
+                   [&](int second) { s.found[3] = count + c0 + (second ? c1 : 0); }, s);
+    // (past the last bin nothing lies below: both are reached)
+    counted = s.found[1];
+    between = s.found[3] - counted;
+}
+
+// s.list[0, n) in falling order.  A short list by each entry's rank, the number of larger ones (they are all
+// different), counted by several threads each; a long one by merging in LDS, step by step of all threads.
+__device__ inline void sort(uint32_t n, Shared& s) {
+    constexpr uint32_t kRanked = 512;
+    if (n <= kRanked) {
+        uint32_t places = 64;  // whole waves
+        while (places < n) places *= 2;
+        const uint32_t i = threadIdx.x & (places - 1), part = threadIdx.x / places, parts = kThreads / places;
+        const uint32_t per = (n + parts - 1) / parts, from = part * per, to = from + per < n ? from + per : n;
+        if (threadIdx.x < kRanked) s.rank[threadIdx.x] = 0;
+        const u64 own = i < n ? s.list[i] : 0;
+        __syncthreads();
+        uint32_t larger = 0;
+#pragma unroll 8
+        for (uint32_t j = from; j < to; ++j) larger += s.list[j] > own;
+        if (i < n && larger > 0) atomicAdd(&s.rank[i], larger);
+        __syncthreads();
+        if (threadIdx.x < n) s.list[s.rank[threadIdx.x]] = own;
+        __syncthreads();
+        return;
+    }
+    uint32_t size = 2;
+    while (size < n) size *= 2;
+    for (uint32_t k = 2; k <= size; k *= 2)
+        for (uint32_t j = k / 2; j > 0; j /= 2) {
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
+                const uint32_t a = 2 * i - (i & (j - 1)), b = k == 2 * j ? a + 2 * j - 1 - 2 * (a & (j - 1)) : a + j;
+                // entries past n count as the smallest; the first step of each merge compares mirrored places, so
+                // that all steps sort downwards and those entries stay behind
+                if (b < n) {
+                    const u64 x = s.list[a], y = s.list[b];
+                    if (x < y) s.list[a] = y, s.list[b] = x;
+                }
+            }
         }
-    });
     __syncthreads();
 }
 
-// The row's order is walked to where the sum of counts (by_mass: of masses) reaches `want` > 0: the cut there, and in
-// `left` the mass that stays, where it is wanted (`weigh`).  False: it is not reached within the windows, or too many
-// logits share a bin.  filled: the window that the bins hold.
+// The logits from `from` on: those below `sure` from the front of s.list on, the others from its back, where
+// `certain`.  false: they are too many.
 template <class R>
-__device__ inline bool find(const R& row, const Scale& sc, bool by_mass, u64 want, bool weigh, int& filled, Cut& cut, u64& left, Shared& s) {
-    u64 before = 0, mass_before = 0;
-    for (int w = 0; w < kWindows; ++w) {
-        if (filled != w) {
-            fill(row, sc, w, weigh, s);
-            filled = w;
-        }
-        const int b0 = 2 * threadIdx.x, b1 = b0 + 1;
-        const u64 c0 = s.count[b0], c1 = s.count[b1], m0 = s.mass[b0], m1 = s.mass[b1];
-        u64 all, all_mass;
-        const u64 mass = mass_before + block_scan(m0 + m1, s.parts, all_mass);
-        u64 sum = before + block_scan(c0 + c1, s.parts, all);
-        if (by_mass) sum = mass, all = all_mass;
-        const u64 v0 = by_mass ? m0 : c0, v1 = by_mass ? m1 : c1;
-        if (sum < want && want <= sum + v0) s.found[0] = b0, s.found[1] = sum, s.found[2] = mass;
-        if (sum + v0 < want && want <= sum + v0 + v1) s.found[0] = b1, s.found[1] = sum + v0, s.found[2] = mass + m0;
-        __syncthreads();
-        if (before + all < want) {
-            before += all;
-            mass_before += all_mass;
-            continue;
-        }
-        const int bin = (int)s.found[0];
-        before = s.found[1];
-        mass_before = s.found[2];
-        const uint32_t n = s.count[bin];
-        if (n > kList) return false;
-        // the bin's logits in order: by key, then from the lowest index on
-        if (threadIdx.x == 0) s.listed = 0;
-        uint32_t size = 64;
-        while (size < n) size *= 2;
-        for (uint32_t i = threadIdx.x; i < size; i += kThreads) s.list[i] = 0;
-        __syncthreads();
-        const Window win = window(w);
-        row.each([&](int i, const float (&x)[R::N]) {
+__device__ inline bool gather(const R& row, float from, float sure, bool certain, Shared& s) {
+    __syncthreads();
+    if (threadIdx.x == 0) s.front = s.back = 0;
+    __syncthreads();
+    row.each([&](int i, const float (&x)[R::N]) {
+        uint32_t mine = 0, rest = 0;
 #pragma unroll
-            for (int q = 0; q < R::N; ++q)
-                if (win.bin(exponent_of(x[q], sc)) == bin)
-                    s.list[atomicAdd(&s.listed, 1u)] = (u64)key_of(x[q]) << 32 | ~(uint32_t)(i + q);
-        });
-        __syncthreads();
-        for (uint32_t k = 2; k <= size; k *= 2)
-            for (uint32_t j = k / 2; j > 0; j /= 2) {
-                for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
-                    const uint32_t a = 2 * i - (i & (j - 1)), b = a + j;
-                    const u64 x = s.list[a], y = s.list[b];
-                    if ((x < y) == ((a & k) == 0)) s.list[a] = y, s.list[b] = x;
-                }
-                __syncthreads();
-            }
-        const u64 e0 = (uint32_t)b0 < n ? s.list[b0] : 0, e1 = (uint32_t)b1 < n ? s.list[b1] : 0;
-        const uint32_t k0 = (uint32_t)(e0 >> 32), k1 = (uint32_t)(e1 >> 32);
-        const u64 w0 = (uint32_t)b0 < n && weigh ? units(weight_of(value_of(k0), sc)) : 0;
-        const u64 w1 = (uint32_t)b1 < n && weigh ? units(weight_of(value_of(k1), sc)) : 0;
-        const u64 at = mass_before + block_scan(w0 + w1, s.parts, all);
-        // the first of them that reaches it is the last that stays
-        if ((uint32_t)b0 < n && (by_mass ? at < want && want <= at + w0 : before + b0 + 1 == want))
-            s.found[0] = b0, s.found[1] = at + w0;
-        if ((uint32_t)b1 < n && (by_mass ? at + w0 < want && want <= at + w0 + w1 : before + b1 + 1 == want))
-            s.found[0] = b1, s.found[1] = at + w0 + w1;
-        __syncthreads();
-        const uint32_t last = (uint32_t)s.found[0];
-        left = s.found[1];
-        cut.key = (uint32_t)(s.list[last] >> 32);
-        u64 same = 0, equal;
-        for (uint32_t i = threadIdx.x; i <= last; i += kThreads) same += (uint32_t)(s.list[i] >> 32) == cut.key;
-        block_scan(same, s.parts, equal);
-        cut.equal = (uint32_t)equal;
-        __syncthreads();
-        return true;
+        for (int q = 0; q < R::N; ++q) mine |= (uint32_t)(x[q] >= from && x[q] < sure) << q;
+        if (certain)
+#pragma unroll
+            for (int q = 0; q < R::N; ++q) rest |= (uint32_t)(x[q] >= sure) << q;
+        if (!__any((mine | rest) != 0)) return;
+        if (*(volatile uint32_t*)&s.front + *(volatile uint32_t*)&s.back > kList) return;
+        // places by the wave's sums, both in one word
+        const uint32_t own = __popc(mine) | __popc(rest) << 16;
+        const u64 sums = wave_scan(own), all = of_lane(sums, 63);
+        uint32_t at = 0;
+        if ((threadIdx.x & 63) == 63) at = atomicAdd(&s.front, (uint32_t)all & 0xffff) | atomicAdd(&s.back, (uint32_t)all >> 16) << 16;
+        at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63);
+        uint32_t f = (at & 0xffff) + (((uint32_t)sums & 0xffff) - __popc(mine));
+        uint32_t b = (at >> 16) + (((uint32_t)sums >> 16) - __popc(rest));
+#pragma unroll
+        for (int q = 0; q < R::N; ++q) {
+            const bool front = mine >> q & 1, back = rest >> q & 1;
+            const uint32_t place = front ? f : kList - 1 - b;
+            if ((front || back) && place < kList) s.list[place] = (u64)key_of(x[q]) << 32 | ~(uint32_t)(i + q);
+            f += front;
+            b += back;
+        }
+    });
+    __syncthreads();
+    return s.front + s.back <= kList;
+}
+__device__ inline float value_at(uint32_t i, const Shared& s) { return value_of((uint32_t)(s.list[i] >> 32)); }
+__device__ inline int index_at(uint32_t i, const Shared& s) { return (int)~(uint32_t)s.list[i]; }
+
+// Tiles of the row for the sum by index: blocks of a wave's vector, 2^k of them each.
+template <class R>
+struct Tiles {
+    static constexpr int BLOCK = 64 * R::N;
+    int k, size;
+    __device__ Tiles(int n) : k(0), size(n) {
+        while (((n - 1) / BLOCK) >> k >= kBins) ++k;
     }
-    return false;
+    __device__ int of(int i) const { return i / BLOCK >> k; }
+};
+// Each tile's mass that stays, in s.mass; EQUAL: some of those equal to the edge do.
+template <bool EQUAL, class R>
+__device__ inline void weigh_tiles(const R& row, const Scale& sc, const Tiles<R>& tiles, Cut cut, Shared& s) {
+    clear(s);
+    row.each([&](int i, const float (&x)[R::N]) {
+        float most = x[0];
+#pragma unroll
+        for (int q = 1; q < R::N; ++q) most = fmaxf(most, x[q]);
+        if (!__any(EQUAL ? most >= cut.edge : most > cut.edge)) return;
+        double sum = 0;
+#pragma unroll
+        for (int q = 0; q < R::N; ++q)
+            sum += (double)((EQUAL ? cut.keeps(x[q], i + q) : x[q] > cut.edge) ? weight_of(x[q], sc) : 0.f);
+        const u64 whole = wave_scan(units(sum));
+        if ((threadIdx.x & 63) == 63 && whole > 0) atomicAdd(&s.mass[tiles.of(i)], whole);
+    });
+    __syncthreads();
+}
+__device__ inline u64 sum_of_tiles(Shared& s) {
+    u64 all;
+    block_scan(s.mass[2 * threadIdx.x] + s.mass[2 * threadIdx.x + 1], s.parts, all);
+    return all;
+}
+// Adds entries [from, to) of the list to the tiles' masses.
+template <class R>
+__device__ inline void add_listed(uint32_t from, uint32_t to, const Scale& sc, const Tiles<R>& tiles, Shared& s) {
+    for (uint32_t i = from + threadIdx.x; i < to; i += kThreads)
+        atomicAdd(&s.mass[tiles.of(index_at(i, s))], units(weight_of(value_at(i, s), sc)));
 }
 
-// The same digit by digit of the keys, for any logits (all equal, or too far below the top for the windows).
+// The cut digit by digit of the keys, for any logits (many equal, or far below the top): where the sum of counts
+// (masses) reaches want > 0.
 template <class R>
-__device__ inline void descend(const R& row, const Scale& sc, bool by_mass, u64 want, Cut& cut, Shared& s) {
+__device__ inline Cut descend(const R& row, const Scale& sc, const Tiles<R>& tiles, bool by_mass, u64 want, Shared& s) {
     uint32_t prefix = 0, mask = 0;
     u64 in_bin = 0;
+    const int b0 = 2 * threadIdx.x, b1 = b0 + 1;
     for (int level = 0; level < 3; ++level) {
         const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
-        __syncthreads();
+        clear(s);
         row.each([&](int, const float (&x)[R::N]) {
 #pragma unroll
             for (int q = 0; q < R::N; ++q) {
                 const uint32_t k = key_of(x[q]);
                 if ((k & mask) != prefix || x[q] == -INFINITY) continue;
-                const int bin = (k >> shift) & ((1 << bits) - 1);
+                const int bin = kBins - 1 - ((k >> shift) & ((1 << bits) - 1));  // the largest keys first
                 atomicAdd(&s.count[bin], 1u);
                 if (by_mass) atomicAdd(&s.mass[bin], units(weight_of(x[q], sc)));
             }
         });
         __syncthreads();
-        // two bins a thread, from the largest keys down
-        const int b1 = kBins - 1 - 2 * threadIdx.x, b0 = b1 - 1;
-        const u64 v1 = by_mass ? s.mass[b1] : s.count[b1], v0 = by_mass ? s.mass[b0] : s.count[b0];
+        const u64 v0 = by_mass ? s.mass[b0] : s.count[b0], v1 = by_mass ? s.mass[b1] : s.count[b1];
         u64 all;
-        const u64 before = block_scan(v1 + v0, s.parts, all);
-        if (before < want && want <= before + v1) s.found[0] = b1, s.found[1] = before, s.found[2] = s.count[b1];
-        if (before + v1 < want && want <= before + v1 + v0)
-            s.found[0] = b0, s.found[1] = before + v1, s.found[2] = s.count[b0];
-        __syncthreads();
-        prefix |= (uint32_t)s.found[0] << shift;
+        const u64 at = block_scan(v0 + v1, s.parts, all);
+        const int bin = first_bin(at >= want, at + v0 >= want, at + v0 + v1 >= want, 0,
+                                  [&](int second) { s.found[1] = second ? at + v0 : at; }, s);
+        prefix |= (uint32_t)(kBins - 1 - bin) << shift;
         mask |= (uint32_t)((1u << bits) - 1) << shift;
         want -= s.found[1];
-        in_bin = s.found[2];
+        in_bin = s.count[bin];
     }
+    const float edge = value_of(prefix);
     u64 need = want;
     if (by_mass) {
-        const u64 w = units(weight_of(value_of(prefix), sc));  // above 0: a mass was reached here
+        const u64 w = units(weight_of(edge, sc));  // above 0: a mass was reached here
         need = (want + w - 1) / w;
     }
-    cut = {prefix, (uint32_t)(need < in_bin ? need : in_bin)};
-}
-
-// The mass that stays.
-template <class R>
-__device__ inline u64 mass_of(const R& row, const Scale& sc, Cut cut, Shared& s) {
-    u64 own = 0, same = 0, all, many;
-    row.each([&](int, const float (&x)[R::N]) {
-        double sum = 0;
+    if (need >= in_bin) return {below(prefix), -1};
+    // the index of the `need`-th of the equal ones: its tile, then its place there
+    clear(s);
+    row.each([&](int i, const float (&x)[R::N]) {
+        uint32_t same = 0;
 #pragma unroll
-        for (int q = 0; q < R::N; ++q) {
-            const uint32_t k = key_of(x[q]);
-            sum += k > cut.key ? (double)weight_of(x[q], sc) : 0.;
-            same += k == cut.key;
-        }
-        own += units(sum);
+        for (int q = 0; q < R::N; ++q) same += __popcll(__ballot(x[q] == edge));
+        if ((threadIdx.x & 63) == 63 && same > 0) atomicAdd(&s.count[tiles.of(i)], same);
     });
-    block_scan(own, s.parts, all);
-    block_scan(same, s.parts, many);
-    return all + (many < cut.equal ? many : cut.equal) * units(weight_of(value_of(cut.key), sc));
-}
-
-template <class R>
-__device__ inline u64 finite_of(const R& row, Shared& s) {
+    __syncthreads();
+    u64 before = 0;
+    const int tile = reach(need, before, s);
+    const int step = Tiles<R>::BLOCK << tiles.k, from = tile * step, to = from + step < tiles.size ? from + step : tiles.size;
+    const int per = (to - from + kThreads - 1) / kThreads, mine = from + threadIdx.x * per, end = mine + per < to ? mine + per : to;
     u64 own = 0, all;
-    row.each([&](int, const float (&x)[R::N]) {
-#pragma unroll
-        for (int q = 0; q < R::N; ++q) own += x[q] > -INFINITY;
-    });
-    block_scan(own, s.parts, all);
-    return all;
+    for (int i = mine; i < end; ++i) own += (float)row.row[i] == edge;
+    u64 at = before + block_scan(own, s.parts, all);
+    if (at < need && need <= at + own)
+        for (int i = mine; i < end; ++i)
+            if ((float)row.row[i] == edge && ++at == need) s.found[0] = i;
+    __syncthreads();
+    return {edge, (int)s.found[0]};
 }
 
-// One row a workgroup.  V: vectors of the row in a thread's registers, 0 for longer ones.
+// Less than this lies before the last that stays of `mass`.
+__device__ inline u64 least_mass(float top_p, u64 mass) {
+    const double p = (double)top_p * (double)mass;
+    return p < 1. ? 1 : (u64)__builtin_ceil(p);
+}
+
+// Of the sorted list's first n the number up to which the sum of weights, with `before`, reaches want, or n;
+// `all`: the sum of all n.
+__device__ inline uint32_t listed_mass(uint32_t n, u64 before, u64 want, const Scale& sc, u64& all, Shared& s) {
+    const uint32_t i0 = 2 * threadIdx.x, i1 = i0 + 1;
+    const u64 w0 = i0 < n ? units(weight_of(value_at(i0, s), sc)) : 0, w1 = i1 < n ? units(weight_of(value_at(i1, s), sc)) : 0;
+    const u64 at = before + block_scan(w0 + w1, s.parts, all);
+    const int last = first_bin(at >= want && i0 > 0, at + w0 >= want && i0 < n, at + w0 + w1 >= want && i1 < n, 0, [](int) {}, s);
+    return last < 0 ? n : (uint32_t)last + 1;
+}
+// Of the sorted list's first n those that are at least `least`.
+__device__ inline uint32_t listed_above(uint32_t n, float least, Shared& s) {
+    const uint32_t i0 = 2 * threadIdx.x, i1 = i0 + 1;
+    u64 many;
+    block_scan((u64)(i0 < n && value_at(i0, s) >= least) + (u64)(i1 < n && value_at(i1, s) >= least), s.parts, many);
+    return (uint32_t)many;
+}
+
+// One row a workgroup.  V: vectors of the row in a thread's registers.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) sample_row_kernel(Args a) {
+    typedef Row<T, V> R;
+    constexpr int N = R::N;
     __shared__ Shared s;
     const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, size = a.vocab;
-    Row<T, V> row;
+    R row;
     row.init((const T*)a.logits + (size_t)r * a.ld, size);
     const float temperature = a.temperatures ? a.temperatures[r] : a.temperature;
     const float top_p = a.top_ps ? a.top_ps[r] : a.top_p, min_p = a.min_ps ? a.min_ps[r] : a.min_p, u = a.u[r];
     const long long top_k = a.top_ks ? a.top_ks[r] : a.top_k;
 
-    float top = -INFINITY;
-    bool bad = false;
-    row.each([&](int, const float (&x)[Row<T, V>::N]) {
+    float top = -INFINITY;  // NaN where there is one
+    row.each([&](int, const float (&x)[N]) {
 #pragma unroll
-        for (int q = 0; q < Row<T, V>::N; ++q) {
-            bad |= x[q] != x[q];
-            top = fmaxf(top, x[q]);
-        }
+        for (int q = 0; q < N; ++q) top = __builtin_elementwise_maximum(top, x[q]);
     });
+    const float own_top = top;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    bad = __any(bad);
-    if (lane == 0) s.keys[wave] = __builtin_bit_cast(uint32_t, top), s.bad[wave] = bad;
+    for (int o = 32; o > 0; o >>= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, o));
+    if (lane == 0) s.tops[wave] = top;
+    if (threadIdx.x == 0) s.token = 0xffffffffu;
     __syncthreads();
-    for (int w = 0; w < kWaves; ++w) {
-        top = fmaxf(top, __builtin_bit_cast(float, s.keys[w]));
-        bad |= s.bad[w] != 0;
-    }
-    bad |= !__builtin_isfinite(top) || !(temperature >= 0.f && temperature < INFINITY) || u != u || top_p != top_p ||
-           min_p != min_p;
-    if (bad) {
+    for (int w = 0; w < kWaves; ++w) top = __builtin_elementwise_maximum(top, s.tops[w]);
+    top = uniform(top);
+    if (!__builtin_isfinite(top) || !(temperature >= 0.f && temperature < INFINITY) || u != u || top_p != top_p || min_p != min_p) {
         if (threadIdx.x == 0) a.token[r] = -1;
         return;
     }
-    const double c = 1.4426950408889634 / (double)temperature;
-    const Scale sc{top, (float)c, (float)(c - (double)(float)c)};
-    Cut cut{key_of(-INFINITY) + 1, kAll};
-    if (temperature == 0.f) {
-        cut = {key_of(top), 1};  // the first of the largest
-    } else {
-        const bool weigh = top_p < 1.f;
-        const bool ranked = top_k > 0 && top_k < size && (u64)top_k < finite_of(row, s);  // else all stay
-        int filled = -1;
-        u64 left = 0;
-        bool weighed = false;
-        for (int by_mass = ranked ? 0 : 1; by_mass < (weigh ? 2 : 1); ++by_mass) {
-            u64 want = (u64)top_k;
-            if (by_mass) {
-                if (!weighed) left = mass_of(row, sc, cut, s);
-                // less than `want` lies before the last that stays
-                const double p = (double)top_p * (double)left;
-                want = p < 1. ? 1 : (u64)__builtin_ceil(p);
+    if (temperature == 0.f || min_p > 1.f) {  // the first alone
+        uint32_t first = 0xffffffffu;
+        row.each([&](int i, const float (&x)[N]) {
+#pragma unroll
+            for (int q = N - 1; q >= 0; --q)
+                if (x[q] == top && (uint32_t)(i + q) < first) first = i + q;
+        });
+        if (first != 0xffffffffu) atomicMin(&s.token, first);
+        __syncthreads();
+        if (threadIdx.x == 0) a.token[r] = s.token;
+        return;
+    }
+    const Scale sc(top, temperature);
+    const Tiles<R> tiles(size);
+    const float lowest = value_of(key_of(-INFINITY) + 1);  // of the finite values
+    // the least logit of at least min_p times the largest one's probability
+    float least = lowest;
+    if (min_p > 0.f) {
+        const double x = (double)top + log((double)min_p) * (double)temperature;
+        if (x > (double)lowest) {
+            least = (float)x;
+            if ((double)least < x) least = value_of(key_of(least) + 1);
+        }
+    }
+    const Cut at_least{below(key_of(least)), -1};
+    const bool weigh = top_p < 1.f, ranked = top_k > 0 && top_k < size;
+
+    // From one stage to the next until what stays is known: all of it as `cut`, or up to a border in a list.
+    enum { QUICK, COUNT, MASS, REST, WHOLE, BORDER, LISTED };
+    int stage = ranked ? (top_k <= kThreads / 2 ? QUICK : COUNT) : weigh ? MASS : REST;
+    Cut cut{below(key_of(lowest)), -1};  // what top_k leaves, then all
+    bool certain = false;                // what lies before the border is listed too
+    u64 want = 0, total = 0;
+    bool filled = false;
+    while (stage < WHOLE) {
+        int lo = 0, hi = -1, next = stage;
+        u64 before = 0;
+        float from = lowest, sure = INFINITY;
+        certain = false;
+        if (stage == QUICK) {
+            // top_k of the threads' own largest logits are as large as the least of those: where no more than the
+            // list holds are, the counts of all are not needed
+            clear(s);
+            if (own_top > -INFINITY) atomicAdd(&s.count[bin_of(own_top, sc)], 1u);
+            __syncthreads();
+            hi = reach((u64)top_k, before, s);
+            if (hi >= 0) from = weigh ? least_of(hi, sc) : fmaxf(least_of(hi, sc), least);
+            next = WHOLE;
+        } else if (stage == COUNT || stage == MASS) {
+            if (!filled) {
+                const u64 own = fill(row, sc, weigh, s);
+                if (weigh) block_scan(own, s.parts, total);
+                filled = true;
             }
-            weighed = find(row, sc, by_mass != 0, want, weigh, filled, cut, left, s);
-            if (!weighed) {
-                descend(row, sc, by_mass != 0, want, cut, s);
-                filled = -1;
+            if (stage == COUNT) {
+                lo = hi = reach((u64)top_k, before, s);
+                next = weigh ? MASS : REST;
+                if (before + s.count[hi] <= kList) {
+                    next = WHOLE;
+                    lo = 0;
+                }
+                from = least_of(hi, sc);
+                if (next == WHOLE && !weigh) from = fmaxf(from, least);
+                if (lo > 0) sure = least_of(lo - 1, sc);
+            } else {
+                if (want == 0) want = least_mass(top_p, total);
+                u64 counted, between;
+                reach_mass(want, total, lo, hi, counted, between, s);
+                next = BORDER;
+                if (lo > 0) sure = least_of(lo - 1, sc);
+                from = least_of(hi, sc);
+                if (least >= sure) {
+                    stage = REST;  // min_p's cut lies before top_p's
+                    continue;
+                }
+                certain = counted + between <= kList;
+                if (between > kList) hi = -1;
+            }
+        } else {
+            if (!(least > lowest && least > cut.edge)) break;
+            // min_p's cut: all that is as large, if it is short
+            cut = at_least;
+            hi = 0;
+            from = least;
+            next = LISTED;
+        }
+        const bool got = hi >= 0 && gather(row, from, sure, certain, s);
+        if (got && (next == WHOLE || next == BORDER || next == LISTED)) {
+            stage = next;
+            break;
+        }
+        if (stage == QUICK) {
+            stage = COUNT;
+            continue;
+        }
+        if (stage == REST) break;
+        // the cut of top_k, or that of top_p where too many lie at its border
+        bool stays = false;
+        if (stage == COUNT && hi == kBins - 1) {  // of fewer finite logits than top_k all stay
+            u64 own = 0, finite;
+            row.each([&](int, const float (&x)[N]) {
+#pragma unroll
+                for (int q = 0; q < N; ++q) own += x[q] > -INFINITY;
+            });
+            block_scan(own, s.parts, finite);
+            stays = finite <= (u64)top_k;
+        }
+        if (!stays) {
+            if (got) {
+                sort(s.front, s);
+                const uint32_t last = (uint32_t)((u64)top_k - before) - 1;
+                cut = {value_at(last, s), index_at(last, s)};
+            } else {
+                cut = descend(row, sc, tiles, stage == MASS, stage == MASS ? want : (u64)top_k, s);
+                filled = false;
             }
         }
-        if (min_p > 0.f) {
-            // the least logit of at least min_p times the largest one's probability
-            const double least = (double)top + log((double)min_p) * (double)temperature;
-            float x = (float)least;
-            if ((double)x < least) x = value_of(key_of(x) + 1);
-            if (min_p > 1.f)
-                cut = {key_of(top), 1};
-            else if (key_of(x) > cut.key)
-                cut = {key_of(x), kAll};
+        stage = stage == COUNT && weigh ? MASS : REST;
+        if (stage == MASS && !stays) {
+            weigh_tiles<true>(row, sc, tiles, cut, s);
+            want = least_mass(top_p, sum_of_tiles(s));
+            filled = false;
         }
     }
 
-    // Blocks of a wave's vector, 2^k of them to a tile: what each tile holds of the mass, and how many of the cut's key
-    constexpr int BLOCK = 64 * Row<T, V>::N;
-    int k = 0;
-    while ((((size - 1) / BLOCK + 1) - 1) >> k >= kBins) ++k;
-    const bool limited = cut.equal != kAll;
-    const bool greedy = temperature == 0.f;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
-    __syncthreads();
-    row.each([&](int i, const float (&x)[Row<T, V>::N]) {
-        double sum = 0;
-        uint32_t same = 0;
-#pragma unroll
-        for (int q = 0; q < Row<T, V>::N; ++q) {
-            const uint32_t key = key_of(x[q]);
-            if (!greedy) sum += key > cut.key || (key == cut.key && !limited) ? (double)weight_of(x[q], sc) : 0.;
-            if (limited) same += __popcll(__ballot(key == cut.key));
+    // the tiles' masses
+    uint32_t n = 0;  // of the list's front that stay
+    if (stage == WHOLE) {
+        sort(s.front, s);
+        n = s.front;
+        if ((u64)top_k < n) n = (uint32_t)top_k;
+        if (weigh) {
+            u64 all;
+            listed_mass(n, 0, (u64)-1, sc, all, s);
+            n = listed_mass(n, 0, least_mass(top_p, all), sc, all, s);
         }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-        if (lane == 0 && i < size) {
-            const int tile = i / BLOCK >> k;
-            if (sum > 0.) atomicAdd(&s.mass[tile], units(sum));
-            if (same > 0) atomicAdd(&s.count[tile], same);
-        }
-    });
-    __syncthreads();
-    const u64 w = greedy ? 1 : limited ? units(weight_of(value_of(cut.key), sc)) : 0;
-    const int t0 = 2 * threadIdx.x, t1 = t0 + 1;
-    u64 many = 0, all, e0 = 0;
-    auto stay = [&](u64 before, u64 n) -> u64 { return before >= cut.equal ? 0 : n < cut.equal - before ? n : cut.equal - before; };
-    u64 m0 = s.mass[t0], m1 = s.mass[t1];
-    const u64 n0 = s.count[t0], n1 = s.count[t1];
-    if (limited) {
-        e0 = block_scan(n0 + n1, s.parts, many);
-        m0 += stay(e0, n0) * w;
-        m1 += stay(e0 + n0, n1) * w;
     }
-    const u64 before = block_scan(m0 + m1, s.parts, all);
-    double at = (double)u * (double)all;
-    at = at > 0. ? at : 0.;
-    u64 target = at < (double)all ? (u64)at : all - 1;
+    if (stage == REST && cut.last >= 0) {
+        weigh_tiles<true>(row, sc, tiles, cut, s);
+    } else if (stage == REST || (stage == BORDER && !certain)) {
+        if (stage == BORDER) {
+            sort(s.front, s);
+            cut = {value_at(0, s), -1};
+        }
+        weigh_tiles<false>(row, sc, tiles, cut, s);
+    } else {
+        if (stage == BORDER) sort(s.front, s);
+        clear(s);
+        if (stage == BORDER) add_listed(kList - s.back, kList, sc, tiles, s);
+        if (stage == LISTED) n = s.front;
+        __syncthreads();
+    }
+    if (stage == BORDER) {
+        u64 all;
+        n = listed_mass(s.front, sum_of_tiles(s), want, sc, all, s);
+    }
+    if (stage == BORDER || stage == WHOLE) {
+        cut = {value_at(n - 1, s), index_at(n - 1, s)};
+        if (least > cut.edge) {
+            n = listed_above(n, least, s);
+            cut = at_least;
+        }
+    }
+    add_listed(0, n, sc, tiles, s);
+    __syncthreads();
+
+    // the tile in which the sum passes u's share, and the place in it
+    const int t0 = 2 * threadIdx.x;
+    const u64 m0 = s.mass[t0], m1 = s.mass[t0 + 1];
+    u64 all;
+    const u64 at = block_scan(m0 + m1, s.parts, all);
+    double share = (double)u * (double)all;
+    share = share > 0. ? share : 0.;
+    u64 target = share < (double)all ? (u64)share : all - 1;
     target = target < all ? target : all - 1;
-    // the tile in which the sum passes the target
-    if (before <= target && target < before + m0) s.found[0] = t0, s.found[1] = before, s.found[2] = e0;
-    if (before + m0 <= target && target < before + m0 + m1) s.found[0] = t1, s.found[1] = before + m0, s.found[2] = e0 + n0;
-    __syncthreads();
-    const int from = (int)s.found[0] * (BLOCK << k), to = from + (BLOCK << k) < size ? from + (BLOCK << k) : size;
-    const u64 done = s.found[1], seen = s.found[2];
-    const int per = (to - from + kThreads - 1) / kThreads, mine = from + threadIdx.x * per;
-    const int end = mine + per < to ? mine + per : to;
-    auto weigh = [&](float x) -> u64 {
-        const uint32_t key = key_of(x);
-        return key > cut.key || (key == cut.key && !limited) ? greedy ? 0 : units(weight_of(x, sc)) : 0;
+    const int tile = first_bin(at > target, at + m0 > target, at + m0 + m1 > target, 0,
+                               [&](int second) { s.found[1] = second ? at + m0 : at; }, s);
+    const int step = Tiles<R>::BLOCK << tiles.k, from = tile * step, to = from + step < size ? from + step : size;
+    const int per = (to - from + kThreads - 1) / kThreads, mine = from + threadIdx.x * per, end = mine + per < to ? mine + per : to;
+    const u64 done = s.found[1];
+    auto mass = [&](int i) -> u64 {
+        const float x = (float)row.row[i];
+        return cut.keeps(x, i) ? units(weight_of(x, sc)) : 0;
     };
-    u64 first = seen, own = 0, same = 0;
-    for (int i = mine; i < end; ++i) {
-        own += weigh((float)row.row[i]);
-        same += key_of((float)row.row[i]) == cut.key;
-    }
-    if (limited) {
-        first += block_scan(same, s.parts, many);
-        own += stay(first, same) * w;
-    }
+    u64 own = 0;
+    for (int i = mine; i < end; ++i) own += mass(i);
     u64 sum = done + block_scan(own, s.parts, all);
-    if (sum <= target && target < sum + own) {
+    if (sum <= target && target < sum + own)
         for (int i = mine; i < end; ++i) {
-            const float x = (float)row.row[i];
-            if (limited && key_of(x) == cut.key)
-                sum += first++ < cut.equal ? w : 0;
-            else
-                sum += weigh(x);
+            sum += mass(i);
             if (sum > target) {
                 a.token[r] = i;
                 return;
             }
         }
-    }
 }
 
 }  // namespace sample

@@ -14,12 +14,8 @@ void launch(int rows, const Args& a, hipStream_t stream) {
     const int vectors = (a.vocab + kThreads * N - 1) / (kThreads * N);
     if (vectors <= 4)
         sample_row_kernel<T, 4><<<rows, kThreads, 0, stream>>>(a);
-    else if (vectors <= 8)
-        sample_row_kernel<T, 8><<<rows, kThreads, 0, stream>>>(a);
-    else if (vectors <= 16)
-        sample_row_kernel<T, 16><<<rows, kThreads, 0, stream>>>(a);
     else
-        sample_row_kernel<T, 0><<<rows, kThreads, 0, stream>>>(a);
+        sample_row_kernel<T, 12><<<rows, kThreads, 0, stream>>>(a);
 }
 
 int run(int dtype, int rows, const Args& a, hipStream_t stream) {

@@ -197,7 +197,7 @@ struct Cut {
 
 constexpr int kList = 2048;
 struct Shared {
-    uint32_t count[kBins];
+    uint32_t count[kBins + 63];  // while they are counted the last bin has a place for each lane
     u64 mass[kBins];
     u64 list[kList];
     uint32_t rank[512];
@@ -229,28 +229,24 @@ __device__ inline float least_of(uint32_t bin, const Scale& s) {
 __device__ inline void clear(Shared& s) {
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = 0, s.mass[i] = 0;
+    if (threadIdx.x < 63) s.count[kBins + threadIdx.x] = 0;
     __syncthreads();
 }
 
-// Counts of the bins, -infinities in the last; where `weigh`, a thread's mass.  The last bin's are counted in
-// registers: most of a row may lie there, and lanes that add to one place wait for each other (96 us, so 17).
+// Counts of the bins, -infinities in the last; where `weigh`, a thread's mass.  Most of a row may lie in the last
+// bin, and lanes that add to one place wait for each other (131072 bf16 logits: 96 us, so 15): each has its own.
 template <class R>
 __device__ inline u64 fill(const R& row, const Scale& sc, bool weigh, Shared& s) {
     clear(s);
     u64 mass = 0;
-    uint32_t far = 0;
-    auto add = [&](uint32_t bin) {
-        if (bin < kBins - 1)
-            atomicAdd(&s.count[bin], 1u);
-        else
-            ++far;
-    };
+    const float most = (float)(kBins - 1 + (threadIdx.x & 63));
+    auto add = [&](float x) { atomicAdd(&s.count[(uint32_t)fminf((x - sc.top) * sc.bins, most)], 1u); };
     if (weigh)
         row.each([&](int, const float (&x)[R::N]) {
             double sum = 0;
 #pragma unroll
             for (int q = 0; q < R::N; ++q) {
-                add(bin_of(x[q], sc));
+                add(x[q]);
                 sum += (double)weight_of(x[q], sc);
             }
             mass += units(sum);
@@ -258,11 +254,10 @@ __device__ inline u64 fill(const R& row, const Scale& sc, bool weigh, Shared& s)
     else
         row.each([&](int, const float (&x)[R::N]) {
 #pragma unroll
-            for (int q = 0; q < R::N; ++q) add(bin_of(x[q], sc));
+            for (int q = 0; q < R::N; ++q) add(x[q]);
         });
-    u64 all;
-    block_scan(far, s.parts, all);
-    if (threadIdx.x == 0) s.count[kBins - 1] = (uint32_t)all;
+    __syncthreads();
+    if (threadIdx.x < 63) atomicAdd(&s.count[kBins - 1], s.count[kBins + threadIdx.x]);
     __syncthreads();
     return mass;
 }
@@ -385,21 +380,18 @@ __device__ inline bool gather(const R& row, float from, float sure, bool certain
             for (int q = 0; q < R::N; ++q) rest |= (uint32_t)(x[q] >= sure) << q;
         if (!__any((mine | rest) != 0)) return;
         if (*(volatile uint32_t*)&s.front + *(volatile uint32_t*)&s.back > kList) return;
-        // places by the wave's sums, both in one word
-        const uint32_t own = __popc(mine) | __popc(rest) << 16;
-        const u64 sums = wave_scan(own), all = of_lane(sums, 63);
-        uint32_t at = 0;
-        if ((threadIdx.x & 63) == 63) at = atomicAdd(&s.front, (uint32_t)all & 0xffff) | atomicAdd(&s.back, (uint32_t)all >> 16) << 16;
-        at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63);
-        uint32_t f = (at & 0xffff) + (((uint32_t)sums & 0xffff) - __popc(mine));
-        uint32_t b = (at >> 16) + (((uint32_t)sums >> 16) - __popc(rest));
+        // few in a vector: a place at a time
 #pragma unroll
         for (int q = 0; q < R::N; ++q) {
-            const bool front = mine >> q & 1, back = rest >> q & 1;
-            const uint32_t place = front ? f : kList - 1 - b;
-            if ((front || back) && place < kList) s.list[place] = (u64)key_of(x[q]) << 32 | ~(uint32_t)(i + q);
-            f += front;
-            b += back;
+            const u64 entry = (u64)key_of(x[q]) << 32 | ~(uint32_t)(i + q);
+            if (mine >> q & 1) {
+                const uint32_t at = atomicAdd(&s.front, 1u);
+                if (at < kList) s.list[at] = entry;
+            }
+            if (rest >> q & 1) {
+                const uint32_t at = atomicAdd(&s.back, 1u);
+                if (at < kList) s.list[kList - 1 - at] = entry;
+            }
         }
     });
     __syncthreads();
@@ -441,11 +433,26 @@ __device__ inline u64 sum_of_tiles(Shared& s) {
     block_scan(s.mass[2 * threadIdx.x] + s.mass[2 * threadIdx.x + 1], s.parts, all);
     return all;
 }
-// Adds entries [from, to) of the list to the tiles' masses.
+// What is listed: the first `front` of s.list and the last `back`.
+struct Listed {
+    uint32_t front, back;
+    __device__ uint32_t size() const { return front + back; }
+    __device__ uint32_t place(uint32_t i) const { return i < front ? i : kList - 1 - (i - front); }
+};
+// Adds those of them that stay to the tiles' masses.
 template <class R>
-__device__ inline void add_listed(uint32_t from, uint32_t to, const Scale& sc, const Tiles<R>& tiles, Shared& s) {
-    for (uint32_t i = from + threadIdx.x; i < to; i += kThreads)
-        atomicAdd(&s.mass[tiles.of(index_at(i, s))], units(weight_of(value_at(i, s), sc)));
+__device__ inline void add_listed(Listed l, Cut cut, const Scale& sc, const Tiles<R>& tiles, Shared& s) {
+    for (uint32_t i = threadIdx.x; i < l.size(); i += kThreads) {
+        const uint32_t at = l.place(i);
+        const float x = value_at(at, s);
+        if (cut.keeps(x, index_at(at, s))) atomicAdd(&s.mass[tiles.of(index_at(at, s))], units(weight_of(x, sc)));
+    }
+}
+__device__ inline u64 mass_listed(Listed l, const Scale& sc, Shared& s) {
+    u64 own = 0, all;
+    for (uint32_t i = threadIdx.x; i < l.size(); i += kThreads) own += units(weight_of(value_at(l.place(i), s), sc));
+    block_scan(own, s.parts, all);
+    return all;
 }
 
 // The cut digit by digit of the keys, for any logits (many equal, or far below the top): where the sum of counts
@@ -524,12 +531,45 @@ __device__ inline uint32_t listed_mass(uint32_t n, u64 before, u64 want, const S
     const int last = first_bin(at >= want && i0 > 0, at + w0 >= want && i0 < n, at + w0 + w1 >= want && i1 < n, 0, [](int) {}, s);
     return last < 0 ? n : (uint32_t)last + 1;
 }
-// Of the sorted list's first n those that are at least `least`.
-__device__ inline uint32_t listed_above(uint32_t n, float least, Shared& s) {
-    const uint32_t i0 = 2 * threadIdx.x, i1 = i0 + 1;
-    u64 many;
-    block_scan((u64)(i0 < n && value_at(i0, s) >= least) + (u64)(i1 < n && value_at(i1, s) >= least), s.parts, many);
-    return (uint32_t)many;
+// The cut within what is listed, a prefix of the row's order itself, where the sum of counts (masses) from its first
+// on reaches want.  A long list is split by bins first, and only the border's put in order: the listed past it
+// are dropped.
+__device__ inline Cut cut_listed(Listed& l, bool by_mass, u64 want, const Scale& sc, Shared& s) {
+    u64 before = 0, all;
+    if (l.back > 0 || l.front > 512) {
+        const uint32_t i0 = threadIdx.x, i1 = i0 + kThreads, n = l.size();
+        const u64 e0 = i0 < n ? s.list[l.place(i0)] : 0, e1 = i1 < n ? s.list[l.place(i1)] : 0;
+        auto value = [](u64 e) { return value_of((uint32_t)(e >> 32)); };
+        const uint32_t bin0 = i0 < n ? bin_of(value(e0), sc) : kBins, bin1 = i1 < n ? bin_of(value(e1), sc) : kBins;
+        clear(s);
+        if (by_mass) {
+            if (i0 < n) atomicAdd(&s.mass[bin0], units(weight_of(value(e0), sc)));
+            if (i1 < n) atomicAdd(&s.mass[bin1], units(weight_of(value(e1), sc)));
+        } else {
+            if (i0 < n) atomicAdd(&s.mass[bin0], 1ull);
+            if (i1 < n) atomicAdd(&s.mass[bin1], 1ull);
+        }
+        __syncthreads();
+        const u64 v0 = s.mass[2 * threadIdx.x], v1 = s.mass[2 * threadIdx.x + 1];
+        const u64 at = block_scan(v0 + v1, s.parts, all);
+        const uint32_t bin = first_bin(at >= want, at + v0 >= want, at + v0 + v1 >= want, 0,
+                                       [&](int second) { s.found[1] = second ? at + v0 : at; }, s);
+        before = s.found[1];
+        if (threadIdx.x == 0) s.front = s.back = 0;
+        __syncthreads();
+        auto put = [&](u64 e, uint32_t b) {
+            if (b == bin) s.list[atomicAdd(&s.front, 1u)] = e;
+            if (b < bin) s.list[kList - 1 - atomicAdd(&s.back, 1u)] = e;
+        };
+        put(e0, bin0);
+        put(e1, bin1);
+        __syncthreads();
+        l = {s.front, s.back};
+    }
+    sort(l.front, s);
+    const uint32_t last = by_mass ? listed_mass(l.front, before, want, sc, all, s) - 1 : (uint32_t)(want - before) - 1;
+    l.front = last + 1;
+    return {value_at(last, s), index_at(last, s)};
 }
 
 // One row a workgroup.  V: vectors of the row in a thread's registers.
@@ -611,9 +651,9 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(Args a) {
             if (hi >= 0) from = weigh ? least_of(hi, sc) : fmaxf(least_of(hi, sc), least);
             next = WHOLE;
         } else if (stage == COUNT || stage == MASS) {
-            if (!filled) {
-                const u64 own = fill(row, sc, weigh, s);
-                if (weigh) block_scan(own, s.parts, total);
+            if (!filled || (stage == MASS && total == 0)) {
+                const u64 own = fill(row, sc, stage == MASS, s);
+                if (stage == MASS) block_scan(own, s.parts, total);
                 filled = true;
             }
             if (stage == COUNT) {
@@ -688,45 +728,34 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(Args a) {
     }
 
     // the tiles' masses
-    uint32_t n = 0;  // of the list's front that stay
+    Listed l{stage == REST ? 0 : s.front, stage == BORDER && certain ? s.back : 0};
     if (stage == WHOLE) {
-        sort(s.front, s);
-        n = s.front;
-        if ((u64)top_k < n) n = (uint32_t)top_k;
-        if (weigh) {
-            u64 all;
-            listed_mass(n, 0, (u64)-1, sc, all, s);
-            n = listed_mass(n, 0, least_mass(top_p, all), sc, all, s);
-        }
+        if ((u64)top_k <= l.front) cut = cut_listed(l, false, (u64)top_k, sc, s);
+        if (weigh) cut = cut_listed(l, true, least_mass(top_p, mass_listed(l, sc, s)), sc, s);
+        if (least > cut.edge) cut = at_least;
     }
     if (stage == REST && cut.last >= 0) {
         weigh_tiles<true>(row, sc, tiles, cut, s);
     } else if (stage == REST || (stage == BORDER && !certain)) {
         if (stage == BORDER) {
-            sort(s.front, s);
+            sort(l.front, s);
             cut = {value_at(0, s), -1};
         }
         weigh_tiles<false>(row, sc, tiles, cut, s);
-    } else {
-        if (stage == BORDER) sort(s.front, s);
-        clear(s);
-        if (stage == BORDER) add_listed(kList - s.back, kList, sc, tiles, s);
-        if (stage == LISTED) n = s.front;
-        __syncthreads();
     }
     if (stage == BORDER) {
+        if (certain) sort(l.front, s);
         u64 all;
-        n = listed_mass(s.front, sum_of_tiles(s), want, sc, all, s);
+        const u64 before = certain ? mass_listed(Listed{0, l.back}, sc, s) : sum_of_tiles(s);
+        l.front = listed_mass(l.front, before, want, sc, all, s);
+        cut = {value_at(l.front - 1, s), index_at(l.front - 1, s)};
+        if (least > cut.edge) cut = at_least;
     }
-    if (stage == BORDER || stage == WHOLE) {
-        cut = {value_at(n - 1, s), index_at(n - 1, s)};
-        if (least > cut.edge) {
-            n = listed_above(n, least, s);
-            cut = at_least;
-        }
+    if (stage != REST) {
+        if (stage != BORDER || certain) clear(s);
+        add_listed(l, cut, sc, tiles, s);
+        __syncthreads();
     }
-    add_listed(0, n, sc, tiles, s);
-    __syncthreads();
 
     // the tile in which the sum passes u's share, and the place in it
     const int t0 = 2 * threadIdx.x;

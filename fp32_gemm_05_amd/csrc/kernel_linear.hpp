@@ -148,15 +148,23 @@ struct Finish {
     long ld;
 };
 
+// The bias of 4 N consecutive columns, `left` of which exist; zeros without one.
+template <typename T, int N>
+__device__ inline void load_bias(const Finish& f, int col, int left, f32x4 (&bias)[N]) {
+#pragma unroll
+    for (int g = 0; g < N; ++g) bias[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (f.bias && left > 0) load((const T*)f.bias + col, left, bias);
+}
 // 4 N consecutive columns of a row, `left` of which exist.  FORWARD: not, the sums are stored as they are.
 template <bool FORWARD, typename T, int N>
-__device__ inline void finish(const Finish& f, long row, int col, int left, f32x4 (&v)[N]) {
+__device__ inline void finish(const Finish& f, const f32x4 (&bias)[N], long row, int col, int left, f32x4 (&v)[N]) {
     auto each = [&](auto body) {
 #pragma unroll
         for (int g = 0; g < N; ++g) body(v[g], col + 4 * g, left - 4 * g);
     };
     if constexpr (FORWARD) {
-        if (f.bias) add<T>(f.bias, 0, 0, col, left, v);
+#pragma unroll
+        for (int g = 0; g < N; ++g) v[g] += bias[g];
         if (f.z) leave<T>(f.z, row, f.ld_z, col, left, v);
         by_act(f.act, [&](auto which) {
             each([&](f32x4& x, int, int) {
@@ -205,6 +213,8 @@ __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
     f32x4* const own = (f32x4*)lds + wave * 32 * QUADS;
     const int m = m0 + (wave / T::WAVES_N) * WM + lane % LANES * 4 * N4, q0 = lane % LANES * N4;
     const int n_wave = n0 + (wave % T::WAVES_N) * T::kWN;
+    f32x4 bias[N4];
+    if constexpr (FORWARD) load_bias<E>(a.f, m, a.f.m - m, bias);
     wait_vm_lgkm0<0>();
     dl_barrier();  // every wave has read its last slab
 #pragma unroll
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
                 own[l * QUADS + ((8 * i + 2 * g + h) ^ (l & (QUADS - 1)))] =
                     f32x4{t.acc[i][j][4 * g], t.acc[i][j][4 * g + 1], t.acc[i][j][4 * g + 2], t.acc[i][j][4 * g + 3]};
         wait_vm_lgkm0<0>();  // a wave's own writes before its reads; it shares them with no other wave
-#pragma unroll 1
+#pragma unroll 2
         for (int r = lane / LANES; r < 32; r += ROWS) {
             const int n = n_wave + j * 32 + r;
             f32x4 v[N4];
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
 #pragma unroll
                 for (int q = 0; q < N4; ++q) *(f32x4*)(out + 4 * q) = v[q];
             } else if (n < a.f.n && m < a.f.m) {
-                finish<FORWARD, E>(a.f, n, m, a.f.m - m, v);
+                finish<FORWARD, E>(a.f, bias, n, m, a.f.m - m, v);
             }
         }
         wait_vm_lgkm0<0>();
@@ -242,24 +252,37 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const float* part, int 
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int z = 0; z < splits; ++z) v += *(const f32x4*)(part + (z * rows + n) * pitch + m);
-    f32x4 one[1] = {v};
-    finish<true, T>(f, n, m, f.m - m, one);
+    f32x4 one[1] = {v}, bias[1];
+    load_bias<T>(f, m, f.m - m, bias);
+    finish<true, T>(f, bias, n, m, f.m - m, one);
 }
 
 // Rows of an operand that cannot be read in place, copied to rows of whole slabs, 16-byte aligned, zeros at
-// their ends.  One workgroup a row.
+// their ends.  Four rows a workgroup.
+struct PackArgs {
+    const void* in;
+    long ld;
+    int rows, cols;  // rows 0: read in place
+    void* out;
+    long pitch;
+    __host__ __device__ int blocks() const { return (rows + 3) / 4; }
+};
 template <typename T>
-__global__ void __launch_bounds__(256) linear_pack_kernel(const T* in, long ld, int cols, T* out, long pitch) {
+__device__ inline void pack(const PackArgs& a, int block) {
     constexpr int V = 16 / sizeof(T);
-    const T* src = in + (size_t)blockIdx.x * ld;
-    T* dst = out + (size_t)blockIdx.x * pitch;
-    for (int c = threadIdx.x * V; c < pitch; c += 256 * V) {
+    const int row = block * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (row >= a.rows) return;
+    const T* src = (const T*)a.in + (size_t)row * a.ld;
+    T* dst = (T*)a.out + (size_t)row * a.pitch;
+#pragma unroll 4
+    for (int c = lane * V; c < a.pitch; c += 64 * V) {
         T v[V] = {};
-        if (c + V <= cols)
+        if (c + V <= a.cols)
             __builtin_memcpy(v, src + c, 16);
         else
+#pragma unroll
             for (int i = 0; i < V; ++i)
-                if (c + i < cols) v[i] = src[c + i];
+                if (c + i < a.cols) v[i] = src[c + i];
         *(u32x4*)(dst + c) = *(const u32x4*)v;
     }
 }
@@ -268,7 +291,7 @@ struct SlopeArgs {
     const void *dy, *z;  // z null: no activation
     long ld_dy, ld_z;
     int rows, cols, act;
-    int per;             // rows of a workgroup
+    int per, groups_x, groups_y;  // rows of a workgroup; workgroups along columns and rows, 0: nothing to do
     void* dz;            // null: dY is read in place by the products, only its sums are wanted
     long pitch;          // whole 16 bytes
     float* sums;         // [workgroup of rows][pitch], null: not wanted
@@ -277,36 +300,34 @@ struct SlopeArgs {
 // dZ = dY act'(Z), in the operands' type for the products, and its column sums over `per` rows, of
 // the values before they are rounded.
 template <typename T>
-__global__ void __launch_bounds__(256) linear_slope_kernel(SlopeArgs a) {
-    constexpr int V = 16 / sizeof(T);
+__device__ inline void slopes(const SlopeArgs& a, int block) {
+    constexpr int V = 16 / sizeof(T), U = 4;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int c = (blockIdx.x * 64 + lane) * V, left = a.cols - c;
-    const int r0 = blockIdx.y * a.per, r1 = imin(r0 + a.per, a.rows);
+    const int c = (block % a.groups_x * 64 + lane) * V, left = a.cols - c, by = block / a.groups_x;
+    const int r0 = by * a.per, r1 = imin(r0 + a.per, a.rows);
     float sum[V] = {};
     if (c < a.pitch)
         by_act(a.z ? a.act : NONE, [&](auto which) {
             constexpr int ACT = decltype(which)::value;
-#pragma unroll 2
-            for (int r = r0 + wave; r < r1; r += 4) {
-                f32x4 d[V / 4];
+            for (int r = r0 + wave; r < r1; r += 4 * U) {
+                f32x4 d[U][V / 4], z[U][V / 4];
 #pragma unroll
-                for (int q = 0; q < V / 4; ++q) {
-                    d[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    const int n = left - 4 * q;
-                    if (n > 0) d[q] = load4((const T*)a.dy + r * a.ld_dy + c + 4 * q, n);
-                    if (ACT != NONE && n > 0) {
-                        const f32x4 z = load4((const T*)a.z + r * a.ld_z + c + 4 * q, n);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) d[q][i] = i < n ? d[q][i] * slope<ACT>(z[i]) : 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[4 * q + i] += d[q][i];
+                for (int u = 0; u < U; ++u) {
+                    const int n = r + 4 * u < r1 ? left : 0;
+                    load((const T*)a.dy + (r + 4 * u) * a.ld_dy + c, n, d[u]);
+                    if (ACT != NONE) load((const T*)a.z + (r + 4 * u) * a.ld_z + c, n, z[u]);
                 }
-                if (a.dz) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
                     T v[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[i] = (T)d[i / 4][i % 4];
-                    *(u32x4*)((T*)a.dz + r * a.pitch + c) = *(const u32x4*)v;
+                    for (int i = 0; i < V; ++i) {
+                        float x = d[u][i / 4][i % 4];
+                        if (ACT != NONE) x = r + 4 * u < r1 && i < left ? x * slope<ACT>(z[u][i / 4][i % 4]) : 0.f;
+                        sum[i] += x;
+                        v[i] = (T)x;
+                    }
+                    if (a.dz && r + 4 * u < r1) *(u32x4*)((T*)a.dz + (r + 4 * u) * a.pitch + c) = *(const u32x4*)v;
                 }
             }
         });
@@ -318,7 +339,22 @@ __global__ void __launch_bounds__(256) linear_slope_kernel(SlopeArgs a) {
     if (wave > 0 || c >= a.pitch) return;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        a.sums[(size_t)blockIdx.y * a.pitch + c + i] = all[0][lane][i] + all[1][lane][i] + all[2][lane][i] + all[3][lane][i];
+        a.sums[(size_t)by * a.pitch + c + i] = all[0][lane][i] + all[1][lane][i] + all[2][lane][i] + all[3][lane][i];
+}
+
+// All that reads a call's operands alone, in one launch.
+struct PrepareArgs {
+    PackArgs w, x;
+    SlopeArgs slope;
+    __host__ __device__ int slopes() const { return slope.groups_x * slope.groups_y; }
+};
+template <typename T>
+__global__ void __launch_bounds__(256) linear_prepare_kernel(PrepareArgs a) {
+    int b = blockIdx.x;
+    if (b < a.slopes()) return slopes<T>(a.slope, b);
+    b -= a.slopes();
+    if (b < a.w.blocks()) return pack<T>(a.w, b);
+    pack<T>(a.x, b - a.w.blocks());
 }
 
 // dbias from the partial sums of `parts` workgroups: 64 columns a workgroup, 16 parts at a time.
@@ -328,6 +364,7 @@ __global__ void __launch_bounds__(1024) linear_bias_kernel(const float* sums, in
     const int x = threadIdx.x & 63, y = threadIdx.x >> 6, c = blockIdx.x * 64 + x;
     float s = 0.f;
     if (c < cols)
+#pragma unroll 8
         for (int p = y; p < parts; p += 16) s += sums[(size_t)p * pitch + c];
     all[y][x] = s;
     __syncthreads();
@@ -429,8 +466,9 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
 #pragma unroll
     for (int m = 0; m < MR; ++m) {
         const int v = r0 + 16 * m + 4 * g;
-        f32x4 one[1] = {z[m]};
-        if (v < a.outs) finish<true, T>(a.f, n, v, a.outs - v, one);
+        f32x4 one[1] = {z[m]}, bias[1];
+        load_bias<T>(a.f, v, a.outs - v, bias);
+        if (v < a.outs) finish<true, T>(a.f, bias, n, v, a.outs - v, one);
     }
 }
 

@@ -167,13 +167,16 @@ bool in_place(const void* p, long ld, long cols, long size) {
     return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0 && cols * size % 16 == 0 && ld * size < kMaxPitch;
 }
 
-template <typename T>
-Operand operand(const Call& c, const void* p, long ld, int rows, int cols, char* packed, long pitch) {
-    constexpr long size = sizeof(T);
-    if (in_place(p, ld, cols, size))
-        return {(const char*)p, (uint32_t)(ld * size), (uint32_t)(cols * size), rows};
-    linear_pack_kernel<T><<<rows, 256, 0, c.stream>>>((const T*)p, ld, cols, (T*)packed, pitch / size);
+// The operand as the products read it, and what is to be packed for it, if anything.
+Operand operand(const void* p, long ld, int rows, int cols, long size, char* packed, long pitch, PackArgs& pack) {
+    if (in_place(p, ld, cols, size)) return {(const char*)p, (uint32_t)(ld * size), (uint32_t)(cols * size), rows};
+    pack = {p, ld, rows, cols, packed, pitch / size};
     return {packed, (uint32_t)pitch, (uint32_t)pitch, rows};
+}
+template <typename T>
+void prepare(const PrepareArgs& a, hipStream_t stream) {
+    const int blocks = a.slopes() + a.w.blocks() + a.x.blocks();
+    if (blocks > 0) linear_prepare_kernel<T><<<blocks, 256, 0, stream>>>(a);
 }
 
 template <int P, class F>
@@ -203,8 +206,10 @@ void product(const Call& c, const Plan& p, const Operand& a, const Operand& b, l
 template <typename T, int P>
 int forward(const Call& c) {
     const Layout l = layout(P, false, c.T, c.N, c.H);
-    const Operand x = operand<T>(c, c.X, c.ldx, c.T, c.H, c.work + l.x, l.hp);
-    const Operand w = operand<T>(c, c.W, c.ldw, c.N, c.H, c.work + l.w, l.hp);
+    PrepareArgs p{};
+    const Operand x = operand(c.X, c.ldx, c.T, c.H, sizeof(T), c.work + l.x, l.hp, p.x);
+    const Operand w = operand(c.W, c.ldw, c.N, c.H, sizeof(T), c.work + l.w, l.hp, p.w);
+    prepare<T>(p, c.stream);
     char* const part = c.work + l.part;
     if (x.row_bytes % 128 == 0 && w.row_bytes % 128 == 0)
         product<T, P, K_ROW, K_ROW, false>(c, l.z, w, x, c.N, c.T, c.H, part, c.forward());
@@ -220,27 +225,28 @@ int gradient(const Call& c) {
     const bool slope = c.activation != NONE, copy = slope || !in_place(c.dY, c.lddy, c.N, size);
     Operand d{(const char*)c.dY, (uint32_t)(c.lddy * size), (uint32_t)(c.N * size), c.T};
     if (copy) d = {c.work + l.dz, (uint32_t)l.np, (uint32_t)l.np, c.T};
-    if (copy || c.dbias) {
-        const SlopeArgs a{c.dY, slope ? c.Z : nullptr, c.lddy, c.ldz, c.T, c.N, c.activation, l.per,
-                          copy ? c.work + l.dz : nullptr, l.np / size, c.dbias ? (float*)(c.work + l.sums) : nullptr};
-        linear_slope_kernel<T><<<dim3((unsigned)(up(l.np, 1024) / 1024), l.row_groups), 256, 0, c.stream>>>(a);
-    }
+    PrepareArgs p{};
+    Operand w{}, x{};
+    if (c.dX) w = operand(c.W, c.ldw, c.N, c.H, size, c.work + l.w, l.hp, p.w);
+    if (c.dW) x = operand(c.X, c.ldx, c.T, c.H, size, c.work + l.x, l.hp, p.x);
+    if (copy || c.dbias)
+        p.slope = {c.dY, slope ? c.Z : nullptr, c.lddy, c.ldz, c.T, c.N, c.activation, l.per,
+                   (int)(up(l.np, 1024) / 1024), l.row_groups, copy ? c.work + l.dz : nullptr, l.np / size,
+                   c.dbias ? (float*)(c.work + l.sums) : nullptr};
+    prepare<T>(p, c.stream);
     if (c.dbias)
         linear_bias_kernel<T><<<(unsigned)(up(c.N, 64) / 64), 1024, 0, c.stream>>>(
             (const float*)(c.work + l.sums), l.row_groups, l.np / size, c.N, (T*)c.dbias);
     char* const part = c.work + l.part;
     if (c.dX) {
-        const Operand w = operand<T>(c, c.W, c.ldw, c.N, c.H, c.work + l.w, l.hp);
         const Finish f = Call::plain(c.T, c.H, c.dX, c.lddx);
         if (d.row_bytes % 128 == 0)
             product<T, P, K_COL, K_ROW, true>(c, l.dx, w, d, c.H, c.T, c.N, part, f);
         else
             product<T, P, K_COL, K_ENDS, true>(c, l.dx, w, d, c.H, c.T, c.N, part, f);
     }
-    if (c.dW) {
-        const Operand x = operand<T>(c, c.X, c.ldx, c.T, c.H, c.work + l.x, l.hp);
+    if (c.dW)
         product<T, P, K_COL, K_COL, true>(c, l.dw, x, d, c.H, c.N, c.T, part, Call::plain(c.N, c.H, c.dW, c.lddw));
-    }
     return (int)hipGetLastError();
 }
 

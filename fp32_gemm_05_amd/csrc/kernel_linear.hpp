@@ -385,11 +385,14 @@ struct FewArgs {
     int tokens, outs, hidden;
     const void *x, *w;
     long ldx, ldw;
+    int blocks, splits;  // workgroups along the output features; parts of the hidden size
+    float* part;         // splits > 1: [split][16 NB][pitch], summed by linear_sum_kernel
+    long pitch;
     Finish f;
 };
 
-// Z of 16 MR output features and all tokens.  The NW waves of a workgroup take every NW-th group of U steps
-// of the hidden size each and add up in LDS.
+// Z of 16 MR output features and all tokens, or a part of the hidden size of it where the features alone do not fill
+// the chip.  The NW waves of a workgroup take every NW-th group of U steps of the hidden size each and add up in LDS.
 template <class C, int NB, int MR, int NW>
 __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
     typedef typename C::T T;
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
     __shared__ f32x4 sums[NW][NB][64];
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
     const int wave = (int)uniform_u32(threadIdx.x >> 6);
-    const int r0 = blockIdx.x * 16 * MR;
+    const int split = blockIdx.x / a.blocks, r0 = (blockIdx.x - split * a.blocks) * 16 * MR;
     const T *w[MR], *x[NB];
 #pragma unroll
     for (int m = 0; m < MR; ++m) w[m] = (const T*)a.w + (size_t)imin(r0 + 16 * m + l, a.outs - 1) * a.ldw + g * C::E;
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
         }
     };
     const int full = a.hidden / C::STEP, groups = full / U;
-    for (int q = wave; q < groups; q += NW) {
+    const int first = (int)((long)groups * split / a.splits), last = (int)((long)groups * (split + 1) / a.splits);
+    for (int q = first + wave; q < last; q += NW) {
         Raw vw[U][MR], vx[U][NB];
 #pragma unroll
         for (int m = 0; m < MR; ++m)
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) multiply(vw[u], vx[u]);
     }
-    const int steps = (a.hidden + C::STEP - 1) / C::STEP;
+    const int steps = split + 1 == a.splits ? (a.hidden + C::STEP - 1) / C::STEP : 0;  // the last part's
     for (int s = groups * U + wave; s < steps; s += NW) {
         const int n = a.hidden - s * C::STEP - g * C::E;  // elements of this lane's chunk, maybe none
         Raw vw[MR], vx[NB];
@@ -466,6 +470,10 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
 #pragma unroll
     for (int m = 0; m < MR; ++m) {
         const int v = r0 + 16 * m + 4 * g;
+        if (a.splits > 1) {
+            *(f32x4*)(a.part + ((long)split * 16 * NB + n) * a.pitch + v) = z[m];
+            continue;
+        }
         f32x4 one[1] = {z[m]}, bias[1];
         load_bias<T>(a.f, v, a.outs - v, bias);
         if (v < a.outs) finish<true, T>(a.f, bias, n, v, a.outs - v, one);

@@ -24,8 +24,8 @@
  *
  * Products: bf16 operands on the bf16 matrix instructions.  fp32 operands on the fp32 ones, with infinities, NaN and
  * values of any scale as in any fp32 sum; of 17 to 64 tokens as three bf16 parts each, 24 bits, of values from
- * 2^-110 to 2^127, where an infinity may come out as NaN.  A row of X, dY or residual reaches its own row of Y and dX
- * alone.
+ * 2^-110 to 2^127, where an infinity may come out as NaN, as it may in a gradient of up to 64 tokens.  A row of X, dY or
+ * residual reaches its own row of Y and dX alone.
  *
  * Memory and streams: device pointers owned by the caller, work enqueued on `stream`, no wait, no allocation, no
  * memset; calls may be captured into a HIP graph.  `work` is scratch memory of at least linear_workspace(...) bytes,

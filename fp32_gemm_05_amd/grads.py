@@ -34,57 +34,80 @@ _library = Entries(_NAMES, _KINDS, {"grad_workspace": ctypes.c_longlong})
 
 def _matrix(t, flip, name):
     """Rows, columns and row stride of a matrix, or of its transpose."""
-    if t.dim() == 2:
-        (rows, cols), (ld, unit) = t.shape, t.stride()
-        if flip:
-            rows, cols, ld, unit = cols, rows, unit, ld
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 2:
+        (rows, cols), (ld, unit) = (shape, strides) if not flip else (shape[::-1], strides[::-1])
         if rows <= 1:
             ld = cols
-        if (cols <= 1 or unit == 1) and ld >= cols:
+        if (unit == 1 or cols <= 1) and ld >= cols:
             if rows > _MOST or ld > _MOST:
                 raise ValueError(f"{name} has {rows} rows with stride {ld}: neither may be above {_MOST}")
             return rows, cols, ld
-    raise ValueError(f"{name} with shape {tuple(t.shape)} and strides {t.stride()} is neither contiguous nor a matrix "
+    raise ValueError(f"{name} with shape {tuple(shape)} and strides {strides} is neither contiguous nor a matrix "
                      f"with unit stride along its rows or columns (those of out as its tensor's); pass a contiguous copy")
 
 
 def _column_major(t):
-    return t.dim() == 2 and t.stride(0) == 1 and t.shape[0] > 1 and t.stride(1) >= t.shape[0]
+    strides = t.stride()
+    return len(strides) == 2 and strides[0] == 1 and t.shape[0] > 1 and strides[1] >= t.shape[0]
+
+
+def _kinds(tensors, name):
+    """The types, of tensors of one device."""
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}] must be a torch tensor")
+    try:
+        kinds = [_TYPES[t.dtype] for t in tensors]
+    except KeyError:
+        i = next(i for i, t in enumerate(tensors) if t.dtype not in _TYPES)
+        raise TypeError(f"{name}[{i}] must be float32 or bfloat16, not {tensors[i].dtype}") from None
+    places = [t.get_device() for t in tensors]
+    first = places[0]
+    if first < 0 or places.count(first) != len(places):
+        for i, t in enumerate(tensors):
+            _require_device(t, f"{name}[{i}]")
+            if t.get_device() != first:
+                raise ValueError(f"{name}[{i}] is on {t.device}, {name}[0] on {tensors[0].device}")
+    return kinds
 
 
 def _table(tensors, out):
-    """The tensors' array for the library; a step has some hundreds of them, so each attribute is read once."""
-    entries = array.array("q")
-    add = entries.extend
-    place = None
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"tensors[{i}] must be a torch tensor")
-        kind = _TYPES.get(t.dtype)
-        if kind is None:
-            raise TypeError(f"tensors[{i}] must be float32 or bfloat16, not {t.dtype}")
-        at = t.get_device()
-        if at != place:
-            _require_device(t, f"tensors[{i}]")
-            if place is not None:
-                raise ValueError(f"tensors[{i}] is on {t.device}, tensors[0] on {tensors[0].device}")
-            place = at
-        o = t
-        if out is not None:
-            o = out[i]
-            if not isinstance(o, torch.Tensor) or o.dtype != t.dtype:
-                raise TypeError(f"out[{i}] must be a {str(t.dtype).replace('torch.', '')} tensor")
-            if o.shape != t.shape:
-                raise ValueError(f"out[{i}] has shape {tuple(o.shape)}, tensors[{i}] {tuple(t.shape)}")
-            if o.get_device() != place:
-                raise ValueError(f"out[{i}] is on {o.device}, tensors[0] on {tensors[0].device}")
-        if t.is_contiguous() and (o is t or o.is_contiguous()):
-            n = t.numel()
-            add((t.data_ptr(), o.data_ptr(), 1, n, n, n, kind))
+    """The tensors' array for the library.  A step has some hundreds of them, and the work on the device takes about
+    half a microsecond each: their attributes are read column by column."""
+    n, kinds = len(tensors), _kinds(tensors, "tensors")
+    outs = tensors if out is None else out
+    if out is not None:
+        if _kinds(out, "out") != kinds:
+            i = next(i for i in range(n) if out[i].dtype != tensors[i].dtype)
+            raise TypeError(f"out[{i}] must be a {str(tensors[i].dtype).replace('torch.', '')} tensor")
+        if out[0].get_device() != tensors[0].get_device():
+            raise ValueError(f"out[0] is on {out[0].device}, tensors[0] on {tensors[0].device}")
+        if [t.shape for t in out] != [t.shape for t in tensors]:
+            i = next(i for i in range(n) if out[i].shape != tensors[i].shape)
+            raise ValueError(f"out[{i}] has shape {tuple(out[i].shape)}, tensors[{i}] {tuple(tensors[i].shape)}")
+    sizes = array.array("q", [t.numel() for t in tensors])
+    entries = array.array("q", bytes(56 * n))
+    entries[0::7] = array.array("q", [t.data_ptr() for t in tensors])
+    entries[1::7] = entries[0::7] if out is None else array.array("q", [t.data_ptr() for t in out])
+    entries[2::7] = array.array("q", [1]) * n
+    for column in (3, 4, 5):
+        entries[column::7] = sizes
+    entries[6::7] = array.array("q", kinds)
+    whole = [t.is_contiguous() for t in tensors]
+    whole_out = whole if out is None else [t.is_contiguous() for t in out]
+    for i in range(n):
+        if whole[i] and whole_out[i]:
+            continue
+        t, o = tensors[i], outs[i]
+        flip = _column_major(o if whole[i] else t)
+        rows, cols, ld = _matrix(t, flip, f"tensors[{i}]")
+        at = 7 * i
+        entries[at + 2], entries[at + 3], entries[at + 4] = rows, cols, ld
+        if o is t:
+            entries[at + 5] = ld
         else:
-            flip = _column_major(t if not t.is_contiguous() else o)
-            rows, cols, ld = _matrix(t, flip, f"tensors[{i}]")
-            add((t.data_ptr(), o.data_ptr(), rows, cols, ld, _matrix(o, flip, f"out[{i}]")[2], kind))
+            entries[at + 5] = cols if whole_out[i] and not flip else _matrix(o, flip, f"out[{i}]")[2]
     return entries
 
 

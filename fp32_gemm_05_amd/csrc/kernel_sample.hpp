@@ -27,6 +27,7 @@ __device__ inline float uniform(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x)));
 }
 __device__ inline int uniform(int x) {
+    x = __builtin_amdgcn_readfirstlane(x);
     asm volatile("" : "+s"(x));
     return x;
 }
@@ -410,9 +411,9 @@ struct Tiles {
     }
     __device__ int of(int i) const { return i / BLOCK >> k; }
 };
-// Each tile's mass that stays, in s.mass; EQUAL: some of those equal to the edge do.
+// Each tile's mass that stays, in s.mass; EQUAL: some of those equal to the edge do.  first: the index of row's first.
 template <bool EQUAL, class R>
-__device__ inline void weigh_tiles(const R& row, const Scale& sc, const Tiles<R>& tiles, Cut cut, Shared& s) {
+__device__ inline void weigh_tiles(const R& row, const Scale& sc, const Tiles<R>& tiles, Cut cut, Shared& s, int first = 0) {
     clear(s);
     row.each([&](int i, const float (&x)[R::N]) {
         float most = x[0];
@@ -424,7 +425,7 @@ __device__ inline void weigh_tiles(const R& row, const Scale& sc, const Tiles<R>
         for (int q = 0; q < R::N; ++q)
             sum += (double)((EQUAL ? cut.keeps(x[q], i + q) : x[q] > cut.edge) ? weight_of(x[q], sc) : 0.f);
         const u64 whole = wave_scan(units(sum));
-        if ((threadIdx.x & 63) == 63 && whole > 0) atomicAdd(&s.mass[tiles.of(i)], whole);
+        if ((threadIdx.x & 63) == 63 && whole > 0) atomicAdd(&s.mass[tiles.of(first + i)], whole);
     });
     __syncthreads();
 }
@@ -572,62 +573,121 @@ __device__ inline Cut cut_listed(Listed& l, bool by_mass, u64 want, const Scale&
     return {value_at(last, s), index_at(last, s)};
 }
 
-// One row a workgroup.  V: vectors of the row in a thread's registers.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) sample_row_kernel(Args a) {
-    typedef Row<T, V> R;
-    constexpr int N = R::N;
-    __shared__ Shared s;
-    const int r = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, size = a.vocab;
-    R row;
-    row.init((const T*)a.logits + (size_t)r * a.ld, size);
-    const float temperature = a.temperatures ? a.temperatures[r] : a.temperature;
-    const float top_p = a.top_ps ? a.top_ps[r] : a.top_p, min_p = a.min_ps ? a.min_ps[r] : a.min_p, u = a.u[r];
-    const long long top_k = a.top_ks ? a.top_ks[r] : a.top_k;
+// A row's settings.
+struct Settings {
+    float temperature, top_p, min_p, u;
+    long long top_k;
+    __device__ Settings(const Args& a, int r)
+        : temperature(a.temperatures ? a.temperatures[r] : a.temperature), top_p(a.top_ps ? a.top_ps[r] : a.top_p),
+          min_p(a.min_ps ? a.min_ps[r] : a.min_p), u(a.u[r]), top_k(a.top_ks ? a.top_ks[r] : a.top_k) {}
+    __device__ bool valid(float top) const {
+        return __builtin_isfinite(top) && temperature >= 0.f && temperature < INFINITY && u == u && top_p == top_p && min_p == min_p;
+    }
+    __device__ bool first_alone() const { return temperature == 0.f || min_p > 1.f; }
+    __device__ bool weigh() const { return top_p < 1.f; }
+    __device__ bool ranked(int size) const { return top_k > 0 && top_k < size; }
+    static __device__ float lowest() { return value_of(key_of(-INFINITY) + 1); }  // of the finite values
+    // The least logit of at least min_p times the largest one's probability.
+    __device__ float least(float top) const {
+        if (!(min_p > 0.f)) return lowest();
+        const double x = (double)top + log((double)min_p) * (double)temperature;
+        if (!(x > (double)lowest())) return lowest();
+        const float y = (float)x;
+        return (double)y < x ? value_of(key_of(y) + 1) : y;
+    }
+};
 
-    float top = -INFINITY;  // NaN where there is one
-    row.each([&](int, const float (&x)[N]) {
+// The largest value, NaN where there is one; of a thread's own, and in every thread of the row's part.
+template <class R>
+__device__ inline float top_of(const R& row, float& own, Shared& s) {
+    own = -INFINITY;
+    row.each([&](int, const float (&x)[R::N]) {
 #pragma unroll
-        for (int q = 0; q < N; ++q) top = __builtin_elementwise_maximum(top, x[q]);
+        for (int q = 0; q < R::N; ++q) own = __builtin_elementwise_maximum(own, x[q]);
     });
-    const float own_top = top;
+    float top = own;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = __builtin_elementwise_maximum(top, __shfl_xor(top, o));
-    if (lane == 0) s.tops[wave] = top;
-    if (threadIdx.x == 0) s.token = 0xffffffffu;
+    if ((threadIdx.x & 63) == 0) s.tops[threadIdx.x >> 6] = top;
     __syncthreads();
     for (int w = 0; w < kWaves; ++w) top = __builtin_elementwise_maximum(top, s.tops[w]);
-    top = uniform(top);
-    if (!__builtin_isfinite(top) || !(temperature >= 0.f && temperature < INFINITY) || u != u || top_p != top_p || min_p != min_p) {
+    return uniform(top);
+}
+// The lowest index of a value, in s.token.
+template <class R>
+__device__ inline void first_of(const R& row, float value, Shared& s) {
+    uint32_t first = 0xffffffffu;
+    if (threadIdx.x == 0) s.token = first;
+    row.each([&](int i, const float (&x)[R::N]) {
+#pragma unroll
+        for (int q = R::N - 1; q >= 0; --q)
+            if (x[q] == value && (uint32_t)(i + q) < first) first = i + q;
+    });
+    __syncthreads();
+    if (first != 0xffffffffu) atomicMin(&s.token, first);
+    __syncthreads();
+}
+
+// The token by the tiles' masses in s.mass: the tile in which the sum passes u's share, and the place in it.
+template <typename T, class R>
+__device__ inline void pick(const T* row, const Tiles<R>& tiles, const Scale& sc, Cut cut, float u, long long* token, Shared& s) {
+    const int t0 = 2 * threadIdx.x;
+    const u64 m0 = s.mass[t0], m1 = s.mass[t0 + 1];
+    u64 all;
+    const u64 at = block_scan(m0 + m1, s.parts, all);
+    double share = (double)u * (double)all;
+    share = share > 0. ? share : 0.;
+    u64 target = share < (double)all ? (u64)share : all - 1;
+    target = target < all ? target : all - 1;
+    const int tile = first_bin(at > target, at + m0 > target, at + m0 + m1 > target, 0,
+                               [&](int second) { s.found[1] = second ? at + m0 : at; }, s);
+    const int step = Tiles<R>::BLOCK << tiles.k, from = tile * step, to = from + step < tiles.size ? from + step : tiles.size;
+    const int per = (to - from + kThreads - 1) / kThreads, mine = from + threadIdx.x * per, end = mine + per < to ? mine + per : to;
+    const u64 done = s.found[1];
+    auto mass = [&](int i) -> u64 {
+        const float x = (float)row[i];
+        return cut.keeps(x, i) ? units(weight_of(x, sc)) : 0;
+    };
+    u64 own = 0;
+    for (int i = mine; i < end; ++i) own += mass(i);
+    u64 sum = done + block_scan(own, s.parts, all);
+    if (sum <= target && target < sum + own)
+        for (int i = mine; i < end; ++i) {
+            sum += mass(i);
+            if (sum > target) {
+                *token = i;
+                return;
+            }
+        }
+}
+
+// One row.  V: vectors of the row in a thread's registers.
+template <typename T, int V>
+__device__ inline void draw_row(const Args& a, int r, Shared& s) {
+    typedef Row<T, V> R;
+    constexpr int N = R::N;
+    const int size = a.vocab;
+    R row;
+    row.init((const T*)a.logits + (size_t)r * a.ld, size);
+    const Settings set(a, r);
+    const float top_p = set.top_p;
+    const long long top_k = set.top_k;
+    float own_top;
+    const float top = top_of(row, own_top, s);
+    if (!set.valid(top)) {
         if (threadIdx.x == 0) a.token[r] = -1;
         return;
     }
-    if (temperature == 0.f || min_p > 1.f) {  // the first alone
-        uint32_t first = 0xffffffffu;
-        row.each([&](int i, const float (&x)[N]) {
-#pragma unroll
-            for (int q = N - 1; q >= 0; --q)
-                if (x[q] == top && (uint32_t)(i + q) < first) first = i + q;
-        });
-        if (first != 0xffffffffu) atomicMin(&s.token, first);
-        __syncthreads();
+    if (set.first_alone()) {
+        first_of(row, top, s);
         if (threadIdx.x == 0) a.token[r] = s.token;
         return;
     }
-    const Scale sc(top, temperature);
+    const Scale sc(top, set.temperature);
     const Tiles<R> tiles(size);
-    const float lowest = value_of(key_of(-INFINITY) + 1);  // of the finite values
-    // the least logit of at least min_p times the largest one's probability
-    float least = lowest;
-    if (min_p > 0.f) {
-        const double x = (double)top + log((double)min_p) * (double)temperature;
-        if (x > (double)lowest) {
-            least = (float)x;
-            if ((double)least < x) least = value_of(key_of(least) + 1);
-        }
-    }
+    const float lowest = Settings::lowest(), least = set.least(top);
     const Cut at_least{below(key_of(least)), -1};
-    const bool weigh = top_p < 1.f, ranked = top_k > 0 && top_k < size;
+    const bool weigh = set.weigh(), ranked = set.ranked(size);
 
     // From one stage to the next until what stays is known: all of it as `cut`, or up to a border in a list.
     enum { QUICK, COUNT, MASS, REST, WHOLE, BORDER, LISTED };
@@ -757,35 +817,216 @@ __global__ void __launch_bounds__(kThreads) sample_row_kernel(Args a) {
         __syncthreads();
     }
 
-    // the tile in which the sum passes u's share, and the place in it
-    const int t0 = 2 * threadIdx.x;
-    const u64 m0 = s.mass[t0], m1 = s.mass[t0 + 1];
+    pick(row.row, tiles, sc, cut, set.u, a.token + r, s);
+}
+
+// One row a workgroup.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) sample_row_kernel(Args a) {
+    __shared__ Shared s;
+    draw_row<T, V>(a, blockIdx.x, s);
+}
+
+// ---- few long rows: several workgroups each ------------------------------------------------------------
+//
+// With fewer rows than compute units a row's passes are shared by `splits` workgroups, each with `vectors` vectors of it a
+// thread, in four launches: the largest; counts of the bins and the mass; what lies at the border and the
+// tiles' masses; the token, by one workgroup again.  What the row kernel does in further passes (a border that many share,
+// top_k beyond the list with top_p) it does here too, alone.
+
+constexpr int kMostSplits = 16;
+enum Mode { NO_ROW, FIRST, TILES, LIST, BORDER_LISTED, BORDER_TILES, BORDER_COUNTED, ALONE };
+struct State {
+    float tops[kMostSplits];
+    u64 total, want;
+    uint32_t front, back, first, mode;
+};
+struct SplitArgs {
+    Args a;
+    int splits, vectors;
+    State* state;    // of each row, as the following
+    uint32_t* count; // [kBins]
+    u64* mass;       // [kBins]: of the tiles
+    u64* list;       // [kList]
+};
+
+// This workgroup's part of its row: `at` its first element.
+template <typename T, int V>
+struct Part {
+    typedef Row<T, V> R;
+    int r, split, at, size;
+    R row;
+    __device__ Part(const SplitArgs& p) {
+        r = blockIdx.x / p.splits, split = blockIdx.x - r * p.splits;
+        const int step = p.vectors * kThreads * R::N;
+        at = split * step;
+        size = p.a.vocab - at < step ? p.a.vocab - at : step;
+        row.init((const T*)p.a.logits + (size_t)r * p.a.ld + at, size);
+    }
+};
+__device__ inline float top_of(const State& st, int splits) {
+    float top = st.tops[0];
+    for (int i = 1; i < splits; ++i) top = __builtin_elementwise_maximum(top, st.tops[i]);
+    return uniform(top);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) sample_top_kernel(SplitArgs p) {
+    __shared__ Shared s;
+    Part<T, V> part(p);
+    State& st = p.state[part.r];
+    for (int i = part.split * kThreads + threadIdx.x; i < kBins; i += p.splits * kThreads) {
+        p.count[(size_t)part.r * kBins + i] = 0;
+        p.mass[(size_t)part.r * kBins + i] = 0;
+    }
+    float own;
+    const float top = top_of(part.row, own, s);
+    if (threadIdx.x == 0) st.tops[part.split] = top;
+    if (part.split == 0 && threadIdx.x == 0) st.total = 0, st.front = st.back = 0, st.first = 0xffffffffu;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) sample_count_kernel(SplitArgs p) {
+    __shared__ Shared s;
+    const int r = blockIdx.x / p.splits;
+    State& st = p.state[r];
+    const Settings set(p.a, r);
+    const float top = top_of(st, p.splits);
+    const bool ranked = set.ranked(p.a.vocab), weigh = set.weigh() && !ranked;
+    if (!set.valid(top) || set.first_alone() || !(ranked || weigh)) return;
+    Part<T, V> part(p);
+    const Scale sc(top, set.temperature);
+    const u64 own = fill(part.row, sc, weigh, s);
     u64 all;
-    const u64 at = block_scan(m0 + m1, s.parts, all);
-    double share = (double)u * (double)all;
-    share = share > 0. ? share : 0.;
-    u64 target = share < (double)all ? (u64)share : all - 1;
-    target = target < all ? target : all - 1;
-    const int tile = first_bin(at > target, at + m0 > target, at + m0 + m1 > target, 0,
-                               [&](int second) { s.found[1] = second ? at + m0 : at; }, s);
-    const int step = Tiles<R>::BLOCK << tiles.k, from = tile * step, to = from + step < size ? from + step : size;
-    const int per = (to - from + kThreads - 1) / kThreads, mine = from + threadIdx.x * per, end = mine + per < to ? mine + per : to;
-    const u64 done = s.found[1];
-    auto mass = [&](int i) -> u64 {
-        const float x = (float)row.row[i];
-        return cut.keeps(x, i) ? units(weight_of(x, sc)) : 0;
-    };
-    u64 own = 0;
-    for (int i = mine; i < end; ++i) own += mass(i);
-    u64 sum = done + block_scan(own, s.parts, all);
-    if (sum <= target && target < sum + own)
-        for (int i = mine; i < end; ++i) {
-            sum += mass(i);
-            if (sum > target) {
-                a.token[r] = i;
-                return;
-            }
+    block_scan(own, s.parts, all);
+    if (weigh && threadIdx.x == 0) atomicAdd(&st.total, all);
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+        if (s.count[i] > 0) atomicAdd(&p.count[(size_t)r * kBins + i], s.count[i]);
+}
+
+// What the border's list and the tiles are made of: listed from `from` on, below `sure` at the border; in the tiles
+// what is above `edge`.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) sample_border_kernel(SplitArgs p) {
+    __shared__ Shared s;
+    Part<T, V> part(p);
+    State& st = p.state[part.r];
+    const Settings set(p.a, part.r);
+    const float top = top_of(st, p.splits);
+    if (!set.valid(top)) {
+        if (part.split == 0 && threadIdx.x == 0) st.mode = NO_ROW;
+        return;
+    }
+    if (set.first_alone()) {
+        first_of(part.row, top, s);
+        if (threadIdx.x == 0 && s.token != 0xffffffffu) atomicMin(&st.first, s.token + part.at);
+        if (part.split == 0 && threadIdx.x == 0) st.mode = FIRST;
+        return;
+    }
+    const Scale sc(top, set.temperature);
+    const float least = set.least(top);
+    const bool ranked = set.ranked(p.a.vocab), weigh = set.weigh();
+    float from = INFINITY, sure = INFINITY, edge = below(key_of(least));
+    Mode mode = TILES;
+    u64 want = 0;
+    if (ranked || weigh) {
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s.count[i] = p.count[(size_t)part.r * kBins + i];
+        __syncthreads();
+        int lo = 0, hi = 0;
+        u64 before = 0, counted = 0, between = 0;
+        if (ranked) {
+            lo = hi = reach((u64)set.top_k, before, s);
+            between = s.count[hi];
+            counted = before;
+            want = (u64)set.top_k - before;
+            mode = counted + between <= kList ? LIST : weigh || hi == kBins - 1 || between > kList ? ALONE : BORDER_COUNTED;
+            if (mode == LIST) lo = 0;
+        } else {
+            want = least_mass(set.top_p, st.total);
+            reach_mass(want, st.total, lo, hi, counted, between, s);
+            mode = between > kList ? ALONE : counted + between <= kList ? BORDER_LISTED : BORDER_TILES;
         }
+        if (lo > 0) sure = least_of(lo - 1, sc);
+        from = least_of(hi, sc);
+        if (mode == LIST && !weigh) from = fmaxf(from, least);
+        if (mode == BORDER_COUNTED || mode == BORDER_TILES) edge = below(key_of(sure));
+        if (mode != LIST && mode != ALONE && least >= sure) {  // min_p's cut lies before theirs
+            mode = TILES;
+            from = INFINITY;
+            edge = below(key_of(least));
+        }
+    }
+    if (part.split == 0 && threadIdx.x == 0) st.mode = mode, st.want = want;
+    if (mode == ALONE) return;
+    if (from < INFINITY) {
+        // (all of it fits the row's list, as the counts say)
+        gather(part.row, from, sure, mode == BORDER_LISTED, s);
+        if (threadIdx.x == 0) {
+            s.found[0] = s.front > 0 ? atomicAdd(&st.front, s.front) : 0;
+            s.found[1] = s.back > 0 ? atomicAdd(&st.back, s.back) : 0;
+        }
+        __syncthreads();
+        u64* const list = p.list + (size_t)part.r * kList;
+        const uint32_t f = (uint32_t)s.found[0], b = (uint32_t)s.found[1];
+        for (uint32_t i = threadIdx.x; i < s.front + s.back; i += kThreads) {
+            const bool front = i < s.front;
+            const uint32_t place = front ? f + i : kList - 1 - (b + i - s.front);
+            // the index counts from the row's start: its complement is in the low half
+            if (place < kList) list[place] = s.list[front ? i : kList - 1 - (i - s.front)] - (u64)part.at;
+        }
+    }
+    if (mode == TILES || mode == BORDER_TILES || mode == BORDER_COUNTED) {
+        const Tiles<Row<T, V>> tiles(p.a.vocab);
+        weigh_tiles<false>(part.row, sc, tiles, Cut{edge, -1}, s, part.at);
+        // (a part is whole tiles)
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
+            if (s.mass[i] > 0) p.mass[(size_t)part.r * kBins + i] = s.mass[i];
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) sample_token_kernel(SplitArgs p) {
+    __shared__ Shared s;
+    const int r = blockIdx.x;
+    const State& st = p.state[r];
+    const int mode = st.mode;
+    if (mode == NO_ROW || mode == FIRST) {
+        if (threadIdx.x == 0) p.a.token[r] = mode == FIRST ? (long long)st.first : -1;
+        return;
+    }
+    if (mode == ALONE) return draw_row<T, V>(p.a, r, s);
+    const Settings set(p.a, r);
+    const float top = top_of(st, p.splits), least = set.least(top);
+    const Scale sc(top, set.temperature);
+    const Tiles<Row<T, V>> tiles(p.a.vocab);
+    Listed l{st.front, st.back};
+    for (uint32_t i = threadIdx.x; i < l.size(); i += kThreads) s.list[l.place(i)] = p.list[(size_t)r * kList + l.place(i)];
+    const bool tiled = mode == TILES || mode == BORDER_TILES || mode == BORDER_COUNTED;
+    clear(s);
+    if (tiled)
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s.mass[i] = p.mass[(size_t)r * kBins + i];
+    __syncthreads();
+    const Cut at_least{below(key_of(least)), -1};
+    Cut cut = at_least;
+    if (mode == LIST) {
+        if ((u64)set.top_k <= l.front) cut = cut_listed(l, false, (u64)set.top_k, sc, s);
+        if (set.weigh()) cut = cut_listed(l, true, least_mass(set.top_p, mass_listed(l, sc, s)), sc, s);
+    } else if (mode != TILES) {
+        sort(l.front, s);
+        if (mode == BORDER_COUNTED) {
+            l.front = (uint32_t)st.want;
+        } else {
+            u64 all;
+            const u64 before = mode == BORDER_LISTED ? mass_listed(Listed{0, l.back}, sc, s) : sum_of_tiles(s);
+            l.front = listed_mass(l.front, before, st.want, sc, all, s);
+        }
+        cut = {value_at(l.front - 1, s), index_at(l.front - 1, s)};
+    }
+    if (least > cut.edge) cut = at_least;
+    if (!tiled) clear(s);
+    add_listed(l, cut, sc, tiles, s);
+    __syncthreads();
+    pick((const T*)p.a.logits + (size_t)r * p.a.ld, tiles, sc, cut, set.u, p.a.token + r, s);
 }
 
 }  // namespace sample

@@ -8,22 +8,56 @@ namespace {
 
 constexpr int kMaxRows = 1 << 21, kMaxVocab = 1 << 23;  // 2^23 probabilities of 2^40 are below 2^64
 
-template <typename T>
-void launch(int rows, const Args& a, hipStream_t stream) {
-    constexpr int N = 16 / sizeof(T);
-    const int vectors = (a.vocab + kThreads * N - 1) / (kThreads * N);
-    if (vectors <= 4)
-        sample_row_kernel<T, 4><<<rows, kThreads, 0, stream>>>(a);
-    else
-        sample_row_kernel<T, 12><<<rows, kThreads, 0, stream>>>(a);
+// Whether a row is shared by several workgroups: of long rows, where the rows leave half of the 256 compute units
+// idle, until about all have a workgroup, each with a vector a thread or more.
+struct Split {
+    int splits, vectors;
+    long state, count, mass, list, bytes;
+};
+Split split_of(long size, long rows, long vocab) {
+    const long n = 16 / size, all = (vocab + kThreads * n - 1) / (kThreads * n);
+    Split p{1, (int)all, 0, 0, 0, 0, 0};
+    if (all <= 8 || rows > 128 || rows == 0) return p;
+    long most = 256 / rows < kMostSplits ? 256 / rows : kMostSplits;
+    if (most > all) most = all;
+    p.vectors = (int)((all + most - 1) / most);
+    p.splits = (int)((all + p.vectors - 1) / p.vectors);
+    auto take = [&](long bytes) {
+        const long at = p.bytes;
+        p.bytes = (at + bytes + 255) / 256 * 256;
+        return at;
+    };
+    p.state = take(sizeof(State) * rows);
+    p.count = take(4L * kBins * rows);
+    p.mass = take(8L * kBins * rows);
+    p.list = take(8L * kList * rows);
+    return p;
 }
 
-int run(int dtype, int rows, const Args& a, hipStream_t stream) {
+template <typename T>
+void launch(int rows, const Args& a, char* work, hipStream_t stream) {
+    constexpr int N = 16 / sizeof(T);
+    const Split p = split_of(sizeof(T), rows, a.vocab);
+    if (p.splits > 1) {
+        const SplitArgs s{a, p.splits, p.vectors, (State*)(work + p.state), (uint32_t*)(work + p.count),
+                          (u64*)(work + p.mass), (u64*)(work + p.list)};
+        sample_top_kernel<T, 4><<<rows * p.splits, kThreads, 0, stream>>>(s);
+        sample_count_kernel<T, 4><<<rows * p.splits, kThreads, 0, stream>>>(s);
+        sample_border_kernel<T, 4><<<rows * p.splits, kThreads, 0, stream>>>(s);
+        sample_token_kernel<T, 4><<<rows, kThreads, 0, stream>>>(s);
+    } else if (a.vocab <= 4 * kThreads * N) {
+        sample_row_kernel<T, 4><<<rows, kThreads, 0, stream>>>(a);
+    } else {
+        sample_row_kernel<T, 12><<<rows, kThreads, 0, stream>>>(a);
+    }
+}
+
+int run(int dtype, int rows, const Args& a, char* work, hipStream_t stream) {
     (void)hipGetLastError();
     if (dtype == SAMPLE_F32)
-        launch<float>(rows, a, stream);
+        launch<float>(rows, a, work, stream);
     else
-        launch<__bf16>(rows, a, stream);
+        launch<__bf16>(rows, a, work, stream);
     return (int)hipGetLastError();
 }
 
@@ -37,7 +71,8 @@ long long vocab_sample_workspace(int dtype, int T, int V) {
     if (dtype != SAMPLE_F32 && dtype != SAMPLE_BF16) return -1;
     if (T < 0 || T > libsgemm::sample::kMaxRows) return -2;
     if (V < 1 || V > libsgemm::sample::kMaxVocab) return -3;
-    return 0;
+    const libsgemm::sample::Split p = libsgemm::sample::split_of(dtype == SAMPLE_F32 ? 4 : 2, T, V);
+    return p.splits > 1 ? p.bytes : 0;
 }
 
 int vocab_sample(int dtype, int T, int V, const void* logits, int ld, const float* u, float temperature,
@@ -58,7 +93,7 @@ int vocab_sample(int dtype, int T, int V, const void* logits, int ld, const floa
     if (work_bytes < need) return -17;
     const libsgemm::sample::Args a{logits, ld, V, u, temperatures, temperature, top_ks, top_k, top_ps, top_p,
                                    min_ps, min_p, token};
-    return libsgemm::sample::run(dtype, T, a, stream);
+    return libsgemm::sample::run(dtype, T, a, (char*)work, stream);
 }
 
 }  // extern "C"

@@ -89,6 +89,39 @@ def test_masks_and_what_is_no_distribution(dtype):
     assert sg.vocab_sample(clean, u2, min_p=bad).tolist()[3] == -1
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,kind", [(3, 140001, "ties"), (3, 140001, "flat"), (17, 70000, "masked"), (100, 66000, "mixed"),
+                                      (1, 600000, "ties"), (128, 98304, "mixed"), (129, 98304, "mixed")])
+def test_few_long_rows(T, V, kind, dtype):
+    """Rows shared by several workgroups: borders among equal logits, more than the list holds, parts without a token."""
+    logits, u, g = rows(T, V, dtype, seed=5)
+    if kind == "ties":
+        logits.copy_(torch.randint(0, 4, (T, V), generator=g, device="cuda") * 0.25)
+    if kind == "flat":
+        logits *= 0.01
+    if kind == "masked":
+        logits[:, 20000:50000] = -math.inf
+        logits[0] = -math.inf
+        logits[1, 1:] = -math.inf
+        logits[2, :-1] = -math.inf
+        logits[3, V - 1] = math.nan
+        logits[4, 40000] = math.inf
+        logits[5] = torch.finfo(DT[dtype]).min
+    many = [dict(top_k=30000), dict(top_k=5000, top_p=0.9), dict(top_k=V - 5), dict(top_p=0.97, min_p=0.2), dict(top_k=2000, min_p=0.5)]
+    if kind != "mixed":
+        for s in SETTINGS + many:
+            check(logits, u, sg.vocab_sample(logits, u, **s), **s)
+        return
+
+    def pick(values, of=torch.float32):
+        return torch.tensor(values, device="cuda", dtype=of)[torch.randint(0, len(values), (T,), generator=g, device="cuda")]
+
+    s = dict(temperature=pick([0.0, 0.5, 1.0, 1.7, -1.0]), top_k=pick([0, 1, 50, 1500, 9000, V], torch.int64),
+             top_p=pick([0.2, 0.9, 0.99, 1.0]), min_p=pick([0.0, 0.01, 0.3, 2.0]))
+    token = sg.vocab_sample(logits, u, **s)
+    check(logits[::4], u[::4], token[::4], **{k: v[::4] for k, v in s.items()})
+
+
 def test_distribution():
     """Evenly spaced u give each token its share."""
     n = 4096

@@ -6,12 +6,12 @@
 // Probabilities are whole multiples of 2^-40 of the largest, so their sums are exact in 64 bits and the same in any
 // order: atomics and any cut of the row give one result.
 //
-// A workgroup has a row, in registers up to 256 KB of it.  It reads the row once from memory; what bounds it then is
-// its own passes over the registers (131072 bf16 logits: 2.9 us for the largest, 12 us for a pass of exponentials)
-// and a dozen steps of all threads together (0.3 - 1 us each).  So it avoids passes: top_p and a large top_k look for
+// A workgroup has a row, part of it in registers.  What bounds it is its own passes over the row (131072 bf16 logits:
+// 3.8 us for the largest, 19 for a pass of exponentials, 21 for one that counts bins as well, bound by the LDS's additions) and a
+// dozen steps of all threads together (0.3 - 1 us each).  So it avoids passes: top_p and a large top_k look for
 // the cut in counts of bins of the exponent, from which masses follow to 1 % of what lies on the lighter side, and order
 // only the few logits at the border; a small top_k needs no counts (1024 threads' own largest bound it); what
-// stays is listed where it is short, and only the listed weighed.
+// stays is listed where it is short, and only the listed weighed.  Few long rows are shared by several workgroups.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -83,9 +83,9 @@ __device__ inline float weight_of(float x, const Scale& s) {
 __device__ inline u64 units(double w) { return __builtin_bit_cast(u64, w + 0x1p12) & ((1ull << 52) - 1); }
 
 // A row's elements: the first V vectors of 16 bytes a thread in registers, the others read from memory (the caches, after
-// the first time) in each pass, U on their way at once.  48 registers are what a thread can keep beside its work: 64
-// spilled, and each pass read the spilled ones again (131072 bf16 logits: 5.3 us for the largest, against 3).  f(index, values)
-// for each vector, of every thread together; past the row's end -infinity.
+// the first time) in each pass, U on their way at once.  32 registers are what a thread keeps beside its work: with 64
+// the compiler spilled, and each pass read the spilled ones again (131072 bf16 logits: 5.3 us for the largest, against 3.8).
+// f(index, values) for each vector, of every thread together; past the row's end -infinity.
 template <typename T, int V>
 struct Row {
     static constexpr int N = 16 / sizeof(T), U = 2;
@@ -196,12 +196,12 @@ struct Cut {
     __device__ bool keeps(float x, int i) const { return x > edge || (x == edge && i <= last); }
 };
 
-constexpr int kList = 2048;
+constexpr int kList = 2048, kRanked = 256;
 struct Shared {
     uint32_t count[kBins + 63];  // while they are counted the last bin has a place for each lane
-    u64 mass[kBins];
-    u64 list[kList];
-    uint32_t rank[512];
+    u64 mass[kBins], bins[kBins];
+    u64 list[kList], range[2];
+    uint32_t rank[kRanked];
     u64 parts[kWaves], found[4];
     float tops[kWaves];
     uint32_t front, back, token;
@@ -326,43 +326,34 @@ __device__ inline void reach_mass(u64 want, u64 total, int& lo, int& hi, u64& co
     between = s.found[3] - counted;
 }
 
-// s.list[0, n) in falling order.  A short list by each entry's rank, the number of larger ones (they are all
-// different), counted by several threads each; a long one by merging in LDS, step by step of all threads.
+// s.list[0, n) in falling order, n <= kRanked: each entry's rank is the number of larger ones (they are all different),
+// counted by several threads each.
 __device__ inline void sort(uint32_t n, Shared& s) {
-    constexpr uint32_t kRanked = 512;
-    if (n <= kRanked) {
-        uint32_t places = 64;  // whole waves
-        while (places < n) places *= 2;
-        const uint32_t i = threadIdx.x & (places - 1), part = threadIdx.x / places, parts = kThreads / places;
-        const uint32_t per = (n + parts - 1) / parts, from = part * per, to = from + per < n ? from + per : n;
-        if (threadIdx.x < kRanked) s.rank[threadIdx.x] = 0;
-        const u64 own = i < n ? s.list[i] : 0;
-        __syncthreads();
-        uint32_t larger = 0;
-#pragma unroll 8
-        for (uint32_t j = from; j < to; ++j) larger += s.list[j] > own;
-        if (i < n && larger > 0) atomicAdd(&s.rank[i], larger);
-        __syncthreads();
-        if (threadIdx.x < n) s.list[s.rank[threadIdx.x]] = own;
-        __syncthreads();
-        return;
-    }
-    uint32_t size = 2;
-    while (size < n) size *= 2;
-    for (uint32_t k = 2; k <= size; k *= 2)
-        for (uint32_t j = k / 2; j > 0; j /= 2) {
-            __syncthreads();
-            for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
-                const uint32_t a = 2 * i - (i & (j - 1)), b = k == 2 * j ? a + 2 * j - 1 - 2 * (a & (j - 1)) : a + j;
-                // entries past n count as the smallest; the first step of each merge compares mirrored places, so
-                // that all steps sort downwards and those entries stay behind
-                if (b < n) {
-                    const u64 x = s.list[a], y = s.list[b];
-                    if (x < y) s.list[a] = y, s.list[b] = x;
-                }
-            }
-        }
+    uint32_t places = 64;  // whole waves
+    while (places < n) places *= 2;
+    const uint32_t i = threadIdx.x & (places - 1), part = threadIdx.x / places, parts = kThreads / places;
+    const uint32_t per = (n + parts - 1) / parts, from = part * per, to = from + per < n ? from + per : n;
+    if (threadIdx.x < kRanked) s.rank[threadIdx.x] = 0;
     __syncthreads();
+    const u64 own = i < n ? s.list[i] : 0;
+    uint32_t larger = 0;
+#pragma unroll 8
+    for (uint32_t j = from; j < to; ++j) larger += s.list[j] > own;
+    if (i < n && larger > 0) atomicAdd(&s.rank[i], larger);
+    __syncthreads();
+    if (threadIdx.x < n) s.list[s.rank[threadIdx.x]] = own;
+    __syncthreads();
+}
+
+// A place behind what is listed already for each lane that `has` one: one addition a wave.
+__device__ inline uint32_t place_of(bool has, uint32_t* listed) {
+    const uint64_t mask = __ballot(has);
+    if (mask == 0) return 0;
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t at = 0;
+    if (lane == 0) at = atomicAdd(listed, (uint32_t)__popcll(mask));
+    at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+    return at + (uint32_t)__popcll(mask & ((1ull << lane) - 1));
 }
 
 // The logits from `from` on: those below `sure` from the front of s.list on, the others from its back, where
@@ -532,43 +523,60 @@ __device__ inline uint32_t listed_mass(uint32_t n, u64 before, u64 want, const S
     const int last = first_bin(at >= want && i0 > 0, at + w0 >= want && i0 < n, at + w0 + w1 >= want && i1 < n, 0, [](int) {}, s);
     return last < 0 ? n : (uint32_t)last + 1;
 }
-// The cut within what is listed, a prefix of the row's order itself, where the sum of counts (masses) from its first
-// on reaches want.  A long list is split by bins first, and only the border's put in order: the listed past it
-// are dropped.
-__device__ inline Cut cut_listed(Listed& l, bool by_mass, u64 want, const Scale& sc, Shared& s) {
-    u64 before = 0, all;
-    if (l.back > 0 || l.front > 512) {
-        const uint32_t i0 = threadIdx.x, i1 = i0 + kThreads, n = l.size();
-        const u64 e0 = i0 < n ? s.list[l.place(i0)] : 0, e1 = i1 < n ? s.list[l.place(i1)] : 0;
-        auto value = [](u64 e) { return value_of((uint32_t)(e >> 32)); };
-        const uint32_t bin0 = i0 < n ? bin_of(value(e0), sc) : kBins, bin1 = i1 < n ? bin_of(value(e1), sc) : kBins;
-        clear(s);
-        if (by_mass) {
-            if (i0 < n) atomicAdd(&s.mass[bin0], units(weight_of(value(e0), sc)));
-            if (i1 < n) atomicAdd(&s.mass[bin1], units(weight_of(value(e1), sc)));
-        } else {
-            if (i0 < n) atomicAdd(&s.mass[bin0], 1ull);
-            if (i1 < n) atomicAdd(&s.mass[bin1], 1ull);
-        }
+// The cut within the list's front, where the sum of counts (masses), with `before`, reaches want; those past it are
+// dropped.  whole: within all that is listed.  A long list is narrowed first, by 2048 bins of what is left of its range
+// (value and index in one number, so equal logits too come apart), what lies before the bin going to the back: merging it
+// in LDS took 17 us for 2048.
+__device__ inline Cut cut_listed(Listed& l, bool whole, bool by_mass, u64 want, u64 before, const Scale& sc, Shared& s) {
+    u64 all;
+    uint32_t n = whole ? l.size() : l.front;
+    bool merge = whole && l.back > 0;
+    while (n > kRanked || merge) {
+        const uint32_t i0 = threadIdx.x, i1 = i0 + kThreads;
+        if (threadIdx.x == 0) s.range[0] = ~0ull, s.range[1] = 0;
+        s.bins[i0] = s.bins[i1] = 0;
         __syncthreads();
-        const u64 v0 = s.mass[2 * threadIdx.x], v1 = s.mass[2 * threadIdx.x + 1];
-        const u64 at = block_scan(v0 + v1, s.parts, all);
+        const u64 e0 = i0 < n ? s.list[l.place(i0)] : 0, e1 = i1 < n ? s.list[l.place(i1)] : 0;
+        u64 low = i0 < n ? e0 : ~0ull, high = e0 > e1 ? e0 : e1;
+        if (i1 < n && e1 < low) low = e1;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const u64 a = __shfl_xor(low, o), b = __shfl_xor(high, o);
+            low = a < low ? a : low;
+            high = b > high ? b : high;
+        }
+        if ((threadIdx.x & 63) == 0 && i0 < n) atomicMin(&s.range[0], low), atomicMax(&s.range[1], high);
+        __syncthreads();
+        const u64 least = s.range[0], most = s.range[1];
+        const int bits = 64 - __builtin_clzll((most - least) | 1), shift = bits > 11 ? bits - 11 : 0;
+        auto bin_at = [&](u64 e) { return (uint32_t)((most - e) >> shift); };
+        auto amount = [&](u64 e) { return by_mass ? units(weight_of(value_of((uint32_t)(e >> 32)), sc)) : 1ull; };
+        if (i0 < n) atomicAdd(&s.bins[bin_at(e0)], amount(e0));
+        if (i1 < n) atomicAdd(&s.bins[bin_at(e1)], amount(e1));
+        __syncthreads();
+        const u64 v0 = s.bins[2 * threadIdx.x], v1 = s.bins[2 * threadIdx.x + 1];
+        const u64 at = before + block_scan(v0 + v1, s.parts, all);
         const uint32_t bin = first_bin(at >= want, at + v0 >= want, at + v0 + v1 >= want, 0,
                                        [&](int second) { s.found[1] = second ? at + v0 : at; }, s);
         before = s.found[1];
-        if (threadIdx.x == 0) s.front = s.back = 0;
+        if (threadIdx.x == 0) s.front = 0, s.back = merge ? 0 : l.back;
         __syncthreads();
-        auto put = [&](u64 e, uint32_t b) {
-            if (b == bin) s.list[atomicAdd(&s.front, 1u)] = e;
-            if (b < bin) s.list[kList - 1 - atomicAdd(&s.back, 1u)] = e;
+        auto put = [&](u64 e, bool is) {
+            const bool front = is && bin_at(e) == bin, back = is && bin_at(e) < bin;
+            const uint32_t f = place_of(front, &s.front), b = place_of(back, &s.back);
+            if (front) s.list[f] = e;
+            if (back) s.list[kList - 1 - b] = e;
         };
-        put(e0, bin0);
-        put(e1, bin1);
+        put(e0, i0 < n);
+        put(e1, i1 < n);
         __syncthreads();
         l = {s.front, s.back};
+        n = l.front;
+        merge = false;
+        __syncthreads();
     }
-    sort(l.front, s);
-    const uint32_t last = by_mass ? listed_mass(l.front, before, want, sc, all, s) - 1 : (uint32_t)(want - before) - 1;
+    sort(n, s);
+    const uint32_t last = by_mass ? listed_mass(n, before, want, sc, all, s) - 1 : (uint32_t)(want - before) - 1;
     l.front = last + 1;
     return {value_at(last, s), index_at(last, s)};
 }
@@ -696,6 +704,7 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
     bool certain = false;                // what lies before the border is listed too
     u64 want = 0, total = 0;
     bool filled = false;
+    float border = INFINITY;             // what lies from it on stays
     while (stage < WHOLE) {
         int lo = 0, hi = -1, next = stage;
         u64 before = 0;
@@ -738,6 +747,7 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
                     continue;
                 }
                 certain = counted + between <= kList;
+                border = sure;
                 if (between > kList) hi = -1;
             }
         } else {
@@ -771,9 +781,8 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
         }
         if (!stays) {
             if (got) {
-                sort(s.front, s);
-                const uint32_t last = (uint32_t)((u64)top_k - before) - 1;
-                cut = {value_at(last, s), index_at(last, s)};
+                Listed border{s.front, 0};
+                cut = cut_listed(border, false, false, (u64)top_k, before, sc, s);
             } else {
                 cut = descend(row, sc, tiles, stage == MASS, stage == MASS ? want : (u64)top_k, s);
                 filled = false;
@@ -790,27 +799,18 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
     // the tiles' masses
     Listed l{stage == REST ? 0 : s.front, stage == BORDER && certain ? s.back : 0};
     if (stage == WHOLE) {
-        if ((u64)top_k <= l.front) cut = cut_listed(l, false, (u64)top_k, sc, s);
-        if (weigh) cut = cut_listed(l, true, least_mass(top_p, mass_listed(l, sc, s)), sc, s);
-        if (least > cut.edge) cut = at_least;
+        if ((u64)top_k <= l.front) cut = cut_listed(l, true, false, (u64)top_k, 0, sc, s);
+        if (weigh) cut = cut_listed(l, true, true, least_mass(top_p, mass_listed(l, sc, s)), 0, sc, s);
     }
     if (stage == REST && cut.last >= 0) {
         weigh_tiles<true>(row, sc, tiles, cut, s);
     } else if (stage == REST || (stage == BORDER && !certain)) {
-        if (stage == BORDER) {
-            sort(l.front, s);
-            cut = {value_at(0, s), -1};
-        }
+        if (stage == BORDER) cut = {below(key_of(border)), -1};
         weigh_tiles<false>(row, sc, tiles, cut, s);
     }
-    if (stage == BORDER) {
-        if (certain) sort(l.front, s);
-        u64 all;
-        const u64 before = certain ? mass_listed(Listed{0, l.back}, sc, s) : sum_of_tiles(s);
-        l.front = listed_mass(l.front, before, want, sc, all, s);
-        cut = {value_at(l.front - 1, s), index_at(l.front - 1, s)};
-        if (least > cut.edge) cut = at_least;
-    }
+    if (stage == BORDER)
+        cut = cut_listed(l, false, true, want, certain ? mass_listed(Listed{0, l.back}, sc, s) : sum_of_tiles(s), sc, s);
+    if (least > cut.edge) cut = at_least;
     if (stage != REST) {
         if (stage != BORDER || certain) clear(s);
         add_listed(l, cut, sc, tiles, s);
@@ -1009,18 +1009,13 @@ __global__ void __launch_bounds__(kThreads) sample_token_kernel(SplitArgs p) {
     const Cut at_least{below(key_of(least)), -1};
     Cut cut = at_least;
     if (mode == LIST) {
-        if ((u64)set.top_k <= l.front) cut = cut_listed(l, false, (u64)set.top_k, sc, s);
-        if (set.weigh()) cut = cut_listed(l, true, least_mass(set.top_p, mass_listed(l, sc, s)), sc, s);
+        if ((u64)set.top_k <= l.front) cut = cut_listed(l, true, false, (u64)set.top_k, 0, sc, s);
+        if (set.weigh()) cut = cut_listed(l, true, true, least_mass(set.top_p, mass_listed(l, sc, s)), 0, sc, s);
+    } else if (mode == BORDER_COUNTED) {
+        cut = cut_listed(l, false, false, st.want, 0, sc, s);
     } else if (mode != TILES) {
-        sort(l.front, s);
-        if (mode == BORDER_COUNTED) {
-            l.front = (uint32_t)st.want;
-        } else {
-            u64 all;
-            const u64 before = mode == BORDER_LISTED ? mass_listed(Listed{0, l.back}, sc, s) : sum_of_tiles(s);
-            l.front = listed_mass(l.front, before, st.want, sc, all, s);
-        }
-        cut = {value_at(l.front - 1, s), index_at(l.front - 1, s)};
+        const u64 before = mode == BORDER_LISTED ? mass_listed(Listed{0, l.back}, sc, s) : sum_of_tiles(s);
+        cut = cut_listed(l, false, true, st.want, before, sc, s);
     }
     if (least > cut.edge) cut = at_least;
     if (!tiled) clear(s);

@@ -263,6 +263,19 @@ __device__ inline u64 fill(const R& row, const Scale& sc, bool weigh, Shared& s)
     return mass;
 }
 
+// The row's mass; a thread's share.
+template <class R>
+__device__ inline u64 mass_of(const R& row, const Scale& sc) {
+    u64 mass = 0;
+    row.each([&](int, const float (&x)[R::N]) {
+        double sum = 0;
+#pragma unroll
+        for (int q = 0; q < R::N; ++q) sum += (double)weight_of(x[q], sc);
+        mass += units(sum);
+    });
+    return mass;
+}
+
 // f(bin) of the first bin for which `is` turns true along the two bins of each thread, or -1 in none.  was: before
 // the thread's first bin.
 template <class F>
@@ -698,8 +711,8 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
     const bool weigh = set.weigh(), ranked = set.ranked(size);
 
     // From one stage to the next until what stays is known: all of it as `cut`, or up to a border in a list.
-    enum { QUICK, COUNT, MASS, REST, WHOLE, BORDER, LISTED };
-    int stage = ranked ? (top_k <= kThreads / 2 ? QUICK : COUNT) : weigh ? MASS : REST;
+    enum { QUICK, COUNT, LEAST, MASS, REST, WHOLE, BORDER, LISTED };
+    int stage = ranked ? (top_k <= kThreads / 2 ? QUICK : COUNT) : !weigh ? REST : least > lowest ? LEAST : MASS;
     Cut cut{below(key_of(lowest)), -1};  // what top_k leaves, then all
     bool certain = false;                // what lies before the border is listed too
     u64 want = 0, total = 0;
@@ -718,6 +731,12 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
             __syncthreads();
             hi = reach((u64)top_k, before, s);
             if (hi >= 0) from = weigh ? least_of(hi, sc) : fmaxf(least_of(hi, sc), least);
+            next = WHOLE;
+        } else if (stage == LEAST) {
+            // min_p's cut first: where what it leaves is short, top_p's lies in that list or past it, and the counts
+            // of all are not needed for it, only their mass
+            hi = 0;
+            from = least;
             next = WHOLE;
         } else if (stage == COUNT || stage == MASS) {
             if (!filled || (stage == MASS && total == 0)) {
@@ -763,8 +782,8 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
             stage = next;
             break;
         }
-        if (stage == QUICK) {
-            stage = COUNT;
+        if (stage == QUICK || stage == LEAST) {
+            stage = stage == QUICK ? COUNT : MASS;
             continue;
         }
         if (stage == REST) break;
@@ -799,8 +818,16 @@ __device__ inline void draw_row(const Args& a, int r, Shared& s) {
     // the tiles' masses
     Listed l{stage == REST ? 0 : s.front, stage == BORDER && certain ? s.back : 0};
     if (stage == WHOLE) {
-        if ((u64)top_k <= l.front) cut = cut_listed(l, true, false, (u64)top_k, 0, sc, s);
-        if (weigh) cut = cut_listed(l, true, true, least_mass(top_p, mass_listed(l, sc, s)), 0, sc, s);
+        if (ranked && (u64)top_k <= l.front) cut = cut_listed(l, true, false, (u64)top_k, 0, sc, s);
+        if (weigh) {
+            const u64 listed = mass_listed(l, sc, s);
+            if (ranked)
+                total = listed;
+            else
+                block_scan(mass_of(row, sc), s.parts, total);
+            want = least_mass(top_p, total);
+            if (want <= listed) cut = cut_listed(l, true, true, want, 0, sc, s);
+        }
     }
     if (stage == REST && cut.last >= 0) {
         weigh_tiles<true>(row, sc, tiles, cut, s);

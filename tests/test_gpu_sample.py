@@ -20,7 +20,8 @@ def rows(T, V, dtype, seed=0, spread=2.0, pad=0):
 
 SETTINGS = [dict(), dict(temperature=0.0), dict(temperature=0.3), dict(top_k=1), dict(top_k=7), dict(top_p=0.9),
             dict(top_p=0.1, temperature=2.0), dict(min_p=0.05), dict(top_k=40, top_p=0.95, min_p=0.01, temperature=0.7),
-            dict(top_p=0.0), dict(min_p=1.0), dict(min_p=2.0), dict(top_p=0.999999), dict(top_k=10 ** 9)]
+            dict(top_p=0.0), dict(min_p=1.0), dict(min_p=2.0), dict(top_p=0.999999), dict(top_k=10 ** 9),
+            dict(top_p=0.3, min_p=0.05), dict(top_p=0.95, min_p=1e-4, temperature=1.5), dict(top_p=0.99, min_p=0.5)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

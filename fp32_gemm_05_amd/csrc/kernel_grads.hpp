@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(1024) grads_norm_kernel(const double* sums, lo
     if (threadIdx.x > 0) return;
     *norm = (float)s;
     if (!factor) return;
-    const double f = (double)max_norm / (s + (double)eps);
+    const double d = s + (double)eps, f = d == 0. ? 1. : (double)max_norm / d;
     *factor = f >= 1. ? 1.f : (float)f;  // a NaN stays
 }
 

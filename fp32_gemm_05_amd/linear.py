@@ -172,5 +172,8 @@ class _Linear(torch.autograd.Function):
 
 
 def linear_layer(X, W, bias=None, residual=None, activation: str = "none"):
-    """linear_act's Y, differentiable with respect to X, W, bias and residual."""
+    """linear_act's Y, differentiable with respect to X, W, bias and residual.
+
+    A backward pass may be captured into a graph, with torch.autograd.grad, or with leaves that no eager graph still
+    holds: torch's own accumulation of gradients of such leaves ends the process in a capture."""
     return _Linear.apply(X, W, bias, residual, activation)

@@ -2,7 +2,7 @@
  * grads.h -- the norm of many gradients and clipping by it, of libsgemm for MI355X (gfx950).
  *
  *     norm = sqrt(sum over all tensors and elements of x^2)
- *     out = x * min(1, max_norm / (norm + eps))
+ *     out = x * min(1, max_norm / (norm + eps))      (x where norm + eps is 0)
  *
  * The tensors are row-major matrices, fp32 or bf16, mixed as they come; a contiguous tensor of any shape is one row.
  * Squares are summed in 64 bits, in an order that goes by the sizes alone: the same call gives the same bits, and

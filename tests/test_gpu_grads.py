@@ -103,6 +103,17 @@ def test_no_number(what):
     assert bool(rest.isnan().all()) if math.isnan(what) else bool((rest == 0).all())
 
 
+def test_nothing_to_clip_by_nothing():
+    """norm + eps is 0: the tensors stay, whatever max_norm is."""
+    for max_norm in (0.0, 1.0):
+        x, y = torch.zeros(70, device="cuda"), torch.zeros(5, device="cuda", dtype=BF16)
+        out = [torch.ones_like(x), torch.ones_like(y)]
+        assert float(sg.clip_grad_norm([x, y], max_norm, eps=0.0, out=out)) == 0
+        assert not out[0].any() and not out[1].any()
+        sg.clip_grad_norm([x, y], max_norm, eps=0.0)
+        assert not x.any() and not y.any()
+
+
 def test_a_factor_of_one_leaves_the_bits():
     t = torch.tensor([math.nan], device="cuda")
     x = torch.randn(1000, device="cuda").to(BF16)

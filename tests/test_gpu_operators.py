@@ -314,6 +314,95 @@ def test_another_stream(handle):
         assert torch.equal(a, b)
 
 
+def test_captured_training_step():
+    """Forward and backward through autograd in one graph, replayed with other values beside eager steps."""
+    g = gen(1)
+    p = model(g, 100, 64, 130, 50, F32)
+    dY = rand(g, 100, 64)
+    names = ["X", "W1", "b1", "W2", "b2"]
+
+    def step():
+        q = {k: p[k].detach().requires_grad_() for k in names}
+        h = sg.linear_layer(q["X"], q["W1"], q["b1"], None, "silu")
+        y = sg.linear_layer(h, q["W2"], q["b2"], q["X"], "none")
+        return [y.detach(), *torch.autograd.grad(y, list(q.values()), dY)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(3):
+        fresh({**{k: p[k] for k in names}, "dY": dY}, seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b), seed
+
+
+def test_two_threads_at_once():
+    """Calls of several host threads, each on a stream of its own."""
+    import threading
+    o = operands()
+    want = every_call(o)
+    torch.cuda.synchronize()
+    results, errors = {}, []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                results[i] = [every_call(o) for _ in range(3)]
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for calls in results.values():
+        for got in calls:
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,N,H", [(1, 5, 3), (20, 70, 33), (60, 9, 500), (100, 131, 77), (300, 260, 264)])
+def test_results_with_row_strides(dtype, T, N, H):
+    """Results whose rows lie further apart than they are long, through the C entry points: what lies between the rows
+    and behind the last one stays, and the rest is as without."""
+    from fp32_gemm_05_amd import linear
+    g = gen(T)
+    X, W, dY = rand(g, T, H, dtype=dtype), rand(g, N, H, dtype=dtype, scale=H ** -0.5), rand(g, T, N, dtype=dtype)
+    b, R = rand(g, N, dtype=dtype), rand(g, T, N, dtype=dtype)
+    Y, Z = sg.linear_act(X, W, b, R, "gelu", keep=True)
+    dX, dW, db = sg.linear_act_grad(X, W, dY, Z, "gelu")
+    d, stream = int(dtype == BF16), torch.cuda.current_stream().cuda_stream
+
+    def padded(rows, cols, pad):
+        return torch.full((rows * (cols + pad) + 40,), 7.0, dtype=dtype, device="cuda")
+
+    def unpadded(t, rows, cols, pad):
+        whole = t[: rows * (cols + pad)].view(rows, cols + pad)
+        assert bool((whole[:, cols:] == 7).all()) and bool((t[rows * (cols + pad):] == 7).all())
+        return whole[:, :cols]
+    y, z, x, w, s = padded(T, N, 3), padded(T, N, 8), padded(T, H, 1), padded(N, H, 5), padded(1, N, 0)
+    work = [torch.empty(max(16, sg.linear_workspace(dtype, grad, T, N, H)), dtype=torch.uint8, device="cuda") for grad in (False, True)]
+    linear._library.call("linear_act", d, d, T, N, H, X.data_ptr(), H, W.data_ptr(), H, b.data_ptr(), R.data_ptr(), N, 2,
+                         y.data_ptr(), N + 3, z.data_ptr(), N + 8, work[0].data_ptr(), work[0].numel(), stream)
+    assert torch.equal(unpadded(y, T, N, 3), Y) and torch.equal(unpadded(z, T, N, 8), Z)
+    linear._library.call("linear_act_grad", d, T, N, H, X.data_ptr(), H, W.data_ptr(), H, dY.data_ptr(), N, z.data_ptr(),
+                         N + 8, 2, x.data_ptr(), H + 1, w.data_ptr(), H + 5, s.data_ptr(), work[1].data_ptr(),
+                         work[1].numel(), stream)
+    assert torch.equal(unpadded(x, T, H, 1), dX) and torch.equal(unpadded(w, N, H, 5), dW)
+    assert torch.equal(unpadded(s, 1, N, 0)[0], db)
+
+
 def test_two_streams_at_once():
     o, streams = operands(), [torch.cuda.Stream() for _ in range(3)]
     want = every_call(o)

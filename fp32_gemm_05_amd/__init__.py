@@ -7,7 +7,9 @@ the first call, and a missing library raises instead of falling back to any
 other implementation.
 
 ``vocab_*`` are the vocabulary-head operators (``include/vocab.h``; cross entropy and distillation
-over X @ W.T without keeping the logits), in ``vocab.py``, which is imported at their first use.
+over X @ W.T without keeping the logits), in ``vocab.py``, which is imported at their first use.  So are
+``linear_*`` (a linear layer with bias, activation and residual; ``include/linear.h``), ``vocab_sample`` (drawing
+tokens from logits; ``include/sample.h``), ``grad_norm`` and ``clip_grad_norm`` (``include/grads.h``).
 """
 from ._binding import (  # noqa: F401
     SgemmArgumentError,

@@ -192,6 +192,11 @@ struct ProductArgs {
 
 // One product.  With few tiles the long axis is cut, so that the chip is filled, and the parts are
 // summed in a fixed order.
+//
+// What bounds it: large bf16 products power, as the vocabulary head's (8192 x 8192 x 4096: 430 us, 1.28 PFLOP/s, with gelu
+// and Z kept 512); fp32 ones the MFMA (4096 x 4096 x 1024: 251 us, 137 TFLOP/s of 157, pipes 87 % busy; 2048 x 4096 x 1024:
+// 134 - 150 us, 81 % busy, the rest the first loads and the stores of two rounds of tiles); short bf16 ones latency (777 x
+// 5003 x 1001: 20 - 27 us where the matrix pipes need 5: 16 slabs a tile, one round and a part).
 template <class T, Order OA, Order OB, bool TAIL, bool FORWARD>
 __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
     typedef typename Planes<T::kP>::Half E;
@@ -205,8 +210,8 @@ __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
     t.template run<OA, OB, TAIL>(lds, a.a, m0, a.b, n0, first, last - first, a.k - (last - 1) * T::BK);
     // The tile leaves through LDS, 32 rows of the result at a time and wave by wave: a lane's accumulators are four
     // columns of 32 rows, and stored from there a line of memory would be written in eight pieces (8192 x 8192 x 4096
-    // bf16 with Z kept: 677 us, so 490).  Row r holds its quad q at q ^ r: writes of 16 rows at one quad and
-    // reads of a row's quads in a row are both spread over the banks.
+    // bf16 with gelu and Z kept: 677 us, so 512).  Row r holds its quad q at q ^ r: writes of 16 rows at one quad
+    // and reads of a row's quads in a row are both spread over the banks.
     constexpr int WM = T::kWM, QUADS = WM / 4, N4 = sizeof(E) == 2 ? 2 : 1, LANES = QUADS / N4, ROWS = 64 / LANES;
     static_assert(T::NW * 32 * WM * 4 <= T::LDS_BYTES, "a place for each wave");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 31, h = lane >> 5;
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(T::NT) linear_product_kernel(ProductArgs a) {
     }
 }
 
-// The sum of a product's parts, finished.
+// The sum of a product's parts, finished: bound by its reads (4 parts of 2048 x 1024: 7.8 us, 5.4 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(256) linear_sum_kernel(const float* part, int splits, long rows, long pitch, Finish f) {
     const int n = blockIdx.x, m = (blockIdx.y * 256 + threadIdx.x) * 4;
@@ -342,7 +347,8 @@ __device__ inline void slopes(const SlopeArgs& a, int block) {
         a.sums[(size_t)by * a.pitch + c + i] = all[0][lane][i] + all[1][lane][i] + all[2][lane][i] + all[3][lane][i];
 }
 
-// All that reads a call's operands alone, in one launch.
+// All that reads a call's operands alone, in one launch.  Bound by memory: dY and Z of 8192 x 8192 bf16 to dZ and its sums 87
+// us, 4.6 TB/s.
 struct PrepareArgs {
     PackArgs w, x;
     SlopeArgs slope;
@@ -392,7 +398,10 @@ struct FewArgs {
 };
 
 // Z of 16 MR output features and all tokens, or a part of the hidden size of it where the features alone do not fill
-// the chip.  The NW waves of a workgroup take every NW-th group of U steps of the hidden size each and add up in LDS.
+// the chip.  Bound by the read of W (32768 x 1024 bf16 to 64 tokens' fp32 logits: 20.3 us, 3.7 TB/s with the 8 MB written; the
+// read alone is 14 us), of 17 to 64 fp32 tokens by cutting both sides into three parts (37 tokens, 5003 x 777: 14.5 us where the
+// bytes take 3.6), of one token by the launch and one trip to memory (4096 x 1024: 4.3 us, an empty kernel 1.65).
+// The NW waves of a workgroup take every NW-th group of U steps of the hidden size each and add up in LDS.
 template <class C, int NB, int MR, int NW>
 __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
     typedef typename C::T T;

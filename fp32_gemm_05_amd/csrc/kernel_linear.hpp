@@ -399,7 +399,7 @@ struct FewArgs {
 
 // Z of 16 MR output features and all tokens, or a part of the hidden size of it where the features alone do not fill
 // the chip.  Bound by the read of W (32768 x 1024 bf16 to 64 tokens' fp32 logits: 20.3 us, 3.7 TB/s with the 8 MB written; the
-// read alone is 14 us), of 17 to 64 fp32 tokens by cutting both sides into three parts (37 tokens, 5003 x 777: 14.5 us where the
+// read alone is 14 us), of 17 to 64 fp32 tokens by cutting both sides into three parts (37 tokens, 5003 x 777: 11.8 us where the
 // bytes take 3.6), of one token by the launch and one trip to memory (4096 x 1024: 4.3 us, an empty kernel 1.65).
 // The NW waves of a workgroup take every NW-th group of U steps of the hidden size each and add up in LDS.
 template <class C, int NB, int MR, int NW>

@@ -264,7 +264,8 @@ int gradient(const Call& c) {
 // 1x8/1; 8192 x 4096: 23.4 with 4x4/2, 33.9 with 4x4/1, 27.7 with 2x4/1; 4096 x 1024: 8.3 with 1x8/1, 10.5 with 2x4/1; 2048 x
 // 4096: 14.8 with 1x8/4, 20.1 with 1x8/1; 20 tokens, 32768 x 1024: 16.5 with 2x4/1, 20.5 with 1x8/1; 24 tokens, 3000 x 3000: 8.5 with
 // 1x4/1, 10.4 with 1x4/4; 1 token, 1024 x 8192: 8.9 with 1x4/8, 11.3 with 1x4/1; 3 tokens, 500 x 4000: 6.6 with 1x8/1, 8.6 with
-// 1x8/2; fp32 20 tokens, 4096 x 1024: 8.4 with 1x8/1, 10.6 with 1x4/1; 33 tokens, 500 x 4000: 11.3 with 1x8/8, 41 with 1x8/1.
+// 1x8/2; 32 tokens, 500 x 4000: 6.6 with 1x8/8, 9.8 with 1x8/1; fp32 1 token, 500 x 4000: 6.0 with 1x8/8, 11.6 with 1x8/1; 32
+// tokens, 2048 x 4096: 16.4 with 1x8/2, 24.4 with 1x8/1; 20 tokens, 4096 x 1024: 8.4 with 1x8/1, 10.6 with 1x4/1; 33 tokens, 500 x 4000: 11.3 with 1x8/8, 41 with 1x8/1.
 struct FewPlan {
     int mr, nw, splits;
     long pitch;
@@ -282,7 +283,7 @@ FewPlan few_plan(bool f32, int T, int N, int H) {
     }
     const long blocks = up(N, 16) / 16;
     if (!(f32 && nb == 2) && nb < 4 && blocks >= 64) p.nw = 4;
-    const int from = nb == 4 ? 12 : 32, to = nb < 4 ? 8 : f32 ? 2 : 4;  // steps of a wave
+    const int from = p.nw == 4 ? 32 : nb > 1 ? 12 : f32 ? 16 : 32, to = nb == 1 ? (f32 ? 4 : 8) : f32 ? 2 : 4;  // steps of a wave
     if (steps / p.nw >= from)
         while (steps / (p.nw * p.splits) > to && blocks * p.splits < 256 && p.splits < 16) p.splits *= 2;
     return p;
@@ -293,9 +294,10 @@ int few_forward(const Call& c) {
     const FewPlan p = few_plan(c.f32, c.T, c.N, c.H);
     const int blocks = (int)(up(c.N, 16 * p.mr) / (16 * p.mr)), grid = blocks * p.splits;
     const FewArgs a{c.T, c.N, c.H, c.X, c.W, c.ldx, c.ldw, blocks, p.splits, (float*)c.work, p.pitch, c.forward()};
+    constexpr int MR = NB == 3 ? 4 : NB;
     if constexpr (NB > 1)
-        if (p.mr == NB) linear_few_kernel<C, NB, NB, 4><<<grid, 256, 0, c.stream>>>(a);
-    if constexpr (NB < 4)
+        if (p.mr == MR) linear_few_kernel<C, NB, MR, 4><<<grid, 256, 0, c.stream>>>(a);
+    if constexpr (NB < 3)
         if (p.mr == 1 && p.nw == 4) linear_few_kernel<C, NB, 1, 4><<<grid, 256, 0, c.stream>>>(a);
     if (p.mr == 1 && p.nw == 8) linear_few_kernel<C, NB, 1, 8><<<grid, 512, 0, c.stream>>>(a);
     if (p.splits > 1)
@@ -354,6 +356,11 @@ int run(const Call& c, bool grad) {
     if (c.T == 0 && !c.dW && !c.dbias) return 0;
     (void)hipGetLastError();
     if (c.T == 0) return c.f32 ? zeros<float>(c) : zeros<__bf16>(c);
+    // 33 to 48 tokens are three blocks of 16 forward (40 tokens, with four us, so: fp32 5003 x 777: 13.7, 11.7; 2048 x
+    // 4096: 26.7, 19.3; bf16 5003 x 777: 16.4, 15.0; 32768 x 1024: 19.4, 18.0), but not in fp32 with four rows of features
+    // (32768 x 1024: 34.8 with four blocks, 40.1 with three; 8192 x 4096: 41.2, 46.6)
+    if (!grad && c.T > 32 && c.T <= 48 && !(c.f32 && few_plan(true, c.T, c.N, c.H).mr == 4))
+        return c.f32 ? few_forward<vocab::Fp32Split, 3>(c) : few_forward<vocab::Bf16, 3>(c);
     if (few(c.T))
         return by_mode(c.f32, c.T, [&](auto* mode, auto nb) {
             using C = typename std::remove_pointer<decltype(mode)>::type;

@@ -50,6 +50,14 @@ def test_sizes(T, N, H, dtype, pad):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,H", [(33, 12300, 70), (40, 12290, 1000), (48, 300, 2000), (37, 500, 4001), (44, 6200, 2100),
+                                   (49, 300, 1500), (20, 70, 2000), (32, 1100, 3001), (5, 40, 4000), (16, 1000, 2050)])
+def test_few_tokens(T, N, H, dtype):
+    """Numbers of tokens between those that fill the matrix instructions, long sums of few output features."""
+    step(T, N, H, dtype, "silu", 3)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("name", ACTS)
 @pytest.mark.parametrize("T,N,H", [(3, 200, 100), (40, 256, 64), (200, 384, 256)])
 @pytest.mark.parametrize("bias,residual", [(True, False), (False, True), (False, False), (True, True)])

@@ -199,12 +199,13 @@ void by_shape(Shape shape, F f) {
 
 template <typename T, int P, Order OA, Order OB, bool TAIL>
 void product(const Call& c, const Plan& p, const Operand& a, const Operand& b, long rows_m, long rows_n, long k,
-             char* part, const Finish& f) {
+             char* part, const Finish& f, const BiasArgs& bias = {}) {
     by_shape<P>(p.shape, [&](auto* shape) {
         using S = typename std::remove_pointer<decltype(shape)>::type;
         const int tm = (int)(up(rows_m, S::kBM) / S::kBM), tn = (int)(up(rows_n, S::kBN) / S::kBN);
-        const ProductArgs args{a, b, tm, tn, (int)k, (int)(up(k, S::BK) / S::BK), p.splits, (float*)part, p.rows, p.pitch, f};
-        linear_product_kernel<S, OA, OB, TAIL, OA != K_COL><<<(unsigned)((long)tm * tn * p.splits), S::NT, 0, c.stream>>>(args);
+        const ProductArgs args{a, b, tm, tn, (int)k, (int)(up(k, S::BK) / S::BK), p.splits, (float*)part, p.rows, p.pitch, f, bias};
+        const long blocks = (long)tm * tn * p.splits + bias.blocks();
+        linear_product_kernel<S, OA, OB, TAIL, OA != K_COL><<<(unsigned)blocks, S::NT, 0, c.stream>>>(args);
     });
     if (p.splits > 1)
         linear_sum_kernel<T><<<dim3((unsigned)rows_n, (unsigned)(up(rows_m, 1024) / 1024)), 256, 0, c.stream>>>(
@@ -242,19 +243,20 @@ int gradient(const Call& c) {
                    (int)(up(l.np, 1024) / 1024), l.row_groups, copy ? c.work + l.dz : nullptr, l.np / size,
                    c.dbias ? (float*)(c.work + l.sums) : nullptr};
     prepare<T>(p, c.stream);
-    if (c.dbias)
-        linear_bias_kernel<T><<<(unsigned)(up(c.N, 64) / 64), 1024, 0, c.stream>>>(
-            (const float*)(c.work + l.sums), l.row_groups, l.np / size, c.N, (T*)c.dbias);
+    BiasArgs bias{};
+    if (c.dbias) bias = {(const float*)(c.work + l.sums), l.row_groups, c.N, l.np / size, c.dbias};
+    if (c.dbias && !c.dX && !c.dW) linear_bias_kernel<T><<<(unsigned)bias.blocks(), 256, 0, c.stream>>>(bias);
     char* const part = c.work + l.part;
     if (c.dX) {
         const Finish f = Call::plain(c.T, c.H, c.dX, c.lddx);
         if (d.row_bytes % 128 == 0)
-            product<T, P, K_COL, K_ROW, true>(c, l.dx, w, d, c.H, c.T, c.N, part, f);
+            product<T, P, K_COL, K_ROW, true>(c, l.dx, w, d, c.H, c.T, c.N, part, f, bias);
         else
-            product<T, P, K_COL, K_ENDS, true>(c, l.dx, w, d, c.H, c.T, c.N, part, f);
+            product<T, P, K_COL, K_ENDS, true>(c, l.dx, w, d, c.H, c.T, c.N, part, f, bias);
     }
     if (c.dW)
-        product<T, P, K_COL, K_COL, true>(c, l.dw, x, d, c.H, c.N, c.T, part, Call::plain(c.N, c.H, c.dW, c.lddw));
+        product<T, P, K_COL, K_COL, true>(c, l.dw, x, d, c.H, c.N, c.T, part, Call::plain(c.N, c.H, c.dW, c.lddw),
+                                          c.dX ? BiasArgs{} : bias);
     return (int)hipGetLastError();
 }
 

@@ -181,6 +181,24 @@ def test_infinities_and_nan_stay_in_their_rows(dtype, T, N, H):
         same(db, d.double().sum(0))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,N,H", [(40, 300, 70), (66, 9000, 3), (200, 1003, 257), (300, 64, 1024)])
+@pytest.mark.parametrize("name", ["none", "gelu"])
+def test_wanted_gradients_alone(dtype, T, N, H, name):
+    """Each set of gradients has the bits that it has among all."""
+    g = gen(T)
+    X, W, dY = rand(g, T, H, dtype=dtype), rand(g, N, H, dtype=dtype, scale=H ** -0.5), rand(g, T, N, dtype=dtype)
+    b = rand(g, N, dtype=dtype)
+    Z = sg.linear_act(X, W, b, None, name, keep=True)[1]
+    want = sg.linear_act_grad(X, W, dY, Z, name)
+    check_gradients(X, W, b, dY, name, *want)
+    for flags in range(1, 8):
+        wanted = [bool(flags >> i & 1) for i in range(3)]
+        got = sg.linear_act_grad(X, W, dY, Z, name, *wanted)
+        for a, b, is_wanted in zip(got, want, wanted):
+            assert a is None if not is_wanted else torch.equal(a, b), flags
+
+
 def test_activations_far_out():
     """Slopes and values at the ends of the range: the limits, not NaN of an overflow on the way."""
     z = torch.tensor([-3e38, -1e20, -1e4, -60.0, -21.0, 0.0, 21.0, 60.0, 1e4, 1e20, 3e38, math.inf, math.nan], device="cuda")

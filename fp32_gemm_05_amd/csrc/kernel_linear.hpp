@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const float* part, int 
     const int n = blockIdx.x, m = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (m >= f.m) return;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (int z = 0; z < splits; ++z) v += *(const f32x4*)(part + (z * rows + n) * pitch + m);
     f32x4 one[1] = {v}, bias[1];
     load_bias<T>(f, m, f.m - m, bias);

@@ -33,7 +33,7 @@ struct Plan {
 // The plan that takes least by an estimate in us: the rounds of workgroups over the chip's 256 compute units, each with
 // what its slabs take at `rate` TFLOP/s of the whole chip and `end` us for its first loads and its stores; a last round
 // that leaves a unit one workgroup of `places` takes `solo` of a round, of three places two 0.67; and for a cut product 3
-// us and the pass over its parts.  The numbers are fitted to the products of 20 layers, each with every shape and cut:
+// us, 0.1 a part and the pass over them.  The numbers are fitted to the products of 20 layers, each with every shape and cut:
 // the plan takes 1 % more than the best of them in the mean.  Measured (us, M x N x k of the product, shape / splits):
 //   fp32  4096 x 1024 x 4096: M/2 253, M/1 257, S/1 270;   4096 x 4096 x 1024: M/1 252, S/1 267;
 //         5008 x 777 x 1000: S/1 90, M/4 102, M/1 128;     1000 x 777 x 5008: S/2 90, M/8 92, S/1 107;
@@ -41,18 +41,19 @@ struct Plan {
 //   bf16  8192 x 8192 x 4096: B/1 444, M/1 533, S/1 723;   4096 x 2048 x 1024: M/1 24, S/1 29, B/1 37;
 //         1024 x 4096 x 4096: S/1 43, M/1 48, M/2 48;      4096 x 100 x 8192: S/4 22, M/8 29;
 //         2048 x 2048 x 8192: M/2 79, B/4 80, S/1 82;      4096 x 8192 x 100: M/1 29, B/1 36, S/1 36.
+// (64 parts at most: 64 x 128 x 131072 fp32 with its slopes 204 with 16, 83 with 64; bf16 76, 43.)
 Plan plan_of(int P, long rows_m, long rows_n, long k) {
     const long slabs = up(k, P == 0 ? 32 : 64) / (P == 0 ? 32 : 64);
     Plan best{};
     double least = 0;
     auto look = [&](Shape shape, int bm, int bn, int places, double rate, double end, double solo) {
         const long tiles = up(rows_m, bm) / bm * (up(rows_n, bn) / bn), slots = 256L * places;
-        for (int s = 1; s <= 16 && (s == 1 || s * 4 <= slabs); s *= 2) {
+        for (int s = 1; s <= 64 && (s == 1 || s * 4 <= slabs); s *= 2) {
             const long groups = tiles * s, full = groups / slots, rest = groups - full * slots;
             const double last = rest == 0 ? 0 : rest <= 256 ? solo : places == 3 && rest <= 512 ? 0.67 : 1;
             const double flops = 2. * bm * bn * (P == 0 ? 32 : 64) * ((slabs + s - 1) / s);
             double us = (full + last) * (end + places * flops / (rate * 1e6 / 256));
-            if (s > 1) us += 3 + 4. * (s + 1) * rows_m * rows_n / (P == 0 ? 6e6 : 4.5e6);
+            if (s > 1) us += 3 + 0.1 * s + 4. * (s + 1) * rows_m * rows_n / (P == 0 ? 6e6 : 4.5e6);
             if (least == 0 || us < least) {
                 least = us;
                 best = {shape, bm, bn, s, up(rows_n, bn), up(rows_m, bm)};

@@ -182,7 +182,8 @@ def test_infinities_and_nan_stay_in_their_rows(dtype, T, N, H):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("T,N,H", [(40, 300, 70), (66, 9000, 3), (200, 1003, 257), (300, 64, 1024)])
+@pytest.mark.parametrize("T,N,H", [(40, 300, 70), (66, 9000, 3), (200, 1003, 257), (300, 64, 1024), (8191, 65, 33),
+                                   (100, 20001, 63)])
 @pytest.mark.parametrize("name", ["none", "gelu"])
 def test_wanted_gradients_alone(dtype, T, N, H, name):
     """Each set of gradients has the bits that it has among all."""

@@ -268,7 +268,9 @@ int gradient(const Call& c) {
 // 4096: 14.8 with 1x8/4, 20.1 with 1x8/1; 20 tokens, 32768 x 1024: 16.5 with 2x4/1, 20.5 with 1x8/1; 24 tokens, 3000 x 3000: 8.5 with
 // 1x4/1, 10.4 with 1x4/4; 1 token, 1024 x 8192: 8.9 with 1x4/8, 11.3 with 1x4/1; 3 tokens, 500 x 4000: 6.6 with 1x8/1, 8.6 with
 // 1x8/2; 32 tokens, 500 x 4000: 6.6 with 1x8/8, 9.8 with 1x8/1; fp32 1 token, 500 x 4000: 6.0 with 1x8/8, 11.6 with 1x8/1; 32
-// tokens, 2048 x 4096: 16.4 with 1x8/2, 24.4 with 1x8/1; 20 tokens, 4096 x 1024: 8.4 with 1x8/1, 10.6 with 1x4/1; 33 tokens, 500 x 4000: 11.3 with 1x8/8, 41 with 1x8/1.
+// tokens, 2048 x 4096: 16.4 with 1x8/2, 24.4 with 1x8/1; 20 tokens, 4096 x 1024: 8.4 with 1x8/1, 10.6 with 1x4/1; 33 tokens, 500 x 4000: 11.3 with 1x8/8, 41 with 1x8/1; 64
+// tokens, 5504 x 2752: 30.6 with 4x4/4, 53.3 with 1x8/1; 2048 x 4096: 18.7 with 4x4/8, 27.9 with 1x8/2; 8192 x 1024: 17.6 with 4x4/2,
+// 22.9 with 1x8/1.
 struct FewPlan {
     int mr, nw, splits;
     long pitch;
@@ -279,6 +281,16 @@ FewPlan few_plan(bool f32, int T, int N, int H) {
     if (nb == 4 && (N >= 64 * 192 || (N >= 64 * 96 && steps >= 64))) {
         p.mr = 4, p.nw = 4, p.splits = N >= 64 * 192 ? 1 : 2;
         return p;
+    }
+    // fp32: cutting the tokens' values into parts, anew for each workgroup, is what counts
+    if (f32 && nb == 4) {
+        const long groups = up(N, 64) / 64;
+        int s = 1;
+        while (s < 16 && groups * s < 184) s *= 2;
+        if (groups * s >= 184 && steps / (4 * s) >= 4) {
+            p.mr = 4, p.nw = 4, p.splits = s;
+            return p;
+        }
     }
     if (nb == 2 && N >= 32 * 256) {
         p.mr = 2, p.nw = 4;

@@ -51,7 +51,7 @@ def test_sizes(T, N, H, dtype, pad):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,N,H", [(33, 12300, 70), (40, 12290, 1000), (48, 300, 2000), (37, 500, 4001), (44, 6200, 2100),
-                                   (49, 300, 1500), (20, 70, 2000), (32, 1100, 3001), (5, 40, 4000), (16, 1000, 2050)])
+                                   (49, 300, 1500), (53, 3003, 3000), (64, 1500, 4096), (33, 5504, 1100), (20, 70, 2000), (32, 1100, 3001), (5, 40, 4000), (16, 1000, 2050)])
 def test_few_tokens(T, N, H, dtype):
     """Numbers of tokens between those that fill the matrix instructions, long sums of few output features."""
     step(T, N, H, dtype, "silu", 3)

@@ -103,11 +103,22 @@ __device__ inline float act(float z) {
     if constexpr (ACT == SILU) return z * sigmoid(z);
     return z;
 }
+// The slope of z s, s = 1 / (1 + exp(-w)): s (1 + q (1 - s)) with q = z dw/dz.  exp(-|w|) is taken as the square of `half`,
+// so that the slope keeps its digits as long as it is a normal number (exp(-|w|) itself is lost from -87 on, where silu's
+// slope is 10^-36).
+__device__ inline float sigmoid_slope(float w, float q) {
+    const float half = __builtin_amdgcn_exp2f(-0.72134752044448170f * fabsf(w)), e = half * half;
+    const float r = __builtin_amdgcn_rcpf(1.f + e);  // s above 0, 1 - s below
+    return w < 0.f ? half * (half * (r * __builtin_fmaf(q, r, 1.f))) : r * __builtin_fmaf(q, e * r, 1.f);
+}
+
 template <int ACT>
 __device__ inline float slope(float z) {
     if constexpr (ACT == RELU) return z > 0.f ? 1.f : z != z ? z : 0.f;
-    // past 20 each of these slopes is 0 or 1 in fp32, and z^2 below stays finite
-    const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(z, 20.f), -20.f);
+    // from 20 on each of these slopes is 1 in fp32; below -20 that of gelu and of gelu_tanh is 0 (e^-200 and less), that
+    // of silu, z exp(z) there, from -104 on.  With z held to that, z^2 below stays finite.
+    constexpr float LEAST = ACT == SILU ? -110.f : -20.f;
+    const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(z, 20.f), LEAST);
     if constexpr (ACT == GELU) {
         float bell;
         const float q = upper_tail(fabsf(c), bell);
@@ -117,10 +128,7 @@ __device__ inline float slope(float z) {
         const float s = sigmoid(2.f * kTanhA * c * __builtin_fmaf(kTanhB * c, c, 1.f));
         return __builtin_fmaf(2.f * kTanhA * c * __builtin_fmaf(3.f * kTanhB * c, c, 1.f), s * (1.f - s), s);
     }
-    if constexpr (ACT == SILU) {
-        const float s = sigmoid(c);
-        return s * __builtin_fmaf(c, 1.f - s, 1.f);
-    }
+    if constexpr (ACT == SILU) return sigmoid_slope(c, c);
     return 1.f;
 }
 // f(integral_constant) for the activation of a call; uniform.

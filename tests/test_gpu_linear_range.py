@@ -1,0 +1,69 @@
+"""GPU checks of the linear layer over the whole range of its values: activations and their slopes far out, relative to
+themselves, against 64 bits.
+
+With one hidden element and a weight of 1, Z is X, Y the activation and dX of dY = 1 its slope, which passes the products
+whole: exactly in fp32, as three bf16 parts to 2^-24, as two to 2^-16; one rounding of the result, u = 2^-24 or 2^-8.
+"""
+import math
+
+import pytest
+import torch
+
+import fp32_gemm_05_amd as sg
+from linear_reference import DT, rounded
+
+pytestmark = pytest.mark.gpu
+FAR = ("silu",)
+
+
+def slope(z, name):
+    """act' in 64 bits, with all its digits on the far negative side."""
+    if name == "gelu":
+        return 0.5 * torch.special.erfc(-z * math.sqrt(0.5)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    a, b = 2 * math.sqrt(2 / math.pi), 0.044715
+    w, rise = (z, torch.ones_like(z)) if name == "silu" else (a * (z + b * z ** 3), a * (1 + 3 * b * z * z))
+    s = torch.special.expit(w)
+    return s * (1 + z * rise * torch.special.expit(-w))
+
+
+def own_error(z, name):
+    """What a slope may be off by, of itself, where it is not near its zero: 2^-19 for exponential, reciprocal, tail and
+    the products around them, and what the exponent is off by.  It is a product of fp32 roundings: z / 2 times a constant,
+    twice, for silu; z^2 and a constant, and its tail added to it, for gelu; w of five roundings and a constant for gelu_tanh, each 2^-24 of it."""
+    exponent = {"silu": z.abs() * 2, "gelu": 2 * z * z, "gelu_tanh": 7 * 1.6 * (z.abs() + 0.0448 * z.abs() ** 3)}[name]
+    return 2.0 ** -19 + 2.0 ** -24 * exponent
+
+
+def points(dtype):
+    z = torch.cat([torch.tensor([-21.0, -25.0, -30.0, -60.0, -80.0, -86.0, -88.5, -95.0, -103.0, -110.0, -1e4, -1e30, 20.0, 25.0, 1e30]),
+                   torch.linspace(-100, -2, 1171), torch.linspace(1, 22, 37)])
+    return z.to(DT[dtype]).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", FAR)
+@pytest.mark.parametrize("T", [5, 16, 30, 64, 500])
+def test_slopes_far_out(name, dtype, T):
+    one = torch.ones(1, 1, device="cuda", dtype=DT[dtype])
+    for z in points(dtype).split(T):
+        z = z[:, None].contiguous()
+        dY = torch.ones_like(z)
+        dX, dW, dbias = sg.linear_act_grad(z, one, dY, z, activation=name)
+        want = slope(z.double(), name)
+        # below the smallest normal number digits are lost one by one; of 17 to 64 fp32 tokens below 2^-110 (three bf16 parts)
+        floor = 2.0 ** -125
+        parts = 2.0 ** -16 if dtype == "bf16" and z.shape[0] <= 64 else rounded(dX, dX.dtype)
+        tol = want.abs() * (own_error(z.double(), name) + parts + rounded(dX, dX.dtype)) + floor
+        bad = ~((dX.double() - want).abs() <= tol)
+        assert not bool(bad.any()), (z[bad].tolist()[:5], dX[bad].tolist()[:5], want[bad].tolist()[:5])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_unit_that_is_off_gets_nothing(dtype):
+    """dW, dbias and dX of units whose Z is far below 0 for all tokens."""
+    for T in (20, 300):
+        X, W = torch.ones(T, 64, device="cuda", dtype=DT[dtype]), torch.ones(40, 64, device="cuda", dtype=DT[dtype])
+        dY, Z = torch.ones(T, 40, device="cuda", dtype=DT[dtype]), torch.full((T, 40), -200.0, device="cuda", dtype=DT[dtype])
+        for name in FAR:
+            for g in sg.linear_act_grad(X, W, dY, Z, activation=name):
+                assert not g.any(), (name, T)

@@ -70,9 +70,10 @@ __device__ inline f32x4 load4(const T* p, int n = 4) {
 
 // The normal distribution's upper tail Q(t) = erfc(t / sqrt 2) / 2 for t >= 0 as k P(k) exp(-t^2 / 2), k = 1 /
 // (1 + 0.375 t): P of degree 8 fitted to the least largest relative error, 2.3e-7 (with fp32's roundings 5e-7),
-// so that the far negative side of gelu keeps its digits, which 1 + erf loses.  bell: exp(-t^2 / 2).
-__device__ inline float upper_tail(float t, float& bell) {
-    bell = __builtin_amdgcn_exp2f(-0.72134752044448170f * t * t);
+// so that the far negative side of gelu keeps its digits, which 1 + erf loses.  Returns k P(k); half: exp(-t^2 / 4),
+// multiplied twice, so that what is a normal number in the end is not lost on the way.
+__device__ inline float upper_tail(float t, float& half) {
+    half = __builtin_amdgcn_exp2f(-0.36067376022224085f * t * t);
     const float k = __builtin_amdgcn_rcpf(__builtin_fmaf(0.375f, t, 1.f));
     float p = -0.0329474956f;
     p = __builtin_fmaf(p, k, 0.137030736f);
@@ -83,7 +84,7 @@ __device__ inline float upper_tail(float t, float& bell) {
     p = __builtin_fmaf(p, k, 0.128441304f);
     p = __builtin_fmaf(p, k, 0.149604827f);
     p = __builtin_fmaf(p, k, 0.149603382f);
-    return p * k * bell;
+    return p * k;
 }
 __device__ inline float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
@@ -94,9 +95,9 @@ template <int ACT>
 __device__ inline float act(float z) {
     if constexpr (ACT == RELU) return z < 0.f ? 0.f : z;  // a NaN stays
     if constexpr (ACT == GELU) {
-        float bell;
-        const float t = fminf(fabsf(z), 20.f);  // Q is 0 in fp32 from 14 on
-        return (z < 0.f ? 0.f : z) - t * upper_tail(t, bell);
+        float half;
+        const float t = fminf(fabsf(z), 20.f), q = upper_tail(t, half);  // Q is 0 in fp32 from 14 on
+        return (z < 0.f ? 0.f : z) - half * (half * (t * q));
     }
     // (1 + tanh(w)) / 2 = sigmoid(2 w)
     if constexpr (ACT == GELU_TANH) return z * sigmoid(2.f * kTanhA * z * __builtin_fmaf(kTanhB * z, z, 1.f));
@@ -104,8 +105,8 @@ __device__ inline float act(float z) {
     return z;
 }
 // The slope of z s, s = 1 / (1 + exp(-w)): s (1 + q (1 - s)) with q = z dw/dz.  exp(-|w|) is taken as the square of `half`,
-// so that the slope keeps its digits as long as it is a normal number (exp(-|w|) itself is lost from -87 on, where silu's
-// slope is 10^-36).
+// so that the slope keeps its digits as long as it is a normal number (exp(-|w|) itself is lost from w = -87 on, where
+// the slopes are 10^-36).
 __device__ inline float sigmoid_slope(float w, float q) {
     const float half = __builtin_amdgcn_exp2f(-0.72134752044448170f * fabsf(w)), e = half * half;
     const float r = __builtin_amdgcn_rcpf(1.f + e);  // s above 0, 1 - s below
@@ -120,13 +121,13 @@ __device__ inline float slope(float z) {
     constexpr float LEAST = ACT == SILU ? -110.f : -20.f;
     const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(z, 20.f), LEAST);
     if constexpr (ACT == GELU) {
-        float bell;
-        const float q = upper_tail(fabsf(c), bell);
-        return __builtin_fmaf(c * 0.39894228040143268f, bell, c < 0.f ? q : 1.f - q);
+        float half;
+        const float q = upper_tail(fabsf(c), half);
+        return (c < 0.f ? 0.f : 1.f) + half * (half * __builtin_fmaf(c, 0.39894228040143268f, c < 0.f ? q : -q));
     }
     if constexpr (ACT == GELU_TANH) {
-        const float s = sigmoid(2.f * kTanhA * c * __builtin_fmaf(kTanhB * c, c, 1.f));
-        return __builtin_fmaf(2.f * kTanhA * c * __builtin_fmaf(3.f * kTanhB * c, c, 1.f), s * (1.f - s), s);
+        const float w = 2.f * kTanhA * c, b = kTanhB * c;
+        return sigmoid_slope(w * __builtin_fmaf(b, c, 1.f), w * __builtin_fmaf(3.f * b, c, 1.f));
     }
     if constexpr (ACT == SILU) return sigmoid_slope(c, c);
     return 1.f;

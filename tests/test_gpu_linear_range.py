@@ -28,9 +28,9 @@ def slope(z, name):
 
 def own_error(z, name):
     """What a slope may be off by, of itself, where it is not near its zero: 2^-19 for exponential, reciprocal, tail and
-    the products around them, and what the exponent is off by.  It is a product of fp32 roundings: z / 2 times a constant,
-    twice, for silu; z^2 and a constant, and its tail added to it, for gelu; w of five roundings and a constant for gelu_tanh, each 2^-24 of it."""
-    exponent = {"silu": z.abs() * 2, "gelu": 2 * z * z, "gelu_tanh": 7 * 1.6 * (z.abs() + 0.0448 * z.abs() ** 3)}[name]
+    the products around them, and what the exponent is off by.  It is a product of fp32 roundings, each 2^-24 of it: z / 2
+    times a constant, twice, for silu; w of five roundings and a constant for gelu_tanh; of gelu it is held in two parts."""
+    exponent = {"silu": z.abs() * 2, "gelu": torch.zeros_like(z), "gelu_tanh": 7 * 1.6 * (z.abs() + 0.0448 * z.abs() ** 3)}[name]
     return 2.0 ** -19 + 2.0 ** -24 * exponent
 
 
@@ -67,3 +67,20 @@ def test_a_unit_that_is_off_gets_nothing(dtype):
         for name in FAR:
             for g in sg.linear_act_grad(X, W, dY, Z, activation=name):
                 assert not g.any(), (name, T)
+
+
+@pytest.mark.parametrize("T", [5, 30, 500])
+def test_far_side_of_gelu(T):
+    """gelu(z) = z Phi(z) of negative z, relative to itself.
+
+    The tail's polynomial is off by 2.3e-7; in steps u = 2^-24 of fp32, its steps by 2 u (each adds less than 0.6 of the one
+    before), its argument by 3 u (a reciprocal and its sum) times 1.7, how steep it is, the exponential's square by 2 (2 u + u),
+    its last place and the low part's factor, and three products by u each: 16 u + 2.3e-7 < 1.2e-6 < 2^-19."""
+    z = torch.linspace(-13, -1, 3000).cuda()
+    one = torch.ones(1, 1, device="cuda")
+    for x in z.split(T):
+        Y = sg.linear_act(x[:, None].contiguous(), one, activation="gelu")[:, 0]
+        x = x.double()
+        want = x * 0.5 * torch.special.erfc(-x * math.sqrt(0.5))
+        bad = ~((Y.double() - want).abs() <= 2.0 ** -19 * want.abs() + 2.0 ** -126)
+        assert not bool(bad.any()), (x[bad].tolist()[:5], Y[bad].tolist()[:5], want[bad].tolist()[:5])

@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
     typedef typename C::Raw Raw;
     typedef typename C::Part Part;
     constexpr int U = C::P == 3 ? (NB == 4 && MR == 2 ? 2 : 1) : MR == 4 ? 2 : 4;  // steps held in registers
-    constexpr bool HOLD = sizeof(T) == 2 || NB == 1;
+    // all loads of a group before its products; not with several rows of features in fp32, where the compiler's order is faster
+    constexpr bool HOLD = sizeof(T) == 2 || MR == 1;
     static_assert(NW >= NB, "a wave for each block of tokens");
     __shared__ f32x4 sums[NW][NB][64];
     const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
@@ -490,6 +491,46 @@ __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) vx[b] = C::template load<Raw>(x[b] + (size_t)s * C::STEP, n);
         multiply(vw, vx);
+    }
+    // An infinity, and what rounds up to one as bf16, has a NaN among its three parts, and makes NaN of all its sums: a wave
+    // that finds such sums makes them anew from the values as they are (the others stay, so that a row of X or W reaches
+    // its own sums alone).
+    if constexpr (C::P == 3) {
+        bool nan = false;
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) nan |= acc[m][b][i] != acc[m][b][i];
+        if (__any(nan)) {
+            int k = g * C::E;  // anew, so that the passes above keep no address for this
+            asm volatile("" : "+v"(k));
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const T* const vw = (const T*)a.w + (size_t)imin(r0 + 16 * m + l, a.outs - 1) * a.ldw;
+                    const T* const vx = (const T*)a.x + (size_t)imin(16 * b + l, a.tokens - 1) * a.ldx;
+                    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+                    auto exact = [&](int h, int end) {  // hidden [h, end), whole steps
+#pragma unroll 1
+                        for (; h < end; h += C::STEP)
+#pragma unroll 1
+                            for (int q = 0; q < C::E; ++q) {
+                                const bool in = h + k + q < a.hidden;
+                                c = __builtin_amdgcn_mfma_f32_16x16x4f32(in ? vw[h + k + q] : 0.f, in ? vx[h + k + q] : 0.f, c, 0, 0, 0);
+                            }
+                    };
+#pragma unroll 1
+                    for (int q = first + wave; q < last; q += NW) exact(q * U * C::STEP, (q + 1) * U * C::STEP);
+#pragma unroll 1
+                    for (int s = groups * U + wave; s < steps; s += NW) exact(s * C::STEP, (s + 1) * C::STEP);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (acc[m][b][i] != acc[m][b][i]) acc[m][b][i] = c[i];
+                }
+        }
     }
     // wave b gets tokens 16 b + l, output features r0 + 16 m + 4 g + i
     f32x4 z[MR];

@@ -22,9 +22,10 @@
  * computed from the unrounded Z, dX, dW and dbias from fp32 sums.  In bf16 the kept Z is rounded to bf16, and so is
  * dZ on its way into dX and dW (of up to 64 tokens it enters as two bf16 parts, 16 bits); dbias sums it before that.
  *
- * Products: bf16 operands on the bf16 matrix instructions.  fp32 operands on the fp32 ones, with infinities, NaN and
- * values of any scale as in any fp32 sum; of 17 to 64 tokens as three bf16 parts each, 24 bits, of values from
- * 2^-110 to 2^127, where an infinity may come out as NaN, as it may in a gradient of up to 64 tokens.  A row of X, dY or
+ * Products: bf16 operands on the bf16 matrix instructions.  fp32 operands on the fp32 ones; of 17 to 64 tokens as three
+ * bf16 parts each, 24 bits, without what lies below 2^-126 (the last digits of values below 2^-110).  Infinities, NaN
+ * and the largest values come out as in any fp32 sum, whatever the number of tokens, but in a gradient of up to 64:
+ * there an infinity, and of 17 to 64 fp32 tokens a value from 2^127 on, may come out as NaN.  A row of X, dY or
  * residual reaches its own row of Y and dX alone.
  *
  * Memory and streams: device pointers owned by the caller, work enqueued on `stream`, no wait, no allocation, no

@@ -84,3 +84,75 @@ def test_far_side_of_gelu(T):
         want = x * 0.5 * torch.special.erfc(-x * math.sqrt(0.5))
         bad = ~((Y.double() - want).abs() <= 2.0 ** -19 * want.abs() + 2.0 ** -126)
         assert not bool(bad.any()), (x[bad].tolist()[:5], Y[bad].tolist()[:5], want[bad].tolist()[:5])
+
+
+def same(got, want):
+    """Infinities and NaN where 64 bits have them."""
+    assert bool((got.isnan() == want.isnan()).all()) and bool((got.isinf() == want.isinf()).all())
+    assert bool((got.sign() == want.sign())[got.isinf()].all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,H", [(16, 70, 100), (17, 70, 100), (20, 9000, 70), (32, 300, 2051), (37, 77, 1000), (50, 130, 33),
+                                   (64, 12300, 64), (64, 6200, 2100), (65, 70, 100)])
+def test_infinities_whatever_the_number_of_tokens(dtype, T, N, H):
+    """In X, in W, and both signs in one sum; the other rows' and columns' bits stay as they are."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    X = torch.randn(T, H, generator=g, device="cuda").to(DT[dtype])
+    W = torch.randn(N, H, generator=g, device="cuda").to(DT[dtype])
+    clean = sg.linear_act(X, W)
+    for value in (math.inf, -math.inf, math.nan):
+        for t, n, h in ((T - 1, N - 1, H - 1), (0, 0, 0), (T // 2, N // 2, H // 2)):
+            x = X.clone()
+            x[t, h] = value
+            y = sg.linear_act(x, W)
+            same(y, x.double() @ W.double().t())
+            y[t] = clean[t]
+            assert torch.equal(y, clean)
+            w = W.clone()
+            w[n, h] = value
+            y = sg.linear_act(X, w)
+            same(y, X.double() @ w.double().t())
+            y[:, n] = clean[:, n]
+            assert torch.equal(y, clean)
+    x, w = X.clone(), W.clone()
+    x[1, 0], x[1, H - 1], w[2, 1] = math.inf, -math.inf, -math.inf
+    x[3, 1] = 0.0  # times an infinity
+    same(sg.linear_act(x, w), x.double() @ w.double().t())
+    x = X.clone()
+    x[T - 1] = -math.inf
+    w = W.abs() + 1
+    y = sg.linear_act(x, w, activation="relu")
+    assert not y[T - 1].any() and bool(y.isfinite().all())
+
+
+@pytest.mark.parametrize("T", [5, 20, 37, 50, 64, 100])
+@pytest.mark.parametrize("name", ["none", "relu"])
+def test_largest_numbers(T, name):
+    """fp32 values up to the largest: sums of one such product and others of its scale, within an fp32 sum's error."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    most, N, H = torch.finfo(torch.float32).max, 90, 77
+    X = torch.randn(T, H, generator=g, device="cuda") * 1e30
+    X[:, 5] = most * (1 - 2.0 ** -12 * torch.rand(T, generator=g, device="cuda"))
+    X[::3, 5] = -most
+    W = torch.randn(N, H, generator=g, device="cuda")
+    W[:, 5] = 0.25 + 0.5 * torch.rand(N, generator=g, device="cuda")
+    Y = sg.linear_act(X, W, activation=name)
+    x, w = X.double(), W.double()
+    want, S = x @ w.t(), x.abs() @ w.abs().t()
+    want = want.clamp(min=0) if name == "relu" else want
+    assert bool(((Y.double() - want).abs() <= (H + 8) * 2.0 ** -24 * S).all())
+
+
+def test_far_out_whatever_the_number_of_tokens():
+    """Activations at the ends of the range."""
+    z = torch.tensor([-3e38, -1e20, -1e4, -60.0, 21.0, 60.0, 1e4, 1e20, 3e38, math.inf, math.nan], device="cuda")
+    n, W = len(z), torch.ones(1, 1, device="cuda")
+    for times in (1, 2, 4, 5, 10):
+        x = z.repeat(times)[:, None].contiguous()
+        for name in ("relu", "gelu", "gelu_tanh", "silu"):
+            Y, Z = sg.linear_act(x, W, activation=name, keep=True)
+            assert torch.equal(Z[:n - 1], x[:n - 1]) and bool(Z[n - 1].isnan())
+            assert torch.equal(Y[4:n - 1], x[4:n - 1]) and bool(Y[n - 1].isnan())
+            # z exp(z) at -60: 5e-25
+            assert bool((Y[:4].abs() < 1e-24).all())

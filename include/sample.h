@@ -17,7 +17,7 @@
  *
  * Probabilities are added up as whole multiples of 2^-40 of the largest one, in 64 bits, so that a token does not
  * depend on timing or on how the work is cut.  exp(-x) of the distance x from the largest logit is off by up to
- * 2^-22 + 2^-24 x of itself.  A token whose probability is below 2^-41 of the largest one's is not drawn, nor is one
+ * 2^-22 + 2^-23 x of itself.  A token whose probability is below 2^-41 of the largest one's is not drawn, nor is one
  * whose logit lies more than 3.4e38 below it, at any temperature; a temperature below 2^-119 counts as 2^-119.
  *
  * temperature, top_k, top_p and min_p are one value for all rows, or with a pointer (device memory) one for each.

@@ -129,6 +129,8 @@ def _call(name, tensors, out, stream, *settings):
         norm = torch.empty((), dtype=torch.float32, device=device)
         work = torch.empty(n, dtype=torch.uint8, device=device)
         _library.call(name, count, at, *settings, norm.data_ptr(), work.data_ptr(), n, handle_of(device))
+        if settings:  # clipping has written them: autograd must not take them for what it saved
+            torch.autograd.graph.increment_version(tensors if out is None else out)
         return norm
     return on_stream(device, stream, tensors if out is None else tensors + out, body)
 
@@ -140,7 +142,8 @@ def grad_norm(tensors, stream=None):
 
 def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, out=None, stream=None):
     """Multiplies the tensors by min(1, max_norm / (norm + eps)), in place or into the tensors `out` (each of its
-    tensor's shape and type); returns their norm as it was.  No autograd graph sees it."""
+    tensor's shape and type); returns their norm as it was.  It is no part of autograd, which sees a change in place, as of
+    torch's own operations: a backward pass that has saved a tensor clipped since raises an error."""
     return _call("clip_grad_norm", tensors, out, stream, float(max_norm), float(eps))
 
 

@@ -261,16 +261,13 @@ int gradient(const Call& c) {
     return (int)hipGetLastError();
 }
 
-// Few tokens' forward product: 16 mr output features a workgroup of nw waves, the hidden size in `splits` parts.
-// Many features a workgroup read the tokens' side less often, few fill the chip; long sums of few workgroups are cut.
-// Measured (us, features x waves / splits): bf16 64 tokens, 32768 x 1024: 21.2 with 4x4/1, 27.0 with 2x4/1, 40.3 with
-// 1x8/1; 8192 x 4096: 23.4 with 4x4/2, 33.9 with 4x4/1, 27.7 with 2x4/1; 4096 x 1024: 8.3 with 1x8/1, 10.5 with 2x4/1; 2048 x
-// 4096: 14.8 with 1x8/4, 20.1 with 1x8/1; 20 tokens, 32768 x 1024: 16.5 with 2x4/1, 20.5 with 1x8/1; 24 tokens, 3000 x 3000: 8.5 with
-// 1x4/1, 10.4 with 1x4/4; 1 token, 1024 x 8192: 8.9 with 1x4/8, 11.3 with 1x4/1; 3 tokens, 500 x 4000: 6.6 with 1x8/1, 8.6 with
-// 1x8/2; 32 tokens, 500 x 4000: 6.6 with 1x8/8, 9.8 with 1x8/1; fp32 1 token, 500 x 4000: 6.0 with 1x8/8, 11.6 with 1x8/1; 32
-// tokens, 2048 x 4096: 16.4 with 1x8/2, 24.4 with 1x8/1; 20 tokens, 4096 x 1024: 8.4 with 1x8/1, 10.6 with 1x4/1; 33 tokens, 500 x 4000: 11.3 with 1x8/8, 41 with 1x8/1; 64
-// tokens, 5504 x 2752: 30.6 with 4x4/4, 53.3 with 1x8/1; 2048 x 4096: 18.7 with 4x4/8, 27.9 with 1x8/2; 8192 x 1024: 17.6 with 4x4/2,
-// 22.9 with 1x8/1.
+// Few tokens' forward product: 16 mr output features a workgroup of nw waves, the hidden size in `splits` parts ("mr x nw /
+// splits" below).  Many features a workgroup read the tokens' side less often, and cut it into parts less often in fp32; few,
+// and parts of the hidden size, fill the chip, but parts cost a second launch and a pass over their sums, some 2.5 us and
+// more.  Each rule stands with the figures (us) of both its sides.  Of 98 sizes a type and number of tokens, 500 x 256 to
+// 32768 x 2048 and 6144 x 8192, the plan takes 4 - 5 % more than the best of all in the mean with up to 16 tokens, 7 - 11 %
+// with more: long sums of few features are cut too little there (fp32 64 tokens, 500 x 2048: 20.8, best 8.3 with 1x8/8; 20
+// tokens, 6144 x 8192: 75, best 45 with 2x4/4).
 struct FewPlan {
     int mr, nw, splits;
     long pitch;
@@ -278,11 +275,18 @@ struct FewPlan {
 FewPlan few_plan(bool f32, int T, int N, int H) {
     const int nb = T > 32 ? 4 : T > 16 ? 2 : 1, steps = (int)(up(H, 32) / (f32 && nb == 1 ? 16 : 32));
     FewPlan p{1, 8, 1, up(N, 64)};
+    // 33 tokens and more: 64 features a workgroup once three of four compute units have one (bf16 64 tokens, 32768 x 1024: 20
+    // with 4x4/1, 39 with 1x8/1; 12288 x 1024: 12.5, 16.7; 8192 x 1024 they are even, 12.1, 12.2; fp32 12288 x 1024: 23.5,
+    // 31.2); from half of that on with the hidden size in two, where it is long (bf16 64 tokens, 6144 x 2048: 15.3 with
+    // 4x4/2, 18.8 with 4x4/1, 20.9 with 1x8/1; 4096 x 2048: 14.6, 18.7, 12.4)
     if (nb == 4 && (N >= 64 * 192 || (N >= 64 * 96 && steps >= 64))) {
         p.mr = 4, p.nw = 4, p.splits = N >= 64 * 192 ? 1 : 2;
         return p;
     }
-    // fp32: cutting the tokens' values into parts, anew for each workgroup, is what counts
+    // fp32: cutting the tokens' values into parts, anew for each workgroup, is what counts: 64 features a workgroup as above,
+    // with as many parts as give about as many workgroups, if each wave keeps four steps (64 tokens, 2048 x 4096: 18.9 with
+    // 4x4/8, 25 with 1x8/4, 38 with 1x8/1; 8192 x 1024: 18.2 with 4x4/2, 21.7 with 1x8/1; with two steps, 4096 x 1024: 14.9
+    // with 4x4/4, 12.9 with 1x8/1)
     if (f32 && nb == 4) {
         const long groups = up(N, 64) / 64;
         int s = 1;
@@ -292,12 +296,22 @@ FewPlan few_plan(bool f32, int T, int N, int H) {
             return p;
         }
     }
+    // 17 to 32: 32 features once all compute units have a workgroup (20 tokens, 32768 x 1024: bf16 16.5 with 2x4/1, 20.5 with
+    // 1x8/1; 8192 x 1024: fp32 11.7, 13.3; bf16 7.1, 7.4; 4096 x 1024: fp32 11.3, 8.4; bf16 6.5, 5.0)
     if (nb == 2 && N >= 32 * 256) {
         p.mr = 2, p.nw = 4;
         return p;
     }
+    // else 16 features a workgroup, of four waves from 64 workgroups on, of eight before, and of eight with 33 tokens or more
+    // and where fp32 is cut into parts (bf16 1 token, 32768 x 1024: 12.0 with 1x4/1, 12.1 with 1x8/1; 2048 x 1024: 4.4, 4.4;
+    // 1000 x 1024: 4.6, 4.4; fp32 20 tokens, 4096 x 1024: 8.9, 8.4)
     const long blocks = up(N, 16) / 16;
     if (!(f32 && nb == 2) && nb < 4 && blocks >= 64) p.nw = 4;
+    // a sum is cut once a wave has `from` steps or more of it, in two again and again until it has at most `to` or the
+    // workgroups are 256 (bf16 1 token, 1000 x 8192: 8.0 with 1x8/4, 11.3 with 1x8/1; 500 x 4096, 16 steps: 6.7, 6.9; 4096 x
+    // 4096: 8.9 with 1x4/1, 10.8 with 1x4/2; fp32 1 token, 500 x 4096: 7.1 with 1x8/8, 11.7 with 1x8/1; 500 x 2048: 7.3 with
+    // 1x8/4, 7.2 with 1x8/1; 32 tokens, 2048 x 4096: 16.5 with 1x8/2, 23.7 with 1x8/1; 40 tokens, 500 x 4096: 9.4 with 1x8/8,
+    // 28.5 with 1x8/1; 4096 x 1024: 10.3 with 1x8/1, 13.3 with 1x8/2)
     const int from = p.nw == 4 ? 32 : nb > 1 ? 12 : f32 ? 16 : 32, to = nb == 1 ? (f32 ? 4 : 8) : f32 ? 2 : 4;  // steps of a wave
     if (steps / p.nw >= from)
         while (steps / (p.nw * p.splits) > to && blocks * p.splits < 256 && p.splits < 16) p.splits *= 2;

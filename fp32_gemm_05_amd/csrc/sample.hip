@@ -8,8 +8,15 @@ namespace {
 
 constexpr int kMaxRows = 1 << 21, kMaxVocab = 1 << 23;  // 2^23 probabilities of 2^40 are below 2^64
 
-// Whether a row is shared by several workgroups: of long rows, where the rows leave half of the 256 compute units
-// idle, until about all have a workgroup, each with a vector a thread or more.
+// Whether a row is shared by several workgroups: rows of more than 8 vectors a thread (32768 fp32 logits, 65536 bf16), what the
+// row kernel keeps in registers, where at most 128 rows leave half of the 256 compute units idle, until about all have a
+// workgroup, each with a vector a thread or more.  Four launches cost some 10 us more than one, which the passes over
+// 131072 logits win back (us, shared / a workgroup a row; top_p 0.9, no filter, top_k 2000):
+//   1 row    fp32 65536: 35 / 29, 23 / 20, 37 / 35;   fp32 131072: 35 / 43, 23 / 34, 37 / 53;   bf16 131072: 36 / 41, 24 / 27, 36 / 54
+//   64 rows  fp32 65536: 43 / 39, 27 / 20, 42 / 36;   fp32 131072: 54 / 71, 33 / 35, 49 / 54;   bf16 131072: 50 / 64, 28 / 28, 50 / 55
+//   128 rows fp32 36864: 44 / 29, 28 / 15, 44 / 28;   fp32 131072: 78 / 83, 47 / 41, 69 / 67;   bf16 131072: 66 / 66, 38 / 28, 170 / 107
+// With 8 vectors or fewer sharing loses throughout (1 row of fp32 32768: 33 / 21, 22 / 12, 35 / 24; 64 of bf16 65536: 43 / 38,
+// 25 / 16, 42 / 34).  In between, and of 128 rows, it loses too but for top_p of bf16: the limits stand early.
 struct Split {
     int splits, vectors;
     long state, count, mass, list, bytes;
@@ -38,8 +45,9 @@ template <typename T>
 void launch(int rows, const Args& a, char* work, hipStream_t stream) {
     constexpr int N = 16 / sizeof(T);
     const Split p = split_of(sizeof(T), rows, a.vocab);
-    // a small top_k of all rows needs one pass after the largest, which sharing does not pay for (64 rows of 131072 bf16,
-    // top_k 50, top_p 0.9: 24 us, shared 40; without top_k 68, shared 53)
+    // a small top_k of all rows needs one pass after the largest, which sharing does not pay for (64 rows of 131072 bf16, us,
+    // in the row kernel / shared: top_k 50 24 / 38, 512 37 / 43; with top_p 0.9 26 / 40, 42 / 48; 1 row of 131072 fp32: 22 /
+    // 31, 36 / 35)
     const bool quick = !a.top_ks && a.top_k > 0 && a.top_k <= kThreads / 2;
     if (p.splits > 1 && !quick) {
         const SplitArgs s{a, p.splits, p.vectors, (State*)(work + p.state), (uint32_t*)(work + p.count),

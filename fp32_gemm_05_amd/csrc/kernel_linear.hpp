@@ -155,7 +155,8 @@ struct Finish {
     const void* bias;   // [m] or null
     const void* residual;
     long ld_residual;
-    void* z;            // null: not kept
+    void* z;            // null: not kept; in the operands' type: fp32 beside bf16 operands would move twice the bytes for slopes
+                        // off by 1e-3 less (the gradients by 6e-5 of their norm)
     long ld_z;
     void* out;
     long ld;
@@ -344,6 +345,12 @@ struct SlopeArgs {
 
 // dZ = dY act'(Z), in the operands' type for the products, and its column sums over `per` rows, of
 // the values before they are rounded.
+//
+// In bf16 dZ is rounded to 8 bits for the products, as the upstream gradient of a bf16 layer is: dX and dW are off by 2.35e-3
+// of their norm so, with the kept Z's rounding, which moves the slopes, by 2.41e-3 (777 x 5003 x 1001 and 8192 x 8192 x 4096
+// alike), where the rounding of the results alone makes 1.66e-3.  As two bf16 parts, which up to 64 tokens take since the read of
+// W hides them, dZ would make the products' long axis twice as long: dX and dW of 8192 x 8192 x 4096 908 us, so 1753; of 776 x
+// 5008 x 1000 46, so 66.
 template <typename T>
 __device__ inline void slopes(const SlopeArgs& a, int block) {
     constexpr int V = 16 / sizeof(T), U = 4;
@@ -430,8 +437,10 @@ struct FewArgs {
 
 // Z of 16 MR output features and all tokens, or a part of the hidden size of it where the features alone do not fill
 // the chip.  Bound by the read of W (32768 x 1024 bf16 to 64 tokens' fp32 logits: 20.3 us, 3.7 TB/s with the 8 MB written; the
-// read alone is 14 us), of 17 to 64 fp32 tokens by cutting both sides into three parts (37 tokens, 5003 x 777: 11.8 us where the
-// bytes take 3.6), of one token by the launch and one trip to memory (4096 x 1024: 4.3 us, an empty kernel 1.65).
+// read alone is 14 us), of 17 to 64 fp32 tokens by latency: a step's loads in flight a wave,
+// and cutting both sides into three parts before the next (37 tokens, 5003 x 777: 11.6 us where the bytes take 3.6; half of the waves'
+// time waits for loads, a quarter to issue, the VALU is busy for a third of it), of one token by the launch and one trip to memory (4096 x
+// 1024: 4.3 us, an empty kernel 1.65).
 // The NW waves of a workgroup take every NW-th group of U steps of the hidden size each and add up in LDS.
 template <class C, int NB, int MR, int NW>
 __global__ void __launch_bounds__(64 * NW) linear_few_kernel(FewArgs a) {
